@@ -17,6 +17,9 @@
  *   - the writer side: a batched page copy (copy-on-write) and the zeroing of the
  *     slots no sequence reads,
  *   - decode attention that reads K and V through the block table,
+ *   - the operators of a serving step around them: block tables and slot maps from the
+ *     requests' lengths, norm + rotation + append in one pass, and attention over a cache
+ *     of shared latent rows (absorbed for decode, expanded for prompts),
  *   - conversions between a kernel-internal cache layout and the interchange layout,
  *     and between a padded block table and the descriptor's slices.
  *
@@ -483,6 +486,252 @@ int hp_attention_decode_planned(const hp_paged_desc* k_desc, const void* v_pool,
                                 uint32_t num_q_heads, float scale, float* out,
                                 const void* workspace, uint64_t workspace_bytes, int* d_status,
                                 void* stream);
+
+/* ------------------------------------------------------------- a serving step */
+/*
+ * A serving step over the paged cache, as the calls line up on one stream: hp_step_tables
+ * grows the block tables and says which slot each new token takes; hp_qk_norm_rope_append
+ * (K/V heads) or hp_latent_append (one shared latent row per token) finishes a projection's
+ * output and stores it in those slots, layer by layer; then hp_attention_decode, or
+ * hp_latent_decode / hp_latent_prefill, reads the pages.  (The pages cited above define the
+ * layout these operators read and write; the operators themselves are this library's.)
+ */
+
+/*
+ * One step's block tables.  Sequence s holds seq_lens[s] tokens and the slice
+ * block_table[seq_ptr[s] .. seq_ptr[s+1]) and adds new_lens[s] tokens:
+ *   need[s] = max(slice length, ceil((seq_lens[s] + new_lens[s]) / page_size)) pages;
+ *   the grown table holds, sequence after sequence, the old slice and then the pages it is
+ *   given: sequence 0 takes the first need[0] - (slice length) entries of free_pages, sequence
+ *   1 the next ones, and so on.  (A finished request is left out by the caller, who keeps the
+ *   free list; a reserved page beyond need stays in its slice.)
+ * Outputs (device):
+ *   table_out     table_cap entries; the first total are written
+ *   seq_ptr_out   num_seqs+1 entries; lens_out: seq_lens + new_lens
+ *   new_ptr_out   num_seqs+1 entries: prefix sums of new_lens (an append's new_ptr)
+ *   slot_map      token_cap entries, int64: page * page_size + slot of each new token, in
+ *                 sequence order; -1 from the last new token on (the rows of a padded batch)
+ *   positions     token_cap entries: the token's index in its sequence; 0 past the last
+ *   totals        3 uint64 (may be NULL): table entries, new tokens, pages taken
+ * block_table, free_pages: device arrays of `index_type`, as are all others without a type.
+ * Their entries are copied as they are (the readers check them against the pool).
+ */
+typedef struct hp_step_desc {
+    uint32_t index_type;      /* hp_index_type */
+    uint32_t reserved;        /* 0 */
+    uint64_t num_seqs;
+    uint64_t page_size;
+    uint64_t table_len;       /* entries of block_table */
+    uint64_t num_free;        /* entries of free_pages */
+    uint64_t table_cap;       /* entries table_out has room for */
+    uint64_t token_cap;       /* entries slot_map and positions have room for */
+    const void* block_table;  /* may be NULL iff table_len == 0 */
+    const void* seq_ptr;
+    const void* seq_lens;     /* may be NULL iff num_seqs == 0, as new_lens */
+    const void* new_lens;
+    const void* free_pages;   /* may be NULL iff num_free == 0 */
+    void* table_out;          /* may be NULL iff table_cap == 0 */
+    void* seq_ptr_out;
+    void* lens_out;           /* may be NULL iff num_seqs == 0 */
+    void* new_ptr_out;
+    int64_t* slot_map;        /* may be NULL iff token_cap == 0, as positions */
+    void* positions;
+    uint64_t* totals;
+} hp_step_desc;
+
+/* Device workspace (256-byte aligned) hp_step_tables needs for num_seqs sequences. */
+int hp_step_tables_workspace_bytes(uint64_t num_seqs, uint64_t* bytes);
+
+/*
+ * ASYNC.  Builds the tables of one step (hp_step_desc).  Host checks, in order: step NULL
+ * (HP_ERR_NULL), index type, page_size 0 (HP_ERR_ZERO_PAGE_SIZE), reserved not 0 (HP_ERR_ARG),
+ * sizes beyond 2^58 (HP_ERR_OVERFLOW), NULL and misaligned buffers (element alignment),
+ * workspace.  On the device, in this order: seq_ptr (HP_ERR_SEQ_PTR_START, _ORDER, _END), a
+ * sequence whose seq_lens exceed its slice, or whose grown length does not fit the index type
+ * or 2^58 (HP_ERR_LEN), free_pages too short (HP_ERR_CAPACITY), more than table_cap entries or
+ * token_cap tokens, or with uint32 indices more than 2^32-1 of either (HP_ERR_OUT_SIZE);
+ * then nothing but *d_status is written.  The outputs must not overlap the inputs or each
+ * other.
+ */
+int hp_step_tables(const hp_step_desc* step, void* workspace, uint64_t workspace_bytes,
+                   int* d_status, void* stream);
+
+/*
+ * The position rotation of the two appends below.  Pair i of a vector's first rot_dim
+ * dimensions -- dimensions (i, i + rot_dim/2), or (2i, 2i+1) when `interleaved` -- turns by an
+ * angle whose cosine and sine stand in row p of cos_sin at columns i and rot_dim/2 + i, p the
+ * token's position on the pair's axis: (a, b) -> (a cos - b sin, b cos + a sin).  Pairs 0 ..
+ * section[0]-1 follow axis 0, the next section[1] axis 1, and so on (text uses one axis;
+ * images and video time, height and width).  A caller fills the table once, with whatever
+ * frequencies and scaling its model uses.
+ */
+typedef struct hp_rope_desc {
+    const float* cos_sin;   /* device, fp32 [max_pos, rot_dim], 16-byte aligned */
+    const void* positions;  /* device, [axes, num_tokens] of index_type */
+    uint64_t max_pos;
+    uint32_t rot_dim;       /* a multiple of 16 */
+    uint32_t axes;          /* 1 .. 4 */
+    uint32_t section[4];    /* pairs of each axis; the first `axes` add up to rot_dim / 2 */
+    uint32_t interleaved;   /* 0 or 1 */
+    uint32_t index_type;    /* of positions */
+} hp_rope_desc;
+
+/*
+ * Queries, keys and values of num_tokens tokens, as a projection leaves them: element
+ * (t, h, d) of q at q[t * q_stride + h * head_dim + d], k and v likewise (strides in
+ * elements, so the three may be slices of one fused projection's rows).
+ */
+typedef struct hp_qk_desc {
+    uint32_t dtype;         /* HP_F32, HP_F16 or HP_BF16: every buffer below */
+    uint32_t num_q_heads;   /* may be 0 (a layer that appends only); q and q_out then unused */
+    uint32_t num_kv_heads;  /* at least 1 */
+    uint32_t head_dim;      /* a multiple of 8 up to 256 */
+    float eps;
+    uint32_t reserved;      /* 0 */
+    uint64_t num_tokens;
+    const void* q;
+    const void* k;
+    const void* v;
+    uint64_t q_stride, k_stride, v_stride;
+    void* q_out;            /* (t, h, d) at t * q_out_stride + h * head_dim + d; may be q itself
+                               with the same stride */
+    uint64_t q_out_stride;
+    const void* q_weight;   /* head_dim gains of the norm; NULL: q is not normalised */
+    const void* k_weight;   /* the same for k */
+    const int64_t* slot_map;/* num_tokens slots (hp_step_tables); negative: a padding token */
+    void* k_pool;           /* [num_pages, page_size, num_kv_heads, head_dim] */
+    void* v_pool;
+    uint64_t num_pages;
+    uint64_t page_size;
+} hp_qk_desc;
+
+/*
+ * ASYNC.  For each token t with slot_map[t] >= 0: every query and key head is normalised,
+ * x <- x / sqrt(mean_d x_d^2 + eps) * weight_d (where its weight is given), its first rot_dim
+ * dimensions are rotated (hp_rope_desc; rope NULL: no rotation), the query goes to q_out, the
+ * key and the value (copied as it is) to slot slot_map[t] of k_pool and v_pool.  Arithmetic
+ * is fp32, rounded once to `dtype`.  A padding token's rows are left as they were.  A token
+ * whose slot lies outside the pool (HP_ERR_PAGE_ID) or whose position is not below max_pos
+ * (HP_ERR_LEN) is skipped; the first such token's code goes to *d_status.  Two tokens naming
+ * one slot leave an unspecified one of them.  q, k, v, q_out, weights and pools: 16-byte
+ * aligned, strides multiples of 16 bytes (HP_ERR_ALIGN); rot_dim at most head_dim
+ * (HP_ERR_ARG).  q_out must not overlap k, v or the pools.
+ */
+int hp_qk_norm_rope_append(const hp_qk_desc* qk, const hp_rope_desc* rope, int* d_status,
+                           void* stream);
+
+/*
+ * Shared-latent attention ("latent attention"): a token's cache row is one latent vector c of
+ * latent_dim elements, from which the keys and values of every head are linear maps, followed
+ * by one rotated key of rope_dim elements shared by all heads.  The cache is a block-paged
+ * pool with num_heads = 1 and head_dim = latent_dim + rope_dim.
+ */
+typedef struct hp_latent_desc {
+    uint32_t dtype;          /* HP_F32, HP_F16 or HP_BF16: every buffer below */
+    uint32_t latent_dim;     /* a multiple of 8 up to 1024 */
+    uint32_t num_q_heads;    /* may be 0; q_rope and q_out are then unused */
+    float eps;
+    uint64_t num_tokens;
+    const void* latent;      /* (t, d) at t * latent_stride + d */
+    uint64_t latent_stride;
+    const void* latent_weight; /* latent_dim gains of the norm; NULL: not normalised */
+    const void* k_rope;      /* (t, d) at t * k_rope_stride + d, d < rope->rot_dim */
+    uint64_t k_rope_stride;
+    const void* q_rope;      /* (t, h, d) at t * q_stride + h * q_head_stride + d */
+    uint64_t q_stride, q_head_stride;
+    void* q_out;             /* (t, h, d) at t * q_out_stride + h * q_out_head_stride + d; may
+                                be q_rope itself with the same strides */
+    uint64_t q_out_stride, q_out_head_stride;
+    const int64_t* slot_map; /* num_tokens slots; negative: a padding token */
+    void* pool;              /* [num_pages, page_size, latent_dim + rot_dim] */
+    uint64_t num_pages;
+    uint64_t page_size;
+} hp_latent_desc;
+
+/*
+ * ASYNC.  For each token with slot_map[t] >= 0: the latent vector normalised as in
+ * hp_qk_norm_rope_append, then the rotated k_rope (all its rot_dim elements), go to slot
+ * slot_map[t] of the pool; each query head's rot_dim rotary elements are rotated into q_out.
+ * `rope` is required.  Rounding, padding tokens, errors and alignment are as in
+ * hp_qk_norm_rope_append.
+ */
+int hp_latent_append(const hp_latent_desc* latent, const hp_rope_desc* rope, int* d_status,
+                     void* stream);
+
+/*
+ * Bytes of device workspace hp_latent_decode needs: the plan's (hp_workspace_bytes) plus
+ * fp32 records (max, sum and latent_dim accumulators) of the row tiles that workers share.
+ * It depends on num_seqs, latent_dim and the device's limits only, not on the lengths.
+ */
+int hp_latent_decode_workspace_bytes(const hp_paged_desc* desc, uint32_t latent_dim,
+                                     uint64_t total_q, uint32_t num_q_heads, uint64_t* bytes);
+
+/*
+ * ASYNC.  Attention over a paged latent cache, absorbed form: the queries were multiplied by
+ * the key projection beforehand, so that scores and values come from the cache rows as they
+ * are.  desc: the latent pool (num_heads 1, head_dim = latent_dim + rope_dim), HP_F16 or
+ * HP_BF16, with the lengths AFTER the append.  q (device, [total_q, num_q_heads, head_dim] of
+ * the pool's type): sequence s has the n = q_ptr[s+1] - q_ptr[s] queries q_ptr[s] ..., its last
+ * n tokens in order, so query i of them sees the tokens t < len_s - n + 1 + i:
+ *   score_t = scale * sum_{d < head_dim} q[d] * C(s, t)[d],  weights = softmax over t,
+ *   out[d] = sum_t weight_t * C(s, t)[d],  d < latent_dim,
+ * C(s, t) the pool row of token t.  A query that sees no token (an empty sequence, or more
+ * queries than tokens) gets zeros.  q_ptr (device, num_seqs+1 entries of the index type;
+ * q_ptr[num_seqs] <= total_q: the rows of q and out behind the last sequence are neither read
+ * nor written) may be NULL: one query per sequence, total_q = num_seqs.
+ * out (device, [total_q, num_q_heads, latent_dim], the pool's type).  Scores, softmax
+ * statistics and sums are fp32; the weights enter the value product rounded to the pool's
+ * type, and the result is rounded once.  The values of every token below seq_lens have to be
+ * finite (a query's weight for a later token of its sequence is zero, not absent); slots past
+ * a sequence's length may hold anything.
+ * Supported: latent_dim a multiple of 64 up to 512; rope_dim a multiple of 8 from 8 to 64;
+ * page_size <= 2^26 (HP_ERR_ARG otherwise); device memory.  latent_dim 512 with rope_dim 64
+ * and pages of 8, 16, 32 or a multiple of 64 slots run on the tensor cores, the others on the
+ * CUDA cores (HP_ATTN_CUDA_CORES in desc->flags asks for those always).  The descriptor is
+ * always validated, as in hp_attention_decode; q_ptr with the codes of an append's new_ptr.
+ */
+int hp_latent_decode(const hp_paged_desc* desc, uint32_t latent_dim, const void* q,
+                     const void* q_ptr, uint64_t total_q, uint32_t num_q_heads, float scale,
+                     void* out, void* workspace, uint64_t workspace_bytes, int* d_status,
+                     void* stream);
+
+/* The two halves of hp_latent_decode, for layers that share a table: as hp_attention_plan and
+ * hp_attention_decode_planned.  The planned calls name the plan's descriptor (but for
+ * page_pool), q_ptr, total_q and num_q_heads. */
+int hp_latent_plan(const hp_paged_desc* desc, uint32_t latent_dim, const void* q_ptr,
+                   uint64_t total_q, uint32_t num_q_heads, void* workspace,
+                   uint64_t workspace_bytes, int* d_status, void* stream);
+int hp_latent_decode_planned(const hp_paged_desc* desc, uint32_t latent_dim, const void* q,
+                             const void* q_ptr, uint64_t total_q, uint32_t num_q_heads,
+                             float scale, void* out, void* workspace, uint64_t workspace_bytes,
+                             int* d_status, void* stream);
+
+/* Bytes of device workspace hp_latent_prefill needs: the plan's, the latent rows and the
+ * expanded keys and values of up to kv_tokens tokens, each sequence padded to 128. */
+int hp_latent_prefill_workspace_bytes(const hp_paged_desc* desc, uint32_t latent_dim,
+                                      uint32_t nope_dim, uint32_t v_dim, uint64_t total_q,
+                                      uint32_t num_q_heads, uint64_t kv_tokens, uint64_t* bytes);
+
+/*
+ * ASYNC.  Attention over a paged latent cache, expanded form (prompts): the keys and values of
+ * every head are projected up from the latent rows once, K_h(t) = [W_h^K c_t | rotated key of
+ * t], V_h(t) = W_h^V c_t, and each query attends to them.  w_kv (device, [num_q_heads, nope_dim
+ * + v_dim, latent_dim] of the pool's type): head h's nope_dim rows of W^K, then its v_dim rows
+ * of W^V.  q (device, [total_q, num_q_heads, nope_dim + rope_dim]) and q_ptr as in
+ * hp_latent_decode (so a prompt behind a cached prefix sees the prefix); out (device, [total_q,
+ * num_q_heads, v_dim]).  K and V are rounded to the pool's type after fp32 accumulation over
+ * latent_dim, the weights before the value product, the result once; scores, statistics and
+ * sums are fp32.  kv_tokens: at least the sum of seq_lens, or nothing is written and
+ * HP_ERR_OUT_SIZE stored.  Finite values, empty rows and validation are as in hp_latent_decode.
+ * Supported: latent_dim and rope_dim as there; nope_dim a multiple of 16 and v_dim a multiple
+ * of 16 up to 256 (HP_ERR_ARG otherwise).  latent_dim 512, rope_dim 64, nope_dim 128 and v_dim
+ * 128 run on the tensor cores, the others on the CUDA cores.
+ */
+int hp_latent_prefill(const hp_paged_desc* desc, uint32_t latent_dim, const void* w_kv,
+                      uint32_t nope_dim, uint32_t v_dim, const void* q, const void* q_ptr,
+                      uint64_t total_q, uint32_t num_q_heads, float scale, void* out,
+                      uint64_t kv_tokens, void* workspace, uint64_t workspace_bytes,
+                      int* d_status, void* stream);
 
 /* --------------------------------------------------------- layout conversions */
 /*

@@ -89,7 +89,7 @@ inline WsView ws_view(void* ws, uint64_t num_seqs)
 }
 
 // ------------------------------------------------------------------ plan step
-enum PlanMode { kPlanGather = 0, kPlanAppend = 1, kPlanAttention = 2 };
+enum PlanMode { kPlanGather = 0, kPlanAppend = 1, kPlanAttention = 2, kPlanLatent = 3 };
 
 struct PlanArgs {
     const void* seq_ptr;
@@ -100,6 +100,11 @@ struct PlanArgs {
     uint64_t out_tokens;      // gather: expected total rows
     uint64_t total_new;       // append: expected new_ptr[S]
     uint64_t step_tokens;     // attention: tokens per step (its units are steps)
+    // latent attention: new_ptr holds the queries' offsets (NULL: one per sequence) and
+    // total_new bounds them; rows are tokens rounded up to row_round.  heads > 0 (absorbed):
+    // units are the steps of each group of group_rows (query, head) rows; heads 0 (expanded):
+    // units are blocks of group_rows queries, and the tokens must not exceed out_tokens.
+    uint64_t heads, group_rows, row_round;
     int strict;               // check the storage invariants
     int check_out;            // gather: compare the total with out_tokens
     int* d_status;

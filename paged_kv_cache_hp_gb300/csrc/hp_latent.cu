@@ -1,0 +1,509 @@
+// hp_latent.cu -- attention over a paged cache of shared latent rows on the CUDA cores (the
+// shapes the tensor-core kernels do not take), the merge of the absorbed form's records, and
+// the gather of the latent rows in front of the expanded form.
+//
+// Absorbed form: row r = (query, head) of a sequence scores every token it sees against the
+// whole cache row, s_t = scale q_r . C_t over W dims, and sums the row's first R dims,
+// o_r = sum_t p_t C_t[:R] with p the softmax of s: the row is read once for both.  Running
+// maximum and sum (fp32, log2 units); a worker takes an equal range of (row group, step of 64
+// tokens) units, so one long sequence spreads over the whole GPU and its partial results are
+// joined by latent_merge_kernel in the order of the workers.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "hp_attn_merge.cuh"
+#include "hp_internal.cuh"
+#include "hp_latent.cuh"
+#include "hp_resolve.cuh"
+
+namespace hp {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <typename T> struct Pair;
+template <> struct Pair<__half> {
+    __device__ static float2 up(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
+    __device__ static uint32_t down(float a, float b)
+    {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    __device__ static __half one(float x) { return __float2half_rn(x); }
+};
+template <> struct Pair<__nv_bfloat16> {
+    __device__ static float2 up(uint32_t u) { return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u)); }
+    __device__ static uint32_t down(float a, float b)
+    {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    __device__ static __nv_bfloat16 one(float x) { return __float2bfloat16_rn(x); }
+};
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+constexpr int kRowsWarp = 2;   // rows of a warp
+constexpr int kMaxPairs = 9;   // element pairs per lane: W <= 576
+constexpr int kAccPairs = 8;   // R <= 512
+constexpr int kKeys = 4;       // tokens per pass
+
+template <typename T>
+__global__ void __launch_bounds__(256, 2) latent_cc_kernel(const LatentArgs a)
+{
+    pdl_wait();
+    if (a.hdr->verdict != kVerdictOk) return;
+    const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t pairs = a.W / 2, accp = a.R / 64;
+    uint32_t* out = static_cast<uint32_t*>(a.out);
+    for (uint64_t s = (uint64_t)blockIdx.x * 8 + warp; s < a.num_seqs; s += (uint64_t)gridDim.x * 8)
+        if (a.units_off[s] == a.units_off[s + 1]) {  // no token: zeros for its queries
+            const uint64_t q0 = a.q_ptr ? index_at(a.q_ptr, a.idx64, s) : s;
+            const uint64_t q1 = a.q_ptr ? index_at(a.q_ptr, a.idx64, s + 1) : s + 1;
+            for (uint64_t i = q0 * a.H * (a.R / 2) + lane; i < q1 * a.H * (a.R / 2); i += 32) out[i] = 0u;
+        }
+    const uint64_t total = a.hdr->total_units, Lw = (total + a.workers - 1) / a.workers;
+    const uint64_t v = blockIdx.x, beg = umin(v * Lw, total), end = umin(beg + Lw, total);
+    const float qscale = a.scale * kLog2e;
+    uint64_t pos = beg;
+    while (pos < end) {
+        const uint64_t s = find_seq(a.units_off, a.num_seqs, pos);
+        const uint64_t len = index_at(a.lens, a.idx64, s), tab0 = index_at(a.seq_ptr, a.idx64, s);
+        const uint64_t q0 = a.q_ptr ? index_at(a.q_ptr, a.idx64, s) : s;
+        const uint64_t n = (a.q_ptr ? index_at(a.q_ptr, a.idx64, s + 1) : s + 1) - q0;
+        const uint64_t steps = (len + kLatentStep - 1) / kLatentStep, off = pos - a.units_off[s];
+        const uint64_t g = off / steps, k0 = off % steps, k1 = umin(steps, k0 + (end - pos));
+        const uint64_t ustart = a.units_off[s] + g * steps;
+        pos += k1 - k0;
+        // this warp's rows, and the tokens each sees
+        const uint64_t r0 = g * a.group_rows + warp * kRowsWarp;
+        uint64_t vis[kRowsWarp];
+        float q[kRowsWarp][2 * kMaxPairs], acc[kRowsWarp][2 * kAccPairs], m[kRowsWarp], l[kRowsWarp];
+#pragma unroll
+        for (int i = 0; i < kRowsWarp; ++i) {
+            const uint64_t r = r0 + i, qi = r / a.H;
+            const bool on = r < n * a.H;
+            vis[i] = on && len + 1 + qi > n ? len + 1 + qi - n : 0;
+            const uint32_t* src = static_cast<const uint32_t*>(a.q) + (q0 * a.H + r) * pairs;
+#pragma unroll
+            for (int j = 0; j < kMaxPairs; ++j) {
+                const uint32_t p = lane + 32 * j;
+                const float2 x = Pair<T>::up(on && p < pairs ? src[p] : 0u);
+                q[i][2 * j] = x.x * qscale;
+                q[i][2 * j + 1] = x.y * qscale;
+            }
+#pragma unroll
+            for (int j = 0; j < 2 * kAccPairs; ++j) acc[i][j] = 0.0f;
+            m[i] = -INFINITY;
+            l[i] = 0.0f;
+        }
+        uint64_t tend = 0;
+#pragma unroll
+        for (int i = 0; i < kRowsWarp; ++i) tend = umax(tend, vis[i]);
+        tend = umin(tend, umin(k1 * kLatentStep, len));
+        for (uint64_t t0 = k0 * kLatentStep; t0 < tend; t0 += 32) {
+            // the pool rows of 32 tokens, one per lane
+            unsigned long long at = 0;
+            if (t0 + lane < tend) {
+                const uint64_t t = t0 + lane;
+                at = index_at(a.table, a.idx64, tab0 + t / a.page_size) * a.page_size + t % a.page_size;
+            }
+            const uint32_t cnt = (uint32_t)umin(32, tend - t0);
+            for (uint32_t c = 0; c < cnt; c += kKeys) {
+                uint32_t kv[kKeys][kMaxPairs];
+                float sc[kRowsWarp][kKeys];
+#pragma unroll
+                for (int u = 0; u < kKeys; ++u) {
+                    const unsigned long long row = __shfl_sync(0xffffffffu, at, (int)umin(c + u, cnt - 1));
+                    const uint32_t* src = static_cast<const uint32_t*>(a.pool) + row * pairs;
+#pragma unroll
+                    for (int j = 0; j < kMaxPairs; ++j) {
+                        const uint32_t p = lane + 32 * j;
+                        kv[u][j] = p < pairs ? __ldg(src + p) : 0u;
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kKeys; ++u) {
+                    float d[kRowsWarp];
+#pragma unroll
+                    for (int i = 0; i < kRowsWarp; ++i) d[i] = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < kMaxPairs; ++j) {
+                        const float2 x = Pair<T>::up(kv[u][j]);
+#pragma unroll
+                        for (int i = 0; i < kRowsWarp; ++i)
+                            d[i] = fmaf(q[i][2 * j + 1], x.y, fmaf(q[i][2 * j], x.x, d[i]));
+                    }
+#pragma unroll
+                    for (int i = 0; i < kRowsWarp; ++i)
+                        sc[i][u] = warp_sum(d[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < kRowsWarp; ++i) {
+                    float mn = m[i];
+#pragma unroll
+                    for (int u = 0; u < kKeys; ++u) {
+                        if (c + u >= cnt || t0 + c + u >= vis[i]) sc[i][u] = -INFINITY;
+                        mn = fmaxf(mn, sc[i][u]);
+                    }
+                    if (mn == -INFINITY) {
+#pragma unroll
+                        for (int u = 0; u < kKeys; ++u) sc[i][u] = 0.0f;
+                        continue;
+                    }
+                    const float f = exp2_approx(m[i] - mn);
+                    m[i] = mn;
+                    l[i] *= f;
+#pragma unroll
+                    for (int u = 0; u < kKeys; ++u) {
+                        sc[i][u] = exp2_approx(sc[i][u] - mn);
+                        l[i] += sc[i][u];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2 * kAccPairs; ++j) acc[i][j] *= f;
+                }
+#pragma unroll
+                for (int u = 0; u < kKeys; ++u)
+#pragma unroll
+                    for (int j = 0; j < kAccPairs; ++j)
+                        if ((uint32_t)j < accp) {
+                            const float2 x = Pair<T>::up(kv[u][j]);
+#pragma unroll
+                            for (int i = 0; i < kRowsWarp; ++i)
+                                // a token the row does not see is absent, not of weight zero
+                                if (sc[i][u] != 0.0f) {
+                                    acc[i][2 * j] = fmaf(sc[i][u], x.x, acc[i][2 * j]);
+                                    acc[i][2 * j + 1] = fmaf(sc[i][u], x.y, acc[i][2 * j + 1]);
+                                }
+                        }
+            }
+        }
+        const bool whole = ustart >= beg && ustart + steps <= end;
+        const uint64_t slot = 2 * v + (ustart <= beg ? 0 : 1);
+#pragma unroll
+        for (int i = 0; i < kRowsWarp; ++i) {
+            const uint64_t r = r0 + i;
+            if (r >= n * a.H) continue;
+            if (whole) {
+                const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
+                uint32_t* o = out + (q0 * a.H + r) * (a.R / 2);
+#pragma unroll
+                for (int j = 0; j < kAccPairs; ++j)
+                    if ((uint32_t)j < accp)
+                        o[lane + 32 * j] = Pair<T>::down(acc[i][2 * j] * inv, acc[i][2 * j + 1] * inv);
+            } else {
+                const uint64_t rec = slot * a.group_rows + warp * kRowsWarp + i;
+                float2* o = reinterpret_cast<float2*>(a.part_acc + rec * a.R);
+#pragma unroll
+                for (int j = 0; j < kAccPairs; ++j)
+                    if ((uint32_t)j < accp) o[lane + 32 * j] = make_float2(acc[i][2 * j], acc[i][2 * j + 1]);
+                if (lane == 0) a.part_ml[rec] = make_float2(m[i], l[i]);
+            }
+        }
+    }
+}
+
+// CTA (v, y): eight rows, one per warp, of the row group that begins in worker v's range and
+// goes on past it.
+template <typename T>
+__global__ void __launch_bounds__(256) latent_merge_kernel(const LatentArgs a)
+{
+    pdl_wait();
+    if (a.hdr->verdict != kVerdictOk) return;
+    const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint64_t total = a.hdr->total_units, Lw = (total + a.workers - 1) / a.workers;
+    const uint64_t v = blockIdx.x, beg = umin(v * Lw, total), end = umin(beg + Lw, total);
+    if (beg >= end || end == total) return;
+    const uint64_t s = find_seq(a.units_off, a.num_seqs, end - 1);
+    const uint64_t len = index_at(a.lens, a.idx64, s);
+    const uint64_t steps = (len + kLatentStep - 1) / kLatentStep;
+    const uint64_t g = (end - 1 - a.units_off[s]) / steps, ustart = a.units_off[s] + g * steps;
+    const uint64_t uend = ustart + steps;
+    if (ustart < beg || uend <= end) return;
+    const uint64_t q0 = a.q_ptr ? index_at(a.q_ptr, a.idx64, s) : s;
+    const uint64_t n = (a.q_ptr ? index_at(a.q_ptr, a.idx64, s + 1) : s + 1) - q0;
+    const uint32_t gr = blockIdx.y * 8 + warp;
+    const uint64_t r = g * a.group_rows + gr;
+    if (gr >= a.group_rows || r >= n * a.H) return;
+    const uint64_t last = (uend - 1) / Lw;
+    auto rec = [&](uint64_t w) { return (2 * w + (w == v && ustart > beg ? 1 : 0)) * a.group_rows + gr; };
+    // maximum and sum over the records, a lane per record, then pairwise
+    float M = -INFINITY, L = 0.0f;
+    for (uint64_t w = v + lane; w <= last; w += 32) {
+        const float2 x = a.part_ml[rec(w)];
+        const float mn = fmaxf(M, x.x);
+        if (mn != -INFINITY) {
+            L = L * exp2_approx(M - mn) + x.y * exp2_approx(x.x - mn);
+            M = mn;
+        }
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float om = __shfl_xor_sync(0xffffffffu, M, o), ol = __shfl_xor_sync(0xffffffffu, L, o);
+        const float mn = fmaxf(M, om);
+        if (mn != -INFINITY) {
+            L = L * exp2_approx(M - mn) + ol * exp2_approx(om - mn);
+            M = mn;
+        }
+    }
+    const uint32_t quads = a.R / 4;  // float4 per record row: at most 4 per lane
+    float4 acc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = make_float4(0, 0, 0, 0);
+    if (M != -INFINITY)
+#pragma unroll 2
+        for (uint64_t w = v; w <= last; ++w) {
+            const uint64_t at = rec(w);
+            const float f = exp2_approx(a.part_ml[at].x - M);
+            const float4* p = reinterpret_cast<const float4*>(a.part_acc + at * a.R);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (lane + 32 * j < quads) {
+                    const float4 x = p[lane + 32 * j];
+                    acc[j].x = fmaf(f, x.x, acc[j].x);
+                    acc[j].y = fmaf(f, x.y, acc[j].y);
+                    acc[j].z = fmaf(f, x.z, acc[j].z);
+                    acc[j].w = fmaf(f, x.w, acc[j].w);
+                }
+        }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    uint2* o = reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (q0 * a.H + r) * a.R);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (lane + 32 * j < quads)
+            o[lane + 32 * j] = make_uint2(Pair<T>::down(acc[j].x * inv, acc[j].y * inv),
+                                          Pair<T>::down(acc[j].z * inv, acc[j].w * inv));
+}
+
+// --------------------------------------------------------------------- expanded form
+
+// The latent rows of each sequence in order, padded with zeros to a multiple of kLatentPad: a
+// block of 128 rows lies in one sequence.  Warp per row, 16 bytes per lane.
+__global__ void __launch_bounds__(256) latent_rows_kernel(const LatentPrefillArgs a)
+{
+    pdl_wait();
+    if (a.hdr->verdict != kVerdictOk) return;
+    const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint64_t blocks = a.hdr->total_rows / kLatentPad;
+    const uint32_t vecs = a.W / 8;
+    for (uint64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
+        const uint64_t row0 = b * kLatentPad, s = find_seq(a.rows_off, a.num_seqs, row0);
+        const uint64_t len = index_at(a.lens, a.idx64, s), tab0 = index_at(a.seq_ptr, a.idx64, s);
+#pragma unroll 2
+        for (uint32_t i = warp; i < kLatentPad; i += 8) {
+            const uint64_t t = row0 - a.rows_off[s] + i;
+            uint4* dst = static_cast<uint4*>(a.rows) + (row0 + i) * vecs;
+            if (t < len) {
+                const uint64_t phys = index_at(a.table, a.idx64, tab0 + t / a.page_size);
+                const uint4* src = static_cast<const uint4*>(a.pool) +
+                                   (phys * a.page_size + t % a.page_size) * vecs;
+                for (uint32_t c = lane; c < vecs; c += 32) dst[c] = __ldg(src + c);
+            } else {
+                for (uint32_t c = lane; c < vecs; c += 32) dst[c] = make_uint4(0, 0, 0, 0);
+            }
+        }
+    }
+}
+
+// kv[row, n] = sum_d rows[row, d] w_kv[n, d]: 64 x 64 tiles, 4 x 4 per thread.
+template <typename T>
+__global__ void __launch_bounds__(256) latent_expand_cc_kernel(const LatentPrefillArgs a)
+{
+    pdl_wait();
+    if (a.hdr->verdict != kVerdictOk) return;
+    const uint64_t row0 = (uint64_t)blockIdx.x * 64;
+    const uint32_t N = a.H * (a.Dn + a.Dv), n0 = blockIdx.y * 64;
+    if (row0 >= a.hdr->total_rows) return;
+    __shared__ float sa[32][65], sb[32][65];  // [k][row], [k][n]
+    const uint32_t tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    float acc[4][4] = {};
+    for (uint32_t k0 = 0; k0 < a.R; k0 += 32) {
+        for (uint32_t i = threadIdx.x; i < 64 * 16; i += 256) {  // 16 pairs of 64 rows
+            const uint32_t r = i / 16, p = i % 16;
+            const float2 x = Pair<T>::up(*reinterpret_cast<const uint32_t*>(
+                static_cast<const T*>(a.rows) + (row0 + r) * a.W + k0 + 2 * p));
+            sa[2 * p][r] = x.x;
+            sa[2 * p + 1][r] = x.y;
+            const float2 y = Pair<T>::up(n0 + r < N ? *reinterpret_cast<const uint32_t*>(
+                static_cast<const T*>(a.w_kv) + (uint64_t)(n0 + r) * a.R + k0 + 2 * p) : 0u);
+            sb[2 * p][r] = y.x;
+            sb[2 * p + 1][r] = y.y;
+        }
+        __syncthreads();
+#pragma unroll 8
+        for (int k = 0; k < 32; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[i][j] = fmaf(sa[k][ty + 16 * i], sb[k][tx + 16 * j], acc[i][j]);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (n0 + tx + 16 * j < N)
+                static_cast<T*>(a.kv)[(row0 + ty + 16 * i) * N + n0 + tx + 16 * j] =
+                    Pair<T>::one(acc[i][j]);
+}
+
+constexpr int kQ = 4;   // queries of a warp
+constexpr int kDp = 4;  // element pairs per lane of a head's nope part or value: up to 256 dims
+
+// CTA (u, h): block u of 32 queries, head h.
+template <typename T>
+__global__ void __launch_bounds__(256) latent_prefill_cc_kernel(const LatentPrefillArgs a)
+{
+    pdl_wait();
+    if (a.hdr->verdict != kVerdictOk) return;
+    const uint64_t u = blockIdx.x;
+    if (u >= a.hdr->total_units) return;
+    const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t h = blockIdx.y, Dr = a.W - a.R;
+    const uint64_t s = find_seq(a.units_off, a.num_seqs, u);
+    const uint64_t len = index_at(a.lens, a.idx64, s);
+    const uint64_t q0 = a.q_ptr ? index_at(a.q_ptr, a.idx64, s) : s;
+    const uint64_t n = (a.q_ptr ? index_at(a.q_ptr, a.idx64, s + 1) : s + 1) - q0;
+    const uint64_t i0 = (u - a.units_off[s]) * a.q_block + warp * kQ;
+    const uint32_t np = a.Dn / 2, rp = Dr / 2, vp = a.Dv / 2;
+    const float qscale = a.scale * kLog2e;
+    uint64_t vis[kQ], tend = 0;
+    float q[kQ][2 * kDp + 2], acc[kQ][2 * kDp], m[kQ], l[kQ];
+#pragma unroll
+    for (int i = 0; i < kQ; ++i) {
+        const bool on = i0 + i < n;
+        vis[i] = on && len + 1 + i0 + i > n ? len + 1 + i0 + i - n : 0;
+        tend = umax(tend, vis[i]);
+        const uint32_t* src =
+            static_cast<const uint32_t*>(a.q) + ((q0 + i0 + i) * a.H + h) * (np + rp);
+#pragma unroll
+        for (int j = 0; j < kDp; ++j) {
+            const uint32_t p = lane + 32 * j;
+            const float2 x = Pair<T>::up(on && p < np ? src[p] : 0u);
+            q[i][2 * j] = x.x * qscale;
+            q[i][2 * j + 1] = x.y * qscale;
+        }
+        const float2 x = Pair<T>::up(on && lane < rp ? src[np + lane] : 0u);
+        q[i][2 * kDp] = x.x * qscale;
+        q[i][2 * kDp + 1] = x.y * qscale;
+#pragma unroll
+        for (int j = 0; j < 2 * kDp; ++j) acc[i][j] = 0.0f;
+        m[i] = -INFINITY;
+        l[i] = 0.0f;
+    }
+    const uint64_t row0 = a.rows_off[s];
+    for (uint64_t t = 0; t < tend; ++t) {
+        const uint32_t* kv = static_cast<const uint32_t*>(a.kv) +
+                             ((row0 + t) * a.H + h) * (uint64_t)(np + vp);
+        const uint32_t* kr = static_cast<const uint32_t*>(a.rows) + (row0 + t) * (a.W / 2) + a.R / 2;
+        float d[kQ];
+        float2 x = Pair<T>::up(lane < rp ? kr[lane] : 0u);
+#pragma unroll
+        for (int i = 0; i < kQ; ++i) d[i] = q[i][2 * kDp] * x.x + q[i][2 * kDp + 1] * x.y;
+#pragma unroll
+        for (int j = 0; j < kDp; ++j) {
+            const uint32_t p = lane + 32 * j;
+            x = Pair<T>::up(p < np ? kv[p] : 0u);
+#pragma unroll
+            for (int i = 0; i < kQ; ++i)
+                d[i] = fmaf(q[i][2 * j + 1], x.y, fmaf(q[i][2 * j], x.x, d[i]));
+        }
+#pragma unroll
+        for (int i = 0; i < kQ; ++i) {
+            d[i] = warp_sum(d[i]);
+            if (t >= vis[i]) continue;  // (the same in every lane)
+            const float mn = fmaxf(m[i], d[i]), f = exp2_approx(m[i] - mn), w = exp2_approx(d[i] - mn);
+            m[i] = mn;
+            l[i] = l[i] * f + w;
+#pragma unroll
+            for (int j = 0; j < kDp; ++j) {
+                const uint32_t p = lane + 32 * j;
+                const float2 y = Pair<T>::up(p < vp ? kv[np + p] : 0u);
+                acc[i][2 * j] = fmaf(w, y.x, acc[i][2 * j] * f);
+                acc[i][2 * j + 1] = fmaf(w, y.y, acc[i][2 * j + 1] * f);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kQ; ++i) {
+        if (i0 + i >= n) continue;
+        const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
+        uint32_t* o = static_cast<uint32_t*>(a.out) + ((q0 + i0 + i) * a.H + h) * vp;
+#pragma unroll
+        for (int j = 0; j < kDp; ++j)
+            if (lane + 32 * j < vp)
+                o[lane + 32 * j] = Pair<T>::down(acc[i][2 * j] * inv, acc[i][2 * j + 1] * inv);
+    }
+}
+
+template <typename T> int launch_prefill_t(const LatentPrefillArgs& a, cudaStream_t st)
+{
+    const uint32_t N = a.H * (a.Dn + a.Dv);
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3((unsigned)(a.cap_rows / 64), (N + 63) / 64);
+    if (cudaLaunchKernelEx(&cfg, latent_expand_cc_kernel<T>, a) != cudaSuccess) return HP_ERR_CUDA;
+    cfg.gridDim = dim3((unsigned)a.max_units, a.H);
+    return cudaLaunchKernelEx(&cfg, latent_prefill_cc_kernel<T>, a) == cudaSuccess ? HP_OK : HP_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_latent_cc(const LatentArgs& a, void* stream)
+{
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e =
+        a.bf16 ? launch_dependent(latent_cc_kernel<__nv_bfloat16>, (unsigned)a.workers, 256, 0, st, a)
+               : launch_dependent(latent_cc_kernel<__half>, (unsigned)a.workers, 256, 0, st, a);
+    return e == cudaSuccess ? HP_OK : HP_ERR_CUDA;
+}
+
+int launch_latent_merge(const LatentArgs& a, void* stream)
+{
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)a.workers, (a.group_rows + 7) / 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = a.bf16 ? cudaLaunchKernelEx(&cfg, latent_merge_kernel<__nv_bfloat16>, a)
+                                 : cudaLaunchKernelEx(&cfg, latent_merge_kernel<__half>, a);
+    return e == cudaSuccess ? HP_OK : HP_ERR_CUDA;
+}
+
+int launch_latent_rows(const LatentPrefillArgs& a, void* stream)
+{
+    int dev = 0;
+    const int sms = current_sms(&dev);
+    if (sms == 0) return HP_ERR_CUDA;
+    const uint64_t blocks = a.cap_rows / kLatentPad, cap = (uint64_t)sms * 8;
+    const uint64_t grid = blocks == 0 ? 1 : (blocks < cap ? blocks : cap);
+    return launch_dependent(latent_rows_kernel, (unsigned)grid, 256, 0,
+                            static_cast<cudaStream_t>(stream), a) == cudaSuccess
+               ? HP_OK
+               : HP_ERR_CUDA;
+}
+
+int launch_latent_prefill_cc(const LatentPrefillArgs& a, void* stream)
+{
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return a.bf16 ? launch_prefill_t<__nv_bfloat16>(a, st) : launch_prefill_t<__half>(a, st);
+}
+
+}  // namespace hp

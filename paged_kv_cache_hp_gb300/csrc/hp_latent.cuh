@@ -1,0 +1,88 @@
+// hp_latent.cuh -- launch interface of attention over a paged cache of shared latent rows
+// (hp_latent.cu on the CUDA cores, hp_latent_tc.cu and hp_latent_prefill_tc.cu on the tensor
+// cores).
+#pragma once
+
+#include <cstdint>
+
+#include "hp_internal.cuh"
+
+namespace hp {
+
+constexpr uint32_t kLatentStep = 64;        // tokens per step of the absorbed form
+constexpr uint32_t kLatentMaxSms = 160;     // workers are counted for at most this many SMs
+constexpr uint32_t kLatentRecordRows = 128; // record rows per SM
+constexpr uint32_t kLatentCcRows = 16;      // (query, head) rows per group, CUDA cores
+constexpr uint32_t kLatentPad = 128;        // expanded form: rows a sequence is padded to
+constexpr uint32_t kLatentCcQueries = 32;   // queries per block, CUDA cores
+constexpr uint32_t kLatentTcQueries = 256;  // queries per block, tensor cores
+
+// Absorbed form, after a kPlanLatent plan on the same stream.  The plan's units are, sequence
+// after sequence and row group after row group, the steps of kLatentStep tokens: a group is
+// group_rows of the sequence's n * H rows (row r: query r / H, head r % H).  The units are
+// split evenly over `workers`; a group that several workers share leaves a record per worker:
+// its first worker's in slot 1 of that worker's two unless the group starts its range, the
+// others' in slot 0 (a range has at most one group that began before it and one that goes on
+// after it).
+struct LatentArgs {
+    const void* pool;
+    const void* q;            // [total_q, H, W]
+    const void* q_ptr;        // NULL: query s is sequence s's
+    const void* table;
+    const void* seq_ptr;
+    const void* lens;
+    uint64_t num_seqs, page_size, num_pages;
+    uint64_t total_q;
+    uint32_t H, R, W;         // heads, latent_dim, latent_dim + rope_dim
+    uint32_t group_rows;
+    uint64_t workers;
+    float scale;
+    int bf16, idx64, test_stall;
+    const WsHeader* hdr;
+    const unsigned long long* units_off;
+    float* part_acc;          // [2 * workers * group_rows, R]
+    float2* part_ml;          // their maxima (log2 units) and sums
+    void* out;                // [total_q, H, R]
+    int* d_status;
+};
+int launch_latent_cc(const LatentArgs& a, void* stream);
+int launch_latent_tc(const LatentArgs& a, void* stream);
+bool latent_tc_fits(uint32_t latent_dim, uint64_t head_dim, uint64_t page_size, uint64_t num_pages);
+int launch_latent_merge(const LatentArgs& a, void* stream);
+
+// Expanded form, after a kPlanLatent plan (rows padded to kLatentPad per sequence, units of
+// q_block queries).
+struct LatentPrefillArgs {
+    const void* pool;
+    const void* w_kv;         // [H, Dn + Dv, R]
+    const void* q;            // [total_q, H, Dn + W - R]
+    const void* q_ptr;
+    const void* table;
+    const void* seq_ptr;
+    const void* lens;
+    uint64_t num_seqs, page_size, num_pages;
+    uint64_t total_q, cap_rows, max_units;
+    uint32_t H, R, W, Dn, Dv, q_block;
+    float scale;
+    int bf16, idx64, test_stall;
+    const WsHeader* hdr;
+    const unsigned long long* rows_off;
+    const unsigned long long* units_off;
+    void* rows;               // [cap_rows, W]: the latent rows, zeros behind each sequence
+    void* kv;                 // [cap_rows, H, Dn + Dv]
+    void* out;                // [total_q, H, Dv]
+    int* d_status;
+};
+int launch_latent_rows(const LatentPrefillArgs& a, void* stream);
+int launch_latent_prefill_cc(const LatentPrefillArgs& a, void* stream);
+int launch_latent_prefill_tc(const LatentPrefillArgs& a, void* stream);
+bool latent_prefill_tc_fits(uint32_t latent_dim, uint64_t head_dim, uint32_t nope, uint32_t v,
+                            uint64_t cap_rows, uint64_t total_q, uint32_t heads);
+
+__device__ __forceinline__ unsigned long long index_at(const void* p, int idx64, uint64_t i)
+{
+    return idx64 ? (unsigned long long)static_cast<const unsigned long long*>(p)[i]
+                 : (unsigned long long)static_cast<const unsigned int*>(p)[i];
+}
+
+}  // namespace hp

@@ -17,68 +17,10 @@
 #include <cuda_runtime.h>
 
 #include "hp_internal.cuh"
+#include "hp_scan.cuh"
 
 namespace hp {
 namespace {
-
-constexpr int kPlanThreads = 1024;
-constexpr int kWarps = kPlanThreads / 32;
-
-__device__ __forceinline__ unsigned long long sat_add(unsigned long long a, unsigned long long b)
-{
-    unsigned long long c = a + b;
-    return c < a ? ~0ull : c;
-}
-
-// Exclusive block scan of two counters at once with saturating addition (which is
-// associative: it is min(a + b, 2^64 - 1) over the naturals).  Returns the
-// exclusive prefixes; *tot receives the block totals.
-__device__ __forceinline__ void block_scan2(unsigned long long v0, unsigned long long v1,
-                                            unsigned long long& ex0, unsigned long long& ex1,
-                                            unsigned long long& tot0, unsigned long long& tot1)
-{
-    __shared__ unsigned long long w0[kWarps], w1[kWarps];
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    unsigned long long i0 = v0, i1 = v1;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        unsigned long long n0 = __shfl_up_sync(0xffffffffu, i0, o);
-        unsigned long long n1 = __shfl_up_sync(0xffffffffu, i1, o);
-        if (lane >= o) {
-            i0 = sat_add(n0, i0);
-            i1 = sat_add(n1, i1);
-        }
-    }
-    unsigned long long e0 = __shfl_up_sync(0xffffffffu, i0, 1);
-    unsigned long long e1 = __shfl_up_sync(0xffffffffu, i1, 1);
-    if (lane == 0) e0 = e1 = 0;
-    if (lane == 31) {
-        w0[wid] = i0;
-        w1[wid] = i1;
-    }
-    __syncthreads();
-    if (wid == 0) {
-        unsigned long long a0 = w0[lane], a1 = w1[lane];  // kWarps == 32
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            unsigned long long n0 = __shfl_up_sync(0xffffffffu, a0, o);
-            unsigned long long n1 = __shfl_up_sync(0xffffffffu, a1, o);
-            if (lane >= o) {
-                a0 = sat_add(n0, a0);
-                a1 = sat_add(n1, a1);
-            }
-        }
-        w0[lane] = a0;
-        w1[lane] = a1;
-    }
-    __syncthreads();
-    unsigned long long p0 = wid ? w0[wid - 1] : 0, p1 = wid ? w1[wid - 1] : 0;
-    ex0 = sat_add(p0, e0);
-    ex1 = sat_add(p1, e1);
-    tot0 = w0[kWarps - 1];
-    tot1 = w1[kWarps - 1];
-    __syncthreads();  // w0/w1 are reused by the next call
-}
 
 // a*b > c with a 128-bit product and a 65-bit c = c_hi*2^64 + c_lo.
 __device__ __forceinline__ bool gt_sum(unsigned long long c_lo, unsigned c_carry,
@@ -98,12 +40,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a)
     const IndexT* np = static_cast<const IndexT*>(a.new_ptr);
     const uint64_t S = a.num_seqs, P = a.page_size;
 
-    __shared__ unsigned long long s_key;
+    __shared__ unsigned long long s_key, s_len;
     __shared__ int s_fault;
     __shared__ unsigned long long s_carry_rows, s_carry_units;
     pdl_trigger();  // let the table check start scanning now
     if (threadIdx.x == 0) {
         s_key = kVerdictOk;
+        s_len = 0;
         s_fault = HP_OK;
         s_carry_rows = 0;
         s_carry_units = 0;
@@ -115,7 +58,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a)
         unsigned long long rows = 0, units = 0;
         if (s < S) {
             const unsigned long long lo = sp[s], hi = sp[s + 1], len = lens[s];
-            if (MODE == kPlanGather || MODE == kPlanAttention) {
+            if (MODE == kPlanGather || MODE == kPlanAttention || MODE == kPlanLatent) {
                 rows = len;
                 units = len / P + (len % P != 0);
                 if (a.strict) {
@@ -126,6 +69,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a)
                 }
                 if (MODE == kPlanAttention)  // tokens -> steps of step_tokens tokens
                     units = len / a.step_tokens + (len % a.step_tokens != 0);
+                if (MODE == kPlanLatent) {
+                    const unsigned long long n0 = np ? np[s] : s, n1 = np ? np[s + 1] : s + 1;
+                    if (n0 > n1) atomicMin(&s_key, verdict_key(kRankNewPtrOrder, s));
+                    const unsigned long long n = n0 <= n1 && n1 <= a.total_new ? n1 - n0 : 0;
+                    if (a.heads) {
+                        units = (n * a.heads + a.group_rows - 1) / a.group_rows *
+                                (len / a.step_tokens + (len % a.step_tokens != 0));
+                    } else {
+                        units = (n + a.group_rows - 1) / a.group_rows;
+                        rows = (len + a.row_round - 1) / a.row_round * a.row_round;
+                        atomicAdd(&s_len, len);  // (wraps only past HP_ERR_LEN, an earlier rule)
+                    }
+                }
             } else {
                 const unsigned long long n0 = np[s], n1 = np[s + 1];
                 const bool ok_new = n0 <= n1 && n1 <= a.total_new;
@@ -174,6 +130,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a)
                 if ((unsigned long long)np[S] != a.total_new)
                     key = min(key, verdict_key(kRankNewPtrEnd, S));
             }
+        }
+        if (MODE == kPlanLatent) {
+            if (np && np[0] != 0) key = min(key, verdict_key(kRankNewPtrStart, 0));
+            if (np && (unsigned long long)np[S] > a.total_new)
+                key = min(key, verdict_key(kRankNewPtrEnd, S));
+            if (!a.heads && s_len > a.out_tokens) key = min(key, verdict_key(kRankOutSize, 0));
         }
         if (MODE == kPlanGather && a.check_out &&
             (total_rows == ~0ull || total_rows != a.out_tokens))
@@ -366,8 +328,10 @@ int launch_plan_t(PlanMode mode, const PlanArgs& a, cudaStream_t st)
         plan_kernel<IndexT, kPlanGather><<<1, kPlanThreads, 0, st>>>(a);
     else if (mode == kPlanAppend)
         plan_kernel<IndexT, kPlanAppend><<<1, kPlanThreads, 0, st>>>(a);
-    else
+    else if (mode == kPlanAttention)
         plan_kernel<IndexT, kPlanAttention><<<1, kPlanThreads, 0, st>>>(a);
+    else
+        plan_kernel<IndexT, kPlanLatent><<<1, kPlanThreads, 0, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return HP_ERR_CUDA;
     if (a.strict && a.table_len > 0) {
         int dev = 0;

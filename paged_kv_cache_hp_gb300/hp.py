@@ -56,6 +56,136 @@ def quant_desc(scheme_tag, scales, zero_points=None, axis=0, block_size=0, count
     return q
 
 
+class HpStepDesc(ctypes.Structure):
+    _fields_ = [("index_type", ctypes.c_uint32), ("reserved", ctypes.c_uint32)] + \
+               [(n, ctypes.c_uint64) for n in
+                ("num_seqs", "page_size", "table_len", "num_free", "table_cap", "token_cap")] + \
+               [(n, ctypes.c_void_p) for n in
+                ("block_table", "seq_ptr", "seq_lens", "new_lens", "free_pages", "table_out",
+                 "seq_ptr_out", "lens_out", "new_ptr_out", "slot_map", "positions", "totals")]
+
+
+class HpRopeDesc(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("max_pos", ctypes.c_uint64), ("rot_dim", ctypes.c_uint32),
+                ("axes", ctypes.c_uint32), ("section", ctypes.c_uint32 * 4),
+                ("interleaved", ctypes.c_uint32), ("index_type", ctypes.c_uint32)]
+
+
+class HpQkDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_uint32) for n in
+                ("dtype", "num_q_heads", "num_kv_heads", "head_dim")] + \
+               [("eps", ctypes.c_float), ("reserved", ctypes.c_uint32),
+                ("num_tokens", ctypes.c_uint64)] + \
+               [(n, ctypes.c_void_p) for n in ("q", "k", "v")] + \
+               [(n, ctypes.c_uint64) for n in ("q_stride", "k_stride", "v_stride")] + \
+               [("q_out", ctypes.c_void_p), ("q_out_stride", ctypes.c_uint64)] + \
+               [(n, ctypes.c_void_p) for n in
+                ("q_weight", "k_weight", "slot_map", "k_pool", "v_pool")] + \
+               [("num_pages", ctypes.c_uint64), ("page_size", ctypes.c_uint64)]
+
+
+class HpLatentDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_uint32) for n in ("dtype", "latent_dim", "num_q_heads")] + \
+               [("eps", ctypes.c_float), ("num_tokens", ctypes.c_uint64),
+                ("latent", ctypes.c_void_p), ("latent_stride", ctypes.c_uint64),
+                ("latent_weight", ctypes.c_void_p), ("k_rope", ctypes.c_void_p),
+                ("k_rope_stride", ctypes.c_uint64), ("q_rope", ctypes.c_void_p),
+                ("q_stride", ctypes.c_uint64), ("q_head_stride", ctypes.c_uint64),
+                ("q_out", ctypes.c_void_p), ("q_out_stride", ctypes.c_uint64),
+                ("q_out_head_stride", ctypes.c_uint64), ("slot_map", ctypes.c_void_p),
+                ("pool", ctypes.c_void_p), ("num_pages", ctypes.c_uint64),
+                ("page_size", ctypes.c_uint64)]
+
+
+def _numel(t):
+    return 0 if t is None else t.numel()
+
+
+def _dtype(d):
+    return DTYPES[d] if isinstance(d, str) else d
+
+
+def step_desc(*, seq_ptr, seq_lens, new_lens, page_size, index_type, seq_ptr_out, lens_out,
+              new_ptr_out, block_table=None, free_pages=None, table_out=None, slot_map=None,
+              positions=None, totals=None, **fields):
+    """An hp_step_desc over device tensors (kept alive on the result's `keep`); the counts
+    come from the tensors unless given by name."""
+    d = HpStepDesc()
+    bufs = dict(block_table=block_table, seq_ptr=seq_ptr, seq_lens=seq_lens, new_lens=new_lens,
+                free_pages=free_pages, table_out=table_out, seq_ptr_out=seq_ptr_out,
+                lens_out=lens_out, new_ptr_out=new_ptr_out, slot_map=slot_map,
+                positions=positions, totals=totals)
+    d.index_type, d.page_size = index_type, page_size
+    d.num_seqs, d.table_len, d.num_free = _numel(seq_lens), _numel(block_table), _numel(free_pages)
+    d.table_cap, d.token_cap = _numel(table_out), _numel(slot_map)
+    for name, t in bufs.items():
+        setattr(d, name, _p(t))
+    for name, v in fields.items():
+        setattr(d, name, v)
+    d.keep = tuple(bufs.values())
+    return d
+
+
+def rope_desc(*, cos_sin, positions, sections, interleaved=False, index_type=IDX_U32, **fields):
+    """An hp_rope_desc: cos_sin fp32 [max_pos, rot_dim], positions [axes, num_tokens]."""
+    d = HpRopeDesc()
+    d.cos_sin, d.positions = _p(cos_sin), _p(positions)
+    d.max_pos, d.rot_dim = cos_sin.shape
+    d.axes = len(sections)
+    for i, n in enumerate(sections[:4]):
+        d.section[i] = n
+    d.interleaved, d.index_type = int(interleaved), index_type
+    for name, v in fields.items():
+        setattr(d, name, v)
+    d.keep = (cos_sin, positions)
+    return d
+
+
+def qk_desc(*, q, k, v, q_out, num_q_heads, num_kv_heads, head_dim, dtype, slot_map, k_pool,
+            v_pool, num_pages, page_size, q_weight=None, k_weight=None, eps=1e-6, **fields):
+    """An hp_qk_desc over device tensors: q, k, v and q_out with the token as their first
+    dimension (its stride is taken from the tensor), heads and dims contiguous in it."""
+    d = HpQkDesc()
+    d.dtype, d.num_q_heads, d.num_kv_heads = _dtype(dtype), num_q_heads, num_kv_heads
+    d.head_dim, d.eps, d.num_tokens = head_dim, eps, slot_map.numel()
+    bufs = dict(q=q, k=k, v=v, q_out=q_out, q_weight=q_weight, k_weight=k_weight,
+                slot_map=slot_map, k_pool=k_pool, v_pool=v_pool)
+    for name, t in bufs.items():
+        setattr(d, name, _p(t))
+    for name, t in (("q", q), ("k", k), ("v", v), ("q_out", q_out)):
+        setattr(d, name + "_stride", 0 if t is None else t.stride(0))
+    d.num_pages, d.page_size = num_pages, page_size
+    for name, val in fields.items():
+        setattr(d, name, val)
+    d.keep = tuple(bufs.values())
+    return d
+
+
+def latent_desc(*, latent, k_rope, dtype, slot_map, pool, num_pages, page_size, q_rope=None,
+                q_out=None, latent_weight=None, eps=1e-6, **fields):
+    """An hp_latent_desc over device tensors: latent [tokens, latent_dim], k_rope [tokens,
+    rope_dim], q_rope and q_out [tokens, heads, rope_dim], each with its own strides."""
+    d = HpLatentDesc()
+    d.dtype, d.latent_dim, d.eps = _dtype(dtype), latent.shape[1], eps
+    d.num_q_heads = 0 if q_rope is None else q_rope.shape[1]
+    d.num_tokens = slot_map.numel()
+    bufs = dict(latent=latent, latent_weight=latent_weight, k_rope=k_rope, q_rope=q_rope,
+                q_out=q_out, slot_map=slot_map, pool=pool)
+    for name, t in bufs.items():
+        setattr(d, name, _p(t))
+    d.latent_stride, d.k_rope_stride = latent.stride(0), k_rope.stride(0)
+    if q_rope is not None:
+        d.q_stride, d.q_head_stride = q_rope.stride(0), q_rope.stride(1)
+    if q_out is not None:
+        d.q_out_stride, d.q_out_head_stride = q_out.stride(0), q_out.stride(1)
+    d.num_pages, d.page_size = num_pages, page_size
+    for name, val in fields.items():
+        setattr(d, name, val)
+    d.keep = tuple(bufs.values())
+    return d
+
+
 def lib():
     """The loaded library; raises RuntimeError when libhp.so is missing."""
     global _lib
@@ -67,6 +197,7 @@ def lib():
                     % LIB_PATH)
             L = ctypes.CDLL(LIB_PATH)
             i, u64, vp = ctypes.c_int, ctypes.c_uint64, ctypes.c_void_p
+            u32 = ctypes.c_uint32
             D = ctypes.POINTER(HpPagedDesc)
             pu64 = ctypes.POINTER(ctypes.c_uint64)
             sig = {
@@ -111,6 +242,21 @@ def lib():
                                             vp]),
                 "hp_gather_dequant_q_planned": (i, [D, ctypes.POINTER(HpQuantDesc), vp, vp, vp,
                                                     vp]),
+                "hp_step_tables_workspace_bytes": (i, [u64, pu64]),
+                "hp_step_tables": (i, [ctypes.POINTER(HpStepDesc), vp, u64, vp, vp]),
+                "hp_qk_norm_rope_append": (i, [ctypes.POINTER(HpQkDesc),
+                                               ctypes.POINTER(HpRopeDesc), vp, vp]),
+                "hp_latent_append": (i, [ctypes.POINTER(HpLatentDesc),
+                                         ctypes.POINTER(HpRopeDesc), vp, vp]),
+                "hp_latent_decode_workspace_bytes": (i, [D, u32, u64, u32, pu64]),
+                "hp_latent_plan": (i, [D, u32, vp, u64, u32, vp, u64, vp, vp]),
+                "hp_latent_decode": (i, [D, u32, vp, vp, u64, u32, ctypes.c_float, vp, vp, u64,
+                                         vp, vp]),
+                "hp_latent_decode_planned": (i, [D, u32, vp, vp, u64, u32, ctypes.c_float, vp,
+                                                 vp, u64, vp, vp]),
+                "hp_latent_prefill_workspace_bytes": (i, [D, u32, u32, u32, u64, u32, u64, pu64]),
+                "hp_latent_prefill": (i, [D, u32, vp, u32, u32, vp, vp, u64, u32, ctypes.c_float,
+                                          vp, u64, vp, u64, vp, vp]),
             }
             for name, (res, args) in sig.items():
                 f = getattr(L, name)
@@ -307,6 +453,72 @@ def hp_attention_decode_planned(desc, v_pool, q, num_q_heads, scale, out, worksp
     return lib().hp_attention_decode_planned(desc.ref, _p(v_pool), _p(q), num_q_heads,
                                              float(scale), _p(out), _p(workspace),
                                              _wsn(workspace), _p(d_status), _stream(stream))
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def hp_step_tables_workspace_bytes(num_seqs):
+    n = ctypes.c_uint64(0)
+    rc = lib().hp_step_tables_workspace_bytes(num_seqs, ctypes.byref(n))
+    return rc, n.value
+
+
+def hp_step_tables(step, workspace, d_status=None, stream=None):
+    return lib().hp_step_tables(_ref(step), _p(workspace), _wsn(workspace), _p(d_status),
+                                _stream(stream))
+
+
+def hp_qk_norm_rope_append(qk, rope, d_status=None, stream=None):
+    return lib().hp_qk_norm_rope_append(_ref(qk), _ref(rope), _p(d_status), _stream(stream))
+
+
+def hp_latent_append(latent, rope, d_status=None, stream=None):
+    return lib().hp_latent_append(_ref(latent), _ref(rope), _p(d_status), _stream(stream))
+
+
+def hp_latent_decode_workspace_bytes(desc, latent_dim, total_q, num_q_heads):
+    n = ctypes.c_uint64(0)
+    rc = lib().hp_latent_decode_workspace_bytes(desc.ref, latent_dim, total_q, num_q_heads,
+                                                ctypes.byref(n))
+    return rc, n.value
+
+
+def hp_latent_decode(desc, latent_dim, q, q_ptr, total_q, num_q_heads, scale, out, workspace,
+                     d_status=None, stream=None):
+    return lib().hp_latent_decode(desc.ref, latent_dim, _p(q), _p(q_ptr), total_q, num_q_heads,
+                                  float(scale), _p(out), _p(workspace), _wsn(workspace),
+                                  _p(d_status), _stream(stream))
+
+
+def hp_latent_plan(desc, latent_dim, q_ptr, total_q, num_q_heads, workspace, d_status=None,
+                   stream=None):
+    return lib().hp_latent_plan(desc.ref, latent_dim, _p(q_ptr), total_q, num_q_heads,
+                                _p(workspace), _wsn(workspace), _p(d_status), _stream(stream))
+
+
+def hp_latent_decode_planned(desc, latent_dim, q, q_ptr, total_q, num_q_heads, scale, out,
+                             workspace, d_status=None, stream=None):
+    return lib().hp_latent_decode_planned(desc.ref, latent_dim, _p(q), _p(q_ptr), total_q,
+                                          num_q_heads, float(scale), _p(out), _p(workspace),
+                                          _wsn(workspace), _p(d_status), _stream(stream))
+
+
+def hp_latent_prefill_workspace_bytes(desc, latent_dim, nope_dim, v_dim, total_q, num_q_heads,
+                                      kv_tokens):
+    n = ctypes.c_uint64(0)
+    rc = lib().hp_latent_prefill_workspace_bytes(desc.ref, latent_dim, nope_dim, v_dim, total_q,
+                                                 num_q_heads, kv_tokens, ctypes.byref(n))
+    return rc, n.value
+
+
+def hp_latent_prefill(desc, latent_dim, w_kv, nope_dim, v_dim, q, q_ptr, total_q, num_q_heads,
+                      scale, out, kv_tokens, workspace, d_status=None, stream=None):
+    return lib().hp_latent_prefill(desc.ref, latent_dim, _p(w_kv), nope_dim, v_dim, _p(q),
+                                   _p(q_ptr), total_q, num_q_heads, float(scale), _p(out),
+                                   kv_tokens, _p(workspace), _wsn(workspace), _p(d_status),
+                                   _stream(stream))
 
 
 def hp_from_kernel_layout(src, dst, num_blocks, block_size, num_heads, head_dim, x, dtype,
