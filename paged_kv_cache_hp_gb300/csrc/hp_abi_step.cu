@@ -261,10 +261,10 @@ int check_q_ptr(const hp_paged_desc& d, const void* q_ptr, u64 total_q)
     return misaligned(q_ptr, index_bytes(d.index_type)) ? HP_ERR_ALIGN : HP_OK;
 }
 
-bool latent_on_tensor_cores(const hp_paged_desc& d, uint32_t latent_dim)
+bool latent_on_tensor_cores(const hp_paged_desc& d, uint32_t latent_dim, u64 q_rows)
 {
     return !(d.flags & (HP_ATTN_CUDA_CORES | HP_HOST_MEMORY)) &&
-           hp::latent_tc_fits(latent_dim, d.head_dim, d.page_size, d.num_pages);
+           hp::latent_tc_fits(latent_dim, d.head_dim, d.page_size, d.num_pages, q_rows);
 }
 
 // Tensor cores: tiles of 64 rows; above 64 heads a worker is a pair of CTAs whose two tiles
@@ -329,7 +329,7 @@ HP_API int hp_latent_plan(const hp_paged_desc* desc, uint32_t latent_dim, const 
     pa.total_new = total_q;
     pa.step_tokens = hp::kLatentStep;
     pa.heads = num_q_heads;
-    pa.group_rows = latent_group_rows(latent_on_tensor_cores(d, latent_dim), num_q_heads);
+    pa.group_rows = latent_group_rows(latent_on_tensor_cores(d, latent_dim, total_q * num_q_heads), num_q_heads);
     pa.row_round = 1;
     return hp::launch_plan(hp::kPlanLatent, d.index_type == HP_IDX_U64, pa, stream);
 }
@@ -350,7 +350,7 @@ HP_API int hp_latent_decode_planned(const hp_paged_desc* desc, uint32_t latent_d
     int dev = 0;
     const u64 sms = std::min<u64>((u64)hp::current_sms(&dev), hp::kLatentMaxSms);
     if (sms == 0) return HP_ERR_CUDA;
-    const bool tc = latent_on_tensor_cores(d, latent_dim);
+    const bool tc = latent_on_tensor_cores(d, latent_dim, total_q * num_q_heads);
     const hp::WsView ws = hp::ws_view(workspace, d.num_seqs);
     hp::LatentArgs a{};
     a.pool = d.page_pool;

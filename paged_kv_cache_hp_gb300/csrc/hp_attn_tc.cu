@@ -64,12 +64,14 @@
 #include "hp_attn_merge.cuh"
 #include "hp_internal.cuh"
 #include "hp_resolve.cuh"
+#include "hp_tcgen05.cuh"
 #include "hp_tma.cuh"
 
 namespace hp {
 namespace {
 
 using namespace tma;
+using namespace tc;
 
 constexpr int kRows = 128;          // rows of a step's tiles: H_kv heads x TS tokens
 constexpr int kD = 128;             // head_dim
@@ -92,169 +94,12 @@ constexpr uint32_t kOffP = kKV * 2 * kTile;
 constexpr uint32_t kOffQ = kOffP + 2 * 2 * kPBuf;
 constexpr uint32_t kSmemTc = kOffQ + 2 * kQBuf + 1024;  // + room to align the base to 1 KiB
 
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t lbo, uint32_t sbo)
-{
-    uint64_t d = (uint64_t)((addr & 0x3FFFF) >> 4);
-    d |= (uint64_t)((lbo >> 4) & 0x3FFF) << 16;
-    d |= (uint64_t)((sbo >> 4) & 0x3FFF) << 32;
-    d |= (uint64_t)1 << 46;  // descriptor version of tcgen05
-    d |= (uint64_t)2 << 61;  // 128-byte swizzle
-    return d;
-}
-
 // kind::f16 instruction descriptor: fp32 accumulator, A and B both bf16 (or both f16),
 // A K-major (S) or M-major (O^T), B K-major, M = 128, N = n.
 __device__ __forceinline__ uint32_t mma_idesc(bool bf16, bool a_mn_major, uint32_t n)
 {
     return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) |
            ((a_mn_major ? 1u : 0u) << 15) | ((n >> 3) << 17) | ((128u >> 4) << 24);
-}
-
-__device__ __forceinline__ void mma_f16(uint32_t tmem, uint64_t ad, uint64_t bd, uint32_t idesc,
-                                        uint32_t accumulate)
-{
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem),
-                 "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate)
-                 : "memory");
-}
-
-__device__ __forceinline__ void mma_commit(uint32_t bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                 : "memory");
-}
-
-// tcgen05.ld of N consecutive TMEM columns of this thread's lane (32x32b shape) into r,
-// not yet waited for; the column is a multiple of N
-template <int N> __device__ __forceinline__ void tmem_issue(uint32_t taddr, uint32_t* r);
-
-template <> __device__ __forceinline__ void tmem_issue<1>(uint32_t taddr, uint32_t* r)
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
-                 : "=r"(r[0])
-                 : "r"(taddr));
-}
-
-template <> __device__ __forceinline__ void tmem_issue<2>(uint32_t taddr, uint32_t* r)
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];"
-                 : "=r"(r[0]), "=r"(r[1])
-                 : "r"(taddr));
-}
-
-template <> __device__ __forceinline__ void tmem_issue<4>(uint32_t taddr, uint32_t* r)
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(taddr));
-}
-
-template <> __device__ __forceinline__ void tmem_issue<8>(uint32_t taddr, uint32_t* r)
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-}
-
-template <> __device__ __forceinline__ void tmem_issue<16>(uint32_t taddr, uint32_t* r)
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                 : "r"(taddr));
-}
-
-// waits for this thread's TMEM loads; the registers they fill are operands of the wait, so
-// no use of them is scheduled above it
-template <int N> __device__ __forceinline__ void tmem_wait(uint32_t (&r)[N]);
-
-template <> __device__ __forceinline__ void tmem_wait<1>(uint32_t (&r)[1])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0])::"memory");
-}
-
-template <> __device__ __forceinline__ void tmem_wait<2>(uint32_t (&r)[2])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1])::"memory");
-}
-
-template <> __device__ __forceinline__ void tmem_wait<4>(uint32_t (&r)[4])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3])::"memory");
-}
-
-template <> __device__ __forceinline__ void tmem_wait<8>(uint32_t (&r)[8])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])::"memory");
-}
-
-template <> __device__ __forceinline__ void tmem_wait<16>(uint32_t (&r)[16])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
-}
-
-template <> __device__ __forceinline__ void tmem_wait<32>(uint32_t (&r)[32])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
-}
-
-// N consecutive TMEM columns of this thread's lane, waited for
-template <int N> __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N])
-{
-    uint32_t r[N];
-    tmem_issue<N>(taddr, r);
-    tmem_wait<N>(r);
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
-                                       uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-        : "memory");
-}
-
-// Byte offset of element (row r, column c) of a 128-byte-swizzled K-major operand whose
-// 8-row groups are 1024 bytes apart, c < 64 (one 128-byte row).
-__device__ __forceinline__ uint32_t sw128_off(uint32_t r, uint32_t c)
-{
-    return (r >> 3) * 1024 + (r & 7) * 128 + ((((c * 2) >> 4) ^ (r & 7)) << 4) + ((c * 2) & 15);
-}
-
-__device__ __forceinline__ void named_sync(int id, int n)
-{
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
-}
-
-// true in every one of the n threads at named barrier `id` iff v is true in all (and) / in
-// any (or) of them; the softmax threads take every decision to stop together, so none is
-// left at a barrier
-__device__ __forceinline__ bool named_and(int id, int n, bool v)
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-                 "barrier.cta.red.and.pred p, %2, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(r)
-                 : "r"((uint32_t)v), "r"(id), "r"(n)
-                 : "memory");
-    return r != 0;
-}
-__device__ __forceinline__ bool named_or(int id, int n, bool v)
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-                 "barrier.cta.red.or.pred p, %2, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(r)
-                 : "r"((uint32_t)v), "r"(id), "r"(n)
-                 : "memory");
-    return r != 0;
 }
 
 // The segments of a worker's step range, in the order every role walks them: the sequences
@@ -781,25 +626,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                      "r"(kTmemCols)
                      : "memory");
-}
-
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn()
-{
-    static EncodeFn fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return (EncodeFn) nullptr;
-        return reinterpret_cast<EncodeFn>(p);
-    }();
-    return fn;
 }
 
 // A pool [num_pages * P tokens, H_kv, 128] as a 3-d tensor (this launch's H_kv heads of the

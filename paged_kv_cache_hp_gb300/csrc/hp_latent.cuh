@@ -47,7 +47,8 @@ struct LatentArgs {
 };
 int launch_latent_cc(const LatentArgs& a, void* stream);
 int launch_latent_tc(const LatentArgs& a, void* stream);
-bool latent_tc_fits(uint32_t latent_dim, uint64_t head_dim, uint64_t page_size, uint64_t num_pages);
+bool latent_tc_fits(uint32_t latent_dim, uint64_t head_dim, uint64_t page_size, uint64_t num_pages,
+                    uint64_t q_rows);
 int launch_latent_merge(const LatentArgs& a, void* stream);
 
 // Expanded form, after a kPlanLatent plan (rows padded to kLatentPad per sequence, units of
