@@ -1,0 +1,554 @@
+// hp_latent_prefill_tc.cu -- the expanded form of latent attention on the tensor cores (tcgen05):
+// latent_dim 512, rope_dim 64, nope_dim 128, v_dim 128.
+//
+// latent_expand_kernel: KV [rows, H * 256] = C [rows, 512] . W^T, a plain product.  Persistent
+// CTAs, tiles of 128 x 256, eight 64-wide slices of the 512 through a ring of three stages (A
+// 16 KiB, B 32 KiB, TMA, 128-byte swizzled), two accumulators of 256 TMEM columns so that a
+// tile's epilogue (TMEM -> registers -> shared memory -> TMA store) overlaps the next tile's
+// products.  A CTA's tiles are consecutive, so all the columns of a few row blocks are in
+// flight at once and both operands come from L2.
+//
+// latent_prefill_kernel: softmax(scale Q K^T) V for one head and 256 queries of a sequence, as
+// two tiles of 128 queries that share the keys' 128-row blocks: K = [expanded 128 | rope 64], V =
+// expanded 128.  Per tile and block:
+//   S [128 x 128] = Q . K^T      12 products of K = 16, operands in shared memory
+//   O [128 x 128] += P . V        8 products; P (16-bit) in TMEM over S, V N-major
+// A thread owns one query row of S: its maximum, its weights and (the same TMEM lane) its row of
+// O, which it rescales only when a score exceeds the row's reference maximum by more than
+// 2^kTau.  While one tile's softmax runs, the other tile's products do: the issue order is
+// O0(j-1) S0(j) O1(j-1) S1(j), so the tensor pipe is what bounds it (2560 cycles for both tiles of a
+// block).  P overwrites S, which is safe because one thread issues both products and they
+// execute in order.  K and V pass through a ring of eight 16 KiB slots (128 keys x 64 dims).
+// Sequences are padded to 128 rows of zeros in the workspace (hp_latent.cu), so no block reads
+// another sequence's rows.
+//
+// Every wait is bounded (about 2 s) and reports HP_ERR_TIMEOUT; operations in flight are waited
+// for (bounded) before TMEM and shared memory go.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "hp_attn_merge.cuh"
+#include "hp_internal.cuh"
+#include "hp_latent.cuh"
+#include "hp_resolve.cuh"
+#include "hp_tcgen05.cuh"
+#include "hp_tma.cuh"
+
+namespace hp {
+namespace {
+
+using namespace tma;
+using namespace tc;
+
+constexpr uint32_t kR = 512, kW = 576, kDn = 128, kDv = 128, kDq = 192, kKv = kDn + kDv;
+constexpr uint32_t kSlot = 128 * 128;  // 128 rows x 64 dims
+constexpr uint32_t kTmemCols = 512;
+
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int c0, int c1, uint32_t src)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(src)
+                 : "memory");
+}
+
+// ------------------------------------------------------------------------ expansion
+constexpr uint32_t kGStages = 3, kGSlices = kR / 64;
+constexpr uint32_t kGStage = 3 * kSlot;                  // A 128 x 64, B 256 x 64
+constexpr uint32_t kGOut = kGStages * kGStage;           // the epilogue's four 128 x 64 blocks
+constexpr uint32_t kGSmem = kGOut + 4 * kSlot + 1024;
+constexpr int kGThreads = 6 * 32;
+
+template <typename T>
+__global__ void __launch_bounds__(kGThreads, 1)
+    latent_expand_kernel(const LatentPrefillArgs a, const __grid_constant__ CUtensorMap tma_a,
+                         const __grid_constant__ CUtensorMap tma_b, const __grid_constant__ CUtensorMap tma_o)
+{
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    __shared__ __align__(8) unsigned long long full[kGStages], freed[kGStages], t_full[2], t_free[2];
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+    pdl_wait();
+    if (a.hdr->verdict != kVerdictOk) return;
+    const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t nt = a.H;                              // column tiles: a head each
+    const uint64_t tiles = a.hdr->total_rows / 128 * nt;
+    const uint64_t per = (tiles + gridDim.x - 1) / gridDim.x;
+    const uint64_t beg = umin(blockIdx.x * per, tiles), end = umin(beg + per, tiles);
+    if (beg >= end) return;
+    const uint32_t sm0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    unsigned char* smem = smem_raw + (sm0 - smem_u32(smem_raw));
+    if (threadIdx.x == 0) {
+        for (uint32_t i = 0; i < kGStages; ++i) {
+            mbar_init(smem_u32(&full[i]), 1);
+            mbar_init(smem_u32(&freed[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&t_full[i]), 1);
+            mbar_init(smem_u32(&t_free[i]), 128);
+        }
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc(smem_u32(&tmem_base), kTmemCols);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = tmem_base;
+    auto failed = [&](bool ok) {
+        if (!ok) {
+            abort_flag = 1;
+            report(a.d_status, HP_ERR_TIMEOUT);
+        }
+        return !ok || *(volatile int*)&abort_flag;
+    };
+    if (warp == 0) {
+        if (lane == 0) {
+            uint64_t i = 0;
+            bool stop = false;
+            for (uint64_t t = beg; t < end && !stop; ++t) {
+                const int row = (int)(t / nt * 128), col = (int)(t % nt * kKv);
+                for (uint32_t s = 0; s < kGSlices; ++s, ++i) {
+                    const uint32_t st = (uint32_t)(i % kGStages), bar = smem_u32(&full[st]);
+                    if (failed(i < kGStages || mbar_wait(smem_u32(&freed[st]), (uint32_t)((i / kGStages - 1) & 1)))) {
+                        stop = true;
+                        break;
+                    }
+                    mbar_expect_tx(bar, kGStage);
+                    const uint32_t d = sm0 + st * kGStage;
+                    tma_2d(d, &tma_a, (int)(s * 64), row, bar);
+                    tma_2d(d + kSlot, &tma_b, (int)(s * 64), col, bar);
+                    tma_2d(d + 2 * kSlot, &tma_b, (int)(s * 64), col + 128, bar);
+                }
+            }
+            for (uint64_t x = i > kGStages ? i - kGStages : 0; x < i; ++x)
+                mbar_wait(smem_u32(&full[x % kGStages]), (uint32_t)((x / kGStages) & 1));
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t id = f16_idesc(a.bf16 != 0, false, false, 128, 256);
+            const uint64_t ad0 = sw128_desc(sm0, 16, 1024), bd0 = sw128_desc(sm0 + kSlot, 16, 1024);
+            uint64_t i = 0, n = 0;
+            bool stop = false;
+            for (uint64_t t = beg; t < end && !stop; ++t, ++n) {
+                const uint32_t acc = (uint32_t)(n & 1);
+                if (failed(n < 2 || mbar_wait(smem_u32(&t_free[acc]), (uint32_t)((n / 2 - 1) & 1)))) break;
+                for (uint32_t s = 0; s < kGSlices; ++s, ++i) {
+                    const uint32_t st = (uint32_t)(i % kGStages);
+                    if (failed(mbar_wait(smem_u32(&full[st]), (uint32_t)((i / kGStages) & 1)))) {
+                        stop = true;
+                        break;
+                    }
+                    fence_after();
+                    const uint32_t o = (st * kGStage) >> 4;
+#pragma unroll
+                    for (uint32_t kk = 0; kk < 4; ++kk)
+                        mma_f16(tmem + acc * 256, ad0 + o + kk * 2, bd0 + o + kk * 2, id, s | kk);
+                    mma_commit(smem_u32(&freed[st]));
+                }
+                mma_commit(smem_u32(&t_full[acc]));
+            }
+            for (uint64_t x = n > 2 ? n - 2 : 0; x < n; ++x)
+                mbar_wait(smem_u32(&t_full[x & 1]), (uint32_t)((x / 2) & 1));
+        }
+        __syncwarp();
+    } else {
+        const uint32_t q4 = warp & 3, row = q4 * 32 + lane;
+        const uint32_t lane_addr = (q4 * 32) << 16;
+        uint64_t n = 0;
+        for (uint64_t t = beg; t < end; ++t, ++n) {
+            const uint32_t acc = (uint32_t)(n & 1);
+            const bool ok = mbar_wait(smem_u32(&t_full[acc]), (uint32_t)((n / 2) & 1));
+            if (!ok) failed(false);
+            // the staging blocks are free once the last tile's stores have read them
+            if (threadIdx.x == 64) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            if (!named_and(1, 128, ok)) break;  // the four warps stop together
+            fence_after();
+#pragma unroll 1
+            for (uint32_t c = 0; c < 256; c += 32) {
+                uint32_t o[32];
+                tmem_issue<32>(tmem + lane_addr + acc * 256 + c, o);
+                tmem_wait<32>(o);
+                unsigned char* blk = smem + kGOut + (c >> 6) * kSlot + row * 128;
+#pragma unroll
+                for (uint32_t v = 0; v < 4; ++v) {
+                    uint4 w;
+                    w.x = pack2<T>(__uint_as_float(o[8 * v]), __uint_as_float(o[8 * v + 1]));
+                    w.y = pack2<T>(__uint_as_float(o[8 * v + 2]), __uint_as_float(o[8 * v + 3]));
+                    w.z = pack2<T>(__uint_as_float(o[8 * v + 4]), __uint_as_float(o[8 * v + 5]));
+                    w.w = pack2<T>(__uint_as_float(o[8 * v + 6]), __uint_as_float(o[8 * v + 7]));
+                    *reinterpret_cast<uint4*>(blk + (((((c & 32) >> 3) + v) ^ (row & 7)) << 4)) = w;
+                }
+            }
+            fence_before();
+            mbar_arrive(smem_u32(&t_free[acc]));
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            named_sync(2, 128);
+            if (threadIdx.x == 64) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    tma_store_2d(&tma_o, (int)(t % nt * kKv) + b * 64, (int)(t / nt * 128), sm0 + kGOut + b * kSlot);
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+        }
+        if (threadIdx.x == 64) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 1) tmem_free(tmem, kTmemCols);
+}
+
+// ------------------------------------------------------------------------ attention
+constexpr uint32_t kSlots = 8;
+constexpr uint32_t kOffKv = 2 * 3 * kSlot;  // Q: two tiles of three 128 x 64 blocks
+constexpr uint32_t kSmem = kOffKv + kSlots * kSlot + 1024;
+constexpr uint32_t kSCol = 0, kOCol = 256;  // S (and P) of tile t at 128 t, O at 256 + 128 t
+constexpr int kThreads = 10 * 32;           // warps 0-3 tile 0, 4-7 tile 1, 8 TMA, 9 products
+constexpr float kTau = 8.0f;
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_prefill_kernel(const LatentPrefillArgs a, const __grid_constant__ CUtensorMap tmq,
+                          const __grid_constant__ CUtensorMap tmkv, const __grid_constant__ CUtensorMap tmr)
+{
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    __shared__ __align__(8) unsigned long long kv_full[kSlots], kv_free[kSlots], q_full[2], s_full[2],
+        p_full[2], o_done[2], all_done;
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+    pdl_wait();
+    if (a.hdr->verdict != kVerdictOk) return;
+    const uint64_t units = a.hdr->total_units;
+    const uint64_t ui = blockIdx.x % a.max_units;
+    if (ui >= units) return;
+    const uint32_t h = (uint32_t)(blockIdx.x / a.max_units);
+    const uint64_t u = units - 1 - ui;  // a sequence's last queries see most: they start first
+    const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint64_t s = find_seq(a.units_off, a.num_seqs, u);
+    const uint64_t len = index_at(a.lens, a.idx64, s);
+    const uint64_t q0 = a.q_ptr ? index_at(a.q_ptr, a.idx64, s) : s;
+    const uint64_t n = (a.q_ptr ? index_at(a.q_ptr, a.idx64, s + 1) : s + 1) - q0;
+    const uint64_t i0 = (u - a.units_off[s]) * kLatentTcQueries;
+    // blocks of 128 keys that each tile's last query reaches
+    uint32_t nblk[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const uint64_t lo = i0 + 128 * t, last = umin(n, lo + 128);  // one past the tile's last query
+        nblk[t] = last > lo && len + last > n ? (uint32_t)((len + last - n + 127) / 128) : 0;
+    }
+    const uint32_t blocks = nblk[0] > nblk[1] ? nblk[0] : nblk[1];
+
+    const uint32_t sm0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    if (threadIdx.x == 0) {
+        for (uint32_t i = 0; i < kSlots; ++i) {
+            mbar_init(smem_u32(&kv_full[i]), 1);
+            mbar_init(smem_u32(&kv_free[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&q_full[i]), 1);
+            mbar_init(smem_u32(&s_full[i]), 1);
+            mbar_init(smem_u32(&p_full[i]), 128);
+            mbar_init(smem_u32(&o_done[i]), 1);
+        }
+        mbar_init(smem_u32(&all_done), 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 9) tmem_alloc(smem_u32(&tmem_base), kTmemCols);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = tmem_base;
+    auto failed = [&](bool ok) {
+        if (!ok) {
+            abort_flag = 1;
+            report(a.d_status, HP_ERR_TIMEOUT);
+        }
+        return !ok || *(volatile int*)&abort_flag;
+    };
+
+    if (warp == 8) {
+        if (lane == 0) {
+            for (int t = 0; t < 2; ++t)
+                if (nblk[t]) {
+                    mbar_expect_tx(smem_u32(&q_full[t]), 3 * kSlot);
+                    for (uint32_t c = 0; c < 3; ++c)
+                        tma_2d(sm0 + (3 * t + c) * kSlot, &tmq, (int)(h * kDq + c * 64), (int)(q0 + i0 + 128 * t),
+                               smem_u32(&q_full[t]));
+                }
+            const uint64_t row0 = a.rows_off[s];
+            uint32_t c = 0;  // slots filled
+            bool stop = false;
+            for (uint32_t j = 0; j < blocks && !stop; ++j)
+                for (uint32_t i = 0; i < 5; ++i, ++c) {  // K: 0, 1 expanded, 2 rope; V: 3, 4
+                    const uint32_t st = c % kSlots, bar = smem_u32(&kv_full[st]);
+                    if (failed(c < kSlots || mbar_wait(smem_u32(&kv_free[st]), (c / kSlots - 1) & 1))) {
+                        stop = true;
+                        break;
+                    }
+                    mbar_expect_tx(bar, kSlot);
+                    const uint32_t d = sm0 + kOffKv + st * kSlot;
+                    const int row = (int)(row0 + (uint64_t)j * 128);
+                    if (a.test_stall && c == 0) continue;
+                    if (i == 2) tma_2d(d, &tmr, (int)kR, row, bar);
+                    else tma_2d(d, &tmkv, (int)(h * kKv + (i < 2 ? i : i - 1) * 64), row, bar);
+                }
+            for (int t = 0; t < 2; ++t)
+                if (nblk[t]) mbar_wait(smem_u32(&q_full[t]), 0);
+            for (uint32_t x = c > kSlots ? c - kSlots : 0; x < c; ++x)
+                mbar_wait(smem_u32(&kv_full[x % kSlots]), (x / kSlots) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        if (lane == 0 && blocks) {
+            const uint32_t id_s = f16_idesc(a.bf16 != 0, false, false, 128, 128);
+            const uint32_t id_o = f16_idesc(a.bf16 != 0, false, true, 128, 128);
+            const uint32_t id_o64 = f16_idesc(a.bf16 != 0, false, true, 128, 64);
+            const uint64_t qd0 = sw128_desc(sm0, 16, 1024), kd0 = sw128_desc(sm0 + kOffKv, 16, 1024);
+            const uint64_t vd0 = sw128_desc(sm0 + kOffKv, kSlot, 1024);
+            bool issued = false;
+            bool ok = true;
+            auto wait_slot = [&](uint32_t c) {
+                ok = ok && !failed(mbar_wait(smem_u32(&kv_full[c % kSlots]), (c / kSlots) & 1));
+            };
+            // V of block j is two slots of 64 dims: neighbours, but for the ring's last and first
+            auto issue_o = [&](int t, uint32_t j) {
+                ok = ok && !failed(mbar_wait(smem_u32(&p_full[t]), j & 1));
+                wait_slot(5 * j + 3);
+                wait_slot(5 * j + 4);
+                if (!ok) return;
+                fence_after();
+                const uint32_t v0 = (5 * j + 3) % kSlots, pa = tmem + kSCol + t * 128, od = tmem + kOCol + t * 128;
+                if (v0 + 1 < kSlots) {
+                    const uint64_t vd = vd0 + ((v0 * kSlot) >> 4);
+#pragma unroll
+                    for (uint32_t kk = 0; kk < 8; ++kk)
+                        mma_f16_ts(od, pa + kk * 8, vd + ((kk * 2048) >> 4), id_o, j | kk);
+                } else {
+#pragma unroll
+                    for (uint32_t kk = 0; kk < 16; ++kk)
+                        mma_f16_ts(od + (kk >> 3) * 64, pa + (kk & 7) * 8,
+                                   vd0 + (((kk >> 3 ? 0 : v0) * kSlot + (kk & 7) * 2048) >> 4), id_o64,
+                                   j | (kk & 7));
+                }
+                if (j + 1 == nblk[t]) mma_commit(smem_u32(&o_done[t]));
+            };
+            for (int t = 0; t < 2; ++t)
+                if (nblk[t]) ok = ok && !failed(mbar_wait(smem_u32(&q_full[t]), 0));
+            for (uint32_t j = 0; j <= blocks && ok; ++j) {
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (j > 0 && j - 1 < nblk[t]) issue_o(t, j - 1);
+                    if (!ok) break;
+                    if (j < nblk[t]) {
+                        for (uint32_t c = 0; c < 3; ++c) wait_slot(5 * j + c);
+                        if (!ok) break;
+                        fence_after();
+#pragma unroll
+                        for (uint32_t c = 0; c < 3; ++c) {
+                            const uint64_t qd = qd0 + (((3 * t + c) * kSlot) >> 4);
+                            const uint64_t kd = kd0 + ((((5 * j + c) % kSlots) * kSlot) >> 4);
+#pragma unroll
+                            for (uint32_t kk = 0; kk < 4; ++kk)
+                                mma_f16(tmem + kSCol + t * 128, qd + kk * 2, kd + kk * 2, id_s, c | kk);
+                        }
+                        mma_commit(smem_u32(&s_full[t]));
+                        issued = true;
+                    }
+                }
+                if (!ok) break;
+                if (j > 0)
+                    for (uint32_t c = 3; c < 5; ++c) mma_commit(smem_u32(&kv_free[(5 * (j - 1) + c) % kSlots]));
+                if (j < blocks)
+                    for (uint32_t c = 0; c < 3; ++c) mma_commit(smem_u32(&kv_free[(5 * j + c) % kSlots]));
+            }
+            // everything issued has completed before the TMEM goes: one more commit covers it
+            if (issued) {
+                mma_commit(smem_u32(&all_done));
+                mbar_wait(smem_u32(&all_done), 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        const int t = warp >> 2;
+        const uint32_t q4 = warp & 3, row = q4 * 32 + lane;
+        const uint32_t sa = tmem + ((q4 * 32) << 16) + kSCol + t * 128;
+        const uint32_t oa = tmem + ((q4 * 32) << 16) + kOCol + t * 128;
+        const uint64_t qi = i0 + 128 * t + row;
+        const uint64_t vis = qi < n && len + 1 + qi > n ? len + 1 + qi - n : 0;
+        const float qscale = a.scale * 1.4426950408889634f;
+        float m = -INFINITY, l = 0.0f;
+        bool stop = false;
+        for (uint32_t j = 0; j < nblk[t]; ++j) {
+            const bool ok = mbar_wait(smem_u32(&s_full[t]), j & 1);
+            if (__any_sync(0xffffffffu, failed(ok))) {
+                stop = true;
+                break;
+            }
+            fence_after();
+            float x[128];
+            uint32_t* xr = reinterpret_cast<uint32_t*>(x);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_issue<32>(sa + 32 * c, xr + 32 * c);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_wait<32>(*reinterpret_cast<uint32_t(*)[32]>(xr + 32 * c));
+            const uint64_t t0 = (uint64_t)j * 128;
+            const int lim = vis > t0 ? (int)umin(vis - t0, 128) : 0;
+            const bool masked = __any_sync(0xffffffffu, lim < 128);
+            // the largest scaled score: the extreme of the raw ones on the scale's side
+            float mx;
+            if (masked) {
+                mx = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    mx = fmaxf(mx, i < lim ? x[i] * qscale : -INFINITY);
+            } else {
+                float e[4] = {x[0], x[1], x[2], x[3]};
+                if (qscale >= 0.0f) {
+#pragma unroll
+                    for (int i = 4; i < 128; ++i) e[i & 3] = fmaxf(e[i & 3], x[i]);
+                    mx = fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])) * qscale;
+                } else {
+#pragma unroll
+                    for (int i = 4; i < 128; ++i) e[i & 3] = fminf(e[i & 3], x[i]);
+                    mx = fminf(fminf(e[0], e[1]), fminf(e[2], e[3])) * qscale;
+                }
+            }
+            if (__any_sync(0xffffffffu, mx > m + kTau)) {
+                const float mn = fmaxf(m, mx);
+                const float f = m == -INFINITY ? 0.0f : exp2_approx(m - mn);
+                m = mn;
+                l *= f;
+                if (j > 0) {  // the scores of this block are complete, so O of the last one is
+#pragma unroll 1
+                    for (uint32_t c = 0; c < 128; c += 32) {
+                        uint32_t o[32];
+                        tmem_issue<32>(oa + c, o);
+                        tmem_wait<32>(o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st32(oa + c, o);
+                    }
+                }
+            }
+            const float mu = m == -INFINITY ? 0.0f : m;
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t p[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int e = 64 * c + 2 * i;
+                    float p0 = exp2_approx(fmaf(x[e], qscale, -mu)), p1 = exp2_approx(fmaf(x[e + 1], qscale, -mu));
+                    if (masked) {
+                        p0 = e < lim ? p0 : 0.0f;
+                        p1 = e + 1 < lim ? p1 : 0.0f;
+                    }
+                    sum[(2 * i) & 3] += p0;
+                    sum[(2 * i + 1) & 3] += p1;
+                    p[i] = pack2<T>(p0, p1);
+                }
+                tmem_st32(sa + 32 * c, p);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_st_wait();
+            fence_before();
+            mbar_arrive(smem_u32(&p_full[t]));
+        }
+        if (!stop && nblk[t]) {
+            const bool ok = mbar_wait(smem_u32(&o_done[t]), 0);
+            stop = __any_sync(0xffffffffu, failed(ok));
+            fence_after();
+        }
+        if (!stop) {
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            uint4* o4 = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + ((q0 + qi) * a.H + h) * kDv);
+#pragma unroll 1
+            for (uint32_t c = 0; c < 128; c += 32) {
+                uint32_t o[32];
+                if (nblk[t]) {
+                    tmem_issue<32>(oa + c, o);
+                    tmem_wait<32>(o);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0u;
+                }
+                if (qi < n) {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        uint4 w;
+                        uint32_t* wp = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            wp[e] = pack2<T>(__uint_as_float(o[8 * v + 2 * e]) * inv,
+                                             __uint_as_float(o[8 * v + 2 * e + 1]) * inv);
+                        o4[c / 8 + v] = w;
+                    }
+                }
+            }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 9) tmem_free(tmem, kTmemCols);
+}
+
+template <typename T>
+int launch_t(const LatentPrefillArgs& a, cudaStream_t st)
+{
+    CUtensorMap ma, mb, mo, mq, mr;
+    const uint64_t kv_row = (uint64_t)a.H * kKv * 2;
+    if (!map_2d(&ma, a.rows, a.cap_rows, kW, kW * 2, 128, a.bf16) ||
+        !map_2d(&mb, a.w_kv, (uint64_t)a.H * kKv, kR, kR * 2, 128, a.bf16) ||
+        !map_2d(&mo, a.kv, a.cap_rows, (uint64_t)a.H * kKv, kv_row, 128, a.bf16) ||
+        !map_2d(&mq, a.q, a.total_q, (uint64_t)a.H * kDq, (uint64_t)a.H * kDq * 2, 128, a.bf16))
+        return HP_ERR_CUDA;
+    mr = ma;
+    int dev = 0;
+    const int sms = current_sms(&dev);
+    if (sms == 0 || !allow_dynamic_smem<latent_expand_kernel<T>>(dev, (int)kGSmem) ||
+        !allow_dynamic_smem<latent_prefill_kernel<T>>(dev, (int)kSmem))
+        return HP_ERR_CUDA;
+    const uint64_t tiles = a.cap_rows / 128 * a.H;
+    const unsigned grid = (unsigned)(tiles < (uint64_t)sms ? tiles : (uint64_t)sms);
+    if (launch_dependent(latent_expand_kernel<T>, grid, kGThreads, (size_t)kGSmem, st, a, ma, mb, mo) != cudaSuccess)
+        return HP_ERR_CUDA;
+    return launch_dependent(latent_prefill_kernel<T>, (unsigned)(a.max_units * a.H), kThreads, (size_t)kSmem, st, a,
+                            mq, mo, mr) == cudaSuccess
+               ? HP_OK
+               : HP_ERR_CUDA;
+}
+
+}  // namespace
+
+bool latent_prefill_tc_fits(uint32_t latent_dim, uint64_t head_dim, uint32_t nope, uint32_t v,
+                            uint64_t cap_rows, uint64_t total_q, uint32_t heads)
+{
+    return latent_dim == kR && head_dim == kW && nope == kDn && v == kDv && cap_rows > 0 &&
+           cap_rows < (1ull << 31) && total_q < (1ull << 31) && 2 * total_q * heads < (1ull << 31);
+}
+
+int launch_latent_prefill_tc(const LatentPrefillArgs& a, void* stream)
+{
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return a.bf16 ? launch_t<__nv_bfloat16>(a, st) : launch_t<__half>(a, st);
+}
+
+}  // namespace hp

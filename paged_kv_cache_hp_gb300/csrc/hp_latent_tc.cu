@@ -486,7 +486,4 @@ int launch_latent_tc(const LatentArgs& a, void* stream)
     return a.bf16 ? launch_t<__nv_bfloat16>(a, st) : launch_t<__half>(a, st);
 }
 
-bool latent_prefill_tc_fits(uint32_t, uint64_t, uint32_t, uint32_t, uint64_t, uint64_t, uint32_t) { return false; }
-int launch_latent_prefill_tc(const LatentPrefillArgs&, void*) { return HP_ERR_CUDA; }
-
 }  // namespace hp
