@@ -510,6 +510,8 @@ HP_API int hp_latent_prefill(const hp_paged_desc* desc, uint32_t latent_dim, con
     a.rows_off = ws.rows_off;
     a.units_off = ws.units_off;
     a.rows = static_cast<char*>(workspace) + w.plan;
+    a.blocked = tc;
+    a.rope_blocks = static_cast<char*>(a.rows) + w.cap_rows * latent_dim * 2;
     a.kv = static_cast<char*>(a.rows) + w.rows_bytes;
     a.out = out;
     a.d_status = d_status;

@@ -284,7 +284,9 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const LatentArgs a)
 // --------------------------------------------------------------------- expanded form
 
 // The latent rows of each sequence in order, padded with zeros to a multiple of kLatentPad: a
-// block of 128 rows lies in one sequence.  Warp per row, 16 bytes per lane.
+// block of 128 rows lies in one sequence.  Warp per row, 16 bytes per lane.  For the tensor cores
+// (blocked) the latent part is a matrix of its own and the rope keys lie as shared memory holds
+// them.
 __global__ void __launch_bounds__(256) latent_rows_kernel(const LatentPrefillArgs a)
 {
     pdl_wait();
@@ -298,14 +300,17 @@ __global__ void __launch_bounds__(256) latent_rows_kernel(const LatentPrefillArg
 #pragma unroll 2
         for (uint32_t i = warp; i < kLatentPad; i += 8) {
             const uint64_t t = row0 - a.rows_off[s] + i;
-            uint4* dst = static_cast<uint4*>(a.rows) + (row0 + i) * vecs;
+            const uint4* src = nullptr;
             if (t < len) {
                 const uint64_t phys = index_at(a.table, a.idx64, tab0 + t / a.page_size);
-                const uint4* src = static_cast<const uint4*>(a.pool) +
-                                   (phys * a.page_size + t % a.page_size) * vecs;
-                for (uint32_t c = lane; c < vecs; c += 32) dst[c] = __ldg(src + c);
-            } else {
-                for (uint32_t c = lane; c < vecs; c += 32) dst[c] = make_uint4(0, 0, 0, 0);
+                src = static_cast<const uint4*>(a.pool) + (phys * a.page_size + t % a.page_size) * vecs;
+            }
+            for (uint32_t c = lane; c < vecs; c += 32) {
+                const uint4 x = src ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                if (!a.blocked) static_cast<uint4*>(a.rows)[(row0 + i) * vecs + c] = x;
+                else if (c < a.R / 8) static_cast<uint4*>(a.rows)[(row0 + i) * (a.R / 8) + c] = x;
+                else  // row i of the block's 128-byte rows, 16-byte pieces swizzled by the row
+                    static_cast<uint4*>(a.rope_blocks)[row0 * 8 + i * 8 + ((c - a.R / 8) ^ (i & 7))] = x;
             }
         }
     }

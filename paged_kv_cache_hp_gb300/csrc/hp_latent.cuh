@@ -69,8 +69,11 @@ struct LatentPrefillArgs {
     const WsHeader* hdr;
     const unsigned long long* rows_off;
     const unsigned long long* units_off;
-    void* rows;               // [cap_rows, W]: the latent rows, zeros behind each sequence
-    void* kv;                 // [cap_rows, H, Dn + Dv]
+    int blocked;              // tensor cores: the buffers below in blocks (hp_latent_prefill_tc.cu)
+    void* rows;               // [cap_rows, W]: the latent rows, zeros behind each sequence; blocked:
+                              // [cap_rows, R]
+    void* rope_blocks;        // blocked: the rope keys, 128 x 64 per 128 rows, swizzled
+    void* kv;                 // [cap_rows, H, Dn + Dv]; blocked: [H, cap_rows / 128, 4, 128 x 64]
     void* out;                // [total_q, H, Dv]
     int* d_status;
 };

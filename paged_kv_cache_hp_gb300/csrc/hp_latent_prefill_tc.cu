@@ -4,9 +4,11 @@
 // latent_expand_kernel: KV [rows, H * 256] = C [rows, 512] . W^T, a plain product.  Persistent
 // CTAs, tiles of 128 x 256, eight 64-wide slices of the 512 through a ring of three stages (A
 // 16 KiB, B 32 KiB, TMA, 128-byte swizzled), two accumulators of 256 TMEM columns so that a
-// tile's epilogue (TMEM -> registers -> shared memory -> TMA store) overlaps the next tile's
+// tile's epilogue (TMEM -> registers -> shared memory -> bulk store) overlaps the next tile's
 // products.  A CTA's tiles are consecutive, so all the columns of a few row blocks are in
-// flight at once and both operands come from L2.
+// flight at once and both operands come from L2.  KV goes to the workspace in blocks of 128 rows x
+// 64 columns laid out as shared memory will hold them (head, row block, K0 K1 V0 V1), so that the
+// attention below loads 16 KiB pieces with untiled bulk copies; the rope keys likewise (hp_latent.cu).
 //
 // latent_prefill_kernel: softmax(scale Q K^T) V for one head and 256 queries of a sequence, as
 // two tiles of 128 queries that share the keys' 128-row blocks: K = [expanded 128 | rope 64], V =
@@ -58,14 +60,6 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int c0, int c1, uint32_t src)
-{
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(c0), "r"(c1), "r"(src)
-                 : "memory");
-}
-
 // ------------------------------------------------------------------------ expansion
 constexpr uint32_t kGStages = 3, kGSlices = kR / 64;
 constexpr uint32_t kGStage = 3 * kSlot;                  // A 128 x 64, B 256 x 64
@@ -76,7 +70,7 @@ constexpr int kGThreads = 6 * 32;
 template <typename T>
 __global__ void __launch_bounds__(kGThreads, 1)
     latent_expand_kernel(const LatentPrefillArgs a, const __grid_constant__ CUtensorMap tma_a,
-                         const __grid_constant__ CUtensorMap tma_b, const __grid_constant__ CUtensorMap tma_o)
+                         const __grid_constant__ CUtensorMap tma_b)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ __align__(8) unsigned long long full[kGStages], freed[kGStages], t_full[2], t_free[2];
@@ -109,12 +103,16 @@ __global__ void __launch_bounds__(kGThreads, 1)
     __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_base;
-    auto failed = [&](bool ok) {
-        if (!ok) {
-            abort_flag = 1;
-            report(a.d_status, HP_ERR_TIMEOUT);
-        }
-        return !ok || *(volatile int*)&abort_flag;
+    // true unless the wait ran out or another role stopped; `warp_wait` for whole warps, whose
+    // lanes then agree
+    auto wait_for = [&](unsigned long long* bar, uint32_t parity) {
+        if (mbar_wait_or(smem_u32(bar), parity, &abort_flag)) return true;
+        abort_flag = 1;
+        report(a.d_status, HP_ERR_TIMEOUT);
+        return false;
+    };
+    auto warp_wait = [&](unsigned long long* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_for(bar, parity)) != 0;
     };
     if (warp == 0) {
         if (lane == 0) {
@@ -124,7 +122,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
                 const int row = (int)(t / nt * 128), col = (int)(t % nt * kKv);
                 for (uint32_t s = 0; s < kGSlices; ++s, ++i) {
                     const uint32_t st = (uint32_t)(i % kGStages), bar = smem_u32(&full[st]);
-                    if (failed(i < kGStages || mbar_wait(smem_u32(&freed[st]), (uint32_t)((i / kGStages - 1) & 1)))) {
+                    if (i >= kGStages && !wait_for(&freed[st], (uint32_t)((i / kGStages - 1) & 1))) {
                         stop = true;
                         break;
                     }
@@ -140,41 +138,42 @@ __global__ void __launch_bounds__(kGThreads, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t id = f16_idesc(a.bf16 != 0, false, false, 128, 256);
-            const uint64_t ad0 = sw128_desc(sm0, 16, 1024), bd0 = sw128_desc(sm0 + kSlot, 16, 1024);
-            uint64_t i = 0, n = 0;
-            bool stop = false;
-            for (uint64_t t = beg; t < end && !stop; ++t, ++n) {
-                const uint32_t acc = (uint32_t)(n & 1);
-                if (failed(n < 2 || mbar_wait(smem_u32(&t_free[acc]), (uint32_t)((n / 2 - 1) & 1)))) break;
-                for (uint32_t s = 0; s < kGSlices; ++s, ++i) {
-                    const uint32_t st = (uint32_t)(i % kGStages);
-                    if (failed(mbar_wait(smem_u32(&full[st]), (uint32_t)((i / kGStages) & 1)))) {
-                        stop = true;
-                        break;
-                    }
-                    fence_after();
-                    const uint32_t o = (st * kGStage) >> 4;
+        const uint32_t id = f16_idesc(a.bf16 != 0, false, false, 128, 256);
+        const uint64_t ad0 = sw128_desc(sm0, 16, 1024), bd0 = sw128_desc(sm0 + kSlot, 16, 1024);
+        uint64_t i = 0, n = 0;
+        bool stop = false;
+        for (uint64_t t = beg; t < end && !stop; ++t, ++n) {
+            const uint32_t acc = (uint32_t)(n & 1);
+            if (n >= 2 && !warp_wait(&t_free[acc], (uint32_t)((n / 2 - 1) & 1))) break;
+            for (uint32_t s = 0; s < kGSlices; ++s, ++i) {
+                const uint32_t st = (uint32_t)(i % kGStages);
+                if (!warp_wait(&full[st], (uint32_t)((i / kGStages) & 1))) {
+                    stop = true;
+                    break;
+                }
+                fence_after();
+                const uint64_t ad = ad0 + ((st * kGStage) >> 4), bd = bd0 + ((st * kGStage) >> 4);
+                if (elect_one()) {
 #pragma unroll
                     for (uint32_t kk = 0; kk < 4; ++kk)
-                        mma_f16(tmem + acc * 256, ad0 + o + kk * 2, bd0 + o + kk * 2, id, s | kk);
+                        mma_f16(tmem + acc * 256, ad + kk * 2, bd + kk * 2, id, s | kk);
                     mma_commit(smem_u32(&freed[st]));
+                    if (s + 1 == kGSlices) mma_commit(smem_u32(&t_full[acc]));
                 }
-                mma_commit(smem_u32(&t_full[acc]));
+                __syncwarp();
             }
-            for (uint64_t x = n > 2 ? n - 2 : 0; x < n; ++x)
-                mbar_wait(smem_u32(&t_full[x & 1]), (uint32_t)((x / 2) & 1));
         }
-        __syncwarp();
+        // every product issued has completed before the TMEM goes
+        for (uint64_t x = n > 2 ? n - 2 : 0; x < n; ++x)
+            mbar_wait(smem_u32(&t_full[x & 1]), (uint32_t)((x / 2) & 1));
+        if (stop && i % kGSlices) mbar_wait(smem_u32(&freed[(i - 1) % kGStages]), (uint32_t)(((i - 1) / kGStages) & 1));
     } else {
         const uint32_t q4 = warp & 3, row = q4 * 32 + lane;
         const uint32_t lane_addr = (q4 * 32) << 16;
         uint64_t n = 0;
         for (uint64_t t = beg; t < end; ++t, ++n) {
             const uint32_t acc = (uint32_t)(n & 1);
-            const bool ok = mbar_wait(smem_u32(&t_full[acc]), (uint32_t)((n / 2) & 1));
-            if (!ok) failed(false);
+            const bool ok = wait_for(&t_full[acc], (uint32_t)((n / 2) & 1));
             // the staging blocks are free once the last tile's stores have read them
             if (threadIdx.x == 64) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             if (!named_and(1, 128, ok)) break;  // the four warps stop together
@@ -200,9 +199,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             named_sync(2, 128);
             if (threadIdx.x == 64) {
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    tma_store_2d(&tma_o, (int)(t % nt * kKv) + b * 64, (int)(t / nt * 128), sm0 + kGOut + b * kSlot);
+                bulk_store_nocommit(static_cast<char*>(a.kv) + (t % nt * (a.cap_rows / 128) + t / nt) * 4 * kSlot,
+                                    sm0 + kGOut, 4 * kSlot);
                 asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
         }
@@ -225,8 +223,7 @@ constexpr float kTau = 8.0f;
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
-    latent_prefill_kernel(const LatentPrefillArgs a, const __grid_constant__ CUtensorMap tmq,
-                          const __grid_constant__ CUtensorMap tmkv, const __grid_constant__ CUtensorMap tmr)
+    latent_prefill_kernel(const LatentPrefillArgs a, const __grid_constant__ CUtensorMap tmq)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ __align__(8) unsigned long long kv_full[kSlots], kv_free[kSlots], q_full[2], s_full[2],
@@ -276,12 +273,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_base;
-    auto failed = [&](bool ok) {
-        if (!ok) {
-            abort_flag = 1;
-            report(a.d_status, HP_ERR_TIMEOUT);
-        }
-        return !ok || *(volatile int*)&abort_flag;
+    // true unless the wait ran out or another role stopped; `warp_wait` for whole warps, whose
+    // lanes then agree
+    auto wait_for = [&](unsigned long long* bar, uint32_t parity) {
+        if (mbar_wait_or(smem_u32(bar), parity, &abort_flag)) return true;
+        abort_flag = 1;
+        report(a.d_status, HP_ERR_TIMEOUT);
+        return false;
+    };
+    auto warp_wait = [&](unsigned long long* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_for(bar, parity)) != 0;
     };
 
     if (warp == 8) {
@@ -293,22 +294,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tma_2d(sm0 + (3 * t + c) * kSlot, &tmq, (int)(h * kDq + c * 64), (int)(q0 + i0 + 128 * t),
                                smem_u32(&q_full[t]));
                 }
-            const uint64_t row0 = a.rows_off[s];
+            const uint64_t b0 = a.rows_off[s] / 128;
+            const char* kv = static_cast<const char*>(a.kv) + (h * (a.cap_rows / 128) + b0) * 4 * kSlot;
+            const char* rope = static_cast<const char*>(a.rope_blocks) + b0 * kSlot;
             uint32_t c = 0;  // slots filled
             bool stop = false;
             for (uint32_t j = 0; j < blocks && !stop; ++j)
                 for (uint32_t i = 0; i < 5; ++i, ++c) {  // K: 0, 1 expanded, 2 rope; V: 3, 4
                     const uint32_t st = c % kSlots, bar = smem_u32(&kv_full[st]);
-                    if (failed(c < kSlots || mbar_wait(smem_u32(&kv_free[st]), (c / kSlots - 1) & 1))) {
+                    if (c >= kSlots && !wait_for(&kv_free[st], (c / kSlots - 1) & 1)) {
                         stop = true;
                         break;
                     }
                     mbar_expect_tx(bar, kSlot);
                     const uint32_t d = sm0 + kOffKv + st * kSlot;
-                    const int row = (int)(row0 + (uint64_t)j * 128);
                     if (a.test_stall && c == 0) continue;
-                    if (i == 2) tma_2d(d, &tmr, (int)kR, row, bar);
-                    else tma_2d(d, &tmkv, (int)(h * kKv + (i < 2 ? i : i - 1) * 64), row, bar);
+                    bulk_load(d, i == 2 ? rope + (uint64_t)j * kSlot : kv + ((uint64_t)j * 4 + (i < 2 ? i : i - 1)) * kSlot,
+                              kSlot, bar);
                 }
             for (int t = 0; t < 2; ++t)
                 if (nblk[t]) mbar_wait(smem_u32(&q_full[t]), 0);
@@ -317,74 +319,82 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == 9) {
-        if (lane == 0 && blocks) {
-            const uint32_t id_s = f16_idesc(a.bf16 != 0, false, false, 128, 128);
-            const uint32_t id_o = f16_idesc(a.bf16 != 0, false, true, 128, 128);
-            const uint32_t id_o64 = f16_idesc(a.bf16 != 0, false, true, 128, 64);
-            const uint64_t qd0 = sw128_desc(sm0, 16, 1024), kd0 = sw128_desc(sm0 + kOffKv, 16, 1024);
-            const uint64_t vd0 = sw128_desc(sm0 + kOffKv, kSlot, 1024);
-            bool issued = false;
-            bool ok = true;
-            auto wait_slot = [&](uint32_t c) {
-                ok = ok && !failed(mbar_wait(smem_u32(&kv_full[c % kSlots]), (c / kSlots) & 1));
-            };
-            // V of block j is two slots of 64 dims: neighbours, but for the ring's last and first
-            auto issue_o = [&](int t, uint32_t j) {
-                ok = ok && !failed(mbar_wait(smem_u32(&p_full[t]), j & 1));
-                wait_slot(5 * j + 3);
-                wait_slot(5 * j + 4);
-                if (!ok) return;
-                fence_after();
-                const uint32_t v0 = (5 * j + 3) % kSlots, pa = tmem + kSCol + t * 128, od = tmem + kOCol + t * 128;
-                if (v0 + 1 < kSlots) {
-                    const uint64_t vd = vd0 + ((v0 * kSlot) >> 4);
+        const uint32_t id_s = f16_idesc(a.bf16 != 0, false, false, 128, 128);
+        const uint32_t id_o = f16_idesc(a.bf16 != 0, false, true, 128, 128);
+        const uint32_t id_o64 = f16_idesc(a.bf16 != 0, false, true, 128, 64);
+        const uint64_t qd0 = sw128_desc(sm0, 16, 1024), kd0 = sw128_desc(sm0 + kOffKv, 16, 1024);
+        const uint64_t vd0 = sw128_desc(sm0 + kOffKv, kSlot, 1024);
+        bool ok = true;
+        auto wait_slots = [&](uint32_t c, uint32_t n) {
+            for (uint32_t x = c; ok && x < c + n; ++x) ok = warp_wait(&kv_full[x % kSlots], (x / kSlots) & 1);
+        };
+        for (int t = 0; t < 2; ++t)
+            if (ok && nblk[t]) ok = warp_wait(&q_full[t], 0);
+        for (uint32_t j = 0; j <= blocks && ok; ++j) {
 #pragma unroll
-                    for (uint32_t kk = 0; kk < 8; ++kk)
-                        mma_f16_ts(od, pa + kk * 8, vd + ((kk * 2048) >> 4), id_o, j | kk);
-                } else {
-#pragma unroll
-                    for (uint32_t kk = 0; kk < 16; ++kk)
-                        mma_f16_ts(od + (kk >> 3) * 64, pa + (kk & 7) * 8,
-                                   vd0 + (((kk >> 3 ? 0 : v0) * kSlot + (kk & 7) * 2048) >> 4), id_o64,
-                                   j | (kk & 7));
-                }
-                if (j + 1 == nblk[t]) mma_commit(smem_u32(&o_done[t]));
-            };
-            for (int t = 0; t < 2; ++t)
-                if (nblk[t]) ok = ok && !failed(mbar_wait(smem_u32(&q_full[t]), 0));
-            for (uint32_t j = 0; j <= blocks && ok; ++j) {
-                for (int t = 0; t < 2 && ok; ++t) {
-                    if (j > 0 && j - 1 < nblk[t]) issue_o(t, j - 1);
+            for (int t = 0; t < 2; ++t) {
+                if (j > 0 && j - 1 < nblk[t]) {
+                    // V of block j - 1 is two slots of 64 dims: neighbours, but for the ring's
+                    // last and first
+                    const uint32_t c = 5 * (j - 1) + 3, v0 = c % kSlots;
+                    if (t == 0 || j > nblk[0]) wait_slots(c, 2);
+                    if (ok) ok = warp_wait(&p_full[t], (j - 1) & 1);
                     if (!ok) break;
-                    if (j < nblk[t]) {
-                        for (uint32_t c = 0; c < 3; ++c) wait_slot(5 * j + c);
-                        if (!ok) break;
-                        fence_after();
+                    fence_after();
+                    const uint32_t pa = tmem + kSCol + t * 128, od = tmem + kOCol + t * 128, acc = j > 1;
+                    const uint64_t vd = vd0 + ((v0 * kSlot) >> 4);
+                    if (elect_one()) {
+                        if (v0 + 1 < kSlots) {
 #pragma unroll
-                        for (uint32_t c = 0; c < 3; ++c) {
-                            const uint64_t qd = qd0 + (((3 * t + c) * kSlot) >> 4);
-                            const uint64_t kd = kd0 + ((((5 * j + c) % kSlots) * kSlot) >> 4);
+                            for (uint32_t kk = 0; kk < 8; ++kk)
+                                mma_f16_ts(od, pa + kk * 8, vd + ((kk * 2048) >> 4), id_o, acc | kk);
+                        } else {
 #pragma unroll
-                            for (uint32_t kk = 0; kk < 4; ++kk)
-                                mma_f16(tmem + kSCol + t * 128, qd + kk * 2, kd + kk * 2, id_s, c | kk);
+                            for (uint32_t kk = 0; kk < 8; ++kk) {
+                                mma_f16_ts(od, pa + kk * 8, vd + ((kk * 2048) >> 4), id_o64, acc | kk);
+                                mma_f16_ts(od + 64, pa + kk * 8, vd0 + ((kk * 2048) >> 4), id_o64, acc | kk);
+                            }
                         }
-                        mma_commit(smem_u32(&s_full[t]));
-                        issued = true;
+                        if (j == nblk[t]) mma_commit(smem_u32(&o_done[t]));
                     }
+                    __syncwarp();
                 }
-                if (!ok) break;
+                if (j < nblk[t]) {
+                    if (t == 0 || j >= nblk[0]) wait_slots(5 * j, 3);
+                    if (!ok) break;
+                    fence_after();
+                    const uint64_t qd = qd0 + ((3 * t * kSlot) >> 4);
+                    const uint64_t k0 = kd0 + ((((5 * j) % kSlots) * kSlot) >> 4);
+                    const uint64_t k1 = kd0 + ((((5 * j + 1) % kSlots) * kSlot) >> 4);
+                    const uint64_t k2 = kd0 + ((((5 * j + 2) % kSlots) * kSlot) >> 4);
+                    const uint32_t sd = tmem + kSCol + t * 128;
+                    if (elect_one()) {
+#pragma unroll
+                        for (uint32_t kk = 0; kk < 4; ++kk) mma_f16(sd, qd + kk * 2, k0 + kk * 2, id_s, kk);
+#pragma unroll
+                        for (uint32_t kk = 0; kk < 4; ++kk)
+                            mma_f16(sd, qd + (kSlot >> 4) + kk * 2, k1 + kk * 2, id_s, 1u);
+#pragma unroll
+                        for (uint32_t kk = 0; kk < 4; ++kk)
+                            mma_f16(sd, qd + (2 * kSlot >> 4) + kk * 2, k2 + kk * 2, id_s, 1u);
+                        mma_commit(smem_u32(&s_full[t]));
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok) break;
+            if (elect_one()) {
                 if (j > 0)
                     for (uint32_t c = 3; c < 5; ++c) mma_commit(smem_u32(&kv_free[(5 * (j - 1) + c) % kSlots]));
                 if (j < blocks)
                     for (uint32_t c = 0; c < 3; ++c) mma_commit(smem_u32(&kv_free[(5 * j + c) % kSlots]));
             }
-            // everything issued has completed before the TMEM goes: one more commit covers it
-            if (issued) {
-                mma_commit(smem_u32(&all_done));
-                mbar_wait(smem_u32(&all_done), 0);
-            }
+            __syncwarp();
         }
+        // everything issued has completed before the TMEM goes: one more commit covers it
+        if (elect_one()) mma_commit(smem_u32(&all_done));
         __syncwarp();
+        mbar_wait(smem_u32(&all_done), 0);
     } else {
         const int t = warp >> 2;
         const uint32_t q4 = warp & 3, row = q4 * 32 + lane;
@@ -396,8 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float m = -INFINITY, l = 0.0f;
         bool stop = false;
         for (uint32_t j = 0; j < nblk[t]; ++j) {
-            const bool ok = mbar_wait(smem_u32(&s_full[t]), j & 1);
-            if (__any_sync(0xffffffffu, failed(ok))) {
+            if (!warp_wait(&s_full[t], j & 1)) {
                 stop = true;
                 break;
             }
@@ -472,8 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(smem_u32(&p_full[t]));
         }
         if (!stop && nblk[t]) {
-            const bool ok = mbar_wait(smem_u32(&o_done[t]), 0);
-            stop = __any_sync(0xffffffffu, failed(ok));
+            stop = !warp_wait(&o_done[t], 0);
             fence_after();
         }
         if (!stop) {
@@ -513,14 +521,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <typename T>
 int launch_t(const LatentPrefillArgs& a, cudaStream_t st)
 {
-    CUtensorMap ma, mb, mo, mq, mr;
-    const uint64_t kv_row = (uint64_t)a.H * kKv * 2;
-    if (!map_2d(&ma, a.rows, a.cap_rows, kW, kW * 2, 128, a.bf16) ||
+    CUtensorMap ma, mb, mq;
+    if (!map_2d(&ma, a.rows, a.cap_rows, kR, kR * 2, 128, a.bf16) ||
         !map_2d(&mb, a.w_kv, (uint64_t)a.H * kKv, kR, kR * 2, 128, a.bf16) ||
-        !map_2d(&mo, a.kv, a.cap_rows, (uint64_t)a.H * kKv, kv_row, 128, a.bf16) ||
         !map_2d(&mq, a.q, a.total_q, (uint64_t)a.H * kDq, (uint64_t)a.H * kDq * 2, 128, a.bf16))
         return HP_ERR_CUDA;
-    mr = ma;
     int dev = 0;
     const int sms = current_sms(&dev);
     if (sms == 0 || !allow_dynamic_smem<latent_expand_kernel<T>>(dev, (int)kGSmem) ||
@@ -528,10 +533,10 @@ int launch_t(const LatentPrefillArgs& a, cudaStream_t st)
         return HP_ERR_CUDA;
     const uint64_t tiles = a.cap_rows / 128 * a.H;
     const unsigned grid = (unsigned)(tiles < (uint64_t)sms ? tiles : (uint64_t)sms);
-    if (launch_dependent(latent_expand_kernel<T>, grid, kGThreads, (size_t)kGSmem, st, a, ma, mb, mo) != cudaSuccess)
+    if (launch_dependent(latent_expand_kernel<T>, grid, kGThreads, (size_t)kGSmem, st, a, ma, mb) != cudaSuccess)
         return HP_ERR_CUDA;
     return launch_dependent(latent_prefill_kernel<T>, (unsigned)(a.max_units * a.H), kThreads, (size_t)kSmem, st, a,
-                            mq, mo, mr) == cudaSuccess
+                            mq) == cudaSuccess
                ? HP_OK
                : HP_ERR_CUDA;
 }

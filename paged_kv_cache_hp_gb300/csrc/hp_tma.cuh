@@ -62,6 +62,17 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity)
     return true;
 }
 
+// As mbar_wait, but also gives up (false) once *abort is set by another role; both are looked at
+// only while the phase is not complete, so a wait that finds it complete costs one poll.
+__device__ __forceinline__ bool mbar_wait_or(uint32_t bar, uint32_t parity, const volatile int* abort)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = now_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (*abort || now_ns() - t0 > kWaitNs) return false;
+    return true;
+}
+
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar)
 {
