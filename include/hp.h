@@ -612,8 +612,8 @@ typedef struct hp_qk_desc {
  * key and the value (copied as it is) to slot slot_map[t] of k_pool and v_pool.  Arithmetic
  * is fp32, rounded once to `dtype`.  A padding token's rows are left as they were.  A token
  * whose slot lies outside the pool (HP_ERR_PAGE_ID) or whose position is not below max_pos
- * (HP_ERR_LEN) is skipped; the first such token's code goes to *d_status.  Two tokens naming
- * one slot leave an unspecified one of them.  q, k, v, q_out, weights and pools: 16-byte
+ * (HP_ERR_LEN) is skipped; *d_status gets HP_ERR_LEN if any token's position is, else
+ * HP_ERR_PAGE_ID if any slot is.  Two tokens naming one slot leave an unspecified one of them.  q, k, v, q_out, weights and pools: 16-byte
  * aligned, strides multiples of 16 bytes (HP_ERR_ALIGN); rot_dim at most head_dim
  * (HP_ERR_ARG).  q_out must not overlap k, v or the pools.
  */

@@ -66,6 +66,8 @@ HP_API int hp_step_tables(const hp_step_desc* step, void* workspace, uint64_t wo
     hp::StepArgs a{};
     a.d = d;
     a.ws = hp::ws_view(workspace, d.num_seqs);
+    a.div_ok = d.page_size <= (1ull << 31);
+    if (a.div_ok) hp::invariant_divisor(d.page_size, &a.div_m, &a.div_l);
     a.d_status = d_status;
     return hp::launch_step_tables(a, stream);
 }

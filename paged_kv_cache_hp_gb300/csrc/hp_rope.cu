@@ -8,9 +8,11 @@
 // keeps that token's cosines and sines in registers over all the heads.  Sums, norm and
 // rotation are fp32, rounded once.
 //
-// Errors come from one extra CTA that looks at every token's slot and positions and stores the
-// first error (or HP_OK); the others skip the tokens it names.  So *d_status costs no launch of
-// its own and does not depend on the order of the CTAs.
+// Errors: a token is skipped by the warp that meets it.  *d_status comes from one extra CTA that
+// looks at every token's slot and positions while the others work (no launch of its own; a
+// batch of 64 tokens takes 3.5 us in a graph), up to kReportTokens; beyond, where that CTA would be the
+// last to finish (16,001 tokens: 69 us for 20 us of work), a memset before the kernel and atomicMin
+// over the codes.  Either way it is the smallest code of the batch, whatever the order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -74,31 +76,38 @@ __device__ __forceinline__ uint64_t position(const RopeArgs& r, uint64_t tokens,
                    : (uint64_t)static_cast<const unsigned int*>(r.positions)[i];
 }
 
-// HP_OK, or why token t is not processed (a padding token: HP_OK, by its slot).
-__device__ __forceinline__ int token_error(const AppendArgs& a, uint64_t t)
+// HP_OK, or why token t, of slot `slot`, is not processed (a padding token: HP_OK).
+__device__ __forceinline__ int token_error(const AppendArgs& a, uint64_t t, int64_t slot)
 {
-    const int64_t slot = a.slot_map[t];
-    if (slot < 0) return HP_OK;
-    if ((uint64_t)slot >= a.num_slots) return HP_ERR_PAGE_ID;
+    bool far = false;
     if (a.rope.rot)
-        for (uint32_t x = 0; x < a.rope.axes; ++x)
-            if (position(a.rope, a.tokens, x, t) >= a.rope.max_pos) return HP_ERR_LEN;
-    return HP_OK;
+        for (uint32_t x = 0; x < a.rope.axes; ++x) far |= position(a.rope, a.tokens, x, t) >= a.rope.max_pos;
+    if (slot < 0) return HP_OK;
+    return far ? HP_ERR_LEN : ((uint64_t)slot >= a.num_slots ? HP_ERR_PAGE_ID : HP_OK);
 }
 
-// The extra CTA: the first token with an error, its code.
-__device__ __forceinline__ void report_first(const AppendArgs& a)
+constexpr uint64_t kReportTokens = 2048;
+
+// The extra CTA: the smallest code of all tokens.
+__device__ __forceinline__ void report_all(const AppendArgs& a)
 {
-    __shared__ unsigned long long s_first;
-    if (threadIdx.x == 0) s_first = ~0ull;
+    __shared__ int s_code;
+    if (threadIdx.x == 0) s_code = HP_OK;
     __syncthreads();
-    for (uint64_t t = threadIdx.x; t < a.tokens; t += kThreads)
-        if (token_error(a, t) != HP_OK) {
-            atomicMin(&s_first, (unsigned long long)t);
-            break;  // t only grows
-        }
+    int code = HP_OK;
+#pragma unroll 4
+    for (uint64_t t = threadIdx.x; t < a.tokens; t += kThreads) code = min(code, token_error(a, t, a.slot_map[t]));
+    if (code != HP_OK) atomicMin(&s_code, code);
     __syncthreads();
-    if (threadIdx.x == 0) *a.d_status = s_first == ~0ull ? HP_OK : token_error(a, s_first);
+    if (threadIdx.x == 0) *a.d_status = s_code;
+}
+
+// Whether token t is to be processed; a large batch's warps report its error themselves.
+__device__ __forceinline__ bool admit(const AppendArgs& a, uint64_t t, int64_t slot, unsigned lane, bool report_here)
+{
+    const int code = token_error(a, t, slot);
+    if (code != HP_OK && report_here && lane == 0) atomicMin(a.d_status, code);
+    return slot >= 0 && code == HP_OK;
 }
 
 // The rotation of the 8 dimensions d0 .. d0 + 7 of token t: y_j = c_j x_j + s_j partner_j.
@@ -110,13 +119,36 @@ struct Turn {
     {
         partner = 0;
         on = d0 < r.rot;
-        if (!on) return;
+        if (!on) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) c[j] = 1.0f, s[j] = 0.0f;
+            return;
+        }
         const uint32_t half = r.rot / 2;
         uint64_t pos[4];
 #pragma unroll
         for (uint32_t x = 0; x < 4; ++x) pos[x] = x < r.axes ? position(r, tokens, x, t) : 0;
         const bool high = !r.inter && d0 >= half;
         if (!r.inter) partner = high ? -(int)(half / 8) : (int)(half / 8);
+        if (r.axes == 1) {  // 16-byte pieces of the token's one row
+            const float* row = r.cos_sin + pos[0] * r.rot;
+            if (r.inter) {
+                const float4 cv = __ldg(reinterpret_cast<const float4*>(row + d0 / 2));
+                const float4 sv = __ldg(reinterpret_cast<const float4*>(row + half + d0 / 2));
+                const float ce[4] = {cv.x, cv.y, cv.z, cv.w}, se[4] = {sv.x, sv.y, sv.z, sv.w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) c[j] = ce[j / 2], s[j] = (j & 1) == 0 ? -se[j / 2] : se[j / 2];
+            } else {
+                const float4* cr = reinterpret_cast<const float4*>(row + d0 - (high ? half : 0));
+                const float4* sr = reinterpret_cast<const float4*>(row + half + d0 - (high ? half : 0));
+                const float4 c0 = __ldg(cr), c1 = __ldg(cr + 1), s0 = __ldg(sr), s1 = __ldg(sr + 1);
+                const float ce[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+                const float se[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) c[j] = ce[j], s[j] = high ? se[j] : -se[j];
+            }
+            return;
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const uint32_t i = r.inter ? (d0 + j) / 2 : d0 + j - (high ? half : 0);
@@ -130,22 +162,46 @@ struct Turn {
             s[j] = (r.inter ? (j & 1) == 0 : !high) ? -sn : sn;
         }
     }
-    // every lane of the warp calls it; lane: this lane's number
-    __device__ __forceinline__ void apply(float (&x)[8], bool inter, unsigned lane) const
-    {
-        float y[8];
-        if (inter) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = x[j ^ 1];
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = __shfl_sync(0xffffffffu, x[j], (int)lane + partner);
-        }
-        if (on)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = x[j] * c[j] + y[j] * s[j];
-    }
 };
+
+// 8 elements of the lane `from`, in this lane's place (whole warps).
+template <typename T> __device__ __forceinline__ Vec8<T> shuffled(const Vec8<T>& v, int from)
+{
+    Vec8<T> r;
+#pragma unroll
+    for (int i = 0; i < Vec8<T>::N; ++i) {
+        r.u[i].x = __shfl_sync(0xffffffffu, v.u[i].x, from);
+        r.u[i].y = __shfl_sync(0xffffffffu, v.u[i].y, from);
+        r.u[i].z = __shfl_sync(0xffffffffu, v.u[i].z, from);
+        r.u[i].w = __shfl_sync(0xffffffffu, v.u[i].w, from);
+    }
+    return r;
+}
+
+// The partners y of the elements x of v (whole warps; `lane`: this lane's number).
+template <typename T>
+__device__ __forceinline__ void partners(const Turn& turn, bool inter, const Vec8<T>& v, unsigned lane,
+                                         const float (&x)[8], float (&y)[8])
+{
+    if (inter) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = x[j ^ 1];
+    } else {
+        shuffled(v, (int)lane + turn.partner).unpack(y);
+    }
+}
+
+// x <- x c + y s; dimensions that do not turn keep x c, infinities included (all: every
+// dimension turns)
+__device__ __forceinline__ void turned(bool all, bool on, float (&x)[8], const float (&y)[8], const float (&c)[8],
+                                       const float (&s)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float z = fmaf(y[j], s[j], x[j] * c[j]);
+        x[j] = all || on ? z : x[j] * c[j];
+    }
+}
 
 template <int L> __device__ __forceinline__ float group_sum(float v)
 {
@@ -154,73 +210,121 @@ template <int L> __device__ __forceinline__ float group_sum(float v)
     return v;
 }
 
-// Warp w of the grid takes token w / parts and, of its heads (queries, keys, values in that
-// order), every parts-th group of 32 / L.
-template <typename T, int L>
-__global__ void __launch_bounds__(kThreads) qk_append_kernel(const AppendArgs a, uint32_t parts)
+// Heads a lane group loads before it works on them: 2 KiB in flight per warp.
+template <typename T> constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;
+
+template <typename T> struct Batch {
+    Vec8<T> v[kBatch<T>];
+    // heads h, h + step, ... of `count`, element d0 of the lane's at src + head * dim
+    __device__ __forceinline__ void load(const T* src, uint32_t h, uint32_t step, uint32_t count, uint32_t dim, bool live)
+    {
+#pragma unroll
+        for (int u = 0; u < kBatch<T>; ++u)
+            if (live && h + u * step < count) v[u].load_rw(src + (uint64_t)(h + u * step) * dim);
+    }
+};
+
+// The factors of a head's elements with the gains folded in: c_j w_j, and s_j w_partner.
+template <typename T>
+__device__ __forceinline__ void fold(const Turn& turn, bool inter, const T* weight, uint32_t d0, bool live, unsigned lane,
+                                     float (&c)[8], float (&s)[8])
 {
-    if (a.d_status && blockIdx.x == gridDim.x - 1) {
-        report_first(a);
+    float g[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[j] = 1.0f;
+    if (live && weight) {
+        Vec8<T> w;
+        w.load(weight + d0);
+        w.unpack(g);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float p = inter ? g[j ^ 1] : __shfl_sync(0xffffffffu, g[j], (int)lane + turn.partner);
+        c[j] = turn.c[j] * g[j];
+        s[j] = turn.s[j] * p;
+    }
+}
+
+// Heads h0 + sub, + step, ... of `count` (h0 the same in the warp; the first batch is loaded):
+// y_j = r (c_j x_j + s_j x_partner) with r the head's inverse root mean square where NORM.
+template <typename T, int L, bool NORM>
+__device__ __forceinline__ void heads_out(const AppendArgs& a, const Turn& turn, Batch<T>& b, const T* src, T* dst,
+                                          uint32_t h0, uint32_t sub, uint32_t step, uint32_t count, bool live,
+                                          unsigned lane, const float (&c)[8], const float (&s)[8])
+{
+    const bool inter = a.rope.inter, all = a.rope.rot == a.dim;
+    const float inv_dim = 1.0f / (float)a.dim;
+    while (h0 < count) {
+#pragma unroll
+        for (int u = 0; u < kBatch<T>; ++u, h0 += step) {
+            if (h0 >= count) break;  // (the same in every lane)
+            float x[8], y[8];
+            b.v[u].unpack(x);
+            partners(turn, inter, b.v[u], lane, x, y);
+            float r = 1.0f;
+            if (NORM) {
+                float ss = 0.0f;
+                if (live) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+                }
+                r = rsqrtf(group_sum<L>(ss) * inv_dim + a.eps);
+            }
+            turned(all, turn.on, x, y, c, s);
+            if (NORM)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] *= r;
+            b.v[u].pack(x);
+            if (live && h0 + sub < count) b.v[u].store(dst + (uint64_t)(h0 + sub) * a.dim);
+        }
+        b.load(src, h0 + sub, step, count, a.dim, live);
+    }
+}
+
+// Warp w of the grid takes token w / parts and, of its query, key and value heads each, every
+// parts-th group of 32 / L.  A token's first queries are loaded before its slot and positions
+// are looked at, so their latencies overlap.
+template <typename T, int L>
+__global__ void __launch_bounds__(kThreads, 3) qk_append_kernel(const AppendArgs a, uint32_t parts, bool report_here)
+{
+    if (!report_here && a.d_status && blockIdx.x == gridDim.x - 1) {
+        report_all(a);
         return;
     }
     const unsigned lane = threadIdx.x & 31, sub = lane / L, l = lane % L;
-    const uint64_t warps = (uint64_t)(gridDim.x - (a.d_status != nullptr)) * kWarpsRope;
-    const uint32_t heads = a.hq + 2 * a.hkv, d0 = l * 8;
-    const bool live = d0 < a.dim;
-    float qw[8], kw[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) qw[j] = kw[j] = 1.0f;
-    if (live && a.q_weight) {
-        Vec8<T> v;
-        v.load(static_cast<const T*>(a.q_weight) + d0);
-        v.unpack(qw);
-    }
-    if (live && a.k_weight) {
-        Vec8<T> v;
-        v.load(static_cast<const T*>(a.k_weight) + d0);
-        v.unpack(kw);
-    }
+    const uint64_t warps = (uint64_t)(gridDim.x - (!report_here && a.d_status != nullptr)) * kWarpsRope;
+    const uint32_t d0 = l * 8, step = parts * (32 / L);
+    const bool live = d0 < a.dim, inter = a.rope.inter;
     for (uint64_t w = (uint64_t)blockIdx.x * kWarpsRope + (threadIdx.x >> 5); w < a.tokens * parts;
          w += warps) {
         const uint64_t t = w / parts;
+        const uint32_t h0 = (uint32_t)(w % parts) * (32 / L);
+        const T* src = static_cast<const T*>(a.q) + t * a.q_stride + d0;
+        Batch<T> b;
+        b.load(src, h0 + sub, step, a.hq, a.dim, live);
         const int64_t slot = a.slot_map[t];
-        if (slot < 0 || token_error(a, t) != HP_OK) continue;
+        if (!admit(a, t, slot, lane, report_here)) continue;
         Turn turn;
         turn.load(a.rope, a.tokens, t, live ? d0 : a.rope.rot);
-        for (uint32_t h0 = (uint32_t)(w % parts) * (32 / L); h0 < heads; h0 += parts * (32 / L)) {
-            const uint32_t h = h0 + sub;
-            const bool on = live && h < heads;
-            const bool is_q = h < a.hq, is_k = !is_q && h < a.hq + a.hkv;
-            const uint32_t g = is_q ? h : (is_k ? h - a.hq : h - a.hq - a.hkv);  // head of its kind
-            const T* src = static_cast<const T*>(is_q ? a.q : (is_k ? a.k : a.v)) +
-                           t * (is_q ? a.q_stride : (is_k ? a.k_stride : a.v_stride)) +
-                           (uint64_t)g * a.dim + d0;
-            Vec8<T> v;
-            float x[8];
+        float c[8], s[8];
+        fold(turn, inter, static_cast<const T*>(a.q_weight), d0, live, lane, c, s);
+        T* dst = static_cast<T*>(a.q_out) + t * a.qo_stride + d0;
+        if (a.q_weight) heads_out<T, L, true>(a, turn, b, src, dst, h0, sub, step, a.hq, live, lane, c, s);
+        else heads_out<T, L, false>(a, turn, b, src, dst, h0, sub, step, a.hq, live, lane, c, s);
+        const uint64_t row = (uint64_t)slot * a.hkv * a.dim + d0;
+        src = static_cast<const T*>(a.k) + t * a.k_stride + d0;
+        b.load(src, h0 + sub, step, a.hkv, a.dim, live);
+        fold(turn, inter, static_cast<const T*>(a.k_weight), d0, live, lane, c, s);
+        dst = static_cast<T*>(a.k_pool) + row;
+        if (a.k_weight) heads_out<T, L, true>(a, turn, b, src, dst, h0, sub, step, a.hkv, live, lane, c, s);
+        else heads_out<T, L, false>(a, turn, b, src, dst, h0, sub, step, a.hkv, live, lane, c, s);
+        src = static_cast<const T*>(a.v) + t * a.v_stride + d0;
+        dst = static_cast<T*>(a.v_pool) + row;
+        for (uint32_t h = h0 + sub; h < a.hkv; h += kBatch<T> * step) {  // values keep their bits
+            b.load(src, h, step, a.hkv, a.dim, live);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-            if (on) {
-                v.load_rw(src);
-                v.unpack(x);
-            }
-            const bool norm = is_q ? a.q_weight != nullptr : a.k_weight != nullptr;
-            float ss = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-            ss = group_sum<L>(ss);
-            const float r = norm ? rsqrtf(ss / (float)a.dim + a.eps) : 1.0f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = x[j] * r * (is_q ? qw[j] : kw[j]);
-            turn.apply(x, a.rope.inter, lane);
-            if (!on) continue;
-            if (is_q) {
-                v.pack(x);
-                v.store(static_cast<T*>(a.q_out) + t * a.qo_stride + (uint64_t)g * a.dim + d0);
-            } else {
-                if (is_k) v.pack(x);  // a value keeps its bits
-                v.store(static_cast<T*>(is_k ? a.k_pool : a.v_pool) +
-                        ((uint64_t)slot * a.hkv + g) * a.dim + d0);
-            }
+            for (int u = 0; u < kBatch<T>; ++u)
+                if (live && h + u * step < a.hkv) b.v[u].store(dst + (uint64_t)(h + u * step) * a.dim);
         }
     }
 }
@@ -229,90 +333,100 @@ constexpr int kLatVec = 4;  // 32 lanes x 8 elements x 4: latent vectors up to 1
 
 // As above; part 0 of a token also takes its latent row (the whole warp) and shared key.
 template <typename T, int L>
-__global__ void __launch_bounds__(kThreads) latent_append_kernel(const AppendArgs a, uint32_t parts)
+__global__ void __launch_bounds__(kThreads, 3) latent_append_kernel(const AppendArgs a, uint32_t parts, bool report_here)
 {
-    if (a.d_status && blockIdx.x == gridDim.x - 1) {
-        report_first(a);
+    if (!report_here && a.d_status && blockIdx.x == gridDim.x - 1) {
+        report_all(a);
         return;
     }
+    constexpr int U = kBatch<T>;
     const unsigned lane = threadIdx.x & 31, sub = lane / L, l = lane % L;
-    const uint64_t warps = (uint64_t)(gridDim.x - (a.d_status != nullptr)) * kWarpsRope;
-    const uint32_t d0 = l * 8, R = a.latent_dim, D = a.rope.rot;
+    const uint64_t warps = (uint64_t)(gridDim.x - (!report_here && a.d_status != nullptr)) * kWarpsRope;
+    const uint32_t d0 = l * 8, R = a.latent_dim, D = a.rope.rot, step = parts * (32 / L);
     const bool live = d0 < D;
     for (uint64_t w = (uint64_t)blockIdx.x * kWarpsRope + (threadIdx.x >> 5); w < a.tokens * parts;
          w += warps) {
         const uint64_t t = w / parts;
         const uint32_t part = (uint32_t)(w % parts);
+        uint32_t h = part * (32 / L) + sub;
+        Vec8<T> v[U], c[kLatVec], k;
+        auto load = [&](int u, uint32_t hh) {
+            if (live && hh < a.hq)
+                v[u].load_rw(static_cast<const T*>(a.q) + t * a.q_stride + (uint64_t)hh * a.q_head + d0);
+        };
+#pragma unroll
+        for (int u = 0; u < U; ++u) load(u, h + u * step);
+        if (part == 0) {
+            const T* src = static_cast<const T*>(a.latent) + t * a.latent_stride;
+#pragma unroll
+            for (int i = 0; i < kLatVec; ++i)
+                if ((i * 32 + lane) * 8 < R) c[i].load(src + (i * 32 + lane) * 8);
+            if (live && sub == 0) k.load(static_cast<const T*>(a.k) + t * a.k_stride + d0);
+        }
         const int64_t slot = a.slot_map[t];
-        if (slot < 0 || token_error(a, t) != HP_OK) continue;
+        if (!admit(a, t, slot, lane, report_here)) continue;
         Turn turn;
         turn.load(a.rope, a.tokens, t, live ? d0 : D);
         if (part == 0) {
             T* row = static_cast<T*>(a.k_pool) + (uint64_t)slot * (R + D);
-            const T* src = static_cast<const T*>(a.latent) + t * a.latent_stride;
-            Vec8<T> v[kLatVec], k;
-            float ss = 0.0f;
+            if (a.latent_weight) {
+                float ss = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kLatVec; ++i) {
-                const uint32_t d = (i * 32 + lane) * 8;
-                if (d < R) v[i].load(src + d);
-            }
-            float kx[8];
+                for (int i = 0; i < kLatVec; ++i)
+                    if ((i * 32 + lane) * 8 < R) {
+                        float x[8];
+                        c[i].unpack(x);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) kx[j] = 0.0f;
-            if (live && sub == 0) {
-                k.load(static_cast<const T*>(a.k) + t * a.k_stride + d0);
-                k.unpack(kx);
-            }
+                        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+                    }
+                const float r = rsqrtf(group_sum<32>(ss) / (float)R + a.eps);
 #pragma unroll
-            for (int i = 0; i < kLatVec; ++i)
-                if ((i * 32 + lane) * 8 < R) {
-                    float x[8];
-                    v[i].unpack(x);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-                }
-            ss = group_sum<32>(ss);
-            const float r = a.latent_weight ? rsqrtf(ss / (float)R + a.eps) : 1.0f;
-#pragma unroll
-            for (int i = 0; i < kLatVec; ++i) {
-                const uint32_t d = (i * 32 + lane) * 8;
-                if (d < R) {
-                    if (a.latent_weight) {
+                for (int i = 0; i < kLatVec; ++i)
+                    if ((i * 32 + lane) * 8 < R) {
                         float x[8], g[8];
                         Vec8<T> wv;
-                        wv.load(static_cast<const T*>(a.latent_weight) + d);
-                        v[i].unpack(x);
+                        wv.load(static_cast<const T*>(a.latent_weight) + (i * 32 + lane) * 8);
+                        c[i].unpack(x);
                         wv.unpack(g);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) x[j] = x[j] * r * g[j];
-                        v[i].pack(x);
+                        c[i].pack(x);
                     }
-                    v[i].store(row + d);
-                }
             }
-            turn.apply(kx, a.rope.inter, lane);
+#pragma unroll
+            for (int i = 0; i < kLatVec; ++i)
+                if ((i * 32 + lane) * 8 < R) c[i].store(row + (i * 32 + lane) * 8);
+            float kx[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) kx[j] = 0.0f;
+            if (live && sub == 0) k.unpack(kx);
+            float ky[8];
+            partners(turn, a.rope.inter, k, lane, kx, ky);
+            turned(true, true, kx, ky, turn.c, turn.s);
             if (live && sub == 0) {
                 k.pack(kx);
                 k.store(row + R + d0);
             }
         }
-        for (uint32_t h0 = part * (32 / L); h0 < a.hq; h0 += parts * (32 / L)) {
-            const uint32_t h = h0 + sub;
-            const bool on = live && h < a.hq;
-            Vec8<T> v;
-            float x[8];
+        while (h - sub < a.hq) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-            if (on) {
-                v.load_rw(static_cast<const T*>(a.q) + t * a.q_stride + (uint64_t)h * a.q_head + d0);
-                v.unpack(x);
+            for (int u = 0; u < U; ++u, h += step) {
+                if (h - sub >= a.hq) break;  // (the same in every lane)
+                const bool on = live && h < a.hq;
+                float x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = 0.0f;
+                if (on) v[u].unpack(x);
+                float y[8];
+                partners(turn, a.rope.inter, v[u], lane, x, y);
+                turned(true, true, x, y, turn.c, turn.s);
+                if (on) {
+                    v[u].pack(x);
+                    v[u].store(static_cast<T*>(a.q_out) + t * a.qo_stride + (uint64_t)h * a.qo_head + d0);
+                }
             }
-            turn.apply(x, a.rope.inter, lane);
-            if (on) {
-                v.pack(x);
-                v.store(static_cast<T*>(a.q_out) + t * a.qo_stride + (uint64_t)h * a.qo_head + d0);
-            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) load(u, h + u * step);
         }
     }
 }
@@ -330,12 +444,14 @@ int launch_l(const AppendArgs& a, cudaStream_t st)
     const uint64_t want = ((uint64_t)sms * 16 + a.tokens - 1) / a.tokens;
     const uint64_t parts = want < 1 ? 1 : (want < groups ? want : (groups ? groups : 1));
     const uint64_t warps = a.tokens * parts, ctas = (warps + kWarpsRope - 1) / kWarpsRope;
-    const uint64_t cap = (uint64_t)sms * 8;
-    const unsigned grid = (unsigned)(ctas < cap ? ctas : cap) + (a.d_status != nullptr);
+    const uint64_t cap = (uint64_t)sms * 64;
+    const bool report_here = a.d_status && a.tokens > kReportTokens;
+    if (report_here && cudaMemsetAsync(a.d_status, 0, sizeof(int), st) != cudaSuccess) return HP_ERR_CUDA;
+    const unsigned grid = (unsigned)(ctas < cap ? ctas : cap) + (a.d_status && !report_here);
     if (LATENT)
-        latent_append_kernel<T, L><<<grid, kThreads, 0, st>>>(a, (uint32_t)parts);
+        latent_append_kernel<T, L><<<grid, kThreads, 0, st>>>(a, (uint32_t)parts, report_here);
     else
-        qk_append_kernel<T, L><<<grid, kThreads, 0, st>>>(a, (uint32_t)parts);
+        qk_append_kernel<T, L><<<grid, kThreads, 0, st>>>(a, (uint32_t)parts, report_here);
     return cudaGetLastError() == cudaSuccess ? HP_OK : HP_ERR_CUDA;
 }
 

@@ -11,6 +11,7 @@ namespace hp {
 struct StepArgs {
     hp_step_desc d;
     WsView ws;  // rows_off: prefix of the new tokens; units_off: prefix of the pages
+    uint32_t div_ok, div_m, div_l;  // div_invariant constants of page_size, where it fits
     int* d_status;
 };
 int launch_step_tables(const StepArgs& a, void* stream);
