@@ -234,9 +234,10 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const LatentArgs a)
     const uint64_t last = (uend - 1) / Lw;
     auto rec = [&](uint64_t w) { return (2 * w + (w == v && ustart > beg ? 1 : 0)) * a.group_rows + gr; };
     // maximum and sum over the records, a lane per record, then pairwise
-    float M = -INFINITY, L = 0.0f;
+    float M = -INFINITY, L = 0.0f, mine = -INFINITY;  // mine: the maximum of record v + lane
     for (uint64_t w = v + lane; w <= last; w += 32) {
         const float2 x = a.part_ml[rec(w)];
+        if (w == v + lane) mine = x.x;
         const float mn = fmaxf(M, x.x);
         if (mn != -INFINITY) {
             L = L * exp2_approx(M - mn) + x.y * exp2_approx(x.x - mn);
@@ -257,20 +258,24 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const LatentArgs a)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[j] = make_float4(0, 0, 0, 0);
     if (M != -INFINITY)
-#pragma unroll 2
-        for (uint64_t w = v; w <= last; ++w) {
-            const uint64_t at = rec(w);
-            const float f = exp2_approx(a.part_ml[at].x - M);
-            const float4* p = reinterpret_cast<const float4*>(a.part_acc + at * a.R);
+        for (uint64_t w0 = v; w0 <= last; w0 += 32) {  // 32 records, their factors one per lane
+            if (w0 != v) mine = w0 + lane <= last ? a.part_ml[rec(w0 + lane)].x : -INFINITY;
+            const float fl = exp2_approx(mine - M);
+            const uint32_t n32 = (uint32_t)umin(32, last + 1 - w0);
+#pragma unroll 4
+            for (uint32_t i = 0; i < n32; ++i) {
+                const float f = __shfl_sync(0xffffffffu, fl, (int)i);
+                const float4* p = reinterpret_cast<const float4*>(a.part_acc + rec(w0 + i) * a.R);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (lane + 32 * j < quads) {
-                    const float4 x = p[lane + 32 * j];
-                    acc[j].x = fmaf(f, x.x, acc[j].x);
-                    acc[j].y = fmaf(f, x.y, acc[j].y);
-                    acc[j].z = fmaf(f, x.z, acc[j].z);
-                    acc[j].w = fmaf(f, x.w, acc[j].w);
-                }
+                for (int j = 0; j < 4; ++j)
+                    if (lane + 32 * j < quads) {
+                        const float4 x = p[lane + 32 * j];
+                        acc[j].x = fmaf(f, x.x, acc[j].x);
+                        acc[j].y = fmaf(f, x.y, acc[j].y);
+                        acc[j].z = fmaf(f, x.z, acc[j].z);
+                        acc[j].w = fmaf(f, x.w, acc[j].w);
+                    }
+            }
         }
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
     uint2* o = reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (q0 * a.H + r) * a.R);

@@ -5,17 +5,20 @@
 // tokens (hp_latent.cuh has the split).  Per step, with C the step's 64 cache rows of 576:
 //   S [64 rows x 64 tokens]     = Q . C^T            36 products of 16 dims, M = N = 64
 //   O^T [512 dims x 64 rows]   += C[:, :512]^T . P^T  4 tiles of 128 dims, 4 products each
-// so the step's rows are loaded once (TMA, 128-byte swizzled, nine 64-dim chunks of 8 KiB) and
+// so the step's rows are loaded once (TMA, 128-byte swizzled, 64 dims to a chunk of 8 KiB) and
 // serve as the B operand of S (K-major) and the A operand of O^T (M-major).  O^T rather than O:
 // 64 rows of 512 fp32 sums are half of TMEM either way, but M = 128 products run at the full
-// rate where M = 64 runs at half of it.  O^T stays in TMEM over the whole range: a row's
+// rate where M = 64 runs at half of it (34 cycles for M = N = 64, 50 for M = 128, N = 64, which
+// its shared-memory reads set: 2,024 a step).  O^T stays in TMEM over the whole range: a row's
 // reference maximum moves (and its column of O^T is rescaled) only when a score exceeds it by
 // more than 2^kTau.  P (weights rounded to the element type) overwrites the step's rope chunk,
 // which S has read.
 //
-// Shared memory: Q 72 KiB, two stages of C of 72 KiB -- 216 of 227 KiB; TMEM: O^T 256 columns,
-// S 2 x 64.  Roles: warp 0 loads C, warp 6 the queries, warp 1 issues the products (S of a step
-// ahead of O^T of the step before), warps 2-5 do the softmax and the epilogue.
+// Shared memory: Q 72 KiB; eight slots of two latent chunks (128 dims) and three of a rope
+// chunk, so two steps and more are held or in flight; a slot goes back to the loader as soon as
+// its tile of O^T is computed.  TMEM: O^T 256 columns, S 2 x 64.  Roles: warp 0 loads C, warp 7
+// the queries, warp 1 issues S, warp 6 O^T (apart, so that neither waits for the other's
+// operands), warps 2-5 do the softmax and the epilogue.
 //
 // Above 64 heads a worker is two neighbouring CTAs whose tiles read the same tokens at the same
 // time, so the second read of a row finds it in L2.
@@ -43,15 +46,15 @@ using namespace tc;
 constexpr int kW = 576, kR = 512;
 constexpr uint32_t kRows = 64;                 // rows of a tile
 constexpr uint32_t kTok = kLatentStep;         // tokens of a step
-constexpr uint32_t kChunks = kW / 64, kVChunks = kR / 64;
+constexpr uint32_t kChunks = kW / 64;
 constexpr uint32_t kChunk = 64 * 128;          // 64 rows x 64 dims
-constexpr uint32_t kStage = kChunks * kChunk;
-constexpr uint32_t kStages = 2;
-constexpr uint32_t kOffC = kChunks * kChunk;   // Q first, then the stages
-constexpr uint32_t kSmem = kOffC + kStages * kStage + 1024;
+constexpr uint32_t kPairs = 8, kRopes = 3;     // slots of two latent chunks, of a rope chunk
+constexpr uint32_t kOffC = kChunks * kChunk;   // Q first, then the slots
+constexpr uint32_t kOffR = kOffC + kPairs * 2 * kChunk;
+constexpr uint32_t kSmem = kOffR + kRopes * kChunk + 1024;
 constexpr uint32_t kOCol = 0, kSCol = 256;     // TMEM columns
 constexpr uint32_t kTmemCols = 512;
-constexpr int kThreads = 7 * 32;
+constexpr int kThreads = 8 * 32;
 constexpr int kSoftmax = 128;
 constexpr float kTau = 8.0f;
 
@@ -103,18 +106,14 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-template <typename T> __device__ __forceinline__ T round1(float a);
-template <> __device__ __forceinline__ __nv_bfloat16 round1<__nv_bfloat16>(float a) { return __float2bfloat16_rn(a); }
-template <> __device__ __forceinline__ __half round1<__half>(float a) { return __float2half_rn(a); }
-
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_tc_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap tmc,
-                     const __grid_constant__ CUtensorMap tmq)
+                     const __grid_constant__ CUtensorMap tmr, const __grid_constant__ CUtensorMap tmq)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ __align__(8) unsigned long long c_full[kStages], c_free[kStages], s_full[2], s_free[2],
-        p_full[2], o_done[2], o_free, q_full, q_free;
+    __shared__ __align__(8) unsigned long long c_full[kPairs], c_free[kPairs], r_full[kRopes], r_free[kRopes],
+        s_full[2], s_free[2], p_full[2], o_done[2], o_free, q_full, q_free, s_end, o_end;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag, fail_s[2];
     __shared__ float corr_s[kRows], inv_s[kRows];
@@ -124,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     T* out = static_cast<T*>(a.out);
     // queries of a sequence without tokens: zeros
-    for (uint64_t s = (uint64_t)blockIdx.x * 7 + warp; s < a.num_seqs; s += (uint64_t)gridDim.x * 7)
+    for (uint64_t s = (uint64_t)blockIdx.x * 8 + warp; s < a.num_seqs; s += (uint64_t)gridDim.x * 8)
         if (a.units_off[s] == a.units_off[s + 1]) {
             const uint64_t q0 = a.q_ptr ? index_at(a.q_ptr, a.idx64, s) : s;
             const uint64_t q1 = a.q_ptr ? index_at(a.q_ptr, a.idx64, s + 1) : s + 1;
@@ -140,9 +139,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sm0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char* smem = smem_raw + (sm0 - smem_u32(smem_raw));
     if (threadIdx.x == 0) {
-        for (uint32_t i = 0; i < kStages; ++i) {
+        for (uint32_t i = 0; i < kPairs; ++i) {
             mbar_init(smem_u32(&c_full[i]), 1);
             mbar_init(smem_u32(&c_free[i]), 1);
+        }
+        for (uint32_t i = 0; i < kRopes; ++i) {
+            mbar_init(smem_u32(&r_full[i]), 1);
+            mbar_init(smem_u32(&r_free[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&s_full[i]), 1);
@@ -153,6 +156,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&o_free), kSoftmax);
         mbar_init(smem_u32(&q_full), 1);
         mbar_init(smem_u32(&q_free), 1);
+        mbar_init(smem_u32(&s_end), 1);
+        mbar_init(smem_u32(&o_end), 1);
         abort_flag = 0;
         fail_s[0] = fail_s[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -164,61 +169,75 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = tmem_base;
     Walk walk{a, beg, end, (uint32_t)(blockIdx.x % tiles)};
     Segment g;
-    auto failed = [&](bool ok) {
-        if (!ok) {
-            abort_flag = 1;
-            report(a.d_status, HP_ERR_TIMEOUT);
-        }
-        return !ok || *(volatile int*)&abort_flag;
+    // true unless the wait ran out or another role stopped; warp_wait for whole warps
+    auto wait_for = [&](unsigned long long* bar, uint32_t parity) {
+        if (mbar_wait_or(smem_u32(bar), parity, &abort_flag)) return true;
+        abort_flag = 1;
+        report(a.d_status, HP_ERR_TIMEOUT);
+        return false;
+    };
+    auto warp_wait = [&](unsigned long long* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_for(bar, parity)) != 0;
     };
 
     if (warp == 0) {
         // ----------------------------------------------------------- cache rows of each step
         const uint32_t P = (uint32_t)a.page_size, box = P < kTok ? P : kTok, ppc = kTok / box;
-        uint64_t j = 0;
-        bool stop = false;
-        while (!stop && walk.next(g)) {
+        const uint32_t spp = P / box, wide = P >= kTok ? 2 : 1;  // steps per page; chunks per box
+        uint64_t j = 0, armed = 0, rarmed = 0;  // steps, slots of each ring given to loads
+        bool ok = true;
+        while (ok && walk.next(g)) {
             const uint64_t tab0 = index_at(a.seq_ptr, a.idx64, g.s);
-            for (uint64_t k = g.k0; k < g.k1; ++k, ++j) {
-                const uint32_t st = (uint32_t)(j % kStages);
-                // lane i < ppc: the pool row of the step's i-th page, if a slot of it is live
-                const uint64_t t = k * kTok + (uint64_t)lane * box;
-                const bool live = lane < ppc && t < g.len;
-                const uint32_t row =
-                    live ? (uint32_t)(index_at(a.table, a.idx64, tab0 + t / P) * P + t % P) : 0u;
-                const uint32_t pages = __popc(__ballot_sync(0xffffffffu, live));
-                int ok = 1;
-                if (lane == 0 && j >= kStages)
-                    ok = mbar_wait(smem_u32(&c_free[st]), (uint32_t)((j / kStages - 1) & 1));
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (__any_sync(0xffffffffu, failed(ok != 0))) {
-                    stop = true;
-                    break;
+            // lane i < ppc: the pool row of step k's i-th page, if a slot of it is live
+            auto pool_row = [&](uint64_t k) {
+                if (lane >= ppc || k >= g.k1 || k * kTok + (uint64_t)lane * box >= g.len) return -1;
+                if (spp == 1) return (int)(index_at(a.table, a.idx64, tab0 + k * ppc + lane) * P);
+                return (int)(index_at(a.table, a.idx64, tab0 + k / spp) * P + k % spp * kTok);
+            };
+            int row = pool_row(g.k0);
+            for (uint64_t k = g.k0; ok && k < g.k1; ++k, ++j) {
+                const int next_row = pool_row(k + 1);  // looked up while this step's slots free up
+                const uint32_t pages = __popc(__ballot_sync(0xffffffffu, row >= 0));
+                // box b of a slot: chunks of the same page next to each other
+                const uint32_t nb = pages * 2 / wide, pg = lane % pages, ch = lane / pages;
+                const int r = __shfl_sync(0xffffffffu, row, (int)pg);
+                for (uint32_t p = 0; p < 4; ++p) {
+                    const uint64_t c = 4 * j + p;
+                    const uint32_t sl = (uint32_t)(c % kPairs);
+                    if (c >= kPairs) ok = warp_wait(&c_free[sl], (uint32_t)((c / kPairs - 1) & 1));
+                    if (!ok) break;
+                    const uint32_t bar = smem_u32(&c_full[sl]), base = sm0 + kOffC + sl * 2 * kChunk;
+                    if (lane == 0) mbar_expect_tx(bar, pages * box * 128 * 2);
+                    armed = c + 1;
+                    __syncwarp();
+                    if (lane < nb && !(a.test_stall && c == 0))
+                        tma_3d(base + ch * kChunk + pg * box * 128, &tmc, 0, r, (int)(2 * p + ch), bar);
                 }
-                const uint32_t bar = smem_u32(&c_full[st]), base = sm0 + kOffC + st * kStage;
-                if (lane == 0) mbar_expect_tx(bar, pages * box * 128 * kChunks);
+                if (!ok) break;
+                const uint32_t rs = (uint32_t)(j % kRopes);
+                if (j >= kRopes) ok = warp_wait(&r_free[rs], (uint32_t)((j / kRopes - 1) & 1));
+                if (!ok) break;
+                if (lane == 0) mbar_expect_tx(smem_u32(&r_full[rs]), pages * box * 128);
+                rarmed = j + 1;
                 __syncwarp();
-                const uint32_t boxes = pages * kChunks;
-                for (uint32_t b0 = 0; b0 < boxes; b0 += 32) {  // box b: chunk b / pages, page b % pages
-                    const uint32_t b = b0 + lane, ch = b / pages, pg = b - ch * pages;
-                    const uint32_t r = __shfl_sync(0xffffffffu, row, pg);
-                    if (b < boxes && !(a.test_stall && j == 0))
-                        tma_2d(base + ch * kChunk + pg * box * 128, &tmc, (int)(ch * 64), (int)r, bar);
-                }
+                if (lane < pages)
+                    tma_3d(sm0 + kOffR + rs * kChunk + pg * box * 128, &tmr, 0, r, (int)kChunks - 1, smem_u32(&r_full[rs]));
+                row = next_row;
             }
         }
-        if (lane == 0)  // the last loads land before the shared memory goes
-            for (uint64_t x = j > kStages ? j - kStages : 0; x < j; ++x)
-                mbar_wait(smem_u32(&c_full[x % kStages]), (uint32_t)((x / kStages) & 1));
+        // the last loads land before the shared memory goes
+        for (uint64_t c = armed > kPairs ? armed - kPairs : 0; c < armed; ++c)
+            mbar_wait(smem_u32(&c_full[c % kPairs]), (uint32_t)((c / kPairs) & 1));
+        for (uint64_t x = rarmed > kRopes ? rarmed - kRopes : 0; x < rarmed; ++x)
+            mbar_wait(smem_u32(&r_full[x % kRopes]), (uint32_t)((x / kRopes) & 1));
         __syncwarp();
-    } else if (warp == 6) {
+    } else if (warp == 7) {
         // ------------------------------------------------------------- queries of each tile
         if (lane == 0) {
             uint64_t seg = 0;
             while (walk.next(g)) {
                 if (g.k0 >= g.k1) continue;
-                const bool ok = seg == 0 || mbar_wait(smem_u32(&q_free), (uint32_t)((seg - 1) & 1));
-                if (failed(ok)) break;
+                if (seg && !wait_for(&q_free, (uint32_t)((seg - 1) & 1))) break;
                 mbar_expect_tx(smem_u32(&q_full), kChunks * kChunk);
                 for (uint32_t c = 0; c < kChunks; ++c)
                     tma_2d(sm0 + c * kChunk, &tmq, (int)(c * 64), (int)(g.q0 * a.H + g.r0), smem_u32(&q_full));
@@ -228,67 +247,98 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ---------------------------------------------------------------- products, one thread
-        if (lane == 0) {
-            const uint32_t id_s = f16_idesc(a.bf16 != 0, false, false, kRows, kTok);
-            const uint32_t id_o = f16_idesc(a.bf16 != 0, true, false, 128, kRows);
-            const uint64_t qd = sw128_desc(sm0, 16, 1024), cd0 = sw128_desc(sm0 + kOffC, 16, 1024);
-            const uint64_t vd0 = sw128_desc(sm0 + kOffC, kChunk, 1024);
-            uint64_t j = 0, seg = 0, done = 0;  // steps with S issued, segments, steps with O issued
-            bool ok = true;
-            // O^T of the step `done`; fresh: the first of its segment
-            auto issue_o = [&](bool fresh) {
-                const uint64_t x = done;
-                ok = mbar_wait(smem_u32(&p_full[x % 2]), (uint32_t)((x / 2) & 1)) &&
-                     (!fresh || seg == 0 || mbar_wait(smem_u32(&o_free), (uint32_t)((seg - 1) & 1)));
-                if (failed(ok)) {
-                    ok = false;
-                    return;
-                }
-                fence_after();
-                const uint32_t so = (uint32_t)(x % kStages) * kStage;
-                const uint64_t vd = vd0 + (so >> 4), pd = cd0 + ((so + kVChunks * kChunk) >> 4);
+        // -------------------------------------------------------------------- S = Q . C^T
+        const uint32_t id_s = f16_idesc(a.bf16 != 0, false, false, kRows, kTok);
+        const uint64_t qd = sw128_desc(sm0, 16, 1024), cd0 = sw128_desc(sm0 + kOffC, 16, 1024);
+        const uint64_t rd0 = sw128_desc(sm0 + kOffR, 16, 1024);
+        uint64_t j = 0, seg = 0;
+        bool ok = true;
+        while (ok && walk.next(g)) {
+            if (g.k0 >= g.k1) continue;
+            ok = warp_wait(&q_full, (uint32_t)(seg & 1));
+            for (uint64_t k = g.k0; ok && k < g.k1; ++k) {
+                if (j >= 2) ok = warp_wait(&s_free[j % 2], (uint32_t)((j / 2 - 1) & 1));
+                const uint32_t d = tmem + kSCol + (uint32_t)(j % 2) * kTok;
 #pragma unroll
-                for (uint32_t m = 0; m < 4; ++m)
-#pragma unroll
-                    for (uint32_t kk = 0; kk < 4; ++kk)
-                        mma_f16(tmem + kOCol + m * kRows, vd + ((m * 2 * kChunk + kk * 2048) >> 4),
-                                pd + ((kk * 32) >> 4), id_o, !fresh || kk > 0);
-                mma_commit(smem_u32(&c_free[x % kStages]));
-                mma_commit(smem_u32(&o_done[x % 2]));
-                ++done;
-            };
-            while (ok && walk.next(g)) {
-                if (g.k0 >= g.k1) continue;
-                for (uint64_t k = g.k0; ok && k < g.k1; ++k) {
-                    ok = mbar_wait(smem_u32(&c_full[j % kStages]), (uint32_t)((j / kStages) & 1)) &&
-                         (k != g.k0 || mbar_wait(smem_u32(&q_full), (uint32_t)(seg & 1))) &&
-                         (j < 2 || mbar_wait(smem_u32(&s_free[j % 2]), (uint32_t)((j / 2 - 1) & 1)));
-                    if (failed(ok)) {
-                        ok = false;
-                        break;
-                    }
+                for (uint32_t p = 0; p < 4; ++p) {
+                    const uint64_t c = 4 * j + p;
+                    const uint32_t sl = (uint32_t)(c % kPairs);
+                    if (ok) ok = warp_wait(&c_full[sl], (uint32_t)((c / kPairs) & 1));
+                    if (!ok) break;
                     fence_after();
-                    const uint64_t cd = cd0 + (((uint32_t)(j % kStages) * kStage) >> 4);
-                    const uint32_t d = tmem + kSCol + (uint32_t)(j % 2) * kTok;
+                    const uint64_t cd = cd0 + ((sl * 2 * kChunk) >> 4), qp = qd + ((p * 2 * kChunk) >> 4);
+                    if (elect_one()) {
 #pragma unroll
-                    for (uint32_t u = 0; u < kChunks * 4; ++u) {
-                        const uint32_t o = ((u >> 2) * kChunk + (u & 3) * 32) >> 4;
-                        mma_f16(d, qd + o, cd + o, id_s, u);
+                        for (uint32_t u = 0; u < 8; ++u) {
+                            const uint32_t o = ((u >> 2) * kChunk + (u & 3) * 32) >> 4;
+                            mma_f16(d, qp + o, cd + o, id_s, p | u);
+                        }
                     }
+                    __syncwarp();
+                }
+                const uint32_t rs = (uint32_t)(j % kRopes);
+                if (ok) ok = warp_wait(&r_full[rs], (uint32_t)((j / kRopes) & 1));
+                if (!ok) break;
+                fence_after();
+                const uint64_t rd = rd0 + ((rs * kChunk) >> 4), qp = qd + (((kChunks - 1) * kChunk) >> 4);
+                if (elect_one()) {
+#pragma unroll
+                    for (uint32_t u = 0; u < 4; ++u) mma_f16(d, qp + u * 2, rd + u * 2, id_s, 1u);
                     mma_commit(smem_u32(&s_full[j % 2]));
                     if (k + 1 == g.k1) mma_commit(smem_u32(&q_free));
-                    ++j;
-                    if (k > g.k0) issue_o(k == g.k0 + 1);
                 }
-                if (ok) issue_o(g.k1 == g.k0 + 1);
-                ++seg;
+                __syncwarp();
+                ++j;
             }
-            // everything issued has completed before the TMEM goes
-            if (j) mbar_wait(smem_u32(&s_full[(j - 1) % 2]), (uint32_t)(((j - 1) / 2) & 1));
-            if (done) mbar_wait(smem_u32(&o_done[(done - 1) % 2]), (uint32_t)(((done - 1) / 2) & 1));
+            ++seg;
         }
+        // every S issued has completed before the TMEM goes (a step cut short is covered by a
+        // commit of its own)
+        if (elect_one()) mma_commit(smem_u32(&s_end));
         __syncwarp();
+        mbar_wait(smem_u32(&s_end), 0);
+    } else if (warp == 6) {
+        // ------------------------------------------------------------------- O^T += C^T . P^T
+        const uint32_t id_o = f16_idesc(a.bf16 != 0, true, false, 128, kRows);
+        const uint64_t vd0 = sw128_desc(sm0 + kOffC, kChunk, 1024), pd0 = sw128_desc(sm0 + kOffR, 16, 1024);
+        uint64_t j = 0, seg = 0;
+        bool ok = true;
+        while (ok && walk.next(g)) {
+            if (g.k0 >= g.k1) continue;
+            for (uint64_t k = g.k0; ok && k < g.k1; ++k) {
+                ok = warp_wait(&p_full[j % 2], (uint32_t)((j / 2) & 1));
+                if (ok && k == g.k0 && seg) ok = warp_wait(&o_free, (uint32_t)((seg - 1) & 1));
+                if (!ok) break;
+                fence_after();
+                const uint64_t pd = pd0 + (((uint32_t)(j % kRopes) * kChunk) >> 4);
+                const uint32_t acc = k > g.k0;
+#pragma unroll
+                for (uint32_t m = 0; m < 4; ++m) {
+                    const uint64_t c = 4 * j + m;
+                    const uint32_t sl = (uint32_t)(c % kPairs);
+                    // (complete since S has read it; waited for here too, as its reader)
+                    if (ok) ok = warp_wait(&c_full[sl], (uint32_t)((c / kPairs) & 1));
+                    if (!ok) break;
+                    const uint64_t vd = vd0 + ((sl * 2 * kChunk) >> 4);
+                    if (elect_one()) {
+#pragma unroll
+                        for (uint32_t kk = 0; kk < 4; ++kk)
+                            mma_f16(tmem + kOCol + m * kRows, vd + kk * 128, pd + kk * 2, id_o, acc | kk);
+                        mma_commit(smem_u32(&c_free[sl]));
+                        if (m == 3) {
+                            mma_commit(smem_u32(&r_free[j % kRopes]));
+                            mma_commit(smem_u32(&o_done[j % 2]));
+                        }
+                    }
+                    __syncwarp();
+                }
+                ++j;
+            }
+            ++seg;
+        }
+        if (elect_one()) mma_commit(smem_u32(&o_end));
+        __syncwarp();
+        mbar_wait(smem_u32(&o_end), 0);
     } else {
         // --------------------------------------------------------------- softmax, epilogue
         const uint32_t q4 = warp & 3, fr = lane >> 2, fc = lane & 3;  // fragment row, column
@@ -298,11 +348,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // a wait that runs out marks the window it falls in (the window of step w ends at that
         // step's vote) and the thread carries on to the vote with values it discards
         bool ok_w = true;
-        auto wait_one = [&](uint32_t bar, uint32_t parity, uint64_t w) {
-            if (!mbar_wait(bar, parity)) {
+        auto wait_one = [&](unsigned long long* bar, uint32_t parity, uint64_t w) {
+            if (!wait_for(bar, parity)) {
                 fail_s[w % 2] = 1;
-                abort_flag = 1;
-                report(a.d_status, HP_ERR_TIMEOUT);
                 ok_w = false;
             }
         };
@@ -318,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
             for (uint64_t k = g.k0; k < g.k1; ++k, ++j) {
-                wait_one(smem_u32(&s_full[j % 2]), (uint32_t)((j / 2) & 1), j);
+                wait_one(&s_full[j % 2], (uint32_t)((j / 2) & 1), j);
                 fence_after();
                 uint32_t xr[32];
                 tmem_issue_frag(tmem + lane_addr + kSCol + (uint32_t)(j % 2) * kTok, xr);
@@ -360,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (k > g.k0) {
                         // rescale O^T, complete up to step j - 1
-                        wait_one(smem_u32(&o_done[(j - 1) % 2]), (uint32_t)(((j - 1) / 2) & 1), j + 1);
+                        wait_one(&o_done[(j - 1) % 2], (uint32_t)(((j - 1) / 2) & 1), j + 1);
                         named_sync(1, kSoftmax);
                         fence_after();
 #pragma unroll 1
@@ -379,8 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 // weights: summed in fp32, rounded to the element type for the product
-                unsigned char* stage = smem + kOffC + (uint32_t)(j % kStages) * kStage;
-                unsigned char* pb = stage + kVChunks * kChunk;
+                unsigned char* pb = smem + kOffR + (uint32_t)(j % kRopes) * kChunk;
                 const float m0 = m[0] == -INFINITY ? 0.0f : m[0], m1 = m[1] == -INFINITY ? 0.0f : m[1];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -395,16 +442,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // rows past the sequence become zeros before they meet their zero weights
                 if (t0 + kTok > g.len) {
                     const uint32_t t = threadIdx.x - 64;
+                    const uint32_t ch = (t & 63) >> 3;  // latent chunk
+                    unsigned char* base =
+                        smem + kOffC + ((uint32_t)((4 * j + (ch >> 1)) % kPairs) * 2 + (ch & 1)) * kChunk + (t & 7) * 16;
                     for (uint32_t r = (uint32_t)(g.len - t0) + (t >> 6); r < kTok; r += 2)
-                        *reinterpret_cast<uint4*>(stage + ((t & 63) >> 3) * kChunk + r * 128 + (t & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(base + r * 128) = make_uint4(0, 0, 0, 0);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 mbar_arrive(smem_u32(&p_full[j % 2]));
             }
             if (stop) break;
             const bool any = g.k0 < g.k1;
-            if (any) wait_one(smem_u32(&o_done[(j - 1) % 2]), (uint32_t)(((j - 1) / 2) & 1), j);
+            if (any) wait_one(&o_done[(j - 1) % 2], (uint32_t)(((j - 1) / 2) & 1), j);
             if (!named_and(2, kSoftmax, ok_w)) break;
             fence_after();
 #pragma unroll
@@ -417,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (fc == 0)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    inv_s[row0 + 8 * i] = whole ? (l[i] == 0.0f ? 0.0f : 1.0f / l[i]) : 1.0f;
+                    inv_s[row0 + 8 * i] = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
                     if (!whole) a.part_ml[rec0 + row0 + 8 * i] = make_float2(m[i], l[i]);
                 }
             named_sync(1, kSoftmax);
@@ -434,13 +483,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 32; ++i) o[i] = 0u;
                 }
                 const uint32_t dim = (c >> 6) * 128 + dim0, rb = c & 32;
+                if (whole) {
+                    // lanes 2x, 2x + 1 hold dims d, d + 1: the even one stores both of an even row,
+                    // the odd one of the odd row after it
+                    T* o0 = out + (g.q0 * a.H + g.r0 + rb + (lane & 1)) * kR + (dim & ~1u);
 #pragma unroll
-                for (uint32_t i = 0; i < 32; ++i)
-                    if (rb + i < g.rows) {
-                        const float y = __uint_as_float(o[i]) * inv_s[rb + i];
-                        if (whole) out[(g.q0 * a.H + g.r0 + rb + i) * kR + dim] = round1<T>(y);
-                        else a.part_acc[(rec0 + rb + i) * kR + dim] = y;
+                    for (uint32_t i = 0; i < 32; i += 2) {
+                        const float e = __uint_as_float(o[i]) * inv_s[rb + i];
+                        const float f = __uint_as_float(o[i + 1]) * inv_s[rb + i + 1];
+                        const float y = __shfl_xor_sync(0xffffffffu, lane & 1 ? e : f, 1);
+                        if (rb + i + (lane & 1) < g.rows)
+                            *reinterpret_cast<uint32_t*>(o0 + i * kR) = lane & 1 ? pack2<T>(y, f) : pack2<T>(e, y);
                     }
+                } else {
+#pragma unroll
+                    for (uint32_t i = 0; i < 32; ++i)
+                        if (rb + i < g.rows) a.part_acc[(rec0 + rb + i) * kR + dim] = __uint_as_float(o[i]);
+                }
             }
             fence_before();
             if (any) mbar_arrive(smem_u32(&o_free));
@@ -453,19 +512,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_free(tmem, kTmemCols);
 }
 
+// The pool [rows, 576] as [chunk 9][row][64 dims]: boxes of 64 dims x box_rows rows x `chunks`.
+bool pool_map(CUtensorMap* m, const LatentArgs& a, uint32_t box_rows, uint32_t chunks)
+{
+    EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {64, a.num_pages * a.page_size, kChunks};
+    const cuuint64_t strides[2] = {kW * 2, 128};
+    const cuuint32_t box[3] = {64, box_rows, chunks};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, a.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+              const_cast<void*>(a.pool), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T>
 int launch_t(const LatentArgs& a, cudaStream_t st)
 {
-    CUtensorMap mc, mq;
+    CUtensorMap mc, mr, mq;
+    // pages of 64 slots and more: a slot's two chunks in one box
     const uint32_t box = a.page_size < kTok ? (uint32_t)a.page_size : kTok;
-    if (!map_2d(&mc, a.pool, a.num_pages * a.page_size, kW, kW * 2, box, a.bf16) ||
+    if (!pool_map(&mc, a, box, a.page_size < kTok ? 1 : 2) || !pool_map(&mr, a, box, 1) ||
         !map_2d(&mq, a.q, a.total_q * a.H, kW, kW * 2, kRows, a.bf16))
         return HP_ERR_CUDA;
     int dev = 0;
     if (current_sms(&dev) == 0 || !allow_dynamic_smem<latent_tc_kernel<T>>(dev, (int)kSmem))
         return HP_ERR_CUDA;
     return launch_dependent(latent_tc_kernel<T>, (unsigned)(a.workers * (a.group_rows / kRows)), kThreads,
-                            (size_t)kSmem, st, a, mc, mq) == cudaSuccess
+                            (size_t)kSmem, st, a, mc, mr, mq) == cudaSuccess
                ? HP_OK
                : HP_ERR_CUDA;
 }
