@@ -685,9 +685,10 @@ int hp_latent_decode_workspace_bytes(const hp_paged_desc* desc, uint32_t latent_
  * finite (a query's weight for a later token of its sequence is zero, not absent); slots past
  * a sequence's length may hold anything.
  * Supported: latent_dim a multiple of 64 up to 512; rope_dim a multiple of 8 from 8 to 64;
- * page_size <= 2^26 (HP_ERR_ARG otherwise); device memory.  latent_dim 512 with rope_dim 64
- * and pages of 8, 16, 32 or a multiple of 64 slots run on the tensor cores, the others on the
- * CUDA cores (HP_ATTN_CUDA_CORES in desc->flags asks for those always).  The descriptor is
+ * page_size <= 2^26 (HP_ERR_ARG otherwise).  latent_dim 512 with rope_dim 64 and pages of a
+ * multiple of 8 slots run on the tensor cores, the others on the CUDA cores
+ * (HP_ATTN_CUDA_CORES in desc->flags asks for those always, and so does HP_HOST_MEMORY, for a
+ * pool in page-locked host memory).  The descriptor is
  * always validated, as in hp_attention_decode; q_ptr with the codes of an append's new_ptr.
  */
 int hp_latent_decode(const hp_paged_desc* desc, uint32_t latent_dim, const void* q,

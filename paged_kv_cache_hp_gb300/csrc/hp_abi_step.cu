@@ -281,6 +281,10 @@ u64 latent_records(uint32_t latent_dim)
     return (u64)hp::kLatentMaxSms * hp::kLatentRecordRows * (latent_dim + 2) * 4;
 }
 
+// Block tables up to this many entries are checked by the plan's one CTA (four loads a thread)
+// instead of a launch of their own, which is 2.5 us.
+constexpr u64 kPlanTable = 4096;
+
 int latent_prepare(const hp_paged_desc* desc, uint32_t latent_dim, const void* q_ptr, u64 total_q,
                    uint32_t heads, const void* ws, u64 ws_bytes_, hp_paged_desc* d, u64* plan_bytes)
 {
@@ -333,6 +337,7 @@ HP_API int hp_latent_plan(const hp_paged_desc* desc, uint32_t latent_dim, const 
     pa.heads = num_q_heads;
     pa.group_rows = latent_group_rows(latent_on_tensor_cores(d, latent_dim, total_q * num_q_heads), num_q_heads);
     pa.row_round = 1;
+    pa.check_table = d.table_len <= kPlanTable;
     return hp::launch_plan(hp::kPlanLatent, d.index_type == HP_IDX_U64, pa, stream);
 }
 
@@ -369,6 +374,7 @@ HP_API int hp_latent_decode_planned(const hp_paged_desc* desc, uint32_t latent_d
     a.R = latent_dim;
     a.W = (uint32_t)d.head_dim;
     a.group_rows = latent_group_rows(tc, num_q_heads);
+    if (tc) hp::invariant_divisor(d.page_size / 8, &a.g_m, &a.g_l);
     a.workers = tc ? sms / (a.group_rows / 64) : 2 * sms;
     a.scale = scale;
     a.bf16 = d.dtype == HP_BF16;
@@ -480,6 +486,7 @@ HP_API int hp_latent_prefill(const hp_paged_desc* desc, uint32_t latent_dim, con
     pa.group_rows = block;
     pa.row_round = hp::kLatentPad;
     pa.out_tokens = kv_tokens;
+    pa.check_table = d.table_len <= kPlanTable;
     rc = hp::launch_plan(hp::kPlanLatent, d.index_type == HP_IDX_U64, pa, stream);
     if (rc) return rc;
     if (d.num_seqs == 0 || total_q == 0) return HP_OK;

@@ -105,6 +105,7 @@ struct PlanArgs {
     // units are the steps of each group of group_rows (query, head) rows; heads 0 (expanded):
     // units are blocks of group_rows queries, and the tokens must not exceed out_tokens.
     uint64_t heads, group_rows, row_round;
+    int check_table;          // latent: the plan itself checks block_table (short tables)
     int strict;               // check the storage invariants
     int check_out;            // gather: compare the total with out_tokens
     int* d_status;

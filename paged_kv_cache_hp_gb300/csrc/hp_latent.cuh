@@ -35,6 +35,7 @@ struct LatentArgs {
     uint64_t total_q;
     uint32_t H, R, W;         // heads, latent_dim, latent_dim + rope_dim
     uint32_t group_rows;
+    uint32_t g_m, g_l;        // div_invariant constants of page_size / 8 (tensor cores)
     uint64_t workers;
     float scale;
     int bf16, idx64, test_stall;

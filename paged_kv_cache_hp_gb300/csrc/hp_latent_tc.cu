@@ -5,20 +5,23 @@
 // tokens (hp_latent.cuh has the split).  Per step, with C the step's 64 cache rows of 576:
 //   S [64 rows x 64 tokens]     = Q . C^T            36 products of 16 dims, M = N = 64
 //   O^T [512 dims x 64 rows]   += C[:, :512]^T . P^T  4 tiles of 128 dims, 4 products each
-// so the step's rows are loaded once (TMA, 128-byte swizzled, 64 dims to a chunk of 8 KiB) and
-// serve as the B operand of S (K-major) and the A operand of O^T (M-major).  O^T rather than O:
-// 64 rows of 512 fp32 sums are half of TMEM either way, but M = 128 products run at the full
-// rate where M = 64 runs at half of it (34 cycles for M = N = 64, 50 for M = 128, N = 64, which
-// its shared-memory reads set: 2,024 a step).  O^T stays in TMEM over the whole range: a row's
-// reference maximum moves (and its column of O^T is rescaled) only when a score exceeds it by
-// more than 2^kTau.  P (weights rounded to the element type) overwrites the step's rope chunk,
-// which S has read.
+// so the step's rows are loaded once and serve as the B operand of S (K-major) and the A operand of
+// O^T (M-major).  O^T rather than O: 64 rows of 512 fp32 sums are half of TMEM either way, but M =
+// 128 products run at the full rate where M = 64 runs at half of it (34 cycles for M = N = 64, 50
+// for M = 128, N = 64, which its shared-memory reads set: 2,024 a step).  O^T stays in TMEM over
+// the whole range: a row's reference maximum moves (and its column of O^T is rescaled) only when
+// a score exceeds it by more than 2^kTau.
 //
-// Shared memory: Q 72 KiB; eight slots of two latent chunks (128 dims) and three of a rope
-// chunk, so two steps and more are held or in flight; a slot goes back to the loader as soon as
-// its tile of O^T is computed.  TMEM: O^T 256 columns, S 2 x 64.  Roles: warp 0 loads C, warp 7
-// the queries, warp 1 issues S, warp 6 O^T (apart, so that neither waits for the other's
-// operands), warps 2-5 do the softmax and the epilogue.
+// A TMA box is 8 tokens: [9 chunks of 64 dims][8 rows][128 bytes], 128-byte swizzled, 9 KiB, so
+// that eight rows are one swizzle atom for every chunk and the operands' 8-row groups lie 9 KiB
+// apart whatever the page size (a multiple of 8).  Eight boxes a step: issuing a box takes the
+// loader about 100 cycles, and boxes of one chunk (36 a step on 16-slot pages) held it to 4,400
+// a step.  Slots of two boxes go back to the loader as the products of their 16 tokens end.
+//
+// Shared memory: Q 72 KiB, two steps of C 144 KiB, P (weights rounded to the element type)
+// 8 KiB.  TMEM: O^T 256 columns, S 2 x 64.  Roles: warp 0 loads C, warp 7 the queries, warp 1
+// issues S, warp 6 O^T (apart, so that neither waits for the other's operands), warps 2-5 do
+// the softmax and the epilogue.
 //
 // Above 64 heads a worker is two neighbouring CTAs whose tiles read the same tokens at the same
 // time, so the second read of a row finds it in L2.
@@ -48,10 +51,11 @@ constexpr uint32_t kRows = 64;                 // rows of a tile
 constexpr uint32_t kTok = kLatentStep;         // tokens of a step
 constexpr uint32_t kChunks = kW / 64;
 constexpr uint32_t kChunk = 64 * 128;          // 64 rows x 64 dims
-constexpr uint32_t kPairs = 8, kRopes = 3;     // slots of two latent chunks, of a rope chunk
-constexpr uint32_t kOffC = kChunks * kChunk;   // Q first, then the slots
-constexpr uint32_t kOffR = kOffC + kPairs * 2 * kChunk;
-constexpr uint32_t kSmem = kOffR + kRopes * kChunk + 1024;
+constexpr uint32_t kGroup = kChunks * 1024;    // 8 tokens
+constexpr uint32_t kSlots = 8;                 // of two groups each: two steps
+constexpr uint32_t kOffC = kChunks * kChunk;   // Q first, then the slots, then P
+constexpr uint32_t kOffP = kOffC + kSlots * 2 * kGroup;
+constexpr uint32_t kSmem = kOffP + kRows * 128 + 1024;
 constexpr uint32_t kOCol = 0, kSCol = 256;     // TMEM columns
 constexpr uint32_t kTmemCols = 512;
 constexpr int kThreads = 8 * 32;
@@ -95,6 +99,12 @@ struct Walk {
     }
 };
 
+// Page of a sequence's group of 8 tokens.
+__device__ __forceinline__ uint64_t div_groups(const LatentArgs& a, uint64_t group)
+{
+    return group < (1ull << 32) ? div_invariant((uint32_t)group, a.g_m, a.g_l) : group / (a.page_size / 8);
+}
+
 template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
 template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b)
 {
@@ -109,11 +119,10 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_tc_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap tmc,
-                     const __grid_constant__ CUtensorMap tmr, const __grid_constant__ CUtensorMap tmq)
+                     const __grid_constant__ CUtensorMap tmq)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ __align__(8) unsigned long long c_full[kPairs], c_free[kPairs], r_full[kRopes], r_free[kRopes],
-        s_full[2], s_free[2], p_full[2], o_done[2], o_free, q_full, q_free, s_end, o_end;
+    __shared__ __align__(8) unsigned long long c_full[kSlots], c_free[kSlots], s_full[2], s_free[2], p_full[2], o_done[2], o_free, q_full, q_free, s_end, o_end;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag, fail_s[2];
     __shared__ float corr_s[kRows], inv_s[kRows];
@@ -139,13 +148,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sm0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char* smem = smem_raw + (sm0 - smem_u32(smem_raw));
     if (threadIdx.x == 0) {
-        for (uint32_t i = 0; i < kPairs; ++i) {
+        for (uint32_t i = 0; i < kSlots; ++i) {
             mbar_init(smem_u32(&c_full[i]), 1);
             mbar_init(smem_u32(&c_free[i]), 1);
-        }
-        for (uint32_t i = 0; i < kRopes; ++i) {
-            mbar_init(smem_u32(&r_full[i]), 1);
-            mbar_init(smem_u32(&r_free[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&s_full[i]), 1);
@@ -182,54 +187,49 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         // ----------------------------------------------------------- cache rows of each step
-        const uint32_t P = (uint32_t)a.page_size, box = P < kTok ? P : kTok, ppc = kTok / box;
-        const uint32_t spp = P / box, wide = P >= kTok ? 2 : 1;  // steps per page; chunks per box
-        uint64_t j = 0, armed = 0, rarmed = 0;  // steps, slots of each ring given to loads
+        const uint32_t P = (uint32_t)a.page_size;
+        uint64_t j = 0, armed = 0;  // steps, slots given to loads
         bool ok = true;
         while (ok && walk.next(g)) {
             const uint64_t tab0 = index_at(a.seq_ptr, a.idx64, g.s);
-            // lane i < ppc: the pool row of step k's i-th page, if a slot of it is live
-            auto pool_row = [&](uint64_t k) {
-                if (lane >= ppc || k >= g.k1 || k * kTok + (uint64_t)lane * box >= g.len) return -1;
-                if (spp == 1) return (int)(index_at(a.table, a.idx64, tab0 + k * ppc + lane) * P);
-                return (int)(index_at(a.table, a.idx64, tab0 + k / spp) * P + k % spp * kTok);
+            // The slice's entries 64 at a time, two per lane, the next 32 on their way before they
+            // are needed: a lookup is a shuffle (a load per step cost 1,500 cycles of it).
+            const uint64_t npages = (g.len + P - 1) / P;
+            auto entries = [&](uint64_t i) {
+                return i + lane < npages ? index_at(a.table, a.idx64, tab0 + i + lane) : 0ull;
             };
-            int row = pool_row(g.k0);
+            uint64_t base = div_groups(a, g.k0 * 8);
+            unsigned long long cur = entries(base), nxt = entries(base + 32);
             for (uint64_t k = g.k0; ok && k < g.k1; ++k, ++j) {
-                const int next_row = pool_row(k + 1);  // looked up while this step's slots free up
-                const uint32_t pages = __popc(__ballot_sync(0xffffffffu, row >= 0));
-                // box b of a slot: chunks of the same page next to each other
-                const uint32_t nb = pages * 2 / wide, pg = lane % pages, ch = lane / pages;
-                const int r = __shfl_sync(0xffffffffu, row, (int)pg);
+                // lane i: the pool row of the step's i-th (mod 8) group of 8 tokens
+                const uint64_t gi = k * 8 + (lane & 7), page = div_groups(a, gi);
+                if (__shfl_sync(0xffffffffu, page, 0) >= base + 32) {
+                    base += 32;
+                    cur = nxt;
+                    nxt = entries(base + 32);
+                }
+                const uint32_t rel = (uint32_t)(page - base);  // below 64: a step spans 8 pages at most
+                const unsigned long long e0 = __shfl_sync(0xffffffffu, cur, (int)(rel & 31));
+                const unsigned long long e1 = __shfl_sync(0xffffffffu, nxt, (int)(rel & 31));
+                const int row = (int)((rel < 32 ? e0 : e1) * P + (gi * 8 - page * P));
+                const uint32_t live = (uint32_t)umin(8, (g.len - k * kTok + 7) / 8);  // groups with a token
                 for (uint32_t p = 0; p < 4; ++p) {
                     const uint64_t c = 4 * j + p;
-                    const uint32_t sl = (uint32_t)(c % kPairs);
-                    if (c >= kPairs) ok = warp_wait(&c_free[sl], (uint32_t)((c / kPairs - 1) & 1));
+                    const uint32_t sl = (uint32_t)(c % kSlots), n = live > 2 * p ? (live > 2 * p + 1 ? 2 : 1) : 0;
+                    if (c >= kSlots) ok = warp_wait(&c_free[sl], (uint32_t)((c / kSlots - 1) & 1));
                     if (!ok) break;
-                    const uint32_t bar = smem_u32(&c_full[sl]), base = sm0 + kOffC + sl * 2 * kChunk;
-                    if (lane == 0) mbar_expect_tx(bar, pages * box * 128 * 2);
+                    const uint32_t bar = smem_u32(&c_full[sl]);
+                    if (lane == 0) mbar_expect_tx(bar, n * kGroup);
                     armed = c + 1;
                     __syncwarp();
-                    if (lane < nb && !(a.test_stall && c == 0))
-                        tma_3d(base + ch * kChunk + pg * box * 128, &tmc, 0, r, (int)(2 * p + ch), bar);
+                    if (lane >> 1 == p && (lane & 1) < n && !(a.test_stall && c == 0))
+                        tma_3d(sm0 + kOffC + (sl * 2 + (lane & 1)) * kGroup, &tmc, 0, row, 0, bar);
                 }
-                if (!ok) break;
-                const uint32_t rs = (uint32_t)(j % kRopes);
-                if (j >= kRopes) ok = warp_wait(&r_free[rs], (uint32_t)((j / kRopes - 1) & 1));
-                if (!ok) break;
-                if (lane == 0) mbar_expect_tx(smem_u32(&r_full[rs]), pages * box * 128);
-                rarmed = j + 1;
-                __syncwarp();
-                if (lane < pages)
-                    tma_3d(sm0 + kOffR + rs * kChunk + pg * box * 128, &tmr, 0, r, (int)kChunks - 1, smem_u32(&r_full[rs]));
-                row = next_row;
             }
         }
         // the last loads land before the shared memory goes
-        for (uint64_t c = armed > kPairs ? armed - kPairs : 0; c < armed; ++c)
-            mbar_wait(smem_u32(&c_full[c % kPairs]), (uint32_t)((c / kPairs) & 1));
-        for (uint64_t x = rarmed > kRopes ? rarmed - kRopes : 0; x < rarmed; ++x)
-            mbar_wait(smem_u32(&r_full[x % kRopes]), (uint32_t)((x / kRopes) & 1));
+        for (uint64_t c = armed > kSlots ? armed - kSlots : 0; c < armed; ++c)
+            mbar_wait(smem_u32(&c_full[c % kSlots]), (uint32_t)((c / kSlots) & 1));
         __syncwarp();
     } else if (warp == 7) {
         // ------------------------------------------------------------- queries of each tile
@@ -249,90 +249,66 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         // -------------------------------------------------------------------- S = Q . C^T
         const uint32_t id_s = f16_idesc(a.bf16 != 0, false, false, kRows, kTok);
-        const uint64_t qd = sw128_desc(sm0, 16, 1024), cd0 = sw128_desc(sm0 + kOffC, 16, 1024);
-        const uint64_t rd0 = sw128_desc(sm0 + kOffR, 16, 1024);
+        const uint64_t qd = sw128_desc(sm0, 16, 1024), cd0 = sw128_desc(sm0 + kOffC, 16, kGroup);
         uint64_t j = 0, seg = 0;
         bool ok = true;
         while (ok && walk.next(g)) {
             if (g.k0 >= g.k1) continue;
             ok = warp_wait(&q_full, (uint32_t)(seg & 1));
-            for (uint64_t k = g.k0; ok && k < g.k1; ++k) {
+            for (uint64_t k = g.k0; ok && k < g.k1; ++k, ++j) {
                 if (j >= 2) ok = warp_wait(&s_free[j % 2], (uint32_t)((j / 2 - 1) & 1));
-                const uint32_t d = tmem + kSCol + (uint32_t)(j % 2) * kTok;
-#pragma unroll
-                for (uint32_t p = 0; p < 4; ++p) {
-                    const uint64_t c = 4 * j + p;
-                    const uint32_t sl = (uint32_t)(c % kPairs);
-                    if (ok) ok = warp_wait(&c_full[sl], (uint32_t)((c / kPairs) & 1));
-                    if (!ok) break;
-                    fence_after();
-                    const uint64_t cd = cd0 + ((sl * 2 * kChunk) >> 4), qp = qd + ((p * 2 * kChunk) >> 4);
-                    if (elect_one()) {
-#pragma unroll
-                        for (uint32_t u = 0; u < 8; ++u) {
-                            const uint32_t o = ((u >> 2) * kChunk + (u & 3) * 32) >> 4;
-                            mma_f16(d, qp + o, cd + o, id_s, p | u);
-                        }
-                    }
-                    __syncwarp();
-                }
-                const uint32_t rs = (uint32_t)(j % kRopes);
-                if (ok) ok = warp_wait(&r_full[rs], (uint32_t)((j / kRopes) & 1));
+                for (uint64_t c = 4 * j; ok && c < 4 * j + 4; ++c)
+                    ok = warp_wait(&c_full[c % kSlots], (uint32_t)((c / kSlots) & 1));
                 if (!ok) break;
                 fence_after();
-                const uint64_t rd = rd0 + ((rs * kChunk) >> 4), qp = qd + (((kChunks - 1) * kChunk) >> 4);
+                const uint32_t d = tmem + kSCol + (uint32_t)(j % 2) * kTok;
+                const uint64_t cd = cd0 + (((uint32_t)(j % 2) * 8 * kGroup) >> 4);
                 if (elect_one()) {
 #pragma unroll
-                    for (uint32_t u = 0; u < 4; ++u) mma_f16(d, qp + u * 2, rd + u * 2, id_s, 1u);
+                    for (uint32_t u = 0; u < kChunks * 4; ++u)
+                        mma_f16(d, qd + (((u >> 2) * kChunk + (u & 3) * 32) >> 4),
+                                cd + (((u >> 2) * 1024 + (u & 3) * 32) >> 4), id_s, u);
                     mma_commit(smem_u32(&s_full[j % 2]));
                     if (k + 1 == g.k1) mma_commit(smem_u32(&q_free));
                 }
                 __syncwarp();
-                ++j;
             }
             ++seg;
         }
-        // every S issued has completed before the TMEM goes (a step cut short is covered by a
-        // commit of its own)
+        // every S issued has completed before the TMEM goes
         if (elect_one()) mma_commit(smem_u32(&s_end));
         __syncwarp();
         mbar_wait(smem_u32(&s_end), 0);
     } else if (warp == 6) {
         // ------------------------------------------------------------------- O^T += C^T . P^T
         const uint32_t id_o = f16_idesc(a.bf16 != 0, true, false, 128, kRows);
-        const uint64_t vd0 = sw128_desc(sm0 + kOffC, kChunk, 1024), pd0 = sw128_desc(sm0 + kOffR, 16, 1024);
+        const uint64_t vd0 = sw128_desc(sm0 + kOffC, 1024, kGroup), pd = sw128_desc(sm0 + kOffP, 16, 1024);
         uint64_t j = 0, seg = 0;
         bool ok = true;
         while (ok && walk.next(g)) {
             if (g.k0 >= g.k1) continue;
-            for (uint64_t k = g.k0; ok && k < g.k1; ++k) {
-                ok = warp_wait(&p_full[j % 2], (uint32_t)((j / 2) & 1));
+            for (uint64_t k = g.k0; ok && k < g.k1; ++k, ++j) {
+                // (complete since S has read them; waited for here too, as their reader)
+                for (uint64_t c = 4 * j; ok && c < 4 * j + 4; ++c)
+                    ok = warp_wait(&c_full[c % kSlots], (uint32_t)((c / kSlots) & 1));
                 if (ok && k == g.k0 && seg) ok = warp_wait(&o_free, (uint32_t)((seg - 1) & 1));
+                if (ok) ok = warp_wait(&p_full[j % 2], (uint32_t)((j / 2) & 1));
                 if (!ok) break;
                 fence_after();
-                const uint64_t pd = pd0 + (((uint32_t)(j % kRopes) * kChunk) >> 4);
-                const uint32_t acc = k > g.k0;
+                const uint32_t acc = k > g.k0, half = (uint32_t)(j % 2);
+                const uint64_t vd = vd0 + ((half * 8 * kGroup) >> 4);
+                if (elect_one()) {
 #pragma unroll
-                for (uint32_t m = 0; m < 4; ++m) {
-                    const uint64_t c = 4 * j + m;
-                    const uint32_t sl = (uint32_t)(c % kPairs);
-                    // (complete since S has read it; waited for here too, as its reader)
-                    if (ok) ok = warp_wait(&c_full[sl], (uint32_t)((c / kPairs) & 1));
-                    if (!ok) break;
-                    const uint64_t vd = vd0 + ((sl * 2 * kChunk) >> 4);
-                    if (elect_one()) {
+                    for (uint32_t kk = 0; kk < 4; ++kk) {  // 16 tokens, a slot
 #pragma unroll
-                        for (uint32_t kk = 0; kk < 4; ++kk)
-                            mma_f16(tmem + kOCol + m * kRows, vd + kk * 128, pd + kk * 2, id_o, acc | kk);
-                        mma_commit(smem_u32(&c_free[sl]));
-                        if (m == 3) {
-                            mma_commit(smem_u32(&r_free[j % kRopes]));
-                            mma_commit(smem_u32(&o_done[j % 2]));
-                        }
+                        for (uint32_t m = 0; m < 4; ++m)   // 128 dims
+                            mma_f16(tmem + kOCol + m * kRows, vd + ((kk * 2 * kGroup + m * 2048) >> 4), pd + kk * 2,
+                                    id_o, acc | kk);
+                        mma_commit(smem_u32(&c_free[half * 4 + kk]));
                     }
-                    __syncwarp();
+                    mma_commit(smem_u32(&o_done[half]));
                 }
-                ++j;
+                __syncwarp();
             }
             ++seg;
         }
@@ -427,26 +403,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 // weights: summed in fp32, rounded to the element type for the product
-                unsigned char* pb = smem + kOffR + (uint32_t)(j % kRopes) * kChunk;
                 const float m0 = m[0] == -INFINITY ? 0.0f : m[0], m1 = m[1] == -INFINITY ? 0.0f : m[1];
+                uint32_t w[16];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float p0 = exp2_approx(x[4 * i] - m0), p1 = exp2_approx(x[4 * i + 1] - m0);
                     const float p2 = exp2_approx(x[4 * i + 2] - m1), p3 = exp2_approx(x[4 * i + 3] - m1);
                     l[0] += p0 + p1;
                     l[1] += p2 + p3;
+                    w[2 * i] = pack2<T>(p0, p1);
+                    w[2 * i + 1] = pack2<T>(p2, p3);
+                }
+                // P is free once O^T of the step before has read it
+                if (k > g.k0) wait_one(&o_done[(j - 1) % 2], (uint32_t)(((j - 1) / 2) & 1), j + 1);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
                     const uint32_t c = 8 * i + 2 * fc;
-                    *reinterpret_cast<uint32_t*>(pb + sw128_off(row0, c)) = pack2<T>(p0, p1);
-                    *reinterpret_cast<uint32_t*>(pb + sw128_off(row0 + 8, c)) = pack2<T>(p2, p3);
+                    *reinterpret_cast<uint32_t*>(smem + kOffP + sw128_off(row0, c)) = w[2 * i];
+                    *reinterpret_cast<uint32_t*>(smem + kOffP + sw128_off(row0 + 8, c)) = w[2 * i + 1];
                 }
                 // rows past the sequence become zeros before they meet their zero weights
                 if (t0 + kTok > g.len) {
-                    const uint32_t t = threadIdx.x - 64;
-                    const uint32_t ch = (t & 63) >> 3;  // latent chunk
-                    unsigned char* base =
-                        smem + kOffC + ((uint32_t)((4 * j + (ch >> 1)) % kPairs) * 2 + (ch & 1)) * kChunk + (t & 7) * 16;
+                    const uint32_t t = threadIdx.x - 64;  // chunk (t & 63) / 8, 16-byte piece t & 7
+                    unsigned char* base = smem + kOffC + (uint32_t)(j % 2) * 8 * kGroup + ((t & 63) >> 3) * 1024 + (t & 7) * 16;
                     for (uint32_t r = (uint32_t)(g.len - t0) + (t >> 6); r < kTok; r += 2)
-                        *reinterpret_cast<uint4*>(base + r * 128) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(base + (r >> 3) * kGroup + (r & 7) * 128) = make_uint4(0, 0, 0, 0);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 mbar_arrive(smem_u32(&p_full[j % 2]));
@@ -512,14 +493,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_free(tmem, kTmemCols);
 }
 
-// The pool [rows, 576] as [chunk 9][row][64 dims]: boxes of 64 dims x box_rows rows x `chunks`.
-bool pool_map(CUtensorMap* m, const LatentArgs& a, uint32_t box_rows, uint32_t chunks)
+// The pool [rows, 576] as [chunk 9][row][64 dims]: boxes of 64 dims x 8 rows x 9 chunks.
+bool pool_map(CUtensorMap* m, const LatentArgs& a)
 {
     EncodeFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[3] = {64, a.num_pages * a.page_size, kChunks};
     const cuuint64_t strides[2] = {kW * 2, 128};
-    const cuuint32_t box[3] = {64, box_rows, chunks};
+    const cuuint32_t box[3] = {64, 8, kChunks};
     const cuuint32_t estr[3] = {1, 1, 1};
     return fn(m, a.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
               const_cast<void*>(a.pool), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -530,17 +511,13 @@ bool pool_map(CUtensorMap* m, const LatentArgs& a, uint32_t box_rows, uint32_t c
 template <typename T>
 int launch_t(const LatentArgs& a, cudaStream_t st)
 {
-    CUtensorMap mc, mr, mq;
-    // pages of 64 slots and more: a slot's two chunks in one box
-    const uint32_t box = a.page_size < kTok ? (uint32_t)a.page_size : kTok;
-    if (!pool_map(&mc, a, box, a.page_size < kTok ? 1 : 2) || !pool_map(&mr, a, box, 1) ||
-        !map_2d(&mq, a.q, a.total_q * a.H, kW, kW * 2, kRows, a.bf16))
-        return HP_ERR_CUDA;
+    CUtensorMap mc, mq;
+    if (!pool_map(&mc, a) || !map_2d(&mq, a.q, a.total_q * a.H, kW, kW * 2, kRows, a.bf16)) return HP_ERR_CUDA;
     int dev = 0;
     if (current_sms(&dev) == 0 || !allow_dynamic_smem<latent_tc_kernel<T>>(dev, (int)kSmem))
         return HP_ERR_CUDA;
     return launch_dependent(latent_tc_kernel<T>, (unsigned)(a.workers * (a.group_rows / kRows)), kThreads,
-                            (size_t)kSmem, st, a, mc, mr, mq) == cudaSuccess
+                            (size_t)kSmem, st, a, mc, mq) == cudaSuccess
                ? HP_OK
                : HP_ERR_CUDA;
 }
@@ -551,8 +528,7 @@ bool latent_tc_fits(uint32_t latent_dim, uint64_t head_dim, uint64_t page_size, 
                     uint64_t q_rows)
 {
     return latent_dim == kR && head_dim == kW &&
-           (page_size == 8 || page_size == 16 || page_size == 32 || page_size % 64 == 0) &&
-           num_pages > 0 && num_pages * page_size < (1ull << 31) && q_rows < (1ull << 31);
+           page_size % 8 == 0 && num_pages > 0 && num_pages * page_size < (1ull << 31) && q_rows < (1ull << 31);
 }
 
 int launch_latent_tc(const LatentArgs& a, void* stream)

@@ -53,6 +53,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a)
     }
     __syncthreads();
 
+    if (MODE == kPlanLatent && a.check_table)  // invariant (3), of a table too short for a kernel of its own
+        for (uint64_t k = threadIdx.x; k < a.table_len; k += kPlanThreads)
+            if ((unsigned long long)static_cast<const IndexT*>(a.table)[k] >= a.num_pages)
+                atomicMin(&s_key, verdict_key(kRankPageId, k));
     for (uint64_t base = 0; base < S; base += kPlanThreads) {
         const uint64_t s = base + threadIdx.x;
         unsigned long long rows = 0, units = 0;
@@ -333,7 +337,7 @@ int launch_plan_t(PlanMode mode, const PlanArgs& a, cudaStream_t st)
     else
         plan_kernel<IndexT, kPlanLatent><<<1, kPlanThreads, 0, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return HP_ERR_CUDA;
-    if (a.strict && a.table_len > 0) {
+    if (a.strict && a.table_len > 0 && !a.check_table) {
         int dev = 0;
         const int sms = current_sms(&dev);
         if (sms == 0) return HP_ERR_CUDA;
