@@ -660,7 +660,8 @@ int hp_latent_append(const hp_latent_desc* latent, const hp_rope_desc* rope, int
 
 /*
  * Bytes of device workspace hp_latent_decode needs: the plan's (hp_workspace_bytes) plus
- * fp32 records (max, sum and latent_dim accumulators) of the row tiles that workers share.
+ * fp32 records (max, sum and latent_dim accumulators) of the row tiles that workers share and
+ * an entry per worker.
  * It depends on num_seqs, latent_dim and the device's limits only, not on the lengths.
  */
 int hp_latent_decode_workspace_bytes(const hp_paged_desc* desc, uint32_t latent_dim,

@@ -278,7 +278,8 @@ uint32_t latent_group_rows(bool tc, uint32_t heads)
 
 u64 latent_records(uint32_t latent_dim)
 {
-    return (u64)hp::kLatentMaxSms * hp::kLatentRecordRows * (latent_dim + 2) * 4;
+    return (u64)hp::kLatentMaxSms * hp::kLatentRecordRows * (latent_dim + 2) * 4 +
+           2 * (u64)hp::kLatentMaxSms * sizeof(hp::LatentMerge);
 }
 
 // Block tables up to this many entries are checked by the plan's one CTA (four loads a thread)
@@ -385,6 +386,7 @@ HP_API int hp_latent_decode_planned(const hp_paged_desc* desc, uint32_t latent_d
     a.part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan);
     a.part_ml = reinterpret_cast<float2*>(a.part_acc +
                                           (u64)hp::kLatentMaxSms * hp::kLatentRecordRows * latent_dim);
+    a.merge = reinterpret_cast<hp::LatentMerge*>(a.part_ml + (u64)hp::kLatentMaxSms * hp::kLatentRecordRows);
     a.out = out;
     a.d_status = d_status;
     rc = tc ? hp::launch_latent_tc(a, stream) : hp::launch_latent_cc(a, stream);

@@ -70,6 +70,7 @@ __global__ void __launch_bounds__(256, 2) latent_cc_kernel(const LatentArgs a)
         }
     const uint64_t total = a.hdr->total_units, Lw = (total + a.workers - 1) / a.workers;
     const uint64_t v = blockIdx.x, beg = umin(v * Lw, total), end = umin(beg + Lw, total);
+    if (threadIdx.x == 255) write_merge(a, v);
     const float qscale = a.scale * kLog2e;
     uint64_t pos = beg;
     while (pos < end) {
@@ -209,33 +210,26 @@ __global__ void __launch_bounds__(256, 2) latent_cc_kernel(const LatentArgs a)
     }
 }
 
-// CTA (v, y): eight rows, one per warp, of the row group that begins in worker v's range and
-// goes on past it.
-template <typename T>
+// CTA (v, y): rows of the group that begins in worker v's range and goes on past it, SPLIT warps
+// to a row (each a stretch of its sums).  With few rows four warps share one, so that a long
+// sequence's many records are read by more of the GPU; with many, one warp's fixed part (the
+// entry, the maxima and sums) is paid once a row (GB300, 128 heads: 16 us against 85 with four).
+template <typename T, int SPLIT>
 __global__ void __launch_bounds__(256) latent_merge_kernel(const LatentArgs a)
 {
+    constexpr int kRowsCta = 8 / SPLIT, kQuads = 4 / SPLIT, kBatch = 2 * SPLIT;  // kQuads float4s a lane
     pdl_wait();
     if (a.hdr->verdict != kVerdictOk) return;
     const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint64_t total = a.hdr->total_units, Lw = (total + a.workers - 1) / a.workers;
-    const uint64_t v = blockIdx.x, beg = umin(v * Lw, total), end = umin(beg + Lw, total);
-    if (beg >= end || end == total) return;
-    const uint64_t s = find_seq(a.units_off, a.num_seqs, end - 1);
-    const uint64_t len = index_at(a.lens, a.idx64, s);
-    const uint64_t steps = (len + kLatentStep - 1) / kLatentStep;
-    const uint64_t g = (end - 1 - a.units_off[s]) / steps, ustart = a.units_off[s] + g * steps;
-    const uint64_t uend = ustart + steps;
-    if (ustart < beg || uend <= end) return;
-    const uint64_t q0 = a.q_ptr ? index_at(a.q_ptr, a.idx64, s) : s;
-    const uint64_t n = (a.q_ptr ? index_at(a.q_ptr, a.idx64, s + 1) : s + 1) - q0;
-    const uint32_t gr = blockIdx.y * 8 + warp;
-    const uint64_t r = g * a.group_rows + gr;
-    if (gr >= a.group_rows || r >= n * a.H) return;
-    const uint64_t last = (uend - 1) / Lw;
-    auto rec = [&](uint64_t w) { return (2 * w + (w == v && ustart > beg ? 1 : 0)) * a.group_rows + gr; };
+    const LatentMerge mg = a.merge[blockIdx.x];
+    const uint32_t gr = blockIdx.y * kRowsCta + warp / SPLIT;
+    if (gr >= mg.rows) return;
+    const uint32_t v = blockIdx.x, last = mg.last;
+    // worker w's record row
+    auto rec = [&](uint32_t w) { return (uint64_t)(2 * w + (w == v ? mg.slot : 0)) * a.group_rows + gr; };
     // maximum and sum over the records, a lane per record, then pairwise
     float M = -INFINITY, L = 0.0f, mine = -INFINITY;  // mine: the maximum of record v + lane
-    for (uint64_t w = v + lane; w <= last; w += 32) {
+    for (uint32_t w = v + lane; w <= last; w += 32) {
         const float2 x = a.part_ml[rec(w)];
         if (w == v + lane) mine = x.x;
         const float mn = fmaxf(M, x.x);
@@ -253,69 +247,87 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const LatentArgs a)
             M = mn;
         }
     }
-    const uint32_t quads = a.R / 4;  // float4 per record row: at most 4 per lane
-    float4 acc[4];
+    // float4s of the row: this warp's stretch of R / 4 / SPLIT, kQuads per lane
+    const uint32_t stretch = a.R / 4 / SPLIT, q0 = (warp % SPLIT) * stretch;
+    float4 acc[kQuads];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] = make_float4(0, 0, 0, 0);
+    for (int j = 0; j < kQuads; ++j) acc[j] = make_float4(0, 0, 0, 0);
     if (M != -INFINITY)
-        for (uint64_t w0 = v; w0 <= last; w0 += 32) {  // 32 records, their factors one per lane
+        for (uint32_t w0 = v; w0 <= last; w0 += 32) {  // 32 records, their factors one per lane
             if (w0 != v) mine = w0 + lane <= last ? a.part_ml[rec(w0 + lane)].x : -INFINITY;
             const float fl = exp2_approx(mine - M);
-            const uint32_t n32 = (uint32_t)umin(32, last + 1 - w0);
-#pragma unroll 4
-            for (uint32_t i = 0; i < n32; ++i) {
-                const float f = __shfl_sync(0xffffffffu, fl, (int)i);
-                const float4* p = reinterpret_cast<const float4*>(a.part_acc + rec(w0 + i) * a.R);
+            const uint32_t n32 = last + 1 - w0 < 32 ? last + 1 - w0 : 32;
+            for (uint32_t i0 = 0; i0 < n32; i0 += kBatch) {
+                float4 x[kBatch][kQuads];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (lane + 32 * j < quads) {
-                        const float4 x = p[lane + 32 * j];
-                        acc[j].x = fmaf(f, x.x, acc[j].x);
-                        acc[j].y = fmaf(f, x.y, acc[j].y);
-                        acc[j].z = fmaf(f, x.z, acc[j].z);
-                        acc[j].w = fmaf(f, x.w, acc[j].w);
+                for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                    for (int j = 0; j < kQuads; ++j)
+                        x[i][j] = lane + 32 * j < stretch && i0 + i < n32
+                                      ? reinterpret_cast<const float4*>(a.part_acc + rec(w0 + i0 + i) * a.R)[q0 + lane + 32 * j]
+                                      : make_float4(0, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const float f = __shfl_sync(0xffffffffu, fl, (int)(i0 + i) & 31);  // (0 past the last)
+#pragma unroll
+                    for (int j = 0; j < kQuads; ++j) {
+                        acc[j].x = fmaf(f, x[i][j].x, acc[j].x);
+                        acc[j].y = fmaf(f, x[i][j].y, acc[j].y);
+                        acc[j].z = fmaf(f, x[i][j].z, acc[j].z);
+                        acc[j].w = fmaf(f, x[i][j].w, acc[j].w);
                     }
+                }
             }
         }
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-    uint2* o = reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (q0 * a.H + r) * a.R);
+    uint2* o = reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (mg.out_row + gr) * a.R);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (lane + 32 * j < quads)
-            o[lane + 32 * j] = make_uint2(Pair<T>::down(acc[j].x * inv, acc[j].y * inv),
-                                          Pair<T>::down(acc[j].z * inv, acc[j].w * inv));
+    for (int j = 0; j < kQuads; ++j)
+        if (lane + 32 * j < stretch)
+            o[q0 + lane + 32 * j] = make_uint2(Pair<T>::down(acc[j].x * inv, acc[j].y * inv),
+                                               Pair<T>::down(acc[j].z * inv, acc[j].w * inv));
 }
 
 // --------------------------------------------------------------------- expanded form
 
-// The latent rows of each sequence in order, padded with zeros to a multiple of kLatentPad: a
-// block of 128 rows lies in one sequence.  Warp per row, 16 bytes per lane.  For the tensor cores
+// The latent rows of each sequence in order, padded with zeros to a multiple of kLatentPad, so
+// that a block of 128 rows lies in one sequence.  Four rows per warp, 16 bytes per lane.  For the tensor cores
 // (blocked) the latent part is a matrix of its own and the rope keys lie as shared memory holds
 // them.
 __global__ void __launch_bounds__(256) latent_rows_kernel(const LatentPrefillArgs a)
 {
+    constexpr int kRowsWarp4 = 4;  // rows of a warp, looked up and loaded together
     pdl_wait();
     if (a.hdr->verdict != kVerdictOk) return;
     const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint64_t blocks = a.hdr->total_rows / kLatentPad;
-    const uint32_t vecs = a.W / 8;
-    for (uint64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
-        const uint64_t row0 = b * kLatentPad, s = find_seq(a.rows_off, a.num_seqs, row0);
+    const uint64_t rows = a.hdr->total_rows;
+    const uint32_t vecs = a.W / 8, lvecs = a.R / 8;
+    for (uint64_t row0 = ((uint64_t)blockIdx.x * 8 + warp) * kRowsWarp4; row0 < rows;
+         row0 += (uint64_t)gridDim.x * 8 * kRowsWarp4) {
+        const uint64_t s = find_seq(a.rows_off, a.num_seqs, row0);  // (128 divides its rows_off)
+        const uint64_t t0 = row0 - a.rows_off[s];
         const uint64_t len = index_at(a.lens, a.idx64, s), tab0 = index_at(a.seq_ptr, a.idx64, s);
-#pragma unroll 2
-        for (uint32_t i = warp; i < kLatentPad; i += 8) {
-            const uint64_t t = row0 - a.rows_off[s] + i;
-            const uint4* src = nullptr;
-            if (t < len) {
-                const uint64_t phys = index_at(a.table, a.idx64, tab0 + t / a.page_size);
-                src = static_cast<const uint4*>(a.pool) + (phys * a.page_size + t % a.page_size) * vecs;
-            }
-            for (uint32_t c = lane; c < vecs; c += 32) {
-                const uint4 x = src ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                if (!a.blocked) static_cast<uint4*>(a.rows)[(row0 + i) * vecs + c] = x;
-                else if (c < a.R / 8) static_cast<uint4*>(a.rows)[(row0 + i) * (a.R / 8) + c] = x;
-                else  // row i of the block's 128-byte rows, 16-byte pieces swizzled by the row
-                    static_cast<uint4*>(a.rope_blocks)[row0 * 8 + i * 8 + ((c - a.R / 8) ^ (i & 7))] = x;
+        const uint4* src[kRowsWarp4];
+#pragma unroll
+        for (int i = 0; i < kRowsWarp4; ++i) {
+            const uint64_t t = t0 + i;
+            src[i] = nullptr;
+            if (t < len)
+                src[i] = static_cast<const uint4*>(a.pool) +
+                         (index_at(a.table, a.idx64, tab0 + t / a.page_size) * a.page_size + t % a.page_size) * vecs;
+        }
+#pragma unroll 3
+        for (uint32_t c = lane; c < vecs; c += 32) {
+            uint4 x[kRowsWarp4];
+#pragma unroll
+            for (int i = 0; i < kRowsWarp4; ++i) x[i] = src[i] ? __ldg(src[i] + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < kRowsWarp4; ++i) {
+                const uint64_t r = row0 + i;
+                if (!a.blocked) static_cast<uint4*>(a.rows)[r * vecs + c] = x[i];
+                else if (c < lvecs) static_cast<uint4*>(a.rows)[r * lvecs + c] = x[i];
+                else  // 128-byte rows, 16-byte pieces swizzled by the row
+                    static_cast<uint4*>(a.rope_blocks)[r * 8 + ((c - lvecs) ^ (r & 7))] = x[i];
             }
         }
     }
@@ -483,17 +495,21 @@ int launch_latent_cc(const LatentArgs& a, void* stream)
 
 int launch_latent_merge(const LatentArgs& a, void* stream)
 {
+    const bool few = a.total_q * a.H <= 2048;  // rows in all
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)a.workers, (a.group_rows + 7) / 8);
+    cfg.gridDim = dim3((unsigned)a.workers, (a.group_rows + (few ? 1 : 7)) / (few ? 2 : 8));
     cfg.blockDim = dim3(256);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = a.bf16 ? cudaLaunchKernelEx(&cfg, latent_merge_kernel<__nv_bfloat16>, a)
-                                 : cudaLaunchKernelEx(&cfg, latent_merge_kernel<__half>, a);
+    const cudaError_t e =
+        a.bf16 ? (few ? cudaLaunchKernelEx(&cfg, latent_merge_kernel<__nv_bfloat16, 4>, a)
+                      : cudaLaunchKernelEx(&cfg, latent_merge_kernel<__nv_bfloat16, 1>, a))
+               : (few ? cudaLaunchKernelEx(&cfg, latent_merge_kernel<__half, 4>, a)
+                      : cudaLaunchKernelEx(&cfg, latent_merge_kernel<__half, 1>, a));
     return e == cudaSuccess ? HP_OK : HP_ERR_CUDA;
 }
 
@@ -502,8 +518,8 @@ int launch_latent_rows(const LatentPrefillArgs& a, void* stream)
     int dev = 0;
     const int sms = current_sms(&dev);
     if (sms == 0) return HP_ERR_CUDA;
-    const uint64_t blocks = a.cap_rows / kLatentPad, cap = (uint64_t)sms * 8;
-    const uint64_t grid = blocks == 0 ? 1 : (blocks < cap ? blocks : cap);
+    const uint64_t ctas = a.cap_rows / 32, cap = (uint64_t)sms * 32;
+    const uint64_t grid = ctas == 0 ? 1 : (ctas < cap ? ctas : cap);
     return launch_dependent(latent_rows_kernel, (unsigned)grid, 256, 0,
                             static_cast<cudaStream_t>(stream), a) == cudaSuccess
                ? HP_OK

@@ -24,6 +24,14 @@ constexpr uint32_t kLatentTcQueries = 256;  // queries per block, tensor cores
 // its first worker's in slot 1 of that worker's two unless the group starts its range, the
 // others' in slot 0 (a range has at most one group that began before it and one that goes on
 // after it).
+struct LatentMerge {          // the group that begins in a worker's range and goes on past it
+    uint64_t out_row;         // row of out of the group's first row
+    uint32_t rows;            // rows of the group; 0: no such group
+    uint32_t last;            // its last worker
+    uint32_t slot;            // the worker's own record slot (the others': 0)
+    uint32_t pad[3];
+};
+
 struct LatentArgs {
     const void* pool;
     const void* q;            // [total_q, H, W]
@@ -43,6 +51,7 @@ struct LatentArgs {
     const unsigned long long* units_off;
     float* part_acc;          // [2 * workers * group_rows, R]
     float2* part_ml;          // their maxima (log2 units) and sums
+    LatentMerge* merge;       // [workers], written by the attention kernel for the merge
     void* out;                // [total_q, H, R]
     int* d_status;
 };
@@ -88,6 +97,35 @@ __device__ __forceinline__ unsigned long long index_at(const void* p, int idx64,
 {
     return idx64 ? (unsigned long long)static_cast<const unsigned long long*>(p)[i]
                  : (unsigned long long)static_cast<const unsigned int*>(p)[i];
+}
+
+// Worker v's entry of a.merge, by one thread of the attention kernel.
+__device__ __forceinline__ void write_merge(const LatentArgs& a, uint64_t v)
+{
+    const uint64_t total = a.hdr->total_units, Lw = (total + a.workers - 1) / a.workers;
+    const uint64_t b = v * Lw, beg = b < total ? b : total, e = beg + Lw, end = e < total ? e : total;
+    LatentMerge m{};
+    if (beg < end && end < total) {
+        uint64_t lo = 0, hi = a.num_seqs;  // the sequence of the range's last unit
+        while (hi - lo > 1) {
+            const uint64_t mid = (lo + hi) >> 1;
+            if (a.units_off[mid] <= end - 1) lo = mid;
+            else hi = mid;
+        }
+        const uint64_t len = index_at(a.lens, a.idx64, lo);
+        const uint64_t q0 = a.q_ptr ? index_at(a.q_ptr, a.idx64, lo) : lo;
+        const uint64_t n = (a.q_ptr ? index_at(a.q_ptr, a.idx64, lo + 1) : lo + 1) - q0;
+        const uint64_t steps = (len + kLatentStep - 1) / kLatentStep;
+        const uint64_t g = (end - 1 - a.units_off[lo]) / steps, start = a.units_off[lo] + g * steps;
+        if (start >= beg && start + steps > end) {
+            const uint64_t left = n * a.H - g * a.group_rows;
+            m.out_row = q0 * a.H + g * a.group_rows;
+            m.rows = (uint32_t)(left < a.group_rows ? left : a.group_rows);
+            m.last = (uint32_t)((start + steps - 1) / Lw);
+            m.slot = start > beg ? 1 : 0;
+        }
+    }
+    a.merge[v] = m;
 }
 
 }  // namespace hp

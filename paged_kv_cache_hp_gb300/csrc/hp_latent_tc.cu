@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tiles = a.group_rows / kRows;
     const uint64_t total = a.hdr->total_units, Lw = (total + a.workers - 1) / a.workers;
     const uint64_t v = blockIdx.x / tiles, beg = umin(v * Lw, total), end = umin(beg + Lw, total);
+    if (threadIdx.x == 96 && blockIdx.x % tiles == 0) write_merge(a, v);  // (a softmax thread, idle yet)
     if (beg >= end) return;  // the whole CTA, before any barrier or TMEM
 
     const uint32_t sm0 = (smem_u32(smem_raw) + 1023u) & ~1023u;

@@ -32,6 +32,12 @@ __device__ __forceinline__ bool gt_sum(unsigned long long c_lo, unsigned c_carry
     return c_lo > lo;
 }
 
+// a / b, in 32 bits where both fit (a 64-bit division is some hundred instructions).
+__device__ __forceinline__ unsigned long long quotient(unsigned long long a, unsigned long long b)
+{
+    return (a | b) >> 32 ? a / b : (unsigned long long)((unsigned)a / (unsigned)b);
+}
+
 template <typename IndexT, int MODE>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a)
 {
@@ -44,7 +50,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a)
     __shared__ int s_fault;
     __shared__ unsigned long long s_carry_rows, s_carry_units;
     pdl_trigger();  // let the table check start scanning now
+    unsigned long long sp_first = 0, sp_last = 0, np_first = 0, np_last = 0;  // thread 0's, needed last
     if (threadIdx.x == 0) {
+        sp_first = sp[0];
+        sp_last = sp[S];
+        if (np && (MODE == kPlanAppend || MODE == kPlanLatent)) {
+            np_first = np[0];
+            np_last = np[S];
+        }
         s_key = kVerdictOk;
         s_len = 0;
         s_fault = HP_OK;
@@ -64,7 +77,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a)
             const unsigned long long lo = sp[s], hi = sp[s + 1], len = lens[s];
             if (MODE == kPlanGather || MODE == kPlanAttention || MODE == kPlanLatent) {
                 rows = len;
-                units = len / P + (len % P != 0);
+                units = quotient(len, P);
+                units += units * P != len;
                 if (a.strict) {
                     if (lo > hi)
                         atomicMin(&s_key, verdict_key(kRankSeqPtrOrder, s));
@@ -78,11 +92,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a)
                     if (n0 > n1) atomicMin(&s_key, verdict_key(kRankNewPtrOrder, s));
                     const unsigned long long n = n0 <= n1 && n1 <= a.total_new ? n1 - n0 : 0;
                     if (a.heads) {
-                        units = (n * a.heads + a.group_rows - 1) / a.group_rows *
-                                (len / a.step_tokens + (len % a.step_tokens != 0));
+                        units = quotient(n * a.heads + a.group_rows - 1, a.group_rows) *
+                                quotient(len + a.step_tokens - 1, a.step_tokens);
                     } else {
-                        units = (n + a.group_rows - 1) / a.group_rows;
-                        rows = (len + a.row_round - 1) / a.row_round * a.row_round;
+                        units = quotient(n + a.group_rows - 1, a.group_rows);
+                        rows = quotient(len + a.row_round - 1, a.row_round) * a.row_round;
                         atomicAdd(&s_len, len);  // (wraps only past HP_ERR_LEN, an earlier rule)
                     }
                 }
@@ -126,18 +140,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a)
         unsigned long long key = s_key;
         const unsigned long long total_rows = s_carry_rows, total_units = s_carry_units;
         if (a.strict) {
-            if (sp[0] != 0) key = min(key, verdict_key(kRankSeqPtrStart, 0));
-            if ((unsigned long long)sp[S] != a.table_len)
+            if (sp_first != 0) key = min(key, verdict_key(kRankSeqPtrStart, 0));
+            if (sp_last != a.table_len)
                 key = min(key, verdict_key(kRankSeqPtrEnd, S));
             if (MODE == kPlanAppend) {
-                if (np[0] != 0) key = min(key, verdict_key(kRankNewPtrStart, 0));
-                if ((unsigned long long)np[S] != a.total_new)
+                if (np_first != 0) key = min(key, verdict_key(kRankNewPtrStart, 0));
+                if (np_last != a.total_new)
                     key = min(key, verdict_key(kRankNewPtrEnd, S));
             }
         }
         if (MODE == kPlanLatent) {
-            if (np && np[0] != 0) key = min(key, verdict_key(kRankNewPtrStart, 0));
-            if (np && (unsigned long long)np[S] > a.total_new)
+            if (np_first != 0) key = min(key, verdict_key(kRankNewPtrStart, 0));
+            if (np_last > a.total_new)
                 key = min(key, verdict_key(kRankNewPtrEnd, S));
             if (!a.heads && s_len > a.out_tokens) key = min(key, verdict_key(kRankOutSize, 0));
         }

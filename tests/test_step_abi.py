@@ -200,8 +200,9 @@ def test_latent_workspace_sizes(hpc):
         c = paged(hpc, num_seqs=100)
         ref = ctypes.byref(c)
     rc, n = hpc.hp_latent_decode_workspace_bytes(D, 512, 100, 128)
-    # the plan, and 160 SMs x 128 record rows of (max, sum, 512 accumulators) fp32
-    assert rc == 0 and n == 256 + 2 * 1024 + 160 * 128 * 514 * 4
+    # the plan, 160 SMs x 128 record rows of (max, sum, 512 accumulators) fp32, and an entry of
+    # 32 bytes for each of up to 320 workers
+    assert rc == 0 and n == 256 + 2 * 1024 + 160 * 128 * 514 * 4 + 320 * 32
     rc, n = hpc.hp_latent_prefill_workspace_bytes(D, 512, 128, 128, 1000, 16, 5000)
     rows = -(-(5000 + 127 * 100) // 128) * 128
     assert rc == 0 and n == 256 + 2 * 1024 + rows * 576 * 2 + rows * 16 * 256 * 2
