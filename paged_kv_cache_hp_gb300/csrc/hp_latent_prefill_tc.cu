@@ -226,8 +226,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     latent_prefill_kernel(const LatentPrefillArgs a, const __grid_constant__ CUtensorMap tmq)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ __align__(8) unsigned long long kv_full[kSlots], kv_free[kSlots], q_full[2], s_full[2],
-        p_full[2], o_done[2], all_done;
+    __shared__ __align__(8) unsigned long long k_full[2], v_full[2], k_free[2], v_free[2], q_full[2],
+        s_full[2], p_full[2], o_done[2], all_done;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     pdl_wait();
@@ -254,11 +254,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const uint32_t sm0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
     if (threadIdx.x == 0) {
-        for (uint32_t i = 0; i < kSlots; ++i) {
-            mbar_init(smem_u32(&kv_full[i]), 1);
-            mbar_init(smem_u32(&kv_free[i]), 1);
-        }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&k_full[i]), 1);
+            mbar_init(smem_u32(&v_full[i]), 1);
+            mbar_init(smem_u32(&k_free[i]), 1);
+            mbar_init(smem_u32(&v_free[i]), 1);
             mbar_init(smem_u32(&q_full[i]), 1);
             mbar_init(smem_u32(&s_full[i]), 1);
             mbar_init(smem_u32(&p_full[i]), 128);
@@ -297,25 +297,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t b0 = a.rows_off[s] / 128;
             const char* kv = static_cast<const char*>(a.kv) + (h * (a.cap_rows / 128) + b0) * 4 * kSlot;
             const char* rope = static_cast<const char*>(a.rope_blocks) + b0 * kSlot;
-            uint32_t c = 0;  // slots filled
-            bool stop = false;
-            for (uint32_t j = 0; j < blocks && !stop; ++j)
-                for (uint32_t i = 0; i < 5; ++i, ++c) {  // K: 0, 1 expanded, 2 rope; V: 3, 4
-                    const uint32_t st = c % kSlots, bar = smem_u32(&kv_full[st]);
-                    if (c >= kSlots && !wait_for(&kv_free[st], (c / kSlots - 1) & 1)) {
-                        stop = true;
-                        break;
-                    }
-                    mbar_expect_tx(bar, kSlot);
-                    const uint32_t d = sm0 + kOffKv + st * kSlot;
-                    if (a.test_stall && c == 0) continue;
-                    bulk_load(d, i == 2 ? rope + (uint64_t)j * kSlot : kv + ((uint64_t)j * 4 + (i < 2 ? i : i - 1)) * kSlot,
-                              kSlot, bar);
-                }
+            // Piece c = 5 j + i (K: 0, 1 expanded, 2 rope; V: 3, 4) goes to slot c mod 8, where piece
+            // c - 8 was: K's first after the rope keys of block j - 2, its others after V of j - 2,
+            // V after the first keys of j - 1.  One barrier for the three pieces of K, one for V.
+            auto piece = [&](uint32_t j, uint32_t i, unsigned long long* bar) {
+                if (a.test_stall && j == 0 && i == 0) return;
+                bulk_load(sm0 + kOffKv + (5 * j + i) % kSlots * kSlot,
+                          i == 2 ? rope + (uint64_t)j * kSlot : kv + ((uint64_t)j * 4 + (i < 2 ? i : i - 1)) * kSlot,
+                          kSlot, smem_u32(bar));
+            };
+            uint32_t ka = 0, va = 0;  // blocks whose K, whose V barrier has been armed
+            for (uint32_t j = 0; j < blocks; ++j) {
+                unsigned long long *kb = &k_full[j & 1], *vb = &v_full[j & 1];
+                if (j >= 2 && !wait_for(&k_free[j & 1], (j / 2 - 1) & 1)) break;
+                mbar_expect_tx(smem_u32(kb), 3 * kSlot);
+                ++ka;
+                piece(j, 0, kb);
+                if (j >= 2 && !wait_for(&v_free[j & 1], (j / 2 - 1) & 1)) break;
+                piece(j, 1, kb);
+                piece(j, 2, kb);
+                if (j >= 1 && !wait_for(&k_free[(j - 1) & 1], ((j - 1) / 2) & 1)) break;
+                mbar_expect_tx(smem_u32(vb), 2 * kSlot);
+                ++va;
+                piece(j, 3, vb);
+                piece(j, 4, vb);
+            }
+            // the last loads land before the shared memory goes
             for (int t = 0; t < 2; ++t)
                 if (nblk[t]) mbar_wait(smem_u32(&q_full[t]), 0);
-            for (uint32_t x = c > kSlots ? c - kSlots : 0; x < c; ++x)
-                mbar_wait(smem_u32(&kv_full[x % kSlots]), (x / kSlots) & 1);
+            for (uint32_t x = ka > 2 ? ka - 2 : 0; x < ka; ++x) mbar_wait(smem_u32(&k_full[x & 1]), (x / 2) & 1);
+            for (uint32_t x = va > 2 ? va - 2 : 0; x < va; ++x) mbar_wait(smem_u32(&v_full[x & 1]), (x / 2) & 1);
         }
         __syncwarp();
     } else if (warp == 9) {
@@ -325,25 +336,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t qd0 = sw128_desc(sm0, 16, 1024), kd0 = sw128_desc(sm0 + kOffKv, 16, 1024);
         const uint64_t vd0 = sw128_desc(sm0 + kOffKv, kSlot, 1024);
         bool ok = true;
-        auto wait_slots = [&](uint32_t c, uint32_t n) {
-            for (uint32_t x = c; ok && x < c + n; ++x) ok = warp_wait(&kv_full[x % kSlots], (x / kSlots) & 1);
-        };
         for (int t = 0; t < 2; ++t)
             if (ok && nblk[t]) ok = warp_wait(&q_full[t], 0);
+        // round j: O of block j - 1 and S of block j, tile after tile.  A wait costs some 200 cycles
+        // even when its phase is complete, so the operands of a round are waited for together and
+        // nothing stands between the products of O and of S.
         for (uint32_t j = 0; j <= blocks && ok; ++j) {
+            if (j > 0) ok = warp_wait(&v_full[(j - 1) & 1], ((j - 1) / 2) & 1);
+            if (ok && j < blocks) ok = warp_wait(&k_full[j & 1], (j / 2) & 1);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                if (j > 0 && j - 1 < nblk[t]) {
-                    // V of block j - 1 is two slots of 64 dims: neighbours, but for the ring's
-                    // last and first
-                    const uint32_t c = 5 * (j - 1) + 3, v0 = c % kSlots;
-                    if (t == 0 || j > nblk[0]) wait_slots(c, 2);
-                    if (ok) ok = warp_wait(&p_full[t], (j - 1) & 1);
-                    if (!ok) break;
-                    fence_after();
-                    const uint32_t pa = tmem + kSCol + t * 128, od = tmem + kOCol + t * 128, acc = j > 1;
-                    const uint64_t vd = vd0 + ((v0 * kSlot) >> 4);
-                    if (elect_one()) {
+                const bool has_o = j > 0 && j - 1 < nblk[t], has_s = j < nblk[t];
+                if (ok && has_o) ok = warp_wait(&p_full[t], (j - 1) & 1);
+                if (!ok) break;
+                fence_after();
+                // V of block j - 1 is two slots of 64 dims: neighbours, but for the ring's last and first
+                const uint32_t v0 = (5 * j - 2) % kSlots, pa = tmem + kSCol + t * 128, od = tmem + kOCol + t * 128;
+                const uint32_t acc = j > 1, sd = tmem + kSCol + t * 128;
+                const uint64_t vd = vd0 + ((v0 * kSlot) >> 4), qd = qd0 + ((3 * t * kSlot) >> 4);
+                const uint64_t k0 = kd0 + ((((5 * j) % kSlots) * kSlot) >> 4);
+                const uint64_t k1 = kd0 + ((((5 * j + 1) % kSlots) * kSlot) >> 4);
+                const uint64_t k2 = kd0 + ((((5 * j + 2) % kSlots) * kSlot) >> 4);
+                if (elect_one()) {
+                    if (has_o) {
                         if (v0 + 1 < kSlots) {
 #pragma unroll
                             for (uint32_t kk = 0; kk < 8; ++kk)
@@ -357,18 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (j == nblk[t]) mma_commit(smem_u32(&o_done[t]));
                     }
-                    __syncwarp();
-                }
-                if (j < nblk[t]) {
-                    if (t == 0 || j >= nblk[0]) wait_slots(5 * j, 3);
-                    if (!ok) break;
-                    fence_after();
-                    const uint64_t qd = qd0 + ((3 * t * kSlot) >> 4);
-                    const uint64_t k0 = kd0 + ((((5 * j) % kSlots) * kSlot) >> 4);
-                    const uint64_t k1 = kd0 + ((((5 * j + 1) % kSlots) * kSlot) >> 4);
-                    const uint64_t k2 = kd0 + ((((5 * j + 2) % kSlots) * kSlot) >> 4);
-                    const uint32_t sd = tmem + kSCol + t * 128;
-                    if (elect_one()) {
+                    if (has_s) {
 #pragma unroll
                         for (uint32_t kk = 0; kk < 4; ++kk) mma_f16(sd, qd + kk * 2, k0 + kk * 2, id_s, kk);
 #pragma unroll
@@ -379,17 +383,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mma_f16(sd, qd + (2 * kSlot >> 4) + kk * 2, k2 + kk * 2, id_s, 1u);
                         mma_commit(smem_u32(&s_full[t]));
                     }
-                    __syncwarp();
+                    if (t == 1) {  // both tiles have read V of block j - 1 and K of block j
+                        if (j > 0) mma_commit(smem_u32(&v_free[(j - 1) & 1]));
+                        if (j < blocks) mma_commit(smem_u32(&k_free[j & 1]));
+                    }
                 }
+                __syncwarp();
             }
-            if (!ok) break;
-            if (elect_one()) {
-                if (j > 0)
-                    for (uint32_t c = 3; c < 5; ++c) mma_commit(smem_u32(&kv_free[(5 * (j - 1) + c) % kSlots]));
-                if (j < blocks)
-                    for (uint32_t c = 0; c < 3; ++c) mma_commit(smem_u32(&kv_free[(5 * j + c) % kSlots]));
-            }
-            __syncwarp();
         }
         // everything issued has completed before the TMEM goes: one more commit covers it
         if (elect_one()) mma_commit(smem_u32(&all_done));

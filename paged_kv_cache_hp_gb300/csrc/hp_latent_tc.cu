@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap tmq)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ __align__(8) unsigned long long c_full[kSlots], c_free[kSlots], s_full[2], s_free[2], p_full[2], o_done[2], o_free, q_full, q_free, s_end, o_end;
+    __shared__ __align__(8) unsigned long long c_full[2], c_free[kSlots], s_full[2], s_free[2], p_full[2], o_done[2], o_free, q_full, q_free, s_end, o_end;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag, fail_s[2];
     __shared__ float corr_s[kRows], inv_s[kRows];
@@ -149,11 +149,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sm0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char* smem = smem_raw + (sm0 - smem_u32(smem_raw));
     if (threadIdx.x == 0) {
-        for (uint32_t i = 0; i < kSlots; ++i) {
-            mbar_init(smem_u32(&c_full[i]), 1);
-            mbar_init(smem_u32(&c_free[i]), 1);
-        }
+        for (uint32_t i = 0; i < kSlots; ++i) mbar_init(smem_u32(&c_free[i]), 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&c_full[i]), 4);  // a step's four slots
             mbar_init(smem_u32(&s_full[i]), 1);
             mbar_init(smem_u32(&s_free[i]), kSoftmax);
             mbar_init(smem_u32(&p_full[i]), kSoftmax);
@@ -219,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t sl = (uint32_t)(c % kSlots), n = live > 2 * p ? (live > 2 * p + 1 ? 2 : 1) : 0;
                     if (c >= kSlots) ok = warp_wait(&c_free[sl], (uint32_t)((c / kSlots - 1) & 1));
                     if (!ok) break;
-                    const uint32_t bar = smem_u32(&c_full[sl]);
+                    const uint32_t bar = smem_u32(&c_full[j % 2]);
                     if (lane == 0) mbar_expect_tx(bar, n * kGroup);
                     armed = c + 1;
                     __syncwarp();
@@ -228,9 +226,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        // the last loads land before the shared memory goes
-        for (uint64_t c = armed > kSlots ? armed - kSlots : 0; c < armed; ++c)
-            mbar_wait(smem_u32(&c_full[c % kSlots]), (uint32_t)((c / kSlots) & 1));
+        // the last loads land before the shared memory goes (a step that a wait cut short arrives for
+        // its missing slots here, so that its barrier's phase can end)
+        for (; armed % 4; ++armed)
+            if (lane == 0) mbar_arrive(smem_u32(&c_full[armed / 4 % 2]));
+        __syncwarp();
+        for (uint64_t x = armed / 4 > 2 ? armed / 4 - 2 : 0; x < armed / 4; ++x)
+            mbar_wait(smem_u32(&c_full[x % 2]), (uint32_t)((x / 2) & 1));
         __syncwarp();
     } else if (warp == 7) {
         // ------------------------------------------------------------- queries of each tile
@@ -258,8 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = warp_wait(&q_full, (uint32_t)(seg & 1));
             for (uint64_t k = g.k0; ok && k < g.k1; ++k, ++j) {
                 if (j >= 2) ok = warp_wait(&s_free[j % 2], (uint32_t)((j / 2 - 1) & 1));
-                for (uint64_t c = 4 * j; ok && c < 4 * j + 4; ++c)
-                    ok = warp_wait(&c_full[c % kSlots], (uint32_t)((c / kSlots) & 1));
+                if (ok) ok = warp_wait(&c_full[j % 2], (uint32_t)((j / 2) & 1));
                 if (!ok) break;
                 fence_after();
                 const uint32_t d = tmem + kSCol + (uint32_t)(j % 2) * kTok;
@@ -290,8 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (g.k0 >= g.k1) continue;
             for (uint64_t k = g.k0; ok && k < g.k1; ++k, ++j) {
                 // (complete since S has read them; waited for here too, as their reader)
-                for (uint64_t c = 4 * j; ok && c < 4 * j + 4; ++c)
-                    ok = warp_wait(&c_full[c % kSlots], (uint32_t)((c / kSlots) & 1));
+                ok = warp_wait(&c_full[j % 2], (uint32_t)((j / 2) & 1));
                 if (ok && k == g.k0 && seg) ok = warp_wait(&o_free, (uint32_t)((seg - 1) & 1));
                 if (ok) ok = warp_wait(&p_full[j % 2], (uint32_t)((j / 2) & 1));
                 if (!ok) break;
