@@ -60,6 +60,44 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Two fp32 at a time (one issue slot), and the largest of three.
+__device__ __forceinline__ uint64_t pair_of(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 of_pair(uint64_t p)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c)
+{
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // ------------------------------------------------------------------------ expansion
 constexpr uint32_t kGStages = 3, kGSlices = kR / 64;
 constexpr uint32_t kGStage = 3 * kSlot;                  // A 128 x 64, B 256 x 64
@@ -339,11 +377,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < 2; ++t)
             if (ok && nblk[t]) ok = warp_wait(&q_full[t], 0);
         // round j: O of block j - 1 and S of block j, tile after tile.  A wait costs some 200 cycles
-        // even when its phase is complete, so the operands of a round are waited for together and
-        // nothing stands between the products of O and of S.
+        // even when its phase is complete, so each operand is waited for once a round, and where the
+        // products issued before it are still running; V goes back before S of the second tile.
         for (uint32_t j = 0; j <= blocks && ok; ++j) {
             if (j > 0) ok = warp_wait(&v_full[(j - 1) & 1], ((j - 1) / 2) & 1);
-            if (ok && j < blocks) ok = warp_wait(&k_full[j & 1], (j / 2) & 1);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const bool has_o = j > 0 && j - 1 < nblk[t], has_s = j < nblk[t];
@@ -372,6 +409,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (j == nblk[t]) mma_commit(smem_u32(&o_done[t]));
                     }
+                    if (t == 1 && j > 0) mma_commit(smem_u32(&v_free[(j - 1) & 1]));  // both tiles have read it
+                }
+                __syncwarp();
+                if (t == 0 && j < blocks) ok = warp_wait(&k_full[j & 1], (j / 2) & 1);
+                if (!ok) break;
+                fence_after();
+                if (elect_one()) {
                     if (has_s) {
 #pragma unroll
                         for (uint32_t kk = 0; kk < 4; ++kk) mma_f16(sd, qd + kk * 2, k0 + kk * 2, id_s, kk);
@@ -383,10 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mma_f16(sd, qd + (2 * kSlot >> 4) + kk * 2, k2 + kk * 2, id_s, 1u);
                         mma_commit(smem_u32(&s_full[t]));
                     }
-                    if (t == 1) {  // both tiles have read V of block j - 1 and K of block j
-                        if (j > 0) mma_commit(smem_u32(&v_free[(j - 1) & 1]));
-                        if (j < blocks) mma_commit(smem_u32(&k_free[j & 1]));
-                    }
+                    if (t == 1 && j < blocks) mma_commit(smem_u32(&k_free[j & 1]));
                 }
                 __syncwarp();
             }
@@ -411,33 +452,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             fence_after();
-            float x[128];
-            uint32_t* xr = reinterpret_cast<uint32_t*>(x);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_issue<32>(sa + 32 * c, xr + 32 * c);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_wait<32>(*reinterpret_cast<uint32_t(*)[32]>(xr + 32 * c));
             const uint64_t t0 = (uint64_t)j * 128;
             const int lim = vis > t0 ? (int)umin(vis - t0, 128) : 0;
             const bool masked = __any_sync(0xffffffffu, lim < 128);
-            // the largest scaled score: the extreme of the raw ones on the scale's side
-            float mx;
-            if (masked) {
-                mx = -INFINITY;
+            // The largest scaled score: the extreme of the raw ones on the scale's side.  32 columns at
+            // a time, the next ones on their way, from the last to the first; the first two stretches
+            // then stay in registers (all 128 do not fit the 168 that ten warps leave a thread).
+            uint32_t xb[2][32];
+            float mx = -INFINITY;
+            tmem_issue<32>(sa + 96, xb[1]);
+            tmem_wait<32>(xb[1]);
 #pragma unroll
-                for (int i = 0; i < 128; ++i)
-                    mx = fmaxf(mx, i < lim ? x[i] * qscale : -INFINITY);
-            } else {
-                float e[4] = {x[0], x[1], x[2], x[3]};
-                if (qscale >= 0.0f) {
+            for (int c = 3; c >= 0; --c) {
+                if (c > 0) tmem_issue<32>(sa + 32 * (c - 1), xb[(c - 1) & 1]);
+                const float* x = reinterpret_cast<const float*>(xb[c & 1]);
+                if (masked) {
 #pragma unroll
-                    for (int i = 4; i < 128; ++i) e[i & 3] = fmaxf(e[i & 3], x[i]);
-                    mx = fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])) * qscale;
+                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, 32 * c + i < lim ? x[i] * qscale : -INFINITY);
+                } else if (qscale >= 0.0f) {
+                    float e0 = x[0], e1 = x[1];
+#pragma unroll
+                    for (int i = 2; i < 30; i += 4) {
+                        e0 = max3(e0, x[i], x[i + 1]);
+                        e1 = max3(e1, x[i + 2], x[i + 3]);
+                    }
+                    mx = fmaxf(mx, fmaxf(max3(e0, x[30], x[31]), e1) * qscale);
                 } else {
+                    float e0 = x[0], e1 = x[1];
 #pragma unroll
-                    for (int i = 4; i < 128; ++i) e[i & 3] = fminf(e[i & 3], x[i]);
-                    mx = fminf(fminf(e[0], e[1]), fminf(e[2], e[3])) * qscale;
+                    for (int i = 2; i < 30; i += 4) {
+                        e0 = min3(e0, x[i], x[i + 1]);
+                        e1 = min3(e1, x[i + 2], x[i + 3]);
+                    }
+                    mx = fmaxf(mx, fminf(min3(e0, x[30], x[31]), e1) * qscale);
                 }
+                if (c > 0) tmem_wait<32>(xb[(c - 1) & 1]);
             }
             if (__any_sync(0xffffffffu, mx > m + kTau)) {
                 const float mn = fmaxf(m, mx);
@@ -457,25 +506,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             const float mu = m == -INFINITY ? 0.0f : m;
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            const uint64_t qs2 = pair_of(qscale, qscale), mu2 = pair_of(-mu, -mu);
+            uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t p[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int e = 64 * c + 2 * i;
-                    float p0 = exp2_approx(fmaf(x[e], qscale, -mu)), p1 = exp2_approx(fmaf(x[e + 1], qscale, -mu));
-                    if (masked) {
-                        p0 = e < lim ? p0 : 0.0f;
-                        p1 = e + 1 < lim ? p1 : 0.0f;
-                    }
-                    sum[(2 * i) & 3] += p0;
-                    sum[(2 * i + 1) & 3] += p1;
-                    p[i] = pack2<T>(p0, p1);
+            for (int c = 0; c < 4; ++c) {  // xb[c & 1] holds columns 32 c ..; 2 and 3 are read again
+                uint32_t p[16];
+                if (c > 0 && c < 3) {  // into the stretch done last, while this one is worked on
+                    tmem_issue<32>(sa + 32 * (c + 1), xb[(c + 1) & 1]);
                 }
-                tmem_st32(sa + 32 * c, p);
+                const float* x = reinterpret_cast<const float*>(xb[c & 1]);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int e = 32 * c + 2 * i;
+                    const uint64_t t2 = fma2(pair_of(x[2 * i], x[2 * i + 1]), qs2, mu2);
+                    float2 w = of_pair(t2);
+                    w.x = exp2_approx(w.x);
+                    w.y = exp2_approx(w.y);
+                    if (masked) {
+                        w.x = e < lim ? w.x : 0.0f;
+                        w.y = e + 1 < lim ? w.y : 0.0f;
+                    }
+                    sum[i & 1] = add2(sum[i & 1], pair_of(w.x, w.y));
+                    p[i] = pack2<T>(w.x, w.y);
+                }
+                if (c > 0 && c < 3) tmem_wait<32>(xb[(c + 1) & 1]);
+                tmem_st16(sa + 16 * c, p);  // over columns already read
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            const float2 sums = of_pair(add2(sum[0], sum[1]));
+            l += sums.x + sums.y;
             tmem_st_wait();
             fence_before();
             mbar_arrive(smem_u32(&p_full[t]));
