@@ -94,6 +94,6 @@ def attention_row(q, k, v, scale, dtype, ds_extra=0.0, v_err=0.0):
     p = np.exp(s - s.max())
     p /= p.sum()
     o, A = p @ v, p @ np.abs(v)
-    ds = (np.abs(k) @ np.abs(q)).max() * scale * (len(q) * 2.0 ** -23 + ds_extra) + 2.0 ** -22 * np.abs(s).max()
+    ds = (np.abs(k) @ np.abs(q)).max() * abs(scale) * (len(q) * 2.0 ** -23 + ds_extra) + 2.0 ** -22 * np.abs(s).max()
     u = U[dtype]
     return o, u * np.abs(o) + (u + 4 * ds + 2.0 ** -21 + n * 2.0 ** -23) * A + v_err + TINY[dtype]

@@ -494,7 +494,7 @@ def check_prefill(b, got, Dn, Dv, w, scale, exact_kv, sample=None):
             o, tol = ref.attention_row(q[t, h], k[:n], v[:n], scale, b.dtype, ds_extra=u)
             if n and not exact_kv:
                 p = np.exp(k[:n] @ q[t, h] * scale - (k[:n] @ q[t, h] * scale).max())
-                tol = tol + u * (p / p.sum()) @ np.abs(v[:n]) + big * (1 + 4 * scale * np.abs(q[t, h]).sum())
+                tol = tol + u * (p / p.sum()) @ np.abs(v[:n]) + big * (1 + 4 * abs(scale) * np.abs(q[t, h]).sum())
             err = np.abs(got[t, h] - o)
             assert np.isfinite(got[t, h]).all(), (s, t, h)
             assert (err <= tol).all(), (s, t, h, float((err / np.maximum(tol, 1e-30)).max()))
@@ -741,3 +741,115 @@ def test_two_captured_graphs_and_planned_layers(hp):
         assert hp.hp_latent_decode_planned(d, 512, q, b.q_ptr, b.T, 16, 0.07, o, ws, b.status) == 0
     torch.cuda.synchronize()
     assert b.status.item() == 0 and torch.equal(o1, want) and torch.equal(o2, single)
+
+
+# ------------------------------------------------------------ what the calls also allow
+@pytest.mark.parametrize("form", ["decode", "prefill"])
+def test_a_wait_that_runs_out_is_reported(hp, form):
+    """HP_TEST_STALL: the first load of each CTA is armed and never issued, so every role's waits
+    run out in turn; the call reports HP_ERR_TIMEOUT and the next one on the same context is
+    right."""
+    import torch
+    b = Latent(hp, A([300, 70]), A([2, 70]), 8, 512, 576, 16, "bf16", seed=4)
+    w = selecting_weights(8, 128, 128, 512, b.dt, 3)
+    q = b.queries(576 if form == "decode" else 192)
+    out = torch.zeros((b.T, 8, 512 if form == "decode" else 128), dtype=b.dt, device="cuda")
+    if form == "decode":
+        rc, n = hp.hp_latent_decode_workspace_bytes(b.desc, 512, b.T, 8)
+    else:
+        rc, n = hp.hp_latent_prefill_workspace_bytes(b.desc, 512, 128, 128, b.T, 8, 370)
+    ws, wd = torch.zeros(n, dtype=torch.uint8, device="cuda"), w.cuda()
+    for flags, name in ((hp.TEST_STALL, "HP_ERR_TIMEOUT"), (0, "HP_OK")):
+        b.desc.c.flags = flags
+        out.fill_(9)
+        if form == "decode":
+            rc = hp.hp_latent_decode(b.desc, 512, q, b.q_ptr, b.T, 8, 0.07, out, ws, b.status)
+        else:
+            rc = hp.hp_latent_prefill(b.desc, 512, wd, 128, 128, q, b.q_ptr, b.T, 8, 0.07, out, 370, ws, b.status)
+        torch.cuda.synchronize()
+        assert rc == 0 and hp.status_name(b.status.item()) == name
+    if form == "decode":
+        check_decode(b, host(out), 0.07)
+    else:
+        check_prefill(b, host(out), 128, 128, w, 0.07, exact_kv=True)
+
+
+def test_scales_of_any_sign(hp):
+    """A negative scale turns the order of the scores, a zero one weighs every seen token alike."""
+    for scale in (-0.09, 0.0):
+        for kernel in (0, hp.ATTN_CUDA_CORES):
+            b = Latent(hp, A([200, 3]), A([2, 3]), 16, 512, 576, 16, "bf16", seed=8, flags=kernel)
+            check_decode(b, run_decode(b, scale), scale)
+            w = selecting_weights(16, 128, 128, 512, b.dt, 6)
+            check_prefill(b, run_prefill(b, 128, 128, w, scale), 128, 128, w, scale, exact_kv=True)
+
+
+def test_masked_tokens_of_any_value_in_a_one_query_batch(hp):
+    """Slots past a length hold NaN in every test above; here infinities and the type's lowest
+    values, in the last page and in pages no sequence names."""
+    import torch
+    for fill in (float("inf"), float("-inf"), -65504.0):
+        b = Latent(hp, A([65, 1, 127]), A([1, 1, 1]), 16, 512, 576, 32, "f16", seed=12)
+        b.pool[torch.isnan(b.pool)] = fill
+        check_decode(b, run_decode(b, 0.07), 0.07)
+        b.nq = A([65, 1, 100])
+        b.q_ptr_host = np.concatenate([[0], np.cumsum(b.nq)])
+        b.q_ptr = index_tensor(b.q_ptr_host.astype(np.uint32), "cuda")
+        b.T = 166
+        w = selecting_weights(16, 128, 128, 512, b.dt, 6)
+        check_prefill(b, run_prefill(b, 128, 128, w, 0.07), 128, 128, w, 0.07, exact_kv=True)
+
+
+def test_pool_rows_past_32_bits(hp):
+    """A pool of more than 2^32 bytes: the last pages' rows, written by the append, read by both
+    forms."""
+    import torch
+    P, W = 64, 576
+    pages = (1 << 32) // (P * W * 2) + 40
+    pool = torch.zeros((pages, P, W), dtype=torch.bfloat16, device="cuda")
+    T, H = 100, 4
+    slot = (np.arange(T) + (pages - 2) * P).astype(np.int64)
+    g = torch.Generator().manual_seed(1)
+    kv = torch.randn((T, W), generator=g).to(torch.bfloat16)
+    rope = hp.rope_desc(cos_sin=dev(ref.cos_sin(10, 64)), sections=(32,),
+                        positions=torch.zeros((1, T), dtype=torch.int32, device="cuda"))
+    kd = kv.cuda()
+    d = hp.latent_desc(latent=kd[:, :512], k_rope=kd[:, 512:], dtype="bf16", slot_map=dev(slot),
+                       pool=pool, num_pages=pages, page_size=P)
+    st = status_tensor()
+    assert hp.hp_latent_append(d, rope, st) == 0
+    torch.cuda.synchronize()
+    assert st.item() == 0 and torch.equal(pool.view(-1, W)[-128:-28].cpu(), kv)
+    b = Latent(hp, A([T]), A([3]), H, 512, W, P, "bf16", seed=2)
+    b.rows = [kv.double().numpy()]
+    b.pool = pool
+    b.desc = hp.PagedDesc(pool, index_tensor(np.array([pages - 2, pages - 1], np.uint32), "cuda"),
+                          b.desc._keep[2], b.desc._keep[3], num_pages=pages, page_size=P, num_heads=1,
+                          head_dim=W, dtype="bf16", index_type=0)
+    for kernel in (0, hp.ATTN_CUDA_CORES):
+        b.desc.c.flags = kernel
+        check_decode(b, run_decode(b, 0.07), 0.07)
+    b.desc.c.flags = 0
+    w = selecting_weights(H, 128, 128, 512, b.dt, 6)
+    check_prefill(b, run_prefill(b, 128, 128, w, 0.07), 128, 128, w, 0.07, exact_kv=True)
+
+
+def test_two_batches_at_once_on_two_streams(hp):
+    """Calls on two streams, a workspace each, while a large one runs on the other."""
+    import torch
+    big = Latent(hp, np.full(64, 1500), np.ones(64, np.int64), 128, 512, 576, 64, "bf16", seed=1)
+    small = Latent(hp, A([90, 300]), A([1, 2]), 16, 512, 576, 16, "f16", seed=2)
+    runs = []
+    for b in (big, small):
+        q = b.queries(576)
+        rc, n = hp.hp_latent_decode_workspace_bytes(b.desc, 512, b.T, b.H)
+        runs.append((b, q, torch.zeros(n, dtype=torch.uint8, device="cuda"),
+                     torch.zeros((b.T, b.H, 512), dtype=b.dt, device="cuda"), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for b, q, ws, out, s in runs:
+            assert hp.hp_latent_decode(b.desc, 512, q, b.q_ptr, b.T, b.H, 0.07, out, ws, b.status, s) == 0
+    torch.cuda.synchronize()
+    for b, q, ws, out, s in runs:
+        assert b.status.item() == 0
+        check_decode(b, host(out), 0.07, rows={0, 1, 2, 40})
