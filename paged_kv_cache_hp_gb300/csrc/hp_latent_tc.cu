@@ -69,28 +69,53 @@ struct Segment {
     uint32_t rows;  // rows of the tile that exist, at least 1
 };
 
+// The segments of a worker's range in order; every role walks them, whole warps at a time.  The
+// first search takes 32 sums at a time, the rest go forward, and a segment's facts are loaded
+// together: three trips to memory to the first segment, one or two to each next.
 struct Walk {
     const LatentArgs& a;
     uint64_t pos, end;
     uint32_t tile;  // this CTA's tile within the group
+    uint64_t s, first, past;  // the current sequence and its units
+    __device__ Walk(const LatentArgs& args, uint64_t beg, uint64_t e, uint32_t t, unsigned lane)
+        : a(args), pos(beg), end(e), tile(t)
+    {
+        uint64_t lo = 0, hi = a.num_seqs;
+        while (hi - lo > 1) {  // the last sequence whose units start at or before beg
+            const uint64_t step = (hi - lo + 31) / 32, i = lo + lane * step;
+            const unsigned below = __ballot_sync(0xffffffffu, i < hi && a.units_off[i] <= beg);
+            lo += (uint64_t)(31 - __clz(below)) * step;
+            hi = umin(hi, lo + step);
+        }
+        s = lo;
+        first = a.units_off[s];
+        past = a.units_off[s + 1];
+    }
     __device__ bool next(Segment& g)
     {
         while (pos < end) {
-            g.s = find_seq(a.units_off, a.num_seqs, pos);
-            g.len = index_at(a.lens, a.idx64, g.s);
-            g.q0 = a.q_ptr ? index_at(a.q_ptr, a.idx64, g.s) : g.s;
-            g.n = (a.q_ptr ? index_at(a.q_ptr, a.idx64, g.s + 1) : g.s + 1) - g.q0;
+            while (pos >= past) {  // sequences without units are passed over
+                ++s;
+                first = past;
+                past = a.units_off[s + 1];
+            }
+            g.s = s;
+            g.len = index_at(a.lens, a.idx64, s);
+            g.q0 = a.q_ptr ? index_at(a.q_ptr, a.idx64, s) : s;
+            g.n = (a.q_ptr ? index_at(a.q_ptr, a.idx64, s + 1) : s + 1) - g.q0;
             g.steps = (g.len + kTok - 1) / kTok;
-            const uint64_t off = pos - a.units_off[g.s], grp = off / g.steps;
-            g.ustart = a.units_off[g.s] + grp * g.steps;
-            g.k0 = off % g.steps;
+            const uint64_t off = pos - first;
+            // (the usual group is the sequence's only one)
+            const uint64_t grp = off < g.steps ? 0 : off / g.steps;
+            g.ustart = first + grp * g.steps;
+            g.k0 = off - grp * g.steps;
             g.k1 = umin(g.steps, g.k0 + (end - pos));
             pos += g.k1 - g.k0;
             g.r0 = grp * a.group_rows + tile * kRows;
             const uint64_t all = g.n * a.H;
             if (g.r0 >= all) continue;  // the group's last tile may have no rows
             g.rows = (uint32_t)umin(kRows, all - g.r0);
-            const uint64_t last = (g.r0 + g.rows - 1) / a.H;  // the tile's last query sees most
+            const uint64_t last = (uint32_t)(g.r0 + g.rows - 1) / a.H;  // the tile's last query sees most
             const uint64_t seen = g.len + 1 + last > g.n ? g.len + 1 + last - g.n : 0;
             g.k1 = umin(g.k1, (seen + kTok - 1) / kTok);
             return true;
@@ -131,20 +156,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (a.hdr->verdict != kVerdictOk) return;
     const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     T* out = static_cast<T*>(a.out);
-    // queries of a sequence without tokens: zeros
-    for (uint64_t s = (uint64_t)blockIdx.x * 8 + warp; s < a.num_seqs; s += (uint64_t)gridDim.x * 8)
-        if (a.units_off[s] == a.units_off[s + 1]) {
-            const uint64_t q0 = a.q_ptr ? index_at(a.q_ptr, a.idx64, s) : s;
-            const uint64_t q1 = a.q_ptr ? index_at(a.q_ptr, a.idx64, s + 1) : s + 1;
-            uint4* o = reinterpret_cast<uint4*>(out);
-            for (uint64_t i = q0 * a.H * (kR / 8) + lane; i < q1 * a.H * (kR / 8); i += 32)
-                o[i] = make_uint4(0, 0, 0, 0);
+    // queries of sequences without tokens: zeros, 32 sequences to a warp at a time
+    auto zero_empty = [&](uint64_t w, uint64_t warps) {
+        for (uint64_t k = w;; k += warps) {  // the CTA's k-th 32 sequences, whichever warps share them
+            const uint64_t s0 = (blockIdx.x + k * gridDim.x) * 32, s = s0 + lane;
+            if (s0 >= a.num_seqs) break;
+            unsigned empty = __ballot_sync(0xffffffffu, s < a.num_seqs && a.units_off[s] == a.units_off[s + 1]);
+            for (; empty; empty &= empty - 1) {
+                const uint64_t e = s0 + __ffs(empty) - 1;
+                const uint64_t q0 = a.q_ptr ? index_at(a.q_ptr, a.idx64, e) : e;
+                const uint64_t q1 = a.q_ptr ? index_at(a.q_ptr, a.idx64, e + 1) : e + 1;
+                uint4* o = reinterpret_cast<uint4*>(out);
+                for (uint64_t i = q0 * a.H * (kR / 8) + lane; i < q1 * a.H * (kR / 8); i += 32)
+                    o[i] = make_uint4(0, 0, 0, 0);
+            }
         }
+    };
     const uint32_t tiles = a.group_rows / kRows;
     const uint64_t total = a.hdr->total_units, Lw = (total + a.workers - 1) / a.workers;
     const uint64_t v = blockIdx.x / tiles, beg = umin(v * Lw, total), end = umin(beg + Lw, total);
     if (threadIdx.x == 96 && blockIdx.x % tiles == 0) write_merge(a, v);  // (a softmax thread, idle yet)
-    if (beg >= end) return;  // the whole CTA, before any barrier or TMEM
+    if (beg >= end) {  // the whole CTA, before any barrier or TMEM
+        zero_empty(warp, 8);
+        return;
+    }
 
     const uint32_t sm0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char* smem = smem_raw + (sm0 - smem_u32(smem_raw));
@@ -171,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_base;
-    Walk walk{a, beg, end, (uint32_t)(blockIdx.x % tiles)};
+    Walk walk(a, beg, end, (uint32_t)(blockIdx.x % tiles), lane);
     Segment g;
     // true unless the wait ran out or another role stopped; warp_wait for whole warps
     auto wait_for = [&](unsigned long long* bar, uint32_t parity) {
@@ -236,18 +271,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 7) {
         // ------------------------------------------------------------- queries of each tile
-        if (lane == 0) {
-            uint64_t seg = 0;
-            while (walk.next(g)) {
-                if (g.k0 >= g.k1) continue;
-                if (seg && !wait_for(&q_free, (uint32_t)((seg - 1) & 1))) break;
-                mbar_expect_tx(smem_u32(&q_full), kChunks * kChunk);
-                for (uint32_t c = 0; c < kChunks; ++c)
-                    tma_2d(sm0 + c * kChunk, &tmq, (int)(c * 64), (int)(g.q0 * a.H + g.r0), smem_u32(&q_full));
-                ++seg;
-            }
-            if (seg) mbar_wait(smem_u32(&q_full), (uint32_t)((seg - 1) & 1));
+        uint64_t seg = 0;
+        while (walk.next(g)) {
+            if (g.k0 >= g.k1) continue;
+            if (seg && !warp_wait(&q_free, (uint32_t)((seg - 1) & 1))) break;
+            if (lane == 0) mbar_expect_tx(smem_u32(&q_full), kChunks * kChunk);
+            __syncwarp();
+            if (lane < kChunks)
+                tma_2d(sm0 + lane * kChunk, &tmq, (int)(lane * 64), (int)(g.q0 * a.H + g.r0), smem_u32(&q_full));
+            ++seg;
         }
+        zero_empty(0, 1);
+        if (seg) mbar_wait(smem_u32(&q_full), (uint32_t)((seg - 1) & 1));
         __syncwarp();
     } else if (warp == 1) {
         // -------------------------------------------------------------------- S = Q . C^T

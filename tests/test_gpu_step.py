@@ -435,6 +435,15 @@ def test_latent_decode_long_cache(hp, kernel):
     check_decode(b, got, 0.07, rows={0, 7, 150, 299})
 
 
+def test_latent_decode_many_empty_sequences(hp):
+    """3000 sequences, most of them empty: every query of an empty one gets zeros, whichever CTAs
+    have work of their own."""
+    lens = np.where(np.random.default_rng(5).random(3000) < 0.01, 70, 0)
+    for nq in (np.ones(3000, np.int64), np.random.default_rng(6).integers(0, 3, 3000)):
+        b = Latent(hp, lens, nq, 4, 512, 576, 16, "bf16", seed=7)
+        check_decode(b, run_decode(b, 0.07), 0.07)
+
+
 def test_latent_decode_verdicts(hp):
     import torch
     for what, name in (("page", "PAGE_ID"), ("len", "LEN"), ("qstart", "NEW_PTR_START"),
