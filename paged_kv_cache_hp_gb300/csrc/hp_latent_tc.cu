@@ -16,7 +16,7 @@
 // that eight rows are one swizzle atom for every chunk and the operands' 8-row groups lie 9 KiB
 // apart whatever the page size (a multiple of 8).  Eight boxes a step: issuing a box takes the
 // loader about 100 cycles, and boxes of one chunk (36 a step on 16-slot pages) held it to 4,400
-// a step.  Slots of two boxes go back to the loader as the products of their 16 tokens end.
+// a step.  Slots of four boxes go back to the loader as the products of their 32 tokens end.
 //
 // Shared memory: Q 72 KiB, two steps of C 144 KiB, P (weights rounded to the element type)
 // 8 KiB.  TMEM: O^T 256 columns, S 2 x 64.  Roles: warp 0 loads C, warp 7 the queries, warp 1
@@ -52,9 +52,9 @@ constexpr uint32_t kTok = kLatentStep;         // tokens of a step
 constexpr uint32_t kChunks = kW / 64;
 constexpr uint32_t kChunk = 64 * 128;          // 64 rows x 64 dims
 constexpr uint32_t kGroup = kChunks * 1024;    // 8 tokens
-constexpr uint32_t kSlots = 8;                 // of two groups each: two steps
+constexpr uint32_t kSlots = 4;                 // of four groups each: two steps
 constexpr uint32_t kOffC = kChunks * kChunk;   // Q first, then the slots, then P
-constexpr uint32_t kOffP = kOffC + kSlots * 2 * kGroup;
+constexpr uint32_t kOffP = kOffC + kSlots * 4 * kGroup;
 constexpr uint32_t kSmem = kOffP + kRows * 128 + 1024;
 constexpr uint32_t kOCol = 0, kSCol = 256;     // TMEM columns
 constexpr uint32_t kTmemCols = 512;
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < kSlots; ++i) mbar_init(smem_u32(&c_free[i]), 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&c_full[i]), 4);  // a step's four slots
+            mbar_init(smem_u32(&c_full[i]), 2);  // a step's two slots
             mbar_init(smem_u32(&s_full[i]), 1);
             mbar_init(smem_u32(&s_free[i]), kSoftmax);
             mbar_init(smem_u32(&p_full[i]), kSoftmax);
@@ -200,6 +200,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         abort_flag = 0;
         fail_s[0] = fail_s[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (threadIdx.x == 0) {
+        prefetch_map(&tmc);
+        prefetch_map(&tmq);
     }
     if (warp == 1) tmem_alloc(smem_u32(&tmem_base), kTmemCols);
     fence_before();
@@ -228,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t tab0 = index_at(a.seq_ptr, a.idx64, g.s);
             // The slice's entries 64 at a time, two per lane, the next 32 on their way before they
             // are needed: a lookup is a shuffle (a load per step cost 1,500 cycles of it).
-            const uint64_t npages = (g.len + P - 1) / P;
+            const uint64_t npages = g.len ? div_groups(a, (g.len - 1) / 8) + 1 : 0;
             auto entries = [&](uint64_t i) {
                 return i + lane < npages ? index_at(a.table, a.idx64, tab0 + i + lane) : 0ull;
             };
@@ -247,26 +251,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const unsigned long long e1 = __shfl_sync(0xffffffffu, nxt, (int)(rel & 31));
                 const int row = (int)((rel < 32 ? e0 : e1) * P + (gi * 8 - page * P));
                 const uint32_t live = (uint32_t)umin(8, (g.len - k * kTok + 7) / 8);  // groups with a token
-                for (uint32_t p = 0; p < 4; ++p) {
-                    const uint64_t c = 4 * j + p;
-                    const uint32_t sl = (uint32_t)(c % kSlots), n = live > 2 * p ? (live > 2 * p + 1 ? 2 : 1) : 0;
+                for (uint32_t p = 0; p < 2; ++p) {
+                    const uint64_t c = 2 * j + p;
+                    const uint32_t sl = (uint32_t)(c % kSlots), n = live > 4 * p ? (uint32_t)umin(4, live - 4 * p) : 0;
                     if (c >= kSlots) ok = warp_wait(&c_free[sl], (uint32_t)((c / kSlots - 1) & 1));
                     if (!ok) break;
                     const uint32_t bar = smem_u32(&c_full[j % 2]);
                     if (lane == 0) mbar_expect_tx(bar, n * kGroup);
                     armed = c + 1;
                     __syncwarp();
-                    if (lane >> 1 == p && (lane & 1) < n && !(a.test_stall && c == 0))
-                        tma_3d(sm0 + kOffC + (sl * 2 + (lane & 1)) * kGroup, &tmc, 0, row, 0, bar);
+                    if (lane >> 2 == p && (lane & 3) < n && !(a.test_stall && c == 0))
+                        tma_3d(sm0 + kOffC + (sl * 4 + (lane & 3)) * kGroup, &tmc, 0, row, 0, bar);
                 }
             }
         }
         // the last loads land before the shared memory goes (a step that a wait cut short arrives for
-        // its missing slots here, so that its barrier's phase can end)
-        for (; armed % 4; ++armed)
-            if (lane == 0) mbar_arrive(smem_u32(&c_full[armed / 4 % 2]));
+        // its missing slot here, so that its barrier's phase can end)
+        for (; armed % 2; ++armed)
+            if (lane == 0) mbar_arrive(smem_u32(&c_full[armed / 2 % 2]));
         __syncwarp();
-        for (uint64_t x = armed / 4 > 2 ? armed / 4 - 2 : 0; x < armed / 4; ++x)
+        for (uint64_t x = armed / 2 > 2 ? armed / 2 - 2 : 0; x < armed / 2; ++x)
             mbar_wait(smem_u32(&c_full[x % 2]), (uint32_t)((x / 2) & 1));
         __syncwarp();
     } else if (warp == 7) {
@@ -335,12 +339,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t vd = vd0 + ((half * 8 * kGroup) >> 4);
                 if (elect_one()) {
 #pragma unroll
-                    for (uint32_t kk = 0; kk < 4; ++kk) {  // 16 tokens, a slot
+                    for (uint32_t kk = 0; kk < 4; ++kk) {  // 16 tokens, half a slot
 #pragma unroll
                         for (uint32_t m = 0; m < 4; ++m)   // 128 dims
                             mma_f16(tmem + kOCol + m * kRows, vd + ((kk * 2 * kGroup + m * 2048) >> 4), pd + kk * 2,
                                     id_o, acc | kk);
-                        mma_commit(smem_u32(&c_free[half * 4 + kk]));
+                        if (kk & 1) mma_commit(smem_u32(&c_free[half * 2 + kk / 2]));
                     }
                     mma_commit(smem_u32(&o_done[half]));
                 }

@@ -223,6 +223,11 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int
         : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // TMEM columns for the CTA (one warp allocates, later frees); the base goes to *where
 __device__ __forceinline__ void tmem_alloc(uint32_t where, uint32_t cols)
 {
