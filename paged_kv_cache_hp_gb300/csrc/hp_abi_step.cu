@@ -25,7 +25,7 @@ int reset_status(int* d_status, void* stream)
 
 u64 step_ws_bytes(u64 num_seqs)
 {
-    return hp::kWsHeaderBytes + 2 * hp::round_up_256(8 * (num_seqs + 1));
+    return hp::kWsHeaderBytes + 2 * hp::round_up_256(8 * (num_seqs + 1)) + 3 * 8 * hp::kStepBlocks;
 }
 
 }  // namespace
@@ -66,6 +66,7 @@ HP_API int hp_step_tables(const hp_step_desc* step, void* workspace, uint64_t wo
     hp::StepArgs a{};
     a.d = d;
     a.ws = hp::ws_view(workspace, d.num_seqs);
+    a.blocks = a.ws.units_off + hp::round_up_256(8 * (d.num_seqs + 1)) / 8;
     a.div_ok = d.page_size <= (1ull << 31);
     if (a.div_ok) hp::invariant_divisor(d.page_size, &a.div_m, &a.div_l);
     a.d_status = d_status;

@@ -3,14 +3,16 @@
 // need_s = max(have_s, ceil((len_s + new_s) / P)); the grown slices lie at the exclusive prefix
 // sums of need, the new tokens at those of new, and sequence s takes its new pages from the
 // free list at prefix(need) - prefix(have), the latter being seq_ptr itself.  Every output is
-// then a function of one entry or token index and these sums: a scan by one CTA (four
-// sequences per thread), which also applies every rule, and a fill that writes nothing when a
-// rule failed and finds an entry's or token's sequence by a binary search of the sums.
+// then a function of one entry or token index and these sums, whose sequence a binary search
+// finds.  Bytes bound it for a large step, latency for a small one.
 //
 // A step of up to kFusedSeqs sequences and kFusedItems entries and tokens runs as one CTA with
 // the sums in shared memory: one launch, and searches of 30 cycles a step instead of the L2's
-// hundreds.  A larger one spreads its fill over the GPU, 1024 entries or tokens per CTA, each CTA
-// searching the stretch of sums that its own entries meet, copied to shared memory when it fits.
+// hundreds.  A larger one takes two kernels.  The scan's CTAs (up to kMaxBlocks, 1,024 sequences
+// each, more where the sequences are more) leave sums local to their sequences, their totals and
+// the first rule that failed; every CTA of the fill adds the totals up again (a load and a scan of
+// at most 256 numbers), so nothing waits for a CTA, and writes nothing when a rule failed.  One
+// CTA scanning 4,096 sequences took 12.6 us of a step's 24.
 #include <cuda_runtime.h>
 
 #include "hp_internal.cuh"
@@ -22,98 +24,83 @@ namespace hp {
 namespace {
 
 constexpr unsigned long long kMaxTokens = 1ull << 58;
-constexpr int kPer = 4;                    // sequences per thread and chunk of the scan
 constexpr uint32_t kFusedSeqs = 1024;
 constexpr uint64_t kFusedItems = 16384;
-constexpr uint32_t kStretch = 1536;        // sums a fill CTA keeps in shared memory
-constexpr uint32_t kFillItems = 1024;      // entries or tokens of a fill CTA
+constexpr uint32_t kStretch = 2560;        // sums a fill CTA keeps in shared memory
+constexpr uint32_t kFillItems = 2048;      // entries or tokens of a fill CTA
+constexpr uint32_t kMaxBlocks = kStepBlocks;
 
 __device__ __forceinline__ unsigned long long page_of(const StepArgs& a, unsigned long long x)
 {
     return a.div_ok && x < (1ull << 32) ? div_invariant((uint32_t)x, a.div_m, a.div_l) : x / a.d.page_size;
 }
 
-// Prefix sums of the new tokens (tok) and pages, entries 0 .. S, and the verdict: one CTA of
-// kPlanThreads.  KEEP: the inputs seq_ptr and seq_lens are left in sp_copy and len_copy.
+struct Sums {
+    unsigned long long tok, pages, key;  // totals, and the verdict key of the sequences' own rules
+};
+
+// Exclusive prefix sums of the new tokens and pages over sequences s0 .. s1 - 1, at tok[s - s0] and
+// pages[s - s0]; a CTA of kPlanThreads, the result the same in every thread.  KEEP: seq_ptr and
+// seq_lens are left in sp_copy and len_copy.
 template <typename IndexT, bool KEEP, typename SumT>
-__device__ unsigned long long scan_step(const StepArgs& a, SumT* tok, SumT* pages, SumT* sp_copy = nullptr,
-                                        unsigned long long* len_copy = nullptr)
+__device__ Sums scan_range(const StepArgs& a, uint64_t s0, uint64_t s1, SumT* tok, SumT* pages,
+                           SumT* sp_copy = nullptr, unsigned long long* len_copy = nullptr)
 {
-    const hp_step_desc& d = a.d;
-    const IndexT* sp = static_cast<const IndexT*>(d.seq_ptr);
-    const IndexT* lens = static_cast<const IndexT*>(d.seq_lens);
-    const IndexT* nw = static_cast<const IndexT*>(d.new_lens);
-    const uint64_t S = d.num_seqs;
+    const IndexT* sp = static_cast<const IndexT*>(a.d.seq_ptr);
+    const IndexT* lens = static_cast<const IndexT*>(a.d.seq_lens);
+    const IndexT* nw = static_cast<const IndexT*>(a.d.new_lens);
     const unsigned long long most = sizeof(IndexT) == 4 ? 0xFFFFFFFFull : kMaxTokens;
     __shared__ unsigned long long s_key;
     if (threadIdx.x == 0) s_key = kVerdictOk;
     __syncthreads();
-    const unsigned long long sp_first = sp[0], sp_last = sp[S];
-    unsigned long long ct = 0, cp = 0;  // sums before this chunk, the same in every thread
-    for (uint64_t base = 0; base < S; base += kPlanThreads * kPer) {
-        const uint64_t s0 = base + threadIdx.x * kPer;
-        unsigned long long t[kPer], p[kPer], st = 0, sg = 0;
-        unsigned long long lo[kPer + 1], len[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) t[i] = p[i] = len[i] = lo[i] = 0;
-        if (base + (threadIdx.x & ~31u) * kPer < S) {  // warps past the last sequence only scan
-#pragma unroll
-            for (int i = 0; i <= kPer; ++i) lo[i] = s0 + i <= S ? (unsigned long long)sp[s0 + i] : 0;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                len[i] = s0 + i < S ? (unsigned long long)lens[s0 + i] : 0;
-                t[i] = s0 + i < S ? (unsigned long long)nw[s0 + i] : 0;
+    unsigned long long ct = 0, cp = 0;  // sums before this round
+    for (uint64_t base = s0; base < s1; base += kPlanThreads) {
+        const uint64_t s = base + threadIdx.x;
+        unsigned long long t = 0, p = 0;
+        if (s < s1) {
+            const unsigned long long lo = sp[s], hi = sp[s + 1], len = lens[s];
+            t = nw[s];
+            const unsigned long long end = len + t, have = hi - lo;
+            if (lo > hi) {
+                atomicMin(&s_key, verdict_key(kRankSeqPtrOrder, s));
+            } else if (end < len || end > most || (len && page_of(a, len - 1) >= have)) {
+                atomicMin(&s_key, verdict_key(kRankLen, s));
+            } else {
+                const unsigned long long want = end ? page_of(a, end - 1) + 1 : 0;
+                p = want > have ? want : have;
             }
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                if (s0 + i < S) {
-                    const unsigned long long end = len[i] + t[i], have = lo[i + 1] - lo[i];
-                    if (lo[i] > lo[i + 1]) {
-                        atomicMin(&s_key, verdict_key(kRankSeqPtrOrder, s0 + i));
-                    } else if (end < len[i] || end > most || (len[i] && page_of(a, len[i] - 1) >= have)) {
-                        atomicMin(&s_key, verdict_key(kRankLen, s0 + i));
-                    } else {
-                        const unsigned long long want = end ? page_of(a, end - 1) + 1 : 0;
-                        p[i] = want > have ? want : have;
-                    }
-                }
-                st = sat_add(st, t[i]);
-                sg = sat_add(sg, p[i]);
+            if (KEEP) {
+                sp_copy[s - s0] = (SumT)lo;
+                len_copy[s - s0] = len;
             }
         }
         unsigned long long ex_t, ex_p, tot_t, tot_p;
-        block_scan2(st, sg, ex_t, ex_p, tot_t, tot_p);
-        ex_t = sat_add(ct, ex_t);
-        ex_p = sat_add(cp, ex_p);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (s0 + i < S) {
-                tok[s0 + i] = (SumT)ex_t;
-                pages[s0 + i] = (SumT)ex_p;
-                if (KEEP) {
-                    sp_copy[s0 + i] = (SumT)lo[i];
-                    len_copy[s0 + i] = len[i];
-                }
-                ex_t = sat_add(ex_t, t[i]);
-                ex_p = sat_add(ex_p, p[i]);
-            }
+        block_scan2(t, p, ex_t, ex_p, tot_t, tot_p);
+        if (s < s1) {
+            tok[s - s0] = (SumT)sat_add(ct, ex_t);
+            pages[s - s0] = (SumT)sat_add(cp, ex_p);
+        }
         ct = sat_add(ct, tot_t);
         cp = sat_add(cp, tot_p);
     }
     __syncthreads();
-    unsigned long long key = s_key;
+    return Sums{ct, cp, s_key};
+}
+
+// The verdict of the step, given all the sums and the ends of seq_ptr.
+template <typename IndexT>
+__device__ __forceinline__ unsigned long long verdict(const hp_step_desc& d, const Sums& all,
+                                                      unsigned long long sp_first, unsigned long long sp_last)
+{
+    const unsigned long long most = sizeof(IndexT) == 4 ? 0xFFFFFFFFull : kMaxTokens;
+    unsigned long long key = all.key;
     if (sp_first != 0) key = min(key, verdict_key(kRankSeqPtrStart, 0));
-    if (sp_last != d.table_len) key = min(key, verdict_key(kRankSeqPtrEnd, S));
+    if (sp_last != d.table_len) key = min(key, verdict_key(kRankSeqPtrEnd, d.num_seqs));
     // (with the rules above satisfied, the slices add up to table_len)
-    if (cp > d.table_len && cp - d.table_len > d.num_free) key = min(key, verdict_key(kRankCapacity, 0));
-    if (cp > d.table_cap || ct > d.token_cap || cp > most || ct > most)
+    if (all.pages > d.table_len && all.pages - d.table_len > d.num_free)
+        key = min(key, verdict_key(kRankCapacity, 0));
+    if (all.pages > d.table_cap || all.tok > d.token_cap || all.pages > most || all.tok > most)
         key = min(key, verdict_key(kRankOutSize, 0));
-    if (threadIdx.x == 0) {
-        tok[S] = (SumT)ct;
-        pages[S] = (SumT)cp;
-        if (KEEP) sp_copy[S] = (SumT)sp_last;
-        if (a.d_status) *a.d_status = key_status(key);
-    }
     return key;
 }
 
@@ -129,13 +116,14 @@ __device__ __forceinline__ Int find_in(const SumT* sums, Int lo, Int hi, SumT u)
     return lo;
 }
 
-// The same by a whole warp, 32 sums at a time: 3 loads deep for 32,768 sequences.
-__device__ __forceinline__ uint64_t find_wide(const unsigned long long* sums, uint64_t hi, uint64_t u, unsigned lane)
+// The same by a whole warp over sums(0) .. sums(hi - 1), 32 at a time: 3 loads deep for 32,768.
+template <typename F>
+__device__ __forceinline__ uint64_t find_wide(F sums, uint64_t hi, uint64_t u, unsigned lane)
 {
     uint64_t lo = 0;
     while (hi - lo > 1) {
         const uint64_t step = (hi - lo + 31) / 32, i = lo + lane * step;
-        const unsigned below = __ballot_sync(0xffffffffu, i < hi && sums[i] <= u);
+        const unsigned below = __ballot_sync(0xffffffffu, i < hi && sums(i) <= u);
         lo += (uint64_t)(31 - __clz(below)) * step;  // lane 0's sum is not above u
         hi = umin(hi, lo + step);
     }
@@ -192,9 +180,19 @@ __global__ void __launch_bounds__(kPlanThreads) step_fused_kernel(const StepArgs
     // (sums of at most kFusedItems once the rules hold: 32 bits)
     __shared__ uint32_t tok[kFusedSeqs + 1], pages[kFusedSeqs + 1], sp[kFusedSeqs + 1];
     __shared__ unsigned long long len[kFusedSeqs + 1];
-    if (scan_step<IndexT, true, uint32_t>(a, tok, pages, sp, len) != kVerdictOk) return;  // the same in every thread
-    __syncthreads();
     const hp_step_desc& d = a.d;
+    const unsigned long long sp_first = static_cast<const IndexT*>(d.seq_ptr)[0];
+    const unsigned long long sp_last = static_cast<const IndexT*>(d.seq_ptr)[d.num_seqs];
+    const Sums all = scan_range<IndexT, true, uint32_t>(a, 0, d.num_seqs, tok, pages, sp, len);
+    const unsigned long long key = verdict<IndexT>(d, all, sp_first, sp_last);
+    if (threadIdx.x == 0 && a.d_status) *a.d_status = key_status(key);
+    if (key != kVerdictOk) return;  // the same in every thread
+    if (threadIdx.x == 0) {
+        tok[d.num_seqs] = (uint32_t)all.tok;
+        pages[d.num_seqs] = (uint32_t)all.pages;
+        sp[d.num_seqs] = (uint32_t)sp_last;
+    }
+    __syncthreads();
     const uint32_t S = (uint32_t)d.num_seqs, cap = (uint32_t)d.token_cap;
     const uint32_t tokens = tok[S], entries = pages[S];
     for (uint32_t s = threadIdx.x; s <= S; s += kPlanThreads) put_sequence<IndexT>(d, s, tok[s], pages[s]);
@@ -217,52 +215,102 @@ template <typename IndexT>
 __global__ void __launch_bounds__(kPlanThreads) step_scan_kernel(const StepArgs a)
 {
     pdl_trigger();
-    const unsigned long long key = scan_step<IndexT, false, unsigned long long>(a, a.ws.rows_off, a.ws.units_off);
-    if (threadIdx.x == 0) a.ws.hdr->verdict = key;
+    const uint64_t s0 = (uint64_t)blockIdx.x << a.block_log, s1 = umin(s0 + (1ull << a.block_log), a.d.num_seqs);
+    const Sums r = scan_range<IndexT, false, unsigned long long>(a, s0, s1, a.ws.rows_off + s0, a.ws.units_off + s0);
+    if (threadIdx.x == 0) {
+        a.blocks[blockIdx.x] = r.tok;
+        a.blocks[kMaxBlocks + blockIdx.x] = r.pages;
+        a.blocks[2 * kMaxBlocks + blockIdx.x] = r.key;
+    }
 }
 
-// CTA b of the first entry_ctas takes table entries, the others tokens and sequences.
+// CTA b of the first entry_ctas takes table entries, the next token_ctas tokens, the others
+// sequences.
 template <typename IndexT>
-__global__ void __launch_bounds__(256) step_fill_kernel(const StepArgs a, uint64_t entry_ctas, uint64_t token_ctas)
+__global__ void __launch_bounds__(256) step_fill_kernel(const StepArgs a, uint32_t blocks, uint64_t entry_ctas,
+                                                        uint64_t token_ctas)
 {
     __shared__ uint32_t part[kStretch + 1];
     __shared__ uint64_t s_lo, s_hi;
-    pdl_wait();
-    if (a.ws.hdr->verdict != kVerdictOk) return;
+    __shared__ unsigned long long tok0[kMaxBlocks + 1], pages0[kMaxBlocks + 1], w_tok[8], w_pages[8], w_key[8];
     const hp_step_desc& d = a.d;
     const IndexT* sp = static_cast<const IndexT*>(d.seq_ptr);
     const IndexT* lens = static_cast<const IndexT*>(d.seq_lens);
     const uint64_t S = d.num_seqs;
+    const unsigned lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_wait();
+    // the sums before each block of sequences, the totals and the verdict: a block per thread
+    const unsigned long long sp_first = sp[0], sp_last = sp[S];
+    const bool mine = threadIdx.x < blocks;
+    const unsigned long long bt = mine ? a.blocks[threadIdx.x] : 0;
+    const unsigned long long bp = mine ? a.blocks[kMaxBlocks + threadIdx.x] : 0;
+    unsigned long long it = bt, ip = bp, key = mine ? a.blocks[2 * kMaxBlocks + threadIdx.x] : kVerdictOk;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long nt = __shfl_up_sync(0xffffffffu, it, o), np = __shfl_up_sync(0xffffffffu, ip, o);
+        if (lane >= (unsigned)o) {
+            it = sat_add(nt, it);
+            ip = sat_add(np, ip);
+        }
+        key = min(key, __shfl_xor_sync(0xffffffffu, key, o));
+    }
+    if (lane == 31) {
+        w_tok[warp] = it;
+        w_pages[warp] = ip;
+        w_key[warp] = key;
+    }
+    __syncthreads();
+    Sums all{0, 0, kVerdictOk};
+    unsigned long long ct = 0, cp = 0;  // sums of the warps before this one
+#pragma unroll
+    for (unsigned w = 0; w < 8; ++w) {
+        if (w == warp) {
+            ct = all.tok;
+            cp = all.pages;
+        }
+        all.tok = sat_add(all.tok, w_tok[w]);
+        all.pages = sat_add(all.pages, w_pages[w]);
+        all.key = min(all.key, w_key[w]);
+    }
+    if (mine) {  // (nothing saturates once the rules hold)
+        tok0[threadIdx.x] = ct + it - bt;
+        pages0[threadIdx.x] = cp + ip - bp;
+    }
+    __syncthreads();
+    key = verdict<IndexT>(d, all, sp_first, sp_last);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && a.d_status) *a.d_status = key_status(key);
+    if (key != kVerdictOk) return;  // the same in every thread
+    auto tok_at = [&](uint64_t s) { return s < S ? tok0[s >> a.block_log] + a.ws.rows_off[s] : all.tok; };
+    auto pages_at = [&](uint64_t s) { return s < S ? pages0[s >> a.block_log] + a.ws.units_off[s] : all.pages; };
     if (blockIdx.x >= entry_ctas + token_ctas) {
         const uint64_t s = (blockIdx.x - entry_ctas - token_ctas) * 256ull + threadIdx.x;
-        if (s <= S) put_sequence<IndexT>(d, s, a.ws.rows_off[s], a.ws.units_off[s]);
+        if (s <= S) put_sequence<IndexT>(d, s, tok_at(s), pages_at(s));
         return;
     }
     const bool entries = blockIdx.x < entry_ctas;
-    const unsigned long long* sums = entries ? a.ws.units_off : a.ws.rows_off;
-    const unsigned long long total = sums[S];
+    auto sums = [&](uint64_t s) { return entries ? pages_at(s) : tok_at(s); };
+    const unsigned long long total = entries ? all.pages : all.tok;
     const uint64_t u0 = (entries ? blockIdx.x : blockIdx.x - entry_ctas) * (uint64_t)kFillItems;
     const uint64_t u1 = umin(u0 + kFillItems, total);
-    const unsigned lane = threadIdx.x & 31;
     if (u0 < u1) {  // the same in every thread
-        if (threadIdx.x < 32) {
+        if (warp == 0) {
             const uint64_t s = find_wide(sums, S, u0, lane);
             if (lane == 0) s_lo = s;
-        } else if (threadIdx.x < 64) {
+        } else if (warp == 1) {
             const uint64_t s = find_wide(sums, S, u1 - 1, lane);
             if (lane == 0) s_hi = s + 1;
         }
         __syncthreads();
     }
     const uint64_t lo = u0 < u1 ? s_lo : 0, hi = u0 < u1 ? s_hi : 0;
-    const unsigned long long first_sum = u0 < u1 ? sums[lo] : 0;
+    const unsigned long long first_sum = u0 < u1 ? sums(lo) : 0;
     const bool near = hi - lo <= kStretch;
     if (near && u0 < u1) {  // the sums relative to u0; that of lo, which may lie before it, apart
         for (uint32_t i = threadIdx.x; i <= (uint32_t)(hi - lo); i += 256)
-            part[i] = i == 0 ? 0u : (uint32_t)umin(sums[lo + i] - u0, 1u << 30);
+            part[i] = i == 0 ? 0u : (uint32_t)umin(sums(lo + i) - u0, 1u << 30);
         __syncthreads();
     }
-#pragma unroll
+#pragma unroll 4
     for (uint32_t i = 0; i < kFillItems; i += 256) {
         const uint32_t x = i + threadIdx.x;
         const uint64_t u = u0 + x;
@@ -276,14 +324,20 @@ __global__ void __launch_bounds__(256) step_fill_kernel(const StepArgs a, uint64
             s = lo + r;
             off = r == 0 ? u - first_sum : x - part[r];
         } else {
-            s = find_in(sums, lo, hi, (unsigned long long)u);
-            off = u - sums[s];
+            uint64_t l = lo, h = hi;
+            while (h - l > 1) {
+                const uint64_t mid = (l + h) >> 1;
+                if (sums(mid) <= u) l = mid;
+                else h = mid;
+            }
+            s = l;
+            off = u - sums(s);
         }
         const unsigned long long first = sp[s], have = sp[s + 1] - first;
         if (entries)
             static_cast<IndexT*>(d.table_out)[u] = page_entry<IndexT>(d, first, have, u - off, off);
         else
-            put_token<IndexT>(a, u, lens[s] + off, first, have, a.ws.units_off[s]);
+            put_token<IndexT>(a, u, lens[s] + off, first, have, pages_at(s));
     }
 }
 
@@ -298,9 +352,13 @@ int launch_t(const StepArgs& a, cudaStream_t st)
     const uint64_t ec = (d.table_cap + kFillItems - 1) / kFillItems, tc = (d.token_cap + kFillItems - 1) / kFillItems;
     const uint64_t grid = ec + tc + d.num_seqs / 256 + 1;
     if (grid >= (1ull << 31)) return HP_ERR_OVERFLOW;
-    step_scan_kernel<IndexT><<<1, kPlanThreads, 0, st>>>(a);
+    StepArgs b = a;
+    b.block_log = 10;
+    while ((d.num_seqs >> b.block_log) >= kMaxBlocks) ++b.block_log;
+    const unsigned blocks = (unsigned)(d.num_seqs >> b.block_log) + 1;
+    step_scan_kernel<IndexT><<<blocks, kPlanThreads, 0, st>>>(b);
     if (cudaGetLastError() != cudaSuccess) return HP_ERR_CUDA;
-    return launch_dependent(step_fill_kernel<IndexT>, (unsigned)grid, 256, 0, st, a, ec, tc) == cudaSuccess
+    return launch_dependent(step_fill_kernel<IndexT>, (unsigned)grid, 256, 0, st, b, blocks, ec, tc) == cudaSuccess
                ? HP_OK
                : HP_ERR_CUDA;
 }

@@ -8,9 +8,13 @@
 
 namespace hp {
 
+constexpr uint32_t kStepBlocks = 256;  // blocks of sequences whose sums are local
+
 struct StepArgs {
     hp_step_desc d;
-    WsView ws;  // rows_off: prefix of the new tokens; units_off: prefix of the pages
+    WsView ws;  // rows_off: prefix of the new tokens, units_off of the pages, within each block
+    unsigned long long* blocks;  // [3][kStepBlocks]: each block's tokens, pages, verdict key
+    uint32_t block_log;          // log2 of a block's sequences
     uint32_t div_ok, div_m, div_l;  // div_invariant constants of page_size, where it fits
     int* d_status;
 };

@@ -73,6 +73,7 @@ def check_step(hp, s):
 @pytest.mark.parametrize("S,P,hi,prompts", [
     (1, 16, 0, True), (1, 1, 5, False), (2, 5, 40, True), (33, 16, 300, True), (700, 3, 60, True),
     (1024, 16, 100, False), (1025, 16, 100, True), (5000, 64, 500, False), (3, 16, 40000, True),
+    (2048, 16, 300, True), (4097, 1, 9, True), (300000, 16, 3, False),
 ])
 def test_step_tables(hp, S, P, hi, prompts, it):
     rng = np.random.default_rng(S * 7 + P)

@@ -48,7 +48,7 @@ def test_step_tables_refusals(hpc, kw, name):
 
 def test_step_tables_workspace(hpc):
     rc, n = hpc.hp_step_tables_workspace_bytes(100)
-    assert rc == 0 and n == 256 + 2 * 1024
+    assert rc == 0 and n == 256 + 2 * 1024 + 3 * 8 * 256
     d = step(hpc, num_seqs=100)
     for ws, size in ((None, 1 << 20), (A + 16, 1 << 20), (A, n - 1)):
         assert hpc.status_name(hpc.lib().hp_step_tables(ctypes.byref(d), ws, size, None, None)) \
