@@ -709,7 +709,8 @@ int hp_latent_decode_planned(const hp_paged_desc* desc, uint32_t latent_dim, con
                              int* d_status, void* stream);
 
 /* Bytes of device workspace hp_latent_prefill needs: the plan's, the latent rows and the
- * expanded keys and values of up to kv_tokens tokens, each sequence padded to 128. */
+ * expanded keys and values of up to kv_tokens tokens, each sequence padded to 128, and an entry
+ * per block of queries. */
 int hp_latent_prefill_workspace_bytes(const hp_paged_desc* desc, uint32_t latent_dim,
                                       uint32_t nope_dim, uint32_t v_dim, uint64_t total_q,
                                       uint32_t num_q_heads, uint64_t kv_tokens, uint64_t* bytes);

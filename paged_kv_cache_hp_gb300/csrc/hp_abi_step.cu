@@ -417,11 +417,17 @@ namespace {
 
 // Byte offsets of the expanded form's buffers behind the plan.
 struct PrefillWs {
-    u64 plan, cap_rows, rows_bytes, kv_bytes;
-    u64 total() const { return plan + rows_bytes + kv_bytes; }
+    u64 plan, cap_rows, rows_bytes, kv_bytes, unit_bytes;
+    u64 total() const { return plan + rows_bytes + kv_bytes + unit_bytes; }
 };
 
-int prefill_ws(const hp_paged_desc* d, uint32_t nope, uint32_t v, uint32_t heads, u64 kv_tokens,
+// Blocks of `block` queries that total_q queries of num_seqs sequences can make.
+u64 most_units(u64 total_q, u64 num_seqs, uint32_t block)
+{
+    return total_q / block + std::min<u64>(num_seqs, total_q);
+}
+
+int prefill_ws(const hp_paged_desc* d, uint32_t nope, uint32_t v, u64 total_q, uint32_t heads, u64 kv_tokens,
                PrefillWs* w)
 {
     const int rc = ws_bytes(d, &w->plan);
@@ -429,10 +435,12 @@ int prefill_ws(const hp_paged_desc* d, uint32_t nope, uint32_t v, uint32_t heads
     const u128 rows = ((u128)kv_tokens + (u128)(hp::kLatentPad - 1) * d->num_seqs + hp::kLatentPad - 1) /
                       hp::kLatentPad * hp::kLatentPad;
     const u128 row = (u128)d->head_dim * 2, kv = (u128)heads * ((u64)nope + v) * 2;
-    if (rows >> 36 || row >> 24 || (rows * (row + kv)) >> 62) return HP_ERR_OVERFLOW;
+    if (rows >> 36 || row >> 24 || (rows * (row + kv)) >> 60 || total_q >> 48) return HP_ERR_OVERFLOW;
     w->cap_rows = (u64)rows;
     w->rows_bytes = hp::round_up_256((u64)(rows * row));
     w->kv_bytes = hp::round_up_256((u64)(rows * kv));
+    w->unit_bytes =
+        hp::round_up_256(most_units(total_q, d->num_seqs, hp::kLatentTcQueries) * sizeof(hp::LatentUnit));
     return HP_OK;
 }
 
@@ -444,10 +452,9 @@ HP_API int hp_latent_prefill_workspace_bytes(const hp_paged_desc* desc, uint32_t
                                              uint64_t* bytes)
 {
     (void)latent_dim;
-    (void)total_q;
     if (!desc || !bytes) return HP_ERR_NULL;
     PrefillWs w;
-    const int rc = prefill_ws(desc, nope_dim, v_dim, num_q_heads, kv_tokens, &w);
+    const int rc = prefill_ws(desc, nope_dim, v_dim, total_q, num_q_heads, kv_tokens, &w);
     if (rc) return rc;
     *bytes = w.total();
     return HP_OK;
@@ -467,7 +474,7 @@ HP_API int hp_latent_prefill(const hp_paged_desc* desc, uint32_t latent_dim, con
     rc = check_q_ptr(d, q_ptr, total_q);
     if (rc) return rc;
     PrefillWs w;
-    rc = prefill_ws(&d, nope_dim, v_dim, num_q_heads, kv_tokens, &w);
+    rc = prefill_ws(&d, nope_dim, v_dim, total_q, num_q_heads, kv_tokens, &w);
     if (rc) return rc;
     if (!workspace || misaligned(workspace, 256) || workspace_bytes < w.total())
         return HP_ERR_WORKSPACE;
@@ -479,7 +486,7 @@ HP_API int hp_latent_prefill(const hp_paged_desc* desc, uint32_t latent_dim, con
                     hp::latent_prefill_tc_fits(latent_dim, d.head_dim, nope_dim, v_dim, w.cap_rows,
                                                total_q, num_q_heads);
     const uint32_t block = tc ? hp::kLatentTcQueries : hp::kLatentCcQueries;
-    const u64 max_units = total_q / block + std::min<u64>(d.num_seqs, total_q);
+    const u64 max_units = most_units(total_q, d.num_seqs, block);
     if (max_units >= (1ull << 31)) return HP_ERR_OVERFLOW;
     hp::PlanArgs pa = plan_args(&d, workspace, d_status);
     pa.new_ptr = q_ptr;
@@ -525,6 +532,7 @@ HP_API int hp_latent_prefill(const hp_paged_desc* desc, uint32_t latent_dim, con
     a.blocked = tc;
     a.rope_blocks = static_cast<char*>(a.rows) + w.cap_rows * latent_dim * 2;
     a.kv = static_cast<char*>(a.rows) + w.rows_bytes;
+    a.units = reinterpret_cast<hp::LatentUnit*>(static_cast<char*>(a.kv) + w.kv_bytes);
     a.out = out;
     a.d_status = d_status;
     rc = hp::launch_latent_rows(a, stream);

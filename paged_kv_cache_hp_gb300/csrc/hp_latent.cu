@@ -300,6 +300,23 @@ __global__ void __launch_bounds__(256) latent_rows_kernel(const LatentPrefillArg
     pdl_wait();
     if (a.hdr->verdict != kVerdictOk) return;
     const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (a.blocked) {  // the attention's units, from the last to the first: late queries see most
+        const uint64_t units = a.hdr->total_units;
+        for (uint64_t e = (uint64_t)blockIdx.x * 256 + threadIdx.x; e < a.max_units; e += (uint64_t)gridDim.x * 256) {
+            LatentUnit un{};
+            if (e < units) {
+                const uint64_t u = units - 1 - e, s = find_seq(a.units_off, a.num_seqs, u);
+                const uint64_t q0 = a.q_ptr ? index_at(a.q_ptr, a.idx64, s) : s;
+                const uint64_t n = (a.q_ptr ? index_at(a.q_ptr, a.idx64, s + 1) : s + 1) - q0;
+                const uint64_t i0 = (u - a.units_off[s]) * a.q_block;
+                un.block = a.rows_off[s] / kLatentPad;
+                un.q_row = q0 + i0;
+                un.seen0 = (int64_t)(index_at(a.lens, a.idx64, s) + 1 + i0) - (int64_t)n;
+                un.queries = (uint32_t)umin(n - i0, a.q_block);
+            }
+            a.units[e] = un;
+        }
+    }
     const uint64_t rows = a.hdr->total_rows;
     const uint32_t vecs = a.W / 8, lvecs = a.R / 8;
     for (uint64_t row0 = ((uint64_t)blockIdx.x * 8 + warp) * kRowsWarp4; row0 < rows;

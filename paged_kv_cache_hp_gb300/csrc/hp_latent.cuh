@@ -63,6 +63,14 @@ int launch_latent_merge(const LatentArgs& a, void* stream);
 
 // Expanded form, after a kPlanLatent plan (rows padded to kLatentPad per sequence, units of
 // q_block queries).
+struct LatentUnit {           // a block of queries, for the tensor-core attention
+    uint64_t block;           // its sequence's first block of 128 rows in the workspace
+    uint64_t q_row;           // its first query
+    int64_t seen0;            // tokens that query sees (not positive: none)
+    uint32_t queries;         // 0: no unit
+    uint32_t pad;
+};
+
 struct LatentPrefillArgs {
     const void* pool;
     const void* w_kv;         // [H, Dn + Dv, R]
@@ -82,6 +90,7 @@ struct LatentPrefillArgs {
     int blocked;              // tensor cores: the buffers below in blocks (hp_latent_prefill_tc.cu)
     void* rows;               // [cap_rows, W]: the latent rows, zeros behind each sequence; blocked:
                               // [cap_rows, R]
+    LatentUnit* units;        // blocked: [max_units]
     void* rope_blocks;        // blocked: the rope keys, 128 x 64 per 128 rows, swizzled
     void* kv;                 // [cap_rows, H, Dn + Dv]; blocked: [H, cap_rows / 128, 4, 128 x 64]
     void* out;                // [total_q, H, Dv]

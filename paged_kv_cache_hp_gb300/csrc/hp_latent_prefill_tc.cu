@@ -2,10 +2,12 @@
 // latent_dim 512, rope_dim 64, nope_dim 128, v_dim 128.
 //
 // latent_expand_kernel: KV [rows, H * 256] = C [rows, 512] . W^T, a plain product.  Persistent
-// CTAs, tiles of 128 x 256, eight 64-wide slices of the 512 through a ring of three stages (A
-// 16 KiB, B 32 KiB, TMA, 128-byte swizzled), two accumulators of 256 TMEM columns so that a
-// tile's epilogue (TMEM -> registers -> shared memory -> bulk store) overlaps the next tile's
-// products.  A CTA's tiles are consecutive, so all the columns of a few row blocks are in
+// CTAs, tiles of 128 x 256, eight 64-wide slices of the 512 through a ring of four stages (A 16
+// KiB, B 32 KiB, TMA, 128-byte swizzled), two accumulators of 256 TMEM columns so that a tile's
+// epilogue (TMEM -> registers -> shared memory -> bulk store, eight warps) overlaps the next
+// tile's products.  The SM's reads bound it: 384 KiB a tile arrive at 49 bytes a cycle where the
+// tensor pipe would take 94 (tiles of 256 x 256 read a third less and gain nothing, their
+// epilogue standing between the tiles: 144 against 139 us at 21,000 rows and 32 heads).  A CTA's tiles are consecutive, so all the columns of a few row blocks are in
 // flight at once and both operands come from L2.  KV goes to the workspace in blocks of 128 rows x
 // 64 columns laid out as shared memory will hold them (head, row block, K0 K1 V0 V1), so that the
 // attention below loads 16 KiB pieces with untiled bulk copies; the rope keys likewise (hp_latent.cu).
@@ -99,11 +101,12 @@ __device__ __forceinline__ float min3(float a, float b, float c)
 }
 
 // ------------------------------------------------------------------------ expansion
-constexpr uint32_t kGStages = 3, kGSlices = kR / 64;
-constexpr uint32_t kGStage = 3 * kSlot;                  // A 128 x 64, B 256 x 64
-constexpr uint32_t kGOut = kGStages * kGStage;           // the epilogue's four 128 x 64 blocks
-constexpr uint32_t kGSmem = kGOut + 4 * kSlot + 1024;
-constexpr int kGThreads = 6 * 32;
+constexpr uint32_t kGSlices = kR / 64;
+constexpr int kGThreads = 10 * 32;  // warp 0 TMA, 1 products, 2-9 epilogue
+
+constexpr uint32_t kGStages = 4, kGStage = 3 * kSlot;   // A 128 x 64, B 256 x 64
+constexpr uint32_t kGOut = kGStages * kGStage;          // then 4 KiB for each epilogue warp
+constexpr uint32_t kGSmem = kGOut + 8 * 4096 + 1024;
 
 template <typename T>
 __global__ void __launch_bounds__(kGThreads, 1)
@@ -117,8 +120,9 @@ __global__ void __launch_bounds__(kGThreads, 1)
     pdl_wait();
     if (a.hdr->verdict != kVerdictOk) return;
     const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t nt = a.H;                              // column tiles: a head each
-    const uint64_t tiles = a.hdr->total_rows / 128 * nt;
+    const uint32_t nt = a.H;  // column tiles: a head each
+    const uint64_t rblocks = a.hdr->total_rows / 128;
+    const uint64_t tiles = rblocks * nt;
     const uint64_t per = (tiles + gridDim.x - 1) / gridDim.x;
     const uint64_t beg = umin(blockIdx.x * per, tiles), end = umin(beg + per, tiles);
     if (beg >= end) return;
@@ -129,9 +133,9 @@ __global__ void __launch_bounds__(kGThreads, 1)
             mbar_init(smem_u32(&full[i]), 1);
             mbar_init(smem_u32(&freed[i]), 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (uint32_t i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&t_full[i]), 1);
-            mbar_init(smem_u32(&t_free[i]), 128);
+            mbar_init(smem_u32(&t_free[i]), 256);
         }
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -181,8 +185,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
         uint64_t i = 0, n = 0;
         bool stop = false;
         for (uint64_t t = beg; t < end && !stop; ++t, ++n) {
-            const uint32_t acc = (uint32_t)(n & 1);
-            if (n >= 2 && !warp_wait(&t_free[acc], (uint32_t)((n / 2 - 1) & 1))) break;
+            const uint32_t buf = (uint32_t)(n & 1);
+            if (n >= 2 && !warp_wait(&t_free[buf], (uint32_t)((n / 2 - 1) & 1))) break;
             for (uint32_t s = 0; s < kGSlices; ++s, ++i) {
                 const uint32_t st = (uint32_t)(i % kGStages);
                 if (!warp_wait(&full[st], (uint32_t)((i / kGStages) & 1))) {
@@ -194,55 +198,57 @@ __global__ void __launch_bounds__(kGThreads, 1)
                 if (elect_one()) {
 #pragma unroll
                     for (uint32_t kk = 0; kk < 4; ++kk)
-                        mma_f16(tmem + acc * 256, ad + kk * 2, bd + kk * 2, id, s | kk);
+                        mma_f16(tmem + buf * 256, ad + kk * 2, bd + kk * 2, id, s | kk);
                     mma_commit(smem_u32(&freed[st]));
-                    if (s + 1 == kGSlices) mma_commit(smem_u32(&t_full[acc]));
+                    if (s + 1 == kGSlices) mma_commit(smem_u32(&t_full[buf]));
                 }
                 __syncwarp();
             }
         }
         // every product issued has completed before the TMEM goes
-        for (uint64_t x = n > 2 ? n - 2 : 0; x < n; ++x)
-            mbar_wait(smem_u32(&t_full[x & 1]), (uint32_t)((x / 2) & 1));
-        if (stop && i % kGSlices) mbar_wait(smem_u32(&freed[(i - 1) % kGStages]), (uint32_t)(((i - 1) / kGStages) & 1));
+        if (i) mbar_wait(smem_u32(&freed[(i - 1) % kGStages]), (uint32_t)(((i - 1) / kGStages) & 1));
     } else {
-        const uint32_t q4 = warp & 3, row = q4 * 32 + lane;
-        const uint32_t lane_addr = (q4 * 32) << 16;
+        // Epilogue: a warp takes 32 rows (its TMEM quarter) of two of the tile's 64-column pieces; a
+        // piece's 32 rows lie 4 KiB together in the workspace's 16 KiB block, stored by the warp
+        // alone.
+        const uint32_t q4 = warp & 3, g = (warp - 2) >> 2, lane_addr = (q4 * 32) << 16;
+        const uint32_t stage = kGOut + (warp - 2) * 4096;
+        unsigned char* row = smem + stage + lane * 128;
         uint64_t n = 0;
         for (uint64_t t = beg; t < end; ++t, ++n) {
-            const uint32_t acc = (uint32_t)(n & 1);
-            const bool ok = wait_for(&t_full[acc], (uint32_t)((n / 2) & 1));
-            // the staging blocks are free once the last tile's stores have read them
-            if (threadIdx.x == 64) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            if (!named_and(1, 128, ok)) break;  // the four warps stop together
+            const uint32_t buf = (uint32_t)(n & 1);
+            if (!warp_wait(&t_full[buf], (uint32_t)((n / 2) & 1))) break;
             fence_after();
+            char* out = static_cast<char*>(a.kv) + (t % nt * (a.cap_rows / 128) + t / nt) * 4 * kSlot + q4 * 4096;
 #pragma unroll 1
-            for (uint32_t c = 0; c < 256; c += 32) {
-                uint32_t o[32];
-                tmem_issue<32>(tmem + lane_addr + acc * 256 + c, o);
-                tmem_wait<32>(o);
-                unsigned char* blk = smem + kGOut + (c >> 6) * kSlot + row * 128;
+            for (uint32_t c = 2 * g; c < 2 * g + 2; ++c) {
+                uint32_t o[2][32];
+                const uint32_t src = tmem + lane_addr + buf * 256 + c * 64;
+                tmem_issue<32>(src, o[0]);
+                tmem_issue<32>(src + 32, o[1]);
+                tmem_wait<32>(o[0]);
+                tmem_wait<32>(o[1]);
+                // (the warp's last store has read the stage)
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                __syncwarp();
 #pragma unroll
-                for (uint32_t v = 0; v < 4; ++v) {
+                for (uint32_t v = 0; v < 8; ++v) {
+                    const uint32_t* e = o[v >> 2] + 8 * (v & 3);
                     uint4 w;
-                    w.x = pack2<T>(__uint_as_float(o[8 * v]), __uint_as_float(o[8 * v + 1]));
-                    w.y = pack2<T>(__uint_as_float(o[8 * v + 2]), __uint_as_float(o[8 * v + 3]));
-                    w.z = pack2<T>(__uint_as_float(o[8 * v + 4]), __uint_as_float(o[8 * v + 5]));
-                    w.w = pack2<T>(__uint_as_float(o[8 * v + 6]), __uint_as_float(o[8 * v + 7]));
-                    *reinterpret_cast<uint4*>(blk + (((((c & 32) >> 3) + v) ^ (row & 7)) << 4)) = w;
+                    w.x = pack2<T>(__uint_as_float(e[0]), __uint_as_float(e[1]));
+                    w.y = pack2<T>(__uint_as_float(e[2]), __uint_as_float(e[3]));
+                    w.z = pack2<T>(__uint_as_float(e[4]), __uint_as_float(e[5]));
+                    w.w = pack2<T>(__uint_as_float(e[6]), __uint_as_float(e[7]));
+                    *reinterpret_cast<uint4*>(row + ((v ^ (lane & 7)) << 4)) = w;
                 }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) bulk_store(out + c * kSlot, sm0 + stage, 4096, 0);
             }
             fence_before();
-            mbar_arrive(smem_u32(&t_free[acc]));
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            named_sync(2, 128);
-            if (threadIdx.x == 64) {
-                bulk_store_nocommit(static_cast<char*>(a.kv) + (t % nt * (a.cap_rows / 128) + t / nt) * 4 * kSlot,
-                                    sm0 + kGOut, 4 * kSlot);
-                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-            }
+            mbar_arrive(smem_u32(&t_free[buf]));
         }
-        if (threadIdx.x == 64) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         __syncwarp();
     }
     fence_before();
@@ -269,24 +275,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     pdl_wait();
-    if (a.hdr->verdict != kVerdictOk) return;
-    const uint64_t units = a.hdr->total_units;
-    const uint64_t ui = blockIdx.x % a.max_units;
-    if (ui >= units) return;
+    // everything the CTA needs to know, in one trip to memory (hp_latent.cu wrote the units, the
+    // last queries of the batch first)
+    const LatentUnit un = a.units[blockIdx.x % a.max_units];
+    if (a.hdr->verdict != kVerdictOk || un.queries == 0) return;
     const uint32_t h = (uint32_t)(blockIdx.x / a.max_units);
-    const uint64_t u = units - 1 - ui;  // a sequence's last queries see most: they start first
     const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint64_t s = find_seq(a.units_off, a.num_seqs, u);
-    const uint64_t len = index_at(a.lens, a.idx64, s);
-    const uint64_t q0 = a.q_ptr ? index_at(a.q_ptr, a.idx64, s) : s;
-    const uint64_t n = (a.q_ptr ? index_at(a.q_ptr, a.idx64, s + 1) : s + 1) - q0;
-    const uint64_t i0 = (u - a.units_off[s]) * kLatentTcQueries;
     // blocks of 128 keys that each tile's last query reaches
     uint32_t nblk[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        const uint64_t lo = i0 + 128 * t, last = umin(n, lo + 128);  // one past the tile's last query
-        nblk[t] = last > lo && len + last > n ? (uint32_t)((len + last - n + 127) / 128) : 0;
+        const uint32_t q = un.queries > 128u * t ? (un.queries < 128u * t + 128 ? un.queries : 128u * t + 128) : 0;
+        const int64_t seen = un.seen0 + (int64_t)q - 1;  // by the tile's last query
+        nblk[t] = q && seen > 0 ? (uint32_t)((seen + 127) / 128) : 0;
     }
     const uint32_t blocks = nblk[0] > nblk[1] ? nblk[0] : nblk[1];
 
@@ -329,12 +330,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (nblk[t]) {
                     mbar_expect_tx(smem_u32(&q_full[t]), 3 * kSlot);
                     for (uint32_t c = 0; c < 3; ++c)
-                        tma_2d(sm0 + (3 * t + c) * kSlot, &tmq, (int)(h * kDq + c * 64), (int)(q0 + i0 + 128 * t),
+                        tma_2d(sm0 + (3 * t + c) * kSlot, &tmq, (int)(h * kDq + c * 64), (int)(un.q_row + 128 * t),
                                smem_u32(&q_full[t]));
                 }
-            const uint64_t b0 = a.rows_off[s] / 128;
-            const char* kv = static_cast<const char*>(a.kv) + (h * (a.cap_rows / 128) + b0) * 4 * kSlot;
-            const char* rope = static_cast<const char*>(a.rope_blocks) + b0 * kSlot;
+            const char* kv = static_cast<const char*>(a.kv) + (h * (a.cap_rows / 128) + un.block) * 4 * kSlot;
+            const char* rope = static_cast<const char*>(a.rope_blocks) + un.block * kSlot;
             // Piece c = 5 j + i (K: 0, 1 expanded, 2 rope; V: 3, 4) goes to slot c mod 8, where piece
             // c - 8 was: K's first after the rope keys of block j - 2, its others after V of j - 2,
             // V after the first keys of j - 1.  One barrier for the three pieces of K, one for V.
@@ -441,8 +441,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t q4 = warp & 3, row = q4 * 32 + lane;
         const uint32_t sa = tmem + ((q4 * 32) << 16) + kSCol + t * 128;
         const uint32_t oa = tmem + ((q4 * 32) << 16) + kOCol + t * 128;
-        const uint64_t qi = i0 + 128 * t + row;
-        const uint64_t vis = qi < n && len + 1 + qi > n ? len + 1 + qi - n : 0;
+        const uint32_t qi = 128 * t + row;  // query of the unit
+        const bool real = qi < un.queries;
+        const uint64_t vis = real && un.seen0 + qi > 0 ? (uint64_t)(un.seen0 + qi) : 0;
         const float qscale = a.scale * 1.4426950408889634f;
         float m = -INFINITY, l = 0.0f;
         bool stop = false;
@@ -544,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!stop) {
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            uint4* o4 = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + ((q0 + qi) * a.H + h) * kDv);
+            uint4* o4 = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + ((un.q_row + qi) * a.H + h) * kDv);
 #pragma unroll 1
             for (uint32_t c = 0; c < 128; c += 32) {
                 uint32_t o[32];
@@ -555,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = 0u;
                 }
-                if (qi < n) {
+                if (real) {
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
                         uint4 w;

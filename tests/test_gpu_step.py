@@ -564,6 +564,19 @@ def test_latent_prefill_long_and_peaked(hp, kernel):
                   sample={0, 1, 127, 128, 255, 256, 1000, 2047, 2898, 2899})
 
 
+def test_latent_prefill_many_heads(hp):
+    """11 blocks of 128 rows x 64 heads, several tiles of the expansion per CTA: selecting weights
+    (exact keys and values) and random ones, sampled queries."""
+    import torch
+    for exact in (True, False):
+        b = Latent(hp, A([600, 641]), A([600, 300]), 64, 512, 576, 16, "bf16", seed=13)
+        w = selecting_weights(64, 128, 128, 512, b.dt, 5)
+        if not exact:
+            w = (torch.randn((64, 256, 512), generator=torch.Generator().manual_seed(3)) / 512 ** 0.5).to(b.dt)
+        got = run_prefill(b, 128, 128, w, 0.07)
+        check_prefill(b, got, 128, 128, w, 0.07, exact_kv=exact, sample={0, 127, 130, 599, 600, 777, 899})
+
+
 def test_latent_prefill_kv_tokens_too_small(hp):
     import torch
     b = Latent(hp, A([40, 30]), A([4, 4]), 2, 512, 576, 16, "bf16")

@@ -205,4 +205,5 @@ def test_latent_workspace_sizes(hpc):
     assert rc == 0 and n == 256 + 2 * 1024 + 160 * 128 * 514 * 4 + 320 * 32
     rc, n = hpc.hp_latent_prefill_workspace_bytes(D, 512, 128, 128, 1000, 16, 5000)
     rows = -(-(5000 + 127 * 100) // 128) * 128
-    assert rc == 0 and n == 256 + 2 * 1024 + rows * 576 * 2 + rows * 16 * 256 * 2
+    units = -(-(1000 // 256 + 100) * 32 // 256) * 256  # blocks of 256 queries, 32 bytes each
+    assert rc == 0 and n == 256 + 2 * 1024 + rows * 576 * 2 + rows * 16 * 256 * 2 + units
