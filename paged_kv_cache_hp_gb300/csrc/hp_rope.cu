@@ -329,10 +329,9 @@ __global__ void __launch_bounds__(kThreads, 3) qk_append_kernel(const AppendArgs
     }
 }
 
-constexpr int kLatVec = 4;  // 32 lanes x 8 elements x 4: latent vectors up to 1024
-
-// As above; part 0 of a token also takes its latent row (the whole warp) and shared key.
-template <typename T, int L>
+// As above; part 0 of a token also takes its latent row (the whole warp, kLatVec vectors of 8
+// elements a lane: latent_dim up to 256 kLatVec) and shared key.
+template <typename T, int L, int kLatVec>
 __global__ void __launch_bounds__(kThreads, 3) latent_append_kernel(const AppendArgs a, uint32_t parts, bool report_here)
 {
     if (!report_here && a.d_status && blockIdx.x == gridDim.x - 1) {
@@ -448,8 +447,10 @@ int launch_l(const AppendArgs& a, cudaStream_t st)
     const bool report_here = a.d_status && a.tokens > kReportTokens;
     if (report_here && cudaMemsetAsync(a.d_status, 0, sizeof(int), st) != cudaSuccess) return HP_ERR_CUDA;
     const unsigned grid = (unsigned)(ctas < cap ? ctas : cap) + (a.d_status && !report_here);
-    if (LATENT)
-        latent_append_kernel<T, L><<<grid, kThreads, 0, st>>>(a, (uint32_t)parts, report_here);
+    if (LATENT && a.latent_dim <= 512)
+        latent_append_kernel<T, L, 2><<<grid, kThreads, 0, st>>>(a, (uint32_t)parts, report_here);
+    else if (LATENT)
+        latent_append_kernel<T, L, 4><<<grid, kThreads, 0, st>>>(a, (uint32_t)parts, report_here);
     else
         qk_append_kernel<T, L><<<grid, kThreads, 0, st>>>(a, (uint32_t)parts, report_here);
     return cudaGetLastError() == cudaSuccess ? HP_OK : HP_ERR_CUDA;
