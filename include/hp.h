@@ -31,9 +31,9 @@
  *   current CUDA device; pointers described as "host" point to CPU memory.
  *   The page pool and the output of the gathers (dequantising ones included), the
  *   pool and new rows of the appends, the pool of hp_copy_pages, the buffers of the
- *   lane operations and the K and V pools of decode attention may instead be
- *   page-locked host memory (from the CUDA host allocator or cudaHostRegister,
- *   mapped): those operations then read and write it in place over the host link.
+ *   lane operations, the K and V pools of decode attention and the pool of latent
+ *   attention may instead be page-locked host memory (from the CUDA host allocator or
+ *   cudaHostRegister, mapped): those operations then read and write it in place over the host link.
  *   The caller says so with HP_HOST_MEMORY (the copies then take the register
  *   engine); the library never asks the runtime where a pointer lives.  Index
  *   buffers, workspaces, status words and the other operations' buffers are device
@@ -494,7 +494,8 @@ int hp_attention_decode_planned(const hp_paged_desc* k_desc, const void* v_pool,
  * (K/V heads) or hp_latent_append (one shared latent row per token) finishes a projection's
  * output and stores it in those slots, layer by layer; then hp_attention_decode, or
  * hp_latent_decode / hp_latent_prefill, reads the pages.  (The pages cited above define the
- * layout these operators read and write; the operators themselves are this library's.)
+ * layout these operators read and write; the operators themselves are this library's.)  Calls
+ * whose work may overlap on the GPU need workspaces and status words of their own.
  */
 
 /*
@@ -545,7 +546,8 @@ int hp_step_tables_workspace_bytes(uint64_t num_seqs, uint64_t* bytes);
 /*
  * ASYNC.  Builds the tables of one step (hp_step_desc).  Host checks, in order: step NULL
  * (HP_ERR_NULL), index type, page_size 0 (HP_ERR_ZERO_PAGE_SIZE), reserved not 0 (HP_ERR_ARG),
- * sizes beyond 2^58 (HP_ERR_OVERFLOW), NULL and misaligned buffers (element alignment),
+ * sizes beyond 2^58, table_cap + token_cap beyond 2^41 or num_seqs beyond
+ * 2^38 (HP_ERR_OVERFLOW), NULL and misaligned buffers (element alignment),
  * workspace.  On the device, in this order: seq_ptr (HP_ERR_SEQ_PTR_START, _ORDER, _END), a
  * sequence whose seq_lens exceed its slice, or whose grown length does not fit the index type
  * or 2^58 (HP_ERR_LEN), free_pages too short (HP_ERR_CAPACITY), more than table_cap entries or
@@ -613,9 +615,9 @@ typedef struct hp_qk_desc {
  * is fp32, rounded once to `dtype`.  A padding token's rows are left as they were.  A token
  * whose slot lies outside the pool (HP_ERR_PAGE_ID) or whose position is not below max_pos
  * (HP_ERR_LEN) is skipped; *d_status gets HP_ERR_LEN if any token's position is, else
- * HP_ERR_PAGE_ID if any slot is.  Two tokens naming one slot leave an unspecified one of them.  q, k, v, q_out, weights and pools: 16-byte
- * aligned, strides multiples of 16 bytes (HP_ERR_ALIGN); rot_dim at most head_dim
- * (HP_ERR_ARG).  q_out must not overlap k, v or the pools.
+ * HP_ERR_PAGE_ID if any slot is.  Two tokens naming one slot leave a mix of the two in it.
+ * q, k, v, q_out, weights and pools 16-byte aligned, strides multiples of 16 bytes
+ * (HP_ERR_ALIGN); rot_dim at most head_dim (HP_ERR_ARG).  q_out must not overlap k, v or the pools.
  */
 int hp_qk_norm_rope_append(const hp_qk_desc* qk, const hp_rope_desc* rope, int* d_status,
                            void* stream);
@@ -681,10 +683,11 @@ int hp_latent_decode_workspace_bytes(const hp_paged_desc* desc, uint32_t latent_
  * q_ptr[num_seqs] <= total_q: the rows of q and out behind the last sequence are neither read
  * nor written) may be NULL: one query per sequence, total_q = num_seqs.
  * out (device, [total_q, num_q_heads, latent_dim], the pool's type).  Scores, softmax
- * statistics and sums are fp32; the weights enter the value product rounded to the pool's
- * type, and the result is rounded once.  The values of every token below seq_lens have to be
- * finite (a query's weight for a later token of its sequence is zero, not absent); slots past
- * a sequence's length may hold anything.
+ * statistics and sums are fp32; on the tensor cores the weights enter the value product rounded
+ * to the pool's type, and the result is rounded once.  The values of every token below seq_lens
+ * have to be finite (a query's weight for a later token of its sequence is zero, not absent);
+ * slots past a sequence's length may hold anything, and a NaN in a query stays in its own row
+ * of out.
  * Supported: latent_dim a multiple of 64 up to 512; rope_dim a multiple of 8 from 8 to 64;
  * page_size <= 2^26 (HP_ERR_ARG otherwise).  latent_dim 512 with rope_dim 64 and pages of a
  * multiple of 8 slots run on the tensor cores, the others on the CUDA cores
@@ -723,8 +726,8 @@ int hp_latent_prefill_workspace_bytes(const hp_paged_desc* desc, uint32_t latent
  * of W^V.  q (device, [total_q, num_q_heads, nope_dim + rope_dim]) and q_ptr as in
  * hp_latent_decode (so a prompt behind a cached prefix sees the prefix); out (device, [total_q,
  * num_q_heads, v_dim]).  K and V are rounded to the pool's type after fp32 accumulation over
- * latent_dim, the weights before the value product, the result once; scores, statistics and
- * sums are fp32.  kv_tokens: at least the sum of seq_lens, or nothing is written and
+ * latent_dim, on the tensor cores the weights before the value product, the result once;
+ * scores, statistics and sums are fp32.  kv_tokens: at least the sum of seq_lens, or nothing is written and
  * HP_ERR_OUT_SIZE stored.  Finite values, empty rows and validation are as in hp_latent_decode.
  * Supported: latent_dim and rope_dim as there; nope_dim a multiple of 16 and v_dim a multiple
  * of 16 up to 256 (HP_ERR_ARG otherwise).  latent_dim 512, rope_dim 64, nope_dim 128 and v_dim

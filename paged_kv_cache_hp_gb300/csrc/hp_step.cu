@@ -351,7 +351,6 @@ int launch_t(const StepArgs& a, cudaStream_t st)
     }
     const uint64_t ec = (d.table_cap + kFillItems - 1) / kFillItems, tc = (d.token_cap + kFillItems - 1) / kFillItems;
     const uint64_t grid = ec + tc + d.num_seqs / 256 + 1;
-    if (grid >= (1ull << 31)) return HP_ERR_OVERFLOW;
     StepArgs b = a;
     b.block_log = 10;
     while ((d.num_seqs >> b.block_log) >= kMaxBlocks) ++b.block_log;
