@@ -153,17 +153,13 @@ __global__ void __launch_bounds__(256, 2) latent_cc_kernel(const LatentArgs a)
                         if (c + u >= cnt || t0 + c + u >= vis[i]) sc[i][u] = -INFINITY;
                         mn = fmaxf(mn, sc[i][u]);
                     }
-                    if (mn == -INFINITY) {
-#pragma unroll
-                        for (int u = 0; u < kKeys; ++u) sc[i][u] = 0.0f;
-                        continue;
-                    }
-                    const float f = exp2_approx(m[i] - mn);
+                    // (no token seen yet: weights of zero, but a NaN score keeps its NaN)
+                    const float base = mn == -INFINITY ? 0.0f : mn, f = exp2_approx(m[i] - base);
                     m[i] = mn;
                     l[i] *= f;
 #pragma unroll
                     for (int u = 0; u < kKeys; ++u) {
-                        sc[i][u] = exp2_approx(sc[i][u] - mn);
+                        sc[i][u] = exp2_approx(sc[i][u] - base);
                         l[i] += sc[i][u];
                     }
 #pragma unroll
@@ -214,6 +210,8 @@ __global__ void __launch_bounds__(256, 2) latent_cc_kernel(const LatentArgs a)
 // to a row (each a stretch of its sums).  With few rows four warps share one, so that a long
 // sequence's many records are read by more of the GPU; with many, one warp's fixed part (the
 // entry, the maxima and sums) is paid once a row (GB300, 128 heads: 16 us against 85 with four).
+// Records of the range's workers that saw no token of the row have maximum -inf and sum 0; one of
+// NaN scores has maximum -inf and a NaN sum, which stays.
 template <typename T, int SPLIT>
 __global__ void __launch_bounds__(256) latent_merge_kernel(const LatentArgs a)
 {
@@ -227,58 +225,57 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const LatentArgs a)
     const uint32_t v = blockIdx.x, last = mg.last;
     // worker w's record row
     auto rec = [&](uint32_t w) { return (uint64_t)(2 * w + (w == v ? mg.slot : 0)) * a.group_rows + gr; };
+    // float4s of the row: this warp's stretch of R / 4 / SPLIT, kQuads per lane.  The first records'
+    // are on their way while the maxima are looked at.
+    const uint32_t stretch = a.R / 4 / SPLIT, q0 = (warp % SPLIT) * stretch;
+    float4 x[kBatch][kQuads], acc[kQuads];
+    auto fetch = [&](uint32_t w) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+            for (int j = 0; j < kQuads; ++j)
+                x[i][j] = lane + 32 * j < stretch && w + i <= last
+                              ? reinterpret_cast<const float4*>(a.part_acc + rec(w + i) * a.R)[q0 + lane + 32 * j]
+                              : make_float4(0, 0, 0, 0);
+    };
+    fetch(v);
     // maximum and sum over the records, a lane per record, then pairwise
     float M = -INFINITY, L = 0.0f, mine = -INFINITY;  // mine: the maximum of record v + lane
     for (uint32_t w = v + lane; w <= last; w += 32) {
-        const float2 x = a.part_ml[rec(w)];
-        if (w == v + lane) mine = x.x;
-        const float mn = fmaxf(M, x.x);
-        if (mn != -INFINITY) {
-            L = L * exp2_approx(M - mn) + x.y * exp2_approx(x.x - mn);
-            M = mn;
-        }
+        const float2 ml = a.part_ml[rec(w)];
+        if (w == v + lane) mine = ml.x;
+        const float mn = fmaxf(M, ml.x), base = mn == -INFINITY ? 0.0f : mn;
+        L = L * exp2_approx(M - base) + ml.y * exp2_approx(ml.x - base);
+        M = mn;
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const float om = __shfl_xor_sync(0xffffffffu, M, o), ol = __shfl_xor_sync(0xffffffffu, L, o);
-        const float mn = fmaxf(M, om);
-        if (mn != -INFINITY) {
-            L = L * exp2_approx(M - mn) + ol * exp2_approx(om - mn);
-            M = mn;
-        }
+        const float mn = fmaxf(M, om), base = mn == -INFINITY ? 0.0f : mn;
+        L = L * exp2_approx(M - base) + ol * exp2_approx(om - base);
+        M = mn;
     }
-    // float4s of the row: this warp's stretch of R / 4 / SPLIT, kQuads per lane
-    const uint32_t stretch = a.R / 4 / SPLIT, q0 = (warp % SPLIT) * stretch;
-    float4 acc[kQuads];
+    const float top = M == -INFINITY ? 0.0f : M;
+    float fl = exp2_approx(mine - top);  // the factors of 32 records, one per lane
 #pragma unroll
     for (int j = 0; j < kQuads; ++j) acc[j] = make_float4(0, 0, 0, 0);
-    if (M != -INFINITY)
-        for (uint32_t w0 = v; w0 <= last; w0 += 32) {  // 32 records, their factors one per lane
-            if (w0 != v) mine = w0 + lane <= last ? a.part_ml[rec(w0 + lane)].x : -INFINITY;
-            const float fl = exp2_approx(mine - M);
-            const uint32_t n32 = last + 1 - w0 < 32 ? last + 1 - w0 : 32;
-            for (uint32_t i0 = 0; i0 < n32; i0 += kBatch) {
-                float4 x[kBatch][kQuads];
+    for (uint32_t w = v; w <= last;) {
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i)
+        for (int i = 0; i < kBatch; ++i) {
+            const float f = __shfl_sync(0xffffffffu, fl, (int)(w - v + i) & 31);  // (0 past the last)
 #pragma unroll
-                    for (int j = 0; j < kQuads; ++j)
-                        x[i][j] = lane + 32 * j < stretch && i0 + i < n32
-                                      ? reinterpret_cast<const float4*>(a.part_acc + rec(w0 + i0 + i) * a.R)[q0 + lane + 32 * j]
-                                      : make_float4(0, 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const float f = __shfl_sync(0xffffffffu, fl, (int)(i0 + i) & 31);  // (0 past the last)
-#pragma unroll
-                    for (int j = 0; j < kQuads; ++j) {
-                        acc[j].x = fmaf(f, x[i][j].x, acc[j].x);
-                        acc[j].y = fmaf(f, x[i][j].y, acc[j].y);
-                        acc[j].z = fmaf(f, x[i][j].z, acc[j].z);
-                        acc[j].w = fmaf(f, x[i][j].w, acc[j].w);
-                    }
-                }
+            for (int j = 0; j < kQuads; ++j) {
+                acc[j].x = fmaf(f, x[i][j].x, acc[j].x);
+                acc[j].y = fmaf(f, x[i][j].y, acc[j].y);
+                acc[j].z = fmaf(f, x[i][j].z, acc[j].z);
+                acc[j].w = fmaf(f, x[i][j].w, acc[j].w);
             }
         }
+        w += kBatch;
+        if (w > last) break;
+        fetch(w);
+        if ((w - v) % 32 == 0) fl = exp2_approx((w + lane <= last ? a.part_ml[rec(w + lane)].x : -INFINITY) - top);
+    }
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
     uint2* o = reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (mg.out_row + gr) * a.R);
 #pragma unroll
@@ -458,7 +455,8 @@ __global__ void __launch_bounds__(256) latent_prefill_cc_kernel(const LatentPref
         for (int i = 0; i < kQ; ++i) {
             d[i] = warp_sum(d[i]);
             if (t >= vis[i]) continue;  // (the same in every lane)
-            const float mn = fmaxf(m[i], d[i]), f = exp2_approx(m[i] - mn), w = exp2_approx(d[i] - mn);
+            const float mn = fmaxf(m[i], d[i]), base = mn == -INFINITY ? 0.0f : mn;
+            const float f = exp2_approx(m[i] - base), w = exp2_approx(d[i] - base);
             m[i] = mn;
             l[i] = l[i] * f + w;
 #pragma unroll

@@ -876,3 +876,246 @@ def test_two_batches_at_once_on_two_streams(hp):
     for b, q, ws, out, s in runs:
         assert b.status.item() == 0
         check_decode(b, host(out), 0.07, rows={0, 1, 2, 40})
+
+
+@pytest.mark.parametrize("kernel", ["cuda_cores", "default"])
+def test_a_nan_query_keeps_its_nan_to_itself(hp, kernel):
+    """NaN in one (query, head) row: that row of out is NaN, whether one worker saw all its tokens
+    or many share the sequence, and every other row is as it would be; so in both forms, with NaN
+    queries behind the last sequence too."""
+    import torch
+    for lens, nq in ((A([300, 40]), A([3, 2])), (A([30000, 5]), A([1, 2]))):
+        for form in ("decode", "prefill"):
+            b = Latent(hp, lens, nq, 8, 512, 576, 16, "bf16", seed=21, rows_behind=2, flags=cores(hp, kernel))
+            w, real = selecting_weights(8, 128, 128, 512, b.dt, 6), b.queries
+
+            def queries(width):
+                real(width)
+                b.clean = b.q.clone()
+                b.q[0, 3, 5] = float("nan")
+                b.q[-2:] = float("nan")
+                return b.q.cuda()
+            b.queries = queries
+            if form == "decode":
+                got = run_decode(b, 0.07)
+            else:
+                got = run_prefill(b, 128, 128, w, 0.07)
+            assert np.isnan(got[0, 3]).all(), form
+            # the row's clean result in its place, the whole is checked against the formula
+            b.q, b.queries = b.clean, lambda width: b.clean.cuda()
+            if form == "decode":
+                got[0, 3] = run_decode(b, 0.07)[0, 3]
+                check_decode(b, got, 0.07)
+            else:
+                got[0, 3] = run_prefill(b, 128, 128, w, 0.07)[0, 3]
+                check_prefill(b, got, 128, 128, w, 0.07, exact_kv=True)
+
+
+@pytest.mark.parametrize("R,W,P", [(512, 576, 16), (128, 192, 6)])
+def test_latent_attention_over_a_pool_in_host_memory(hp, R, W, P):
+    """HP_HOST_MEMORY: the pool's page-locked copy gives the device pool's results."""
+    import torch
+    for form in ("decode", "prefill"):
+        outs = []
+        for flags in (hp.ATTN_CUDA_CORES if form == "decode" else 0, hp.HOST_MEMORY):
+            b = Latent(hp, A([100, 0, 333]), A([2, 1, 40]), 4, R, W, P, "f16", seed=3, flags=flags)
+            if flags == hp.HOST_MEMORY:
+                pinned = torch.empty(b.pool.shape, dtype=b.pool.dtype, pin_memory=True)
+                pinned.copy_(b.pool)
+                b.desc = hp.PagedDesc(pinned, *b.desc._keep[1:4], num_pages=b.desc.c.num_pages, page_size=P,
+                                      num_heads=1, head_dim=W, dtype="f16", index_type=0, flags=flags)
+            w = selecting_weights(4, 128, 128, R, b.dt, 6)
+            outs.append(run_decode(b, 0.07) if form == "decode" else run_prefill(b, 128, 128, w, 0.07))
+        assert np.array_equal(*outs)
+
+
+def test_many_heads_and_large_pages(hp):
+    """1,000 heads (eight groups of 128 rows a query and a ragged one), and pages of 4,096 slots."""
+    b = Latent(hp, A([130]), A([1]), 1000, 512, 576, 16, "bf16", seed=1)
+    check_decode(b, run_decode(b, 0.07), 0.07)
+    for kernel in (0, hp.ATTN_CUDA_CORES):
+        b = Latent(hp, A([4097, 9000]), A([1, 3]), 4, 512, 576, 4096, "f16", seed=2, flags=kernel)
+        check_decode(b, run_decode(b, 0.07), 0.07)
+    w = selecting_weights(4, 128, 128, 512, b.dt, 6)
+    b = Latent(hp, A([4097, 200]), A([1, 3]), 4, 512, 576, 4096, "f16", seed=2)
+    check_prefill(b, run_prefill(b, 128, 128, w, 0.07), 128, 128, w, 0.07, exact_kv=True)
+
+
+def test_prefill_of_one_query_each_without_offsets(hp):
+    b = Latent(hp, A([40, 0, 333]), np.ones(3, np.int64), 4, 512, 576, 16, "bf16", with_ptr=False)
+    w = selecting_weights(4, 128, 128, 512, b.dt, 6)
+    check_prefill(b, run_prefill(b, 128, 128, w, 0.07), 128, 128, w, 0.07, exact_kv=True)
+
+
+@pytest.mark.parametrize("form", ["decode", "prefill"])
+def test_no_query_at_all(hp, form):
+    """total_q = 0 over sequences that have tokens, and no sequence: the descriptor is checked,
+    nothing is written."""
+    import torch
+    for lens in (A([40, 9]), np.zeros(0, np.int64)):
+        b = Latent(hp, lens, np.zeros(len(lens), np.int64), 4, 512, 576, 16, "bf16")
+        w = selecting_weights(4, 128, 128, 512, b.dt, 6).cuda()
+        ws = torch.zeros(1 << 27, dtype=torch.uint8, device="cuda")
+        if form == "decode":
+            rc = hp.hp_latent_decode(b.desc, 512, None, b.q_ptr, 0, 4, 1.0, None, ws, b.status)
+        else:
+            rc = hp.hp_latent_prefill(b.desc, 512, w, 128, 128, None, b.q_ptr, 0, 4, 1.0, None, 49, ws, b.status)
+        torch.cuda.synchronize()
+        assert hp.status_name(rc) == "HP_OK" and b.status.item() == 0
+        if len(lens):
+            b.desc._keep[3][1] = 33
+            if form == "decode":
+                hp.hp_latent_decode(b.desc, 512, None, b.q_ptr, 0, 4, 1.0, None, ws, b.status)
+            else:
+                hp.hp_latent_prefill(b.desc, 512, w, 128, 128, None, b.q_ptr, 0, 4, 1.0, None, 49, ws, b.status)
+            torch.cuda.synchronize()
+            assert hp.status_name(b.status.item()) == "HP_ERR_LEN"
+
+
+@pytest.mark.parametrize("what,name", [
+    ("start", "SEQ_PTR_START"), ("order", "SEQ_PTR_ORDER"), ("end", "SEQ_PTR_END"), ("len", "LEN"),
+    ("grow", "LEN"), ("free", "CAPACITY"), ("cap", "OUT_SIZE"), ("tokens", "OUT_SIZE"),
+])
+def test_step_tables_verdicts_of_a_large_step(hp, what, name):
+    """The same rules where several CTAs scan: 3,001 sequences, the fault in the last block."""
+    import torch
+    lens, new = np.full(3001, 20), np.full(3001, 20)
+    s = make_step(hp, lens, new, np.full(3001, 2), 16, 0, free=1 if what == "free" else None)
+    d = s["d"]
+    bt, sp, ln, nw = d.keep[0], d.keep[1], d.keep[2], d.keep[3]
+    if what == "start":
+        sp[0] = 1
+    elif what == "order":
+        sp[2900] = 2
+    elif what == "end":
+        sp[3001] = 6003
+    elif what == "len":
+        ln[2999] = 33
+    elif what == "grow":
+        nw[2999] = -20
+    elif what == "cap":
+        d.table_cap = 3001 * 3 - 1
+    elif what == "tokens":
+        d.token_cap = 3001 * 20 - 1
+    assert hp.hp_step_tables(d, s["ws"], s["status"]) == 0
+    torch.cuda.synchronize()
+    assert hp.status_name(s["status"].item()) == "HP_ERR_" + name
+    for t in s["o"].values():
+        assert (t == -9).all()
+
+
+@pytest.mark.parametrize("T", [2, 5000])
+def test_appends_of_tokens_without_a_place(hp, T):
+    """Batches on either side of the two ways of reporting: every token's slot out of the pool,
+    one position out of the table besides; padding alone; the same calls without a status."""
+    import torch
+    P, W, pages = 16, 576, 400
+    kv = torch.randn((T, W)).to(torch.bfloat16).cuda()
+    cs = dev(ref.cos_sin(10, 64))
+    pool = torch.zeros((pages, P, W), dtype=torch.bfloat16, device="cuda")
+    for slot, far, name in ((pages * P, False, "HP_ERR_PAGE_ID"), (pages * P, True, "HP_ERR_LEN"),
+                            (2 ** 62, False, "HP_ERR_PAGE_ID"), (-1, False, "HP_OK"), (-1, True, "HP_OK"),
+                            (-2 ** 63, False, "HP_OK")):
+        pos = torch.zeros((1, T), dtype=torch.int32, device="cuda")
+        pos[0, T - 1] = -1 if far else 9  # 2^32 - 1
+        rope = hp.rope_desc(cos_sin=cs, sections=(32,), positions=pos)
+        d = hp.latent_desc(latent=kv[:, :512], k_rope=kv[:, 512:], dtype="bf16",
+                           slot_map=dev(np.full(T, slot, np.int64)), pool=pool, num_pages=pages, page_size=P)
+        for st in (status_tensor(), None):
+            assert hp.hp_latent_append(d, rope, st) == 0
+            torch.cuda.synchronize()
+            assert st is None or hp.status_name(st.item()) == name
+            assert not pool.any()
+
+
+def test_a_whole_latent_step_in_one_graph(hp):
+    """Tables, append, prompts and decode of one step captured together; replayed on new lengths,
+    rows and queries the graph gives what the calls give one by one."""
+    import torch
+    S, H, R, P, W, pages, T = 5, 4, 512, 16, 576, 64, 90
+    dt = torch.bfloat16
+    lens, new = torch.zeros(S, dtype=torch.int32).cuda(), torch.zeros(S, dtype=torch.int32).cuda()
+    # each sequence has 10 pages, so that its slice does not grow
+    table = torch.randperm(pages)[:10 * S].int().cuda()
+    sp = (torch.arange(S + 1) * 10).int().cuda()
+    o = dict(table_out=torch.empty(10 * S, dtype=torch.int32, device="cuda"),
+             seq_ptr_out=torch.empty(S + 1, dtype=torch.int32, device="cuda"),
+             lens_out=torch.empty(S, dtype=torch.int32, device="cuda"),
+             new_ptr_out=torch.empty(S + 1, dtype=torch.int32, device="cuda"),
+             slot_map=torch.empty(T, dtype=torch.int64, device="cuda"),
+             positions=torch.empty(T, dtype=torch.int32, device="cuda"))
+    sd = hp.step_desc(block_table=table, seq_ptr=sp, seq_lens=lens, new_lens=new, free_pages=None, page_size=P,
+                      index_type=0, **o)
+    rc, n = hp.hp_step_tables_workspace_bytes(S)
+    sws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    pool = torch.zeros((pages, P, W), dtype=dt, device="cuda")
+    kv = torch.zeros((T, W), dtype=dt, device="cuda")
+    q = torch.zeros((T, H, 192), dtype=dt, device="cuda")
+    qa = torch.zeros((T, H, W), dtype=dt, device="cuda")
+    rope = hp.rope_desc(cos_sin=dev(ref.cos_sin(200, 64)), positions=o["positions"], sections=(32,))
+    ld = hp.latent_desc(latent=kv[:, :R], k_rope=kv[:, R:], dtype="bf16", slot_map=o["slot_map"], pool=pool,
+                        num_pages=pages, page_size=P)
+    pd = hp.PagedDesc(pool, o["table_out"], o["seq_ptr_out"], o["lens_out"], num_pages=pages, page_size=P,
+                      num_heads=1, head_dim=W, dtype="bf16", index_type=0)
+    kv_cap = 10 * S * P
+    rc, n1 = hp.hp_latent_prefill_workspace_bytes(pd, R, 128, 128, T, H, kv_cap)
+    rc, n2 = hp.hp_latent_decode_workspace_bytes(pd, R, T, H)
+    ws = torch.zeros(max(n1, n2), dtype=torch.uint8, device="cuda")
+    w = selecting_weights(H, 128, 128, R, dt, 2).cuda()
+    out, lat = torch.zeros((T, H, 128), dtype=dt).cuda(), torch.zeros((T, H, R), dtype=dt).cuda()
+    st = [status_tensor() for _ in range(4)]
+
+    def calls():
+        assert hp.hp_step_tables(sd, sws, st[0]) == 0
+        assert hp.hp_latent_append(ld, rope, st[1]) == 0
+        assert hp.hp_latent_prefill(pd, R, w, 128, 128, q, o["new_ptr_out"], T, H, 0.07, out, kv_cap, ws, st[2]) == 0
+        assert hp.hp_latent_decode(pd, R, qa, o["new_ptr_out"], T, H, 0.07, lat, ws, st[3]) == 0
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for ln, nw in (([0, 0, 0, 0, 0], [90, 0, 0, 0, 0]), ([90, 0, 5, 140, 1], [1, 30, 0, 20, 1]),
+                   ([100, 1, 1, 1, 1], [0, 0, 0, 0, 0]), ([99, 98, 97, 96, 95], [1, 1, 1, 1, 1])):
+        lens.copy_(torch.tensor(ln))
+        new.copy_(torch.tensor(nw))
+        for t in (kv, q, qa):
+            t.copy_(torch.randn(t.shape).to(dt))
+        results = []
+        for run in (graph.replay, calls):
+            pool.copy_(torch.ones(1, dtype=dt))
+            out.fill_(9)
+            lat.fill_(9)
+            run()
+            torch.cuda.synchronize()
+            assert [x.item() for x in st] == [0] * 4
+            results.append([t.clone() for t in (out, lat, pool, *o.values())])
+        for a, c in zip(*results):
+            assert torch.equal(a, c) and torch.isfinite(a.float()).all()
+        assert (out[sum(nw):] == 9).all() and (lat[sum(nw):] == 9).all() and not (lat[:sum(nw)] == 9).all(-1).any()
+
+
+def test_tables_and_appends_on_two_streams(hp):
+    """Steps of different sizes on two streams at once, a workspace each."""
+    import torch
+    rng = np.random.default_rng(8)
+    runs = []
+    for S in (4000, 30):
+        lens, new = rng.integers(0, 300, S), rng.integers(0, 4, S)
+        s = make_step(hp, lens, new, -(-lens // 16), 16, 0, pad=0)
+        T = int(new.sum())
+        kv = torch.randn((T, 576)).to(torch.bfloat16).cuda()
+        rope = hp.rope_desc(cos_sin=dev(ref.cos_sin(310, 64)), sections=(32,), positions=s["o"]["positions"])
+        pages = len(s["table"]) + len(s["free"])
+        pool = torch.zeros((pages, 16, 576), dtype=torch.bfloat16, device="cuda")
+        d = hp.latent_desc(latent=kv[:, :512], k_rope=kv[:, 512:], dtype="bf16", slot_map=s["o"]["slot_map"],
+                           pool=pool, num_pages=pages, page_size=16)
+        runs.append((s, d, rope, pool, kv, status_tensor(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, d, rope, pool, kv, st, stream in runs:
+            assert hp.hp_step_tables(s["d"], s["ws"], s["status"], stream) == 0
+            assert hp.hp_latent_append(d, rope, st, stream) == 0
+    for s, d, rope, pool, kv, st, stream in runs:
+        check_step(hp, s)
+        assert st.item() == 0 and torch.equal(pool.view(-1, 576)[s["o"]["slot_map"]][:, :512], kv[:, :512])
