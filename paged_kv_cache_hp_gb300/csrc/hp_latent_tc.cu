@@ -238,19 +238,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             uint64_t base = div_groups(a, g.k0 * 8);
             unsigned long long cur = entries(base), nxt = entries(base + 32);
-            for (uint64_t k = g.k0; ok && k < g.k1; ++k, ++j) {
-                // lane i: the pool row of the step's i-th (mod 8) group of 8 tokens
+            // lane i: the pool row of step k's i-th (mod 8) group of 8 tokens
+            auto row_of = [&](uint64_t k) {
                 const uint64_t gi = k * 8 + (lane & 7), page = div_groups(a, gi);
-                if (__shfl_sync(0xffffffffu, page, 0) >= base + 32) {
+                const uint32_t rel = (uint32_t)(page - base);  // below 64: two steps span 16 pages at most
+                const unsigned long long e0 = __shfl_sync(0xffffffffu, cur, (int)(rel & 31));
+                const unsigned long long e1 = __shfl_sync(0xffffffffu, nxt, (int)(rel & 31));
+                return (int)((rel < 32 ? e0 : e1) * P + (gi * 8 - page * P));
+            };
+            auto groups_of = [&](uint64_t k) { return (uint32_t)umin(8, (g.len - k * kTok + 7) / 8); };  // with a token
+            for (uint64_t k = g.k0; ok && k < g.k1; ++k, ++j) {
+                if (div_groups(a, k * 8) >= base + 32) {
                     base += 32;
                     cur = nxt;
                     nxt = entries(base + 32);
                 }
-                const uint32_t rel = (uint32_t)(page - base);  // below 64: a step spans 8 pages at most
-                const unsigned long long e0 = __shfl_sync(0xffffffffu, cur, (int)(rel & 31));
-                const unsigned long long e1 = __shfl_sync(0xffffffffu, nxt, (int)(rel & 31));
-                const int row = (int)((rel < 32 ? e0 : e1) * P + (gi * 8 - page * P));
-                const uint32_t live = (uint32_t)umin(8, (g.len - k * kTok + 7) / 8);  // groups with a token
+                const int row = row_of(k);
+                const uint32_t live = groups_of(k);
+                // the next step's rows start for the L2 while this one waits for its slots, a pair's
+                // CTAs half of them each
+                if (k > g.k0 && k + 1 < g.k1) {
+                    const int ahead = row_of(k + 1);
+                    if (lane < 8 && lane < groups_of(k + 1) && lane % tiles == walk.tile) prefetch_3d(&tmc, 0, ahead, 0);
+                    __syncwarp();
+                }
                 for (uint32_t p = 0; p < 2; ++p) {
                     const uint64_t c = 2 * j + p;
                     const uint32_t sl = (uint32_t)(c % kSlots), n = live > 4 * p ? (uint32_t)umin(4, live - 4 * p) : 0;
