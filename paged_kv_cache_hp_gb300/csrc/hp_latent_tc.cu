@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t live = groups_of(k);
                 // the next step's rows start for the L2 while this one waits for its slots, a pair's
                 // CTAs half of them each
-                if (k > g.k0 && k + 1 < g.k1) {
+                if (k + 1 < g.k1) {
                     const int ahead = row_of(k + 1);
                     if (lane < 8 && lane < groups_of(k + 1) && lane % tiles == walk.tile) prefetch_3d(&tmc, 0, ahead, 0);
                     __syncwarp();
