@@ -152,35 +152,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int abort_flag, fail_s[2];
     __shared__ float corr_s[kRows], inv_s[kRows];
 
-    pdl_wait();
-    if (a.hdr->verdict != kVerdictOk) return;
     const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     T* out = static_cast<T*>(a.out);
-    // queries of sequences without tokens: zeros, 32 sequences to a warp at a time
-    auto zero_empty = [&](uint64_t w, uint64_t warps) {
-        for (uint64_t k = w;; k += warps) {  // the CTA's k-th 32 sequences, whichever warps share them
-            const uint64_t s0 = (blockIdx.x + k * gridDim.x) * 32, s = s0 + lane;
-            if (s0 >= a.num_seqs) break;
-            unsigned empty = __ballot_sync(0xffffffffu, s < a.num_seqs && a.units_off[s] == a.units_off[s + 1]);
-            for (; empty; empty &= empty - 1) {
-                const uint64_t e = s0 + __ffs(empty) - 1;
-                const uint64_t q0 = a.q_ptr ? index_at(a.q_ptr, a.idx64, e) : e;
-                const uint64_t q1 = a.q_ptr ? index_at(a.q_ptr, a.idx64, e + 1) : e + 1;
-                uint4* o = reinterpret_cast<uint4*>(out);
-                for (uint64_t i = q0 * a.H * (kR / 8) + lane; i < q1 * a.H * (kR / 8); i += 32)
-                    o[i] = make_uint4(0, 0, 0, 0);
-            }
-        }
-    };
-    const uint32_t tiles = a.group_rows / kRows;
-    const uint64_t total = a.hdr->total_units, Lw = (total + a.workers - 1) / a.workers;
-    const uint64_t v = blockIdx.x / tiles, beg = umin(v * Lw, total), end = umin(beg + Lw, total);
-    if (threadIdx.x == 96 && blockIdx.x % tiles == 0) write_merge(a, v);  // (a softmax thread, idle yet)
-    if (beg >= end) {  // the whole CTA, before any barrier or TMEM
-        zero_empty(warp, 8);
-        return;
-    }
-
+    // what does not depend on the plan, while the plan runs
     const uint32_t sm0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char* smem = smem_raw + (sm0 - smem_u32(smem_raw));
     if (threadIdx.x == 0) {
@@ -201,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fail_s[0] = fail_s[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 64) {
         prefetch_map(&tmc);
         prefetch_map(&tmq);
     }
@@ -210,6 +184,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_base;
+    pdl_wait();
+    // queries of sequences without tokens: zeros, 32 sequences to a warp at a time
+    auto zero_empty = [&](uint64_t w, uint64_t warps) {
+        for (uint64_t k = w;; k += warps) {  // the CTA's k-th 32 sequences, whichever warps share them
+            const uint64_t s0 = (blockIdx.x + k * gridDim.x) * 32, s = s0 + lane;
+            if (s0 >= a.num_seqs) break;
+            unsigned empty = __ballot_sync(0xffffffffu, s < a.num_seqs && a.units_off[s] == a.units_off[s + 1]);
+            for (; empty; empty &= empty - 1) {
+                const uint64_t e = s0 + __ffs(empty) - 1;
+                const uint64_t q0 = a.q_ptr ? index_at(a.q_ptr, a.idx64, e) : e;
+                const uint64_t q1 = a.q_ptr ? index_at(a.q_ptr, a.idx64, e + 1) : e + 1;
+                uint4* o = reinterpret_cast<uint4*>(out);
+                for (uint64_t i = q0 * a.H * (kR / 8) + lane; i < q1 * a.H * (kR / 8); i += 32)
+                    o[i] = make_uint4(0, 0, 0, 0);
+            }
+        }
+    };
+    const uint32_t tiles = a.group_rows / kRows;
+    const bool planned = a.hdr->verdict == kVerdictOk;
+    const uint64_t total = planned ? a.hdr->total_units : 0, Lw = (total + a.workers - 1) / a.workers;
+    const uint64_t v = blockIdx.x / tiles, beg = umin(v * Lw, total), end = umin(beg + Lw, total);
+    if (planned && threadIdx.x == 96 && blockIdx.x % tiles == 0) write_merge(a, v);  // (a softmax thread, idle yet)
+    if (beg >= end) {  // the whole CTA
+        if (planned) zero_empty(warp, 8);
+        if (warp == 1) tmem_free(tmem, kTmemCols);
+        return;
+    }
+
     Walk walk(a, beg, end, (uint32_t)(blockIdx.x % tiles), lane);
     Segment g;
     // true unless the wait ran out or another role stopped; warp_wait for whole warps
