@@ -262,7 +262,8 @@ constexpr uint32_t kSlots = 8;
 constexpr uint32_t kOffKv = 2 * 3 * kSlot;  // Q: two tiles of three 128 x 64 blocks
 constexpr uint32_t kSmem = kOffKv + kSlots * kSlot + 1024;
 constexpr uint32_t kSCol = 0, kOCol = 256;  // S (and P) of tile t at 128 t, O at 256 + 128 t
-constexpr int kThreads = 10 * 32;           // warps 0-3 tile 0, 4-7 tile 1, 8 TMA, 9 products
+constexpr int kThreads = 18 * 32;           // warps 0-7 tile 0, 8-15 tile 1, 16 TMA, 17 products
+constexpr int kTile = 256;                  // softmax threads of a tile: two to a query
 constexpr float kTau = 8.0f;
 
 template <typename T>
@@ -273,7 +274,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) unsigned long long k_full[2], v_full[2], k_free[2], v_free[2], q_full[2],
         s_full[2], p_full[2], o_done[2], all_done;
     __shared__ uint32_t tmem_base;
-    __shared__ int abort_flag;
+    __shared__ int abort_flag, fail_s[2][2];
+    __shared__ float half_s[2][128];  // what a query's two threads tell each other
     pdl_wait();
     // everything the CTA needs to know, in one trip to memory (hp_latent.cu wrote the units, the
     // last queries of the batch first)
@@ -300,14 +302,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&v_free[i]), 1);
             mbar_init(smem_u32(&q_full[i]), 1);
             mbar_init(smem_u32(&s_full[i]), 1);
-            mbar_init(smem_u32(&p_full[i]), 128);
+            mbar_init(smem_u32(&p_full[i]), kTile);
+            fail_s[i][0] = fail_s[i][1] = 0;
             mbar_init(smem_u32(&o_done[i]), 1);
         }
         mbar_init(smem_u32(&all_done), 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 9) tmem_alloc(smem_u32(&tmem_base), kTmemCols);
+    if (warp == 17) tmem_alloc(smem_u32(&tmem_base), kTmemCols);
     fence_before();
     __syncthreads();
     fence_after();
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return __all_sync(0xffffffffu, wait_for(bar, parity)) != 0;
     };
 
-    if (warp == 8) {
+    if (warp == 16) {
         if (lane == 0) {
             for (int t = 0; t < 2; ++t)
                 if (nblk[t]) {
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t x = va > 2 ? va - 2 : 0; x < va; ++x) mbar_wait(smem_u32(&v_full[x & 1]), (x / 2) & 1);
         }
         __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         const uint32_t id_s = f16_idesc(a.bf16 != 0, false, false, 128, 128);
         const uint32_t id_o = f16_idesc(a.bf16 != 0, false, true, 128, 128);
         const uint32_t id_o64 = f16_idesc(a.bf16 != 0, false, true, 128, 64);
@@ -437,10 +440,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         mbar_wait(smem_u32(&all_done), 0);
     } else {
-        const int t = warp >> 2;
-        const uint32_t q4 = warp & 3, row = q4 * 32 + lane;
+        const int t = warp >> 3;
+        const uint32_t q4 = warp & 3, half = (warp >> 2) & 1, row = q4 * 32 + lane;
         const uint32_t sa = tmem + ((q4 * 32) << 16) + kSCol + t * 128;
-        const uint32_t oa = tmem + ((q4 * 32) << 16) + kOCol + t * 128;
+        const uint32_t oa = tmem + ((q4 * 32) << 16) + kOCol + t * 128 + half * 64;
+        float* const told = &half_s[t][row];  // the second one's value, then what the first made of it
         const uint32_t qi = 128 * t + row;  // query of the unit
         const bool real = qi < un.queries;
         const uint64_t vis = real && un.seen0 + qi > 0 ? (uint64_t)(un.seen0 + qi) : 0;
@@ -448,25 +452,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         float m = -INFINITY, l = 0.0f;
         bool stop = false;
         for (uint32_t j = 0; j < nblk[t]; ++j) {
-            if (!warp_wait(&s_full[t], j & 1)) {
-                stop = true;
-                break;
-            }
+            // a wait that runs out marks its block; the tile's threads stop together, at the vote
+            if (!warp_wait(&s_full[t], j & 1)) fail_s[t][j & 1] = 1;
             fence_after();
-            const uint64_t t0 = (uint64_t)j * 128;
-            const int lim = vis > t0 ? (int)umin(vis - t0, 128) : 0;
-            const bool masked = __any_sync(0xffffffffu, lim < 128);
-            // The largest scaled score: the extreme of the raw ones on the scale's side.  32 columns at
-            // a time, the next ones on their way, from the last to the first; the first two stretches
-            // then stay in registers (all 128 do not fit the 168 that ten warps leave a thread).
-            uint32_t xb[2][32];
+            uint32_t xr[2][32];
+            tmem_issue<32>(sa + 64 * half, xr[0]);
+            tmem_issue<32>(sa + 64 * half + 32, xr[1]);
+            const uint64_t t0 = (uint64_t)j * 128 + 64 * half;
+            const int lim = vis > t0 ? (int)umin(vis - t0, 64) : 0;
+            const bool masked = __any_sync(0xffffffffu, lim < 64);
+            tmem_wait<32>(xr[0]);
+            tmem_wait<32>(xr[1]);
+            // the largest scaled score: the extreme of the raw ones on the scale's side
             float mx = -INFINITY;
-            tmem_issue<32>(sa + 96, xb[1]);
-            tmem_wait<32>(xb[1]);
 #pragma unroll
-            for (int c = 3; c >= 0; --c) {
-                if (c > 0) tmem_issue<32>(sa + 32 * (c - 1), xb[(c - 1) & 1]);
-                const float* x = reinterpret_cast<const float*>(xb[c & 1]);
+            for (int c = 0; c < 2; ++c) {
+                const float* x = reinterpret_cast<const float*>(xr[c]);
                 if (masked) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) mx = fmaxf(mx, 32 * c + i < lim ? x[i] * qscale : -INFINITY);
@@ -487,22 +488,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     mx = fmaxf(mx, fminf(min3(e0, x[30], x[31]), e1) * qscale);
                 }
-                if (c > 0) tmem_wait<32>(xb[(c - 1) & 1]);
             }
-            if (__any_sync(0xffffffffu, mx > m + kTau)) {
-                const float mn = fmaxf(m, mx);
+            // (past this barrier every thread of the tile has its scores, and P may overwrite them)
+            if (half) *told = mx;
+            fence_before();
+            const bool need = named_or(1 + t, kTile, mx > m + kTau);
+            fence_after();
+            if (*(volatile int*)&fail_s[t][j & 1]) {
+                stop = true;
+                break;
+            }
+            if (need) {  // the same in the whole tile
+                float mn;
+                if (!half) *told = mn = fmaxf(m, fmaxf(mx, *told));
+                named_sync(1 + t, kTile);
+                if (half) mn = *told;
                 const float f = m == -INFINITY ? 0.0f : exp2_approx(m - mn);
                 m = mn;
                 l *= f;
                 if (j > 0) {  // the scores of this block are complete, so O of the last one is
 #pragma unroll 1
-                    for (uint32_t c = 0; c < 128; c += 32) {
-                        uint32_t o[32];
-                        tmem_issue<32>(oa + c, o);
-                        tmem_wait<32>(o);
+                    for (uint32_t c = 0; c < 64; c += 16) {
+                        uint32_t o[16];
+                        tmem_issue<16>(oa + c, o);
+                        tmem_wait<16>(o);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tmem_st32(oa + c, o);
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st16(oa + c, o);
                     }
                 }
             }
@@ -510,12 +522,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t qs2 = pair_of(qscale, qscale), mu2 = pair_of(-mu, -mu);
             uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {  // xb[c & 1] holds columns 32 c ..; 2 and 3 are read again
+            for (int c = 0; c < 2; ++c) {
                 uint32_t p[16];
-                if (c > 0 && c < 3) {  // into the stretch done last, while this one is worked on
-                    tmem_issue<32>(sa + 32 * (c + 1), xb[(c + 1) & 1]);
-                }
-                const float* x = reinterpret_cast<const float*>(xb[c & 1]);
+                const float* x = reinterpret_cast<const float*>(xr[c]);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int e = 32 * c + 2 * i;
@@ -530,8 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sum[i & 1] = add2(sum[i & 1], pair_of(w.x, w.y));
                     p[i] = pack2<T>(w.x, w.y);
                 }
-                if (c > 0 && c < 3) tmem_wait<32>(xb[(c + 1) & 1]);
-                tmem_st16(sa + 16 * c, p);  // over columns already read
+                tmem_st16(sa + 32 * half + 16 * c, p);
             }
             const float2 sums = of_pair(add2(sum[0], sum[1]));
             l += sums.x + sums.y;
@@ -540,14 +548,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(smem_u32(&p_full[t]));
         }
         if (!stop && nblk[t]) {
-            stop = !warp_wait(&o_done[t], 0);
+            const bool ok = warp_wait(&o_done[t], 0);
+            if (half) *told = l;
+            stop = !named_and(1 + t, kTile, ok);
+            if (!half) *told = l += *told;
+            named_sync(1 + t, kTile);
+            if (half) l = *told;
             fence_after();
         }
         if (!stop) {
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            uint4* o4 = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + ((un.q_row + qi) * a.H + h) * kDv);
+            uint4* o4 = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + ((un.q_row + qi) * a.H + h) * kDv + half * 64);
 #pragma unroll 1
-            for (uint32_t c = 0; c < 128; c += 32) {
+            for (uint32_t c = 0; c < 64; c += 32) {
                 uint32_t o[32];
                 if (nblk[t]) {
                     tmem_issue<32>(oa + c, o);
@@ -574,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_before();
     __syncthreads();
     fence_after();
-    if (warp == 9) tmem_free(tmem, kTmemCols);
+    if (warp == 17) tmem_free(tmem, kTmemCols);
 }
 
 template <typename T>
