@@ -383,11 +383,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         // even when its phase is complete, so each operand is waited for once a round, and where the
         // products issued before it are still running; V goes back before S of the second tile.
         for (uint32_t j = 0; j <= blocks && ok; ++j) {
-            if (j > 0) ok = warp_wait(&v_full[(j - 1) & 1], ((j - 1) / 2) & 1);
+            // the round's first polls together: each is a trip to shared memory and back
+            bool v_ok = j == 0, p_ok = j == 0 || j - 1 >= nblk[0], k_ok = j >= blocks;
+            if (!v_ok) v_ok = mbar_try_wait(smem_u32(&v_full[(j - 1) & 1]), ((j - 1) / 2) & 1);
+            if (!k_ok) k_ok = mbar_test(smem_u32(&k_full[j & 1]), (j / 2) & 1);
+            if (!p_ok) p_ok = mbar_try_wait(smem_u32(&p_full[0]), (j - 1) & 1);
+            const unsigned polls = __reduce_and_sync(0xffffffffu, (v_ok ? 1u : 0u) | (k_ok ? 2u : 0u) | (p_ok ? 4u : 0u));
+            if (!(polls & 1)) ok = warp_wait(&v_full[(j - 1) & 1], ((j - 1) / 2) & 1);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const bool has_o = j > 0 && j - 1 < nblk[t], has_s = j < nblk[t];
-                if (ok && has_o) ok = warp_wait(&p_full[t], (j - 1) & 1);
+                if (ok && has_o && (t == 1 || !(polls & 4))) ok = warp_wait(&p_full[t], (j - 1) & 1);
                 if (!ok) break;
                 fence_after();
                 // V of block j - 1 is two slots of 64 dims: neighbours, but for the ring's last and first
@@ -415,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (t == 1 && j > 0) mma_commit(smem_u32(&v_free[(j - 1) & 1]));  // both tiles have read it
                 }
                 __syncwarp();
-                if (t == 0 && j < blocks) ok = warp_wait(&k_full[j & 1], (j / 2) & 1);
+                if (t == 0 && !(polls & 2)) ok = warp_wait(&k_full[j & 1], (j / 2) & 1);
                 if (!ok) break;
                 fence_after();
                 if (elect_one()) {
@@ -463,14 +469,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool masked = __any_sync(0xffffffffu, lim < 64);
             tmem_wait<32>(xr[0]);
             tmem_wait<32>(xr[1]);
-            // the largest scaled score: the extreme of the raw ones on the scale's side
-            float mx = -INFINITY;
+            // the largest scaled score: the extreme of the raw ones on the scale's side; a block that
+            // ends or is masked inside takes scaled scores with -inf in the places not seen
+            float mx = -INFINITY, qs = qscale;
+            if (masked) qs = 1.0f;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const float* x = reinterpret_cast<const float*>(xr[c]);
+                float* x = reinterpret_cast<float*>(xr[c]);
                 if (masked) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, 32 * c + i < lim ? x[i] * qscale : -INFINITY);
+                    for (int i = 0; i < 32; ++i) {
+                        x[i] = 32 * c + i < lim ? x[i] * qscale : -INFINITY;
+                        mx = fmaxf(mx, x[i]);
+                    }
                 } else if (qscale >= 0.0f) {
                     float e0 = x[0], e1 = x[1];
 #pragma unroll
@@ -519,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             const float mu = m == -INFINITY ? 0.0f : m;
-            const uint64_t qs2 = pair_of(qscale, qscale), mu2 = pair_of(-mu, -mu);
+            const uint64_t qs2 = pair_of(qs, qs), mu2 = pair_of(-mu, -mu);
             uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -527,15 +538,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float* x = reinterpret_cast<const float*>(xr[c]);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int e = 32 * c + 2 * i;
-                    const uint64_t t2 = fma2(pair_of(x[2 * i], x[2 * i + 1]), qs2, mu2);
-                    float2 w = of_pair(t2);
+                    float2 w = of_pair(fma2(pair_of(x[2 * i], x[2 * i + 1]), qs2, mu2));
                     w.x = exp2_approx(w.x);
                     w.y = exp2_approx(w.y);
-                    if (masked) {
-                        w.x = e < lim ? w.x : 0.0f;
-                        w.y = e + 1 < lim ? w.y : 0.0f;
-                    }
                     sum[i & 1] = add2(sum[i & 1], pair_of(w.x, w.y));
                     p[i] = pack2<T>(w.x, w.y);
                 }
