@@ -130,17 +130,6 @@ __device__ __forceinline__ uint64_t div_groups(const LatentArgs& a, uint64_t gro
     return group < (1ull << 32) ? div_invariant((uint32_t)group, a.g_m, a.g_l) : group / (a.page_size / 8);
 }
 
-template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
-template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b)
-{
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
-{
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_tc_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap tmc,
@@ -403,18 +392,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_before();
                 mbar_arrive(smem_u32(&s_free[j % 2]));
                 const uint64_t t0 = k * kTok;
-                float x[32], mx[2] = {-INFINITY, -INFINITY};
+                // The rows' largest scaled scores.  Elements 4 i + 0, 1 are of the first row, 2, 3 of the
+                // second.  A step that a row does not see whole takes scaled scores, -inf where it
+                // sees none; others stay raw, and their extreme on the scale's side is scaled.
+                float* x = reinterpret_cast<float*>(xr);
+                float mx[2], qs = qscale;
                 const int lim0 = vis[0] > t0 ? (int)umin(vis[0] - t0, kTok) : 0;
                 const int lim1 = vis[1] > t0 ? (int)umin(vis[1] - t0, kTok) : 0;
+                if (__any_sync(0xffffffffu, lim0 < (int)kTok || lim1 < (int)kTok)) {
+                    qs = 1.0f;
+                    mx[0] = mx[1] = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int col = 8 * i + 2 * (int)fc + (e & 1);
-                        const float y = __uint_as_float(xr[4 * i + e]) * qscale;
-                        x[4 * i + e] = col < (e < 2 ? lim0 : lim1) ? y : -INFINITY;
-                        mx[e >> 1] = fmaxf(mx[e >> 1], x[4 * i + e]);
+                    for (int i = 0; i < 32; ++i) {
+                        const int col = 8 * (i / 4) + 2 * (int)fc + (i & 1);
+                        x[i] = col < (i & 2 ? lim1 : lim0) ? x[i] * qscale : -INFINITY;
+                        mx[i >> 1 & 1] = fmaxf(mx[i >> 1 & 1], x[i]);
                     }
+                } else if (qscale >= 0.0f) {
+                    mx[0] = fmaxf(x[0], x[1]);
+                    mx[1] = fmaxf(x[2], x[3]);
+#pragma unroll
+                    for (int i = 4; i < 32; i += 2) mx[i >> 1 & 1] = max3(mx[i >> 1 & 1], x[i], x[i + 1]);
+                    mx[0] = fmaxf(-INFINITY, mx[0] * qscale);
+                    mx[1] = fmaxf(-INFINITY, mx[1] * qscale);
+                } else {
+                    mx[0] = fminf(x[0], x[1]);
+                    mx[1] = fminf(x[2], x[3]);
+#pragma unroll
+                    for (int i = 4; i < 32; i += 2) mx[i >> 1 & 1] = min3(mx[i >> 1 & 1], x[i], x[i + 1]);
+                    mx[0] = fmaxf(-INFINITY, mx[0] * qscale);
+                    mx[1] = fmaxf(-INFINITY, mx[1] * qscale);
+                }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
@@ -457,16 +465,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // weights: summed in fp32, rounded to the element type for the product
                 const float m0 = m[0] == -INFINITY ? 0.0f : m[0], m1 = m[1] == -INFINITY ? 0.0f : m[1];
+                const uint64_t qs2 = pair_of(qs, qs), n0 = pair_of(-m0, -m0), n1 = pair_of(-m1, -m1);
+                uint64_t sum0 = 0ull, sum1 = 0ull;
                 uint32_t w[16];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float p0 = exp2_approx(x[4 * i] - m0), p1 = exp2_approx(x[4 * i + 1] - m0);
-                    const float p2 = exp2_approx(x[4 * i + 2] - m1), p3 = exp2_approx(x[4 * i + 3] - m1);
-                    l[0] += p0 + p1;
-                    l[1] += p2 + p3;
-                    w[2 * i] = pack2<T>(p0, p1);
-                    w[2 * i + 1] = pack2<T>(p2, p3);
+                    float2 p0 = of_pair(fma2(pair_of(x[4 * i], x[4 * i + 1]), qs2, n0));
+                    float2 p1 = of_pair(fma2(pair_of(x[4 * i + 2], x[4 * i + 3]), qs2, n1));
+                    p0 = make_float2(exp2_approx(p0.x), exp2_approx(p0.y));
+                    p1 = make_float2(exp2_approx(p1.x), exp2_approx(p1.y));
+                    sum0 = add2(sum0, pair_of(p0.x, p0.y));
+                    sum1 = add2(sum1, pair_of(p1.x, p1.y));
+                    w[2 * i] = pack2<T>(p0.x, p0.y);
+                    w[2 * i + 1] = pack2<T>(p1.x, p1.y);
                 }
+                l[0] += of_pair(sum0).x + of_pair(sum0).y;
+                l[1] += of_pair(sum1).x + of_pair(sum1).y;
                 // P is free once O^T of the step before has read it
                 if (k > g.k0) wait_one(&o_done[(j - 1) % 2], (uint32_t)(((j - 1) / 2) & 1), j + 1);
 #pragma unroll
