@@ -8,7 +8,8 @@
 // tile's products.  The SM's reads bound it: 384 KiB a tile arrive at 49 bytes a cycle where the
 // tensor pipe would take 94 (tiles of 256 x 256 read a third less and gain nothing, their
 // epilogue standing between the tiles: 144 against 139 us at 21,000 rows and 32 heads).  A CTA's tiles are consecutive, so all the columns of a few row blocks are in
-// flight at once and both operands come from L2.  KV goes to the workspace in blocks of 128 rows x
+// flight at once and both operands
+// come from L2.  KV goes to the workspace in blocks of 128 rows x
 // 64 columns laid out as shared memory will hold them (head, row block, K0 K1 V0 V1), so that the
 // attention below loads 16 KiB pieces with untiled bulk copies; the rope keys likewise (hp_latent.cu).
 //
@@ -17,14 +18,17 @@
 // expanded 128.  Per tile and block:
 //   S [128 x 128] = Q . K^T      12 products of K = 16, operands in shared memory
 //   O [128 x 128] += P . V        8 products; P (16-bit) in TMEM over S, V N-major
-// A thread owns one query row of S: its maximum, its weights and (the same TMEM lane) its row of
-// O, which it rescales only when a score exceeds the row's reference maximum by more than
-// 2^kTau.  While one tile's softmax runs, the other tile's products do: the issue order is
-// O0(j-1) S0(j) O1(j-1) S1(j), so the tensor pipe is what bounds it (2560 cycles for both tiles of a
-// block).  P overwrites S, which is safe because one thread issues both products and they
-// execute in order.  K and V pass through a ring of eight 16 KiB slots (128 keys x 64 dims).
-// Sequences are padded to 128 rows of zeros in the workspace (hp_latent.cu), so no block reads
-// another sequence's rows.
+// Two threads own a query's row of S, 64 scores each, all in registers: a barrier of the tile's 256
+// threads says whether any score exceeds its row's reference maximum by more than 2^kTau (only
+// then the two compare their maxima, and rescale half of the row of O each) and that P may
+// overwrite S.  While one tile's softmax runs, the other tile's products do: the issue order is
+// O0(j-1) S0(j) O1(j-1) S1(j), from one thread, whose products execute in order.  A round of 128 keys
+// takes 3,600 cycles where its products need 2,640 (the S operands' reads fill shared memory's
+// bandwidth): a tile's chain S 790, 380 until its threads know, softmax 1,500, 220 until the issuer
+// knows, O 500.  One thread to a query took 3,900 (1,783 against 1,867 us at 21,000 tokens and 32
+// heads); an issuing warp for each tile lets the two fall into step (1,996).  K and V pass through
+// a ring of eight 16 KiB slots (128 keys x 64 dims).  Sequences are padded to 128 rows of zeros in
+// the workspace (hp_latent.cu), so no block reads another sequence's rows.
 //
 // Every wait is bounded (about 2 s) and reports HP_ERR_TIMEOUT; operations in flight are waited
 // for (bounded) before TMEM and shared memory go.

@@ -18,6 +18,12 @@
 // loader about 100 cycles, and boxes of one chunk (36 a step on 16-slot pages) held it to 4,400
 // a step.  Slots of four boxes go back to the loader as the products of their 32 tokens end.
 //
+// A step takes 3,150 cycles: two in flight, each the chain slots free -> loaded 1,400 -> S and the
+// other step's O^T side by side 2,000 -> softmax 1,300 -> O^T 1,500.  The next step's rows are
+// prefetched into L2 while this one waits for its slots (decode of 64 x 128 heads 119 -> 115 us,
+// 16 long sequences 319 -> 308 us: 5.9 TB/s).  Putting O^T(j) before the rest of S(j + 1), by polls
+// or at a fixed place, gained nothing (117 to 120 us): S then ends later by as much.
+//
 // Shared memory: Q 72 KiB, two steps of C 144 KiB, P (weights rounded to the element type)
 // 8 KiB.  TMEM: O^T 256 columns, S 2 x 64.  Roles: warp 0 loads C, warp 7 the queries, warp 1
 // issues S, warp 6 O^T (apart, so that neither waits for the other's operands), warps 2-5 do
