@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(256, 2) latent_cc_kernel(const LatentArgs a)
 // Records of the range's workers that saw no token of the row have maximum -inf and sum 0; one of
 // NaN scores has maximum -inf and a NaN sum, which stays.
 template <typename T, int SPLIT>
-__global__ void __launch_bounds__(256) latent_merge_kernel(const LatentArgs a)
+__global__ void __launch_bounds__(256, 4) latent_merge_kernel(const LatentArgs a)
 {
     constexpr int kRowsCta = 8 / SPLIT, kQuads = 4 / SPLIT, kBatch = 2 * SPLIT;  // kQuads float4s a lane
     pdl_wait();

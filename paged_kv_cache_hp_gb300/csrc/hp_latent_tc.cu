@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t d = tmem + kSCol + (uint32_t)(j % 2) * kTok;
                 const uint64_t cd = cd0 + (((uint32_t)(j % 2) * 8 * kGroup) >> 4);
                 if (elect_one()) {
-#pragma unroll
+#pragma unroll 4  // (all 36 in a row cost more in instruction fetches)
                     for (uint32_t u = 0; u < kChunks * 4; ++u)
                         mma_f16(d, qd + (((u >> 2) * kChunk + (u & 3) * 32) >> 4),
                                 cd + (((u >> 2) * 1024 + (u & 3) * 32) >> 4), id_s, u);
