@@ -284,9 +284,32 @@ u64 latent_records(uint32_t latent_dim)
            2 * (u64)hp::kLatentMaxSms * sizeof(hp::LatentMerge);
 }
 
-// Block tables up to this many entries are checked by the plan's one CTA (four loads a thread)
-// instead of a launch of their own, which is 2.5 us.
-constexpr u64 kPlanTable = 4096;
+// Whether the first kernel of a call makes the plan itself (hp_latent_plan.cuh): few sequences, a
+// short table, and sums that fit 32 bits.
+bool plans_itself(const hp_paged_desc& d, u64 total_q, uint32_t heads, uint32_t group_rows)
+{
+    const u128 groups = (u128)total_q * heads / group_rows + d.num_seqs;
+    const u128 steps = (u128)d.table_len * d.page_size / hp::kLatentStep + 1;
+    return d.num_seqs > 0 && d.num_seqs <= hp::kSmallSeqs && d.table_len <= hp::kPlanTable && total_q > 0 &&
+           (groups * steps) >> 31 == 0 && (steps * hp::kLatentStep + (u128)hp::kLatentPad * d.num_seqs) >> 31 == 0;
+}
+
+// The plan of the absorbed form (q_ptr: see hp_latent_decode).  Block tables up to kPlanTable
+// entries are checked by the plan's one CTA (four loads a thread) instead of a launch of their own,
+// which is 2.5 us.
+hp::PlanArgs decode_plan(const hp_paged_desc& d, const void* q_ptr, u64 total_q, uint32_t heads, uint32_t group_rows,
+                         void* workspace, int* d_status)
+{
+    hp::PlanArgs pa = plan_args(&d, workspace, d_status);
+    pa.new_ptr = q_ptr;
+    pa.total_new = total_q;
+    pa.step_tokens = hp::kLatentStep;
+    pa.heads = heads;
+    pa.group_rows = group_rows;
+    pa.row_round = 1;
+    pa.check_table = d.table_len <= hp::kPlanTable;
+    return pa;
+}
 
 int latent_prepare(const hp_paged_desc* desc, uint32_t latent_dim, const void* q_ptr, u64 total_q,
                    uint32_t heads, const void* ws, u64 ws_bytes_, hp_paged_desc* d, u64* plan_bytes)
@@ -333,21 +356,17 @@ HP_API int hp_latent_plan(const hp_paged_desc* desc, uint32_t latent_dim, const 
     const int rc = latent_prepare(desc, latent_dim, q_ptr, total_q, num_q_heads, workspace,
                                   workspace_bytes, &d, &plan);
     if (rc) return rc;
-    hp::PlanArgs pa = plan_args(&d, workspace, d_status);
-    pa.new_ptr = q_ptr;
-    pa.total_new = total_q;
-    pa.step_tokens = hp::kLatentStep;
-    pa.heads = num_q_heads;
-    pa.group_rows = latent_group_rows(latent_on_tensor_cores(d, latent_dim, total_q * num_q_heads), num_q_heads);
-    pa.row_round = 1;
-    pa.check_table = d.table_len <= kPlanTable;
+    const uint32_t gr = latent_group_rows(latent_on_tensor_cores(d, latent_dim, total_q * num_q_heads), num_q_heads);
+    const hp::PlanArgs pa = decode_plan(d, q_ptr, total_q, num_q_heads, gr, workspace, d_status);
     return hp::launch_plan(hp::kPlanLatent, d.index_type == HP_IDX_U64, pa, stream);
 }
 
-HP_API int hp_latent_decode_planned(const hp_paged_desc* desc, uint32_t latent_dim, const void* q,
-                                    const void* q_ptr, uint64_t total_q, uint32_t num_q_heads,
-                                    float scale, void* out, void* workspace,
-                                    uint64_t workspace_bytes, int* d_status, void* stream)
+namespace {
+
+// The absorbed form behind a plan in the workspace, or, with `alone`, with its own.
+int decode(const hp_paged_desc* desc, uint32_t latent_dim, const void* q, const void* q_ptr, uint64_t total_q,
+           uint32_t num_q_heads, float scale, void* out, void* workspace, uint64_t workspace_bytes, int* d_status,
+           void* stream, bool alone)
 {
     hp_paged_desc d;
     u64 plan = 0;
@@ -356,11 +375,18 @@ HP_API int hp_latent_decode_planned(const hp_paged_desc* desc, uint32_t latent_d
     if (rc) return rc;
     rc = latent_buffers(q, out, total_q);
     if (rc) return rc;
+    const bool tc = latent_on_tensor_cores(d, latent_dim, total_q * num_q_heads);
+    const uint32_t gr = latent_group_rows(tc, num_q_heads);
+    const bool small = alone && tc && plans_itself(d, total_q, num_q_heads, gr);
+    if (alone && !small) {
+        rc = hp_latent_plan(desc, latent_dim, q_ptr, total_q, num_q_heads, workspace, workspace_bytes, d_status,
+                            stream);
+        if (rc) return rc;
+    }
     if (d.num_seqs == 0 || total_q == 0) return HP_OK;
     int dev = 0;
     const u64 sms = std::min<u64>((u64)hp::current_sms(&dev), hp::kLatentMaxSms);
     if (sms == 0) return HP_ERR_CUDA;
-    const bool tc = latent_on_tensor_cores(d, latent_dim, total_q * num_q_heads);
     const hp::WsView ws = hp::ws_view(workspace, d.num_seqs);
     hp::LatentArgs a{};
     a.pool = d.page_pool;
@@ -376,13 +402,15 @@ HP_API int hp_latent_decode_planned(const hp_paged_desc* desc, uint32_t latent_d
     a.H = num_q_heads;
     a.R = latent_dim;
     a.W = (uint32_t)d.head_dim;
-    a.group_rows = latent_group_rows(tc, num_q_heads);
+    a.group_rows = gr;
     if (tc) hp::invariant_divisor(d.page_size / 8, &a.g_m, &a.g_l);
     a.workers = tc ? sms / (a.group_rows / 64) : 2 * sms;
     a.scale = scale;
     a.bf16 = d.dtype == HP_BF16;
     a.idx64 = d.index_type == HP_IDX_U64;
     a.test_stall = (d.flags & HP_TEST_STALL) != 0;
+    a.small = small;
+    a.plan = decode_plan(d, q_ptr, total_q, num_q_heads, gr, workspace, d_status);
     a.hdr = ws.hdr;
     a.units_off = ws.units_off;
     a.part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan);
@@ -395,23 +423,24 @@ HP_API int hp_latent_decode_planned(const hp_paged_desc* desc, uint32_t latent_d
     return rc ? rc : hp::launch_latent_merge(a, stream);
 }
 
+}  // namespace
+
+HP_API int hp_latent_decode_planned(const hp_paged_desc* desc, uint32_t latent_dim, const void* q,
+                                    const void* q_ptr, uint64_t total_q, uint32_t num_q_heads,
+                                    float scale, void* out, void* workspace,
+                                    uint64_t workspace_bytes, int* d_status, void* stream)
+{
+    return decode(desc, latent_dim, q, q_ptr, total_q, num_q_heads, scale, out, workspace, workspace_bytes, d_status,
+                  stream, false);
+}
+
 HP_API int hp_latent_decode(const hp_paged_desc* desc, uint32_t latent_dim, const void* q,
                             const void* q_ptr, uint64_t total_q, uint32_t num_q_heads, float scale,
                             void* out, void* workspace, uint64_t workspace_bytes, int* d_status,
                             void* stream)
 {
-    hp_paged_desc d;
-    u64 plan = 0;
-    int rc = latent_prepare(desc, latent_dim, q_ptr, total_q, num_q_heads, workspace,
-                            workspace_bytes, &d, &plan);
-    if (rc) return rc;
-    rc = latent_buffers(q, out, total_q);
-    if (rc) return rc;
-    rc = hp_latent_plan(desc, latent_dim, q_ptr, total_q, num_q_heads, workspace, workspace_bytes,
-                        d_status, stream);
-    if (rc) return rc;
-    return hp_latent_decode_planned(desc, latent_dim, q, q_ptr, total_q, num_q_heads, scale, out,
-                                    workspace, workspace_bytes, d_status, stream);
+    return decode(desc, latent_dim, q, q_ptr, total_q, num_q_heads, scale, out, workspace, workspace_bytes, d_status,
+                  stream, true);
 }
 
 namespace {
@@ -497,10 +526,13 @@ HP_API int hp_latent_prefill(const hp_paged_desc* desc, uint32_t latent_dim, con
     pa.group_rows = block;
     pa.row_round = hp::kLatentPad;
     pa.out_tokens = kv_tokens;
-    pa.check_table = d.table_len <= kPlanTable;
-    rc = hp::launch_plan(hp::kPlanLatent, d.index_type == HP_IDX_U64, pa, stream);
-    if (rc) return rc;
-    if (d.num_seqs == 0 || total_q == 0) return HP_OK;
+    pa.check_table = d.table_len <= hp::kPlanTable;
+    const bool small = tc && plans_itself(d, total_q, 1, block);
+    if (!small) {
+        rc = hp::launch_plan(hp::kPlanLatent, d.index_type == HP_IDX_U64, pa, stream);
+        if (rc) return rc;
+        if (d.num_seqs == 0 || total_q == 0) return HP_OK;
+    }
     const hp::WsView ws = hp::ws_view(workspace, d.num_seqs);
     hp::LatentPrefillArgs a{};
     a.pool = d.page_pool;
@@ -526,6 +558,8 @@ HP_API int hp_latent_prefill(const hp_paged_desc* desc, uint32_t latent_dim, con
     a.bf16 = d.dtype == HP_BF16;
     a.idx64 = d.index_type == HP_IDX_U64;
     a.test_stall = (d.flags & HP_TEST_STALL) != 0;
+    a.small = small;
+    a.plan = pa;
     a.hdr = ws.hdr;
     a.rows_off = ws.rows_off;
     a.units_off = ws.units_off;

@@ -15,6 +15,7 @@
 #include "hp_attn_merge.cuh"
 #include "hp_internal.cuh"
 #include "hp_latent.cuh"
+#include "hp_latent_plan.cuh"
 #include "hp_resolve.cuh"
 
 namespace hp {
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(256, 2) latent_cc_kernel(const LatentArgs a)
         }
     const uint64_t total = a.hdr->total_units, Lw = (total + a.workers - 1) / a.workers;
     const uint64_t v = blockIdx.x, beg = umin(v * Lw, total), end = umin(beg + Lw, total);
-    if (threadIdx.x == 255) write_merge(a, v);
+    if (threadIdx.x == 255) write_merge(a, v, total, [&](uint64_t s) { return (uint64_t)a.units_off[s]; });
     const float qscale = a.scale * kLog2e;
     uint64_t pos = beg;
     while (pos < end) {
@@ -294,19 +295,41 @@ __global__ void __launch_bounds__(256, 4) latent_merge_kernel(const LatentArgs a
 __global__ void __launch_bounds__(256) latent_rows_kernel(const LatentPrefillArgs a)
 {
     constexpr int kRowsWarp4 = 4;  // rows of a warp, looked up and loaded together
+    __shared__ uint32_t units_s[kSmallSeqs + 1], rows_s[kSmallSeqs + 1];
     pdl_wait();
-    if (a.hdr->verdict != kVerdictOk) return;
+    uint64_t units, rows;
+    if (a.small) {
+        const SmallPlan sp = small_plan(a.plan, a.idx64, units_s, rows_s);
+        if (blockIdx.x == 0 && threadIdx.x == 0) store_plan(a.plan, sp);
+        if (sp.key != kVerdictOk) return;
+        units = sp.units;
+        rows = sp.rows;
+    } else {
+        if (a.hdr->verdict != kVerdictOk) return;
+        units = a.hdr->total_units;
+        rows = a.hdr->total_rows;
+    }
+    auto units_at = [&](uint64_t s) { return a.small ? (uint64_t)units_s[s] : (uint64_t)a.units_off[s]; };
+    auto rows_at = [&](uint64_t s) { return a.small ? (uint64_t)rows_s[s] : (uint64_t)a.rows_off[s]; };
+    auto find = [&](auto sums, uint64_t u) {  // the last sequence whose sum is at most u
+        uint64_t lo = 0, hi = a.num_seqs;
+        while (hi - lo > 1) {
+            const uint64_t mid = (lo + hi) >> 1;
+            if (sums(mid) <= u) lo = mid;
+            else hi = mid;
+        }
+        return lo;
+    };
     const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (a.blocked) {  // the attention's units, from the last to the first: late queries see most
-        const uint64_t units = a.hdr->total_units;
         for (uint64_t e = (uint64_t)blockIdx.x * 256 + threadIdx.x; e < a.max_units; e += (uint64_t)gridDim.x * 256) {
             LatentUnit un{};
             if (e < units) {
-                const uint64_t u = units - 1 - e, s = find_seq(a.units_off, a.num_seqs, u);
+                const uint64_t u = units - 1 - e, s = find(units_at, u);
                 const uint64_t q0 = a.q_ptr ? index_at(a.q_ptr, a.idx64, s) : s;
                 const uint64_t n = (a.q_ptr ? index_at(a.q_ptr, a.idx64, s + 1) : s + 1) - q0;
-                const uint64_t i0 = (u - a.units_off[s]) * a.q_block;
-                un.block = a.rows_off[s] / kLatentPad;
+                const uint64_t i0 = (u - units_at(s)) * a.q_block;
+                un.block = rows_at(s) / kLatentPad;
                 un.q_row = q0 + i0;
                 un.seen0 = (int64_t)(index_at(a.lens, a.idx64, s) + 1 + i0) - (int64_t)n;
                 un.queries = (uint32_t)umin(n - i0, a.q_block);
@@ -314,12 +337,11 @@ __global__ void __launch_bounds__(256) latent_rows_kernel(const LatentPrefillArg
             a.units[e] = un;
         }
     }
-    const uint64_t rows = a.hdr->total_rows;
     const uint32_t vecs = a.W / 8, lvecs = a.R / 8;
     for (uint64_t row0 = ((uint64_t)blockIdx.x * 8 + warp) * kRowsWarp4; row0 < rows;
          row0 += (uint64_t)gridDim.x * 8 * kRowsWarp4) {
-        const uint64_t s = find_seq(a.rows_off, a.num_seqs, row0);  // (128 divides its rows_off)
-        const uint64_t t0 = row0 - a.rows_off[s];
+        const uint64_t s = find(rows_at, row0);  // (128 divides its first row)
+        const uint64_t t0 = row0 - rows_at(s);
         const uint64_t len = index_at(a.lens, a.idx64, s), tab0 = index_at(a.seq_ptr, a.idx64, s);
         const uint4* src[kRowsWarp4];
 #pragma unroll
@@ -533,7 +555,8 @@ int launch_latent_rows(const LatentPrefillArgs& a, void* stream)
     int dev = 0;
     const int sms = current_sms(&dev);
     if (sms == 0) return HP_ERR_CUDA;
-    const uint64_t ctas = a.cap_rows / 32, cap = (uint64_t)sms * 32;
+    // (each CTA that makes the plan itself makes it once: no more of them than reside)
+    const uint64_t ctas = a.cap_rows / 32, cap = (uint64_t)sms * (a.small ? 4 : 32);
     const uint64_t grid = ctas == 0 ? 1 : (ctas < cap ? ctas : cap);
     return launch_dependent(latent_rows_kernel, (unsigned)grid, 256, 0,
                             static_cast<cudaStream_t>(stream), a) == cudaSuccess

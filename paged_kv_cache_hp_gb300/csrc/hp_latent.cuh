@@ -16,6 +16,8 @@ constexpr uint32_t kLatentCcRows = 16;      // (query, head) rows per group, CUD
 constexpr uint32_t kLatentPad = 128;        // expanded form: rows a sequence is padded to
 constexpr uint32_t kLatentCcQueries = 32;   // queries per block, CUDA cores
 constexpr uint32_t kLatentTcQueries = 256;  // queries per block, tensor cores
+constexpr uint32_t kSmallSeqs = 128;        // batches up to this many sequences, and
+constexpr uint64_t kPlanTable = 4096;       // this many table entries, need no plan launch
 
 // Absorbed form, after a kPlanLatent plan on the same stream.  The plan's units are, sequence
 // after sequence and row group after row group, the steps of kLatentStep tokens: a group is
@@ -47,6 +49,8 @@ struct LatentArgs {
     uint64_t workers;
     float scale;
     int bf16, idx64, test_stall;
+    int small;                // tensor cores: the kernel makes the plan itself (hp_latent_plan.cuh)
+    PlanArgs plan;
     const WsHeader* hdr;
     const unsigned long long* units_off;
     float* part_acc;          // [2 * workers * group_rows, R]
@@ -84,6 +88,8 @@ struct LatentPrefillArgs {
     uint32_t H, R, W, Dn, Dv, q_block;
     float scale;
     int bf16, idx64, test_stall;
+    int small;                // blocked: the gather makes the plan itself (hp_latent_plan.cuh)
+    PlanArgs plan;
     const WsHeader* hdr;
     const unsigned long long* rows_off;
     const unsigned long long* units_off;
@@ -108,24 +114,26 @@ __device__ __forceinline__ unsigned long long index_at(const void* p, int idx64,
                  : (unsigned long long)static_cast<const unsigned int*>(p)[i];
 }
 
-// Worker v's entry of a.merge, by one thread of the attention kernel.
-__device__ __forceinline__ void write_merge(const LatentArgs& a, uint64_t v)
+// Worker v's entry of a.merge, by one thread of the attention kernel; units(s): the plan's sums,
+// total = units(num_seqs).
+template <typename F>
+__device__ __forceinline__ void write_merge(const LatentArgs& a, uint64_t v, uint64_t total, F units)
 {
-    const uint64_t total = a.hdr->total_units, Lw = (total + a.workers - 1) / a.workers;
+    const uint64_t Lw = (total + a.workers - 1) / a.workers;
     const uint64_t b = v * Lw, beg = b < total ? b : total, e = beg + Lw, end = e < total ? e : total;
     LatentMerge m{};
     if (beg < end && end < total) {
         uint64_t lo = 0, hi = a.num_seqs;  // the sequence of the range's last unit
         while (hi - lo > 1) {
             const uint64_t mid = (lo + hi) >> 1;
-            if (a.units_off[mid] <= end - 1) lo = mid;
+            if (units(mid) <= end - 1) lo = mid;
             else hi = mid;
         }
         const uint64_t len = index_at(a.lens, a.idx64, lo);
         const uint64_t q0 = a.q_ptr ? index_at(a.q_ptr, a.idx64, lo) : lo;
         const uint64_t n = (a.q_ptr ? index_at(a.q_ptr, a.idx64, lo + 1) : lo + 1) - q0;
         const uint64_t steps = (len + kLatentStep - 1) / kLatentStep;
-        const uint64_t g = (end - 1 - a.units_off[lo]) / steps, start = a.units_off[lo] + g * steps;
+        const uint64_t first = units(lo), g = (end - 1 - first) / steps, start = first + g * steps;
         if (start >= beg && start + steps > end) {
             const uint64_t left = n * a.H - g * a.group_rows;
             m.out_row = q0 * a.H + g * a.group_rows;

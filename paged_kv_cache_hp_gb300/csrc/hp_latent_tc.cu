@@ -42,6 +42,7 @@
 #include "hp_attn_merge.cuh"
 #include "hp_internal.cuh"
 #include "hp_latent.cuh"
+#include "hp_latent_plan.cuh"
 #include "hp_resolve.cuh"
 #include "hp_tcgen05.cuh"
 #include "hp_tma.cuh"
@@ -80,22 +81,24 @@ struct Segment {
 // together: three trips to memory to the first segment, one or two to each next.
 struct Walk {
     const LatentArgs& a;
+    const uint32_t* small;  // the CTA's own sums, or NULL
     uint64_t pos, end;
     uint32_t tile;  // this CTA's tile within the group
     uint64_t s, first, past;  // the current sequence and its units
-    __device__ Walk(const LatentArgs& args, uint64_t beg, uint64_t e, uint32_t t, unsigned lane)
-        : a(args), pos(beg), end(e), tile(t)
+    __device__ uint64_t units(uint64_t i) const { return small ? small[i] : a.units_off[i]; }
+    __device__ Walk(const LatentArgs& args, const uint32_t* sums, uint64_t beg, uint64_t e, uint32_t t, unsigned lane)
+        : a(args), small(sums), pos(beg), end(e), tile(t)
     {
         uint64_t lo = 0, hi = a.num_seqs;
         while (hi - lo > 1) {  // the last sequence whose units start at or before beg
             const uint64_t step = (hi - lo + 31) / 32, i = lo + lane * step;
-            const unsigned below = __ballot_sync(0xffffffffu, i < hi && a.units_off[i] <= beg);
+            const unsigned below = __ballot_sync(0xffffffffu, i < hi && units(i) <= beg);
             lo += (uint64_t)(31 - __clz(below)) * step;
             hi = umin(hi, lo + step);
         }
         s = lo;
-        first = a.units_off[s];
-        past = a.units_off[s + 1];
+        first = units(s);
+        past = units(s + 1);
     }
     __device__ bool next(Segment& g)
     {
@@ -103,7 +106,7 @@ struct Walk {
             while (pos >= past) {  // sequences without units are passed over
                 ++s;
                 first = past;
-                past = a.units_off[s + 1];
+                past = units(s + 1);
             }
             g.s = s;
             g.len = index_at(a.lens, a.idx64, s);
@@ -146,6 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag, fail_s[2];
     __shared__ float corr_s[kRows], inv_s[kRows];
+    __shared__ uint32_t units_s[kSmallSeqs + 1];
 
     const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     T* out = static_cast<T*>(a.out);
@@ -180,12 +184,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_after();
     const uint32_t tmem = tmem_base;
     pdl_wait();
+    bool planned;
+    uint64_t total;
+    if (a.small) {
+        const SmallPlan sp = small_plan(a.plan, a.idx64, units_s, nullptr);
+        if (blockIdx.x == 0 && threadIdx.x == 0) store_plan(a.plan, sp);
+        planned = sp.key == kVerdictOk;
+        total = planned ? sp.units : 0;
+    } else {
+        planned = a.hdr->verdict == kVerdictOk;
+        total = planned ? a.hdr->total_units : 0;
+    }
+    auto units = [&](uint64_t s) { return a.small ? (uint64_t)units_s[s] : (uint64_t)a.units_off[s]; };
     // queries of sequences without tokens: zeros, 32 sequences to a warp at a time
     auto zero_empty = [&](uint64_t w, uint64_t warps) {
         for (uint64_t k = w;; k += warps) {  // the CTA's k-th 32 sequences, whichever warps share them
             const uint64_t s0 = (blockIdx.x + k * gridDim.x) * 32, s = s0 + lane;
             if (s0 >= a.num_seqs) break;
-            unsigned empty = __ballot_sync(0xffffffffu, s < a.num_seqs && a.units_off[s] == a.units_off[s + 1]);
+            unsigned empty = __ballot_sync(0xffffffffu, s < a.num_seqs && units(s) == units(s + 1));
             for (; empty; empty &= empty - 1) {
                 const uint64_t e = s0 + __ffs(empty) - 1;
                 const uint64_t q0 = a.q_ptr ? index_at(a.q_ptr, a.idx64, e) : e;
@@ -197,17 +213,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     };
     const uint32_t tiles = a.group_rows / kRows;
-    const bool planned = a.hdr->verdict == kVerdictOk;
-    const uint64_t total = planned ? a.hdr->total_units : 0, Lw = (total + a.workers - 1) / a.workers;
+    const uint64_t Lw = (total + a.workers - 1) / a.workers;
     const uint64_t v = blockIdx.x / tiles, beg = umin(v * Lw, total), end = umin(beg + Lw, total);
-    if (planned && threadIdx.x == 96 && blockIdx.x % tiles == 0) write_merge(a, v);  // (a softmax thread, idle yet)
+    if (planned && threadIdx.x == 96 && blockIdx.x % tiles == 0) write_merge(a, v, total, units);  // (a softmax thread, idle yet)
     if (beg >= end) {  // the whole CTA
         if (planned) zero_empty(warp, 8);
         if (warp == 1) tmem_free(tmem, kTmemCols);
         return;
     }
 
-    Walk walk(a, beg, end, (uint32_t)(blockIdx.x % tiles), lane);
+    Walk walk(a, a.small ? units_s : nullptr, beg, end, (uint32_t)(blockIdx.x % tiles), lane);
     Segment g;
     // true unless the wait ran out or another role stopped; warp_wait for whole warps
     auto wait_for = [&](unsigned long long* bar, uint32_t parity) {

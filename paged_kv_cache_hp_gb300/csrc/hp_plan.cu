@@ -32,12 +32,6 @@ __device__ __forceinline__ bool gt_sum(unsigned long long c_lo, unsigned c_carry
     return c_lo > lo;
 }
 
-// a / b, in 32 bits where both fit (a 64-bit division is some hundred instructions).
-__device__ __forceinline__ unsigned long long quotient(unsigned long long a, unsigned long long b)
-{
-    return (a | b) >> 32 ? a / b : (unsigned long long)((unsigned)a / (unsigned)b);
-}
-
 template <typename IndexT, int MODE>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a)
 {

@@ -1,5 +1,5 @@
-// hp_scan.cuh -- the saturating block scan of the one-CTA planning kernels (hp_plan.cu,
-// hp_step.cu).
+// hp_scan.cuh -- helpers of the planning kernels (hp_plan.cu, hp_step.cu, hp_latent_plan.cuh): the
+// saturating block scan of the one-CTA ones, a division.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -13,6 +13,12 @@ __device__ __forceinline__ unsigned long long sat_add(unsigned long long a, unsi
 {
     unsigned long long c = a + b;
     return c < a ? ~0ull : c;
+}
+
+// a / b, in 32 bits where both fit (a 64-bit division is some hundred instructions).
+__device__ __forceinline__ unsigned long long quotient(unsigned long long a, unsigned long long b)
+{
+    return (a | b) >> 32 ? a / b : (unsigned long long)((unsigned)a / (unsigned)b);
 }
 
 // Exclusive block scan of two counters at once with saturating addition (which is

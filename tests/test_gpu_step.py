@@ -1119,3 +1119,92 @@ def test_tables_and_appends_on_two_streams(hp):
     for s, d, rope, pool, kv, st, stream in runs:
         check_step(hp, s)
         assert st.item() == 0 and torch.equal(pool.view(-1, 576)[s["o"]["slot_map"]][:, :512], kv[:, :512])
+
+
+@pytest.mark.parametrize("form", ["decode", "prefill"])
+@pytest.mark.parametrize("S", [1, 3, 128, 129])
+def test_plans_of_small_and_large_batches(hp, form, S):
+    """Up to 128 sequences (and 4,096 table entries) the first kernel makes the plan itself, beyond
+    a launch before it does: the same results and the same verdicts on both sides, the first rule
+    that fails naming itself, nothing else written."""
+    import torch
+    rng = np.random.default_rng(S)
+    lens, nq = rng.integers(1, 200, S), rng.integers(0, 3, S)
+    nq[0], lens[-1] = 1, 20
+    nq = np.minimum(nq, lens)
+    w = selecting_weights(4, 128, 128, 512, ref.torch_dtype("bf16"), 6)
+
+    def make():
+        return Latent(hp, lens, nq, 4, 512, 576, 16, "bf16", it=S % 2, seed=S, rows_behind=1)
+    b = make()
+    if form == "decode":
+        check_decode(b, run_decode(b, 0.07), 0.07)
+    else:
+        check_prefill(b, run_prefill(b, 128, 128, w, 0.07), 128, 128, w, 0.07, exact_kv=True)
+    T = b.T
+    faults = ["page", "len", "end", "start", "order", "qstart", "qorder", "qend", "page+len", "start+len"]
+    for what in faults + (["room"] if form == "prefill" else []):
+        if S == 1 and what in ("order", "qorder"):
+            continue
+        b = make()
+        table, sp, ln = b.desc._keep[1], b.desc._keep[2], b.desc._keep[3]
+        kv, name = int(lens.sum()), {"page": "PAGE_ID", "len": "LEN", "end": "SEQ_PTR_END", "start": "SEQ_PTR_START",
+                                     "order": "SEQ_PTR_ORDER", "qstart": "NEW_PTR_START", "qorder": "NEW_PTR_ORDER",
+                                     "qend": "NEW_PTR_END", "room": "OUT_SIZE"}[what.split("+")[0]]
+        if "page" in what:
+            table[len(table) - 1] = 10 ** 6
+        if "len" in what:
+            ln[S - 1] = 33
+        if what == "end":
+            sp[S] += 1
+        if "start" in what and what[0] != "q":
+            sp[0] = 1
+        if what == "order":
+            sp[S // 2] = int(sp[S // 2 + 1]) + 1
+        if what == "qstart":
+            b.q_ptr[0] = 1
+        if what == "qorder":
+            b.q_ptr[S // 2] = T + 5
+        if what == "room":
+            kv -= 1
+        total = T - 2 if what == "qend" else T
+        if form == "decode":
+            q = b.queries(576)
+            out = torch.full((T, 4, 512), 9.0, dtype=b.dt, device="cuda")
+            rc, n = hp.hp_latent_decode_workspace_bytes(b.desc, 512, T, 4)
+        else:
+            q = b.queries(192)
+            out = torch.full((T, 4, 128), 9.0, dtype=b.dt, device="cuda")
+            rc, n = hp.hp_latent_prefill_workspace_bytes(b.desc, 512, 128, 128, T, 4, kv)
+        if total <= 0:
+            continue
+        ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+        if form == "decode":
+            rc = hp.hp_latent_decode(b.desc, 512, q, b.q_ptr, total, 4, 0.1, out, ws, b.status)
+        else:
+            rc = hp.hp_latent_prefill(b.desc, 512, w.cuda(), 128, 128, q, b.q_ptr, total, 4, 0.1, out, kv, ws, b.status)
+        torch.cuda.synchronize()
+        assert hp.status_name(rc) == "HP_OK" and hp.status_name(b.status.item()) == "HP_ERR_" + name, what
+        assert (out == 9).all(), what
+
+
+@pytest.mark.parametrize("pages", [4096, 4097])
+def test_plans_of_short_and_long_tables(hp, pages):
+    """One sequence whose table is as long as its plan's own check takes, and one entry longer; a bad
+    last entry is seen on both sides."""
+    import torch
+    for kind in ("decode", "prefill"):
+        b = Latent(hp, A([pages * 8 - 3]), A([2]), 2, 512, 576, 8, "f16", seed=pages)
+        w = selecting_weights(2, 128, 128, 512, b.dt, 6)
+        if kind == "decode":
+            check_decode(b, run_decode(b, 0.07), 0.07)
+        else:
+            check_prefill(b, run_prefill(b, 128, 128, w, 0.07), 128, 128, w, 0.07, exact_kv=True)
+        b.desc._keep[1][pages - 1] = 2 ** 30
+        rc, n = hp.hp_latent_decode_workspace_bytes(b.desc, 512, 2, 2)
+        ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+        out = torch.full((2, 2, 512), 9.0, dtype=b.dt, device="cuda")
+        q = torch.zeros((2, 2, 576), dtype=b.dt, device="cuda")
+        assert hp.hp_latent_decode(b.desc, 512, q, b.q_ptr, 2, 2, 0.1, out, ws, b.status) == 0
+        torch.cuda.synchronize()
+        assert hp.status_name(b.status.item()) == "HP_ERR_PAGE_ID" and (out == 9).all()
