@@ -289,9 +289,10 @@ __global__ void __launch_bounds__(256, 4) latent_merge_kernel(const LatentArgs a
 // --------------------------------------------------------------------- expanded form
 
 // The latent rows of each sequence in order, padded with zeros to a multiple of kLatentPad, so
-// that a block of 128 rows lies in one sequence.  Four rows per warp, 16 bytes per lane.  For the tensor cores
-// (blocked) the latent part is a matrix of its own and the rope keys lie as shared memory holds
-// them.
+// that a block of 128 rows lies in one sequence.  Four rows per warp, 16 bytes per lane.  For the
+// tensor cores (blocked) the latent part is a matrix of its own, the rope keys lie as shared memory
+// holds them, and the kernel describes each block of queries (a search per CTA of the attention
+// would be ten dependent loads); for a small batch it makes the plan first (hp_latent_plan.cuh).
 __global__ void __launch_bounds__(256) latent_rows_kernel(const LatentPrefillArgs a)
 {
     constexpr int kRowsWarp4 = 4;  // rows of a warp, looked up and loaded together

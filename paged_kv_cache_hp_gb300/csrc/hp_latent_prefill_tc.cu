@@ -7,11 +7,11 @@
 // epilogue (TMEM -> registers -> shared memory -> bulk store, eight warps) overlaps the next
 // tile's products.  The SM's reads bound it: 384 KiB a tile arrive at 49 bytes a cycle where the
 // tensor pipe would take 94 (tiles of 256 x 256 read a third less and gain nothing, their
-// epilogue standing between the tiles: 144 against 139 us at 21,000 rows and 32 heads).  A CTA's tiles are consecutive, so all the columns of a few row blocks are in
-// flight at once and both operands
-// come from L2.  KV goes to the workspace in blocks of 128 rows x
-// 64 columns laid out as shared memory will hold them (head, row block, K0 K1 V0 V1), so that the
-// attention below loads 16 KiB pieces with untiled bulk copies; the rope keys likewise (hp_latent.cu).
+// epilogue standing between the tiles: 144 against 139 us at 21,000 rows and 32 heads).  A CTA's
+// tiles are consecutive, so all the columns of a few row blocks are in flight at once and both
+// operands come from L2.  KV goes to the workspace in blocks of 128 rows x 64 columns laid out as
+// shared memory will hold them (head, row block, K0 K1 V0 V1), so that the attention below loads
+// 16 KiB pieces with untiled bulk copies; the rope keys likewise (hp_latent.cu).
 //
 // latent_prefill_kernel: softmax(scale Q K^T) V for one head and 256 queries of a sequence, as
 // two tiles of 128 queries that share the keys' 128-row blocks: K = [expanded 128 | rope 64], V =
