@@ -10,9 +10,11 @@
 //
 // Errors: a token is skipped by the warp that meets it.  *d_status comes from one extra CTA that
 // looks at every token's slot and positions while the others work (no launch of its own; a
-// batch of 64 tokens takes 3.5 us in a graph), up to kReportTokens; beyond, where that CTA would be the
-// last to finish (16,001 tokens: 69 us for 20 us of work), a memset before the kernel and atomicMin
-// over the codes.  Either way it is the smallest code of the batch, whatever the order.
+// batch of 64 tokens takes 3.5 us in a graph), or from a memset before the kernel and atomicMin over
+// the codes where that CTA would be the last to finish: it takes 2 ns a token, the others 0.23 ns a
+// KiB, so batches of more than kReportTokens go by the bytes of a token (8,193 tokens of 25 KiB:
+// 45.2 us against 47.2 with the memset; 16,001 of 6.7 KiB: 32.5 against 28.8).  Either way it is the
+// smallest code of the batch, whatever the order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -76,27 +78,49 @@ __device__ __forceinline__ uint64_t position(const RopeArgs& r, uint64_t tokens,
                    : (uint64_t)static_cast<const unsigned int*>(r.positions)[i];
 }
 
-// HP_OK, or why token t, of slot `slot`, is not processed (a padding token: HP_OK).
+// HP_OK, or why a token of slot `slot` is not processed (a padding token: HP_OK); far: one of its
+// positions is past the table.
+__device__ __forceinline__ int code_of(const AppendArgs& a, int64_t slot, bool far)
+{
+    if (slot < 0) return HP_OK;
+    return far ? HP_ERR_LEN : ((uint64_t)slot >= a.num_slots ? HP_ERR_PAGE_ID : HP_OK);
+}
+
 __device__ __forceinline__ int token_error(const AppendArgs& a, uint64_t t, int64_t slot)
 {
     bool far = false;
     if (a.rope.rot)
         for (uint32_t x = 0; x < a.rope.axes; ++x) far |= position(a.rope, a.tokens, x, t) >= a.rope.max_pos;
-    if (slot < 0) return HP_OK;
-    return far ? HP_ERR_LEN : ((uint64_t)slot >= a.num_slots ? HP_ERR_PAGE_ID : HP_OK);
+    return code_of(a, slot, far);
 }
 
-constexpr uint64_t kReportTokens = 2048;
+constexpr uint64_t kReportTokens = 2048, kReportBytes = 12288;
 
-// The extra CTA: the smallest code of all tokens.
+// The extra CTA, the grid's first: the smallest code of all tokens, eight of each thread's looked at
+// together (one by one they took 69 us for 16,001).
 __device__ __forceinline__ void report_all(const AppendArgs& a)
 {
+    constexpr int kTogether = 8;
     __shared__ int s_code;
     if (threadIdx.x == 0) s_code = HP_OK;
     __syncthreads();
     int code = HP_OK;
-#pragma unroll 4
-    for (uint64_t t = threadIdx.x; t < a.tokens; t += kThreads) code = min(code, token_error(a, t, a.slot_map[t]));
+    for (uint64_t t0 = threadIdx.x; t0 < a.tokens; t0 += kTogether * kThreads) {
+        int64_t slot[kTogether];
+        bool far[kTogether];
+#pragma unroll
+        for (int u = 0; u < kTogether; ++u) {
+            const uint64_t t = t0 + u * kThreads;
+            slot[u] = t < a.tokens ? a.slot_map[t] : -1;
+            far[u] = false;
+#pragma unroll
+            for (uint32_t x = 0; x < 4; ++x)
+                if (t < a.tokens && a.rope.rot && x < a.rope.axes)
+                    far[u] |= position(a.rope, a.tokens, x, t) >= a.rope.max_pos;
+        }
+#pragma unroll
+        for (int u = 0; u < kTogether; ++u) code = min(code, code_of(a, slot[u], far[u]));
+    }
     if (code != HP_OK) atomicMin(&s_code, code);
     __syncthreads();
     if (threadIdx.x == 0) *a.d_status = s_code;
@@ -287,15 +311,16 @@ __device__ __forceinline__ void heads_out(const AppendArgs& a, const Turn& turn,
 template <typename T, int L>
 __global__ void __launch_bounds__(kThreads, 3) qk_append_kernel(const AppendArgs a, uint32_t parts, bool report_here)
 {
-    if (!report_here && a.d_status && blockIdx.x == gridDim.x - 1) {
+    const unsigned extra = !report_here && a.d_status != nullptr;
+    if (extra && blockIdx.x == 0) {
         report_all(a);
         return;
     }
     const unsigned lane = threadIdx.x & 31, sub = lane / L, l = lane % L;
-    const uint64_t warps = (uint64_t)(gridDim.x - (!report_here && a.d_status != nullptr)) * kWarpsRope;
+    const uint64_t warps = (uint64_t)(gridDim.x - extra) * kWarpsRope;
     const uint32_t d0 = l * 8, step = parts * (32 / L);
     const bool live = d0 < a.dim, inter = a.rope.inter;
-    for (uint64_t w = (uint64_t)blockIdx.x * kWarpsRope + (threadIdx.x >> 5); w < a.tokens * parts;
+    for (uint64_t w = (uint64_t)(blockIdx.x - extra) * kWarpsRope + (threadIdx.x >> 5); w < a.tokens * parts;
          w += warps) {
         const uint64_t t = w / parts;
         const uint32_t h0 = (uint32_t)(w % parts) * (32 / L);
@@ -334,16 +359,17 @@ __global__ void __launch_bounds__(kThreads, 3) qk_append_kernel(const AppendArgs
 template <typename T, int L, int kLatVec>
 __global__ void __launch_bounds__(kThreads, 3) latent_append_kernel(const AppendArgs a, uint32_t parts, bool report_here)
 {
-    if (!report_here && a.d_status && blockIdx.x == gridDim.x - 1) {
+    const unsigned extra = !report_here && a.d_status != nullptr;
+    if (extra && blockIdx.x == 0) {
         report_all(a);
         return;
     }
     constexpr int U = kBatch<T>;
     const unsigned lane = threadIdx.x & 31, sub = lane / L, l = lane % L;
-    const uint64_t warps = (uint64_t)(gridDim.x - (!report_here && a.d_status != nullptr)) * kWarpsRope;
+    const uint64_t warps = (uint64_t)(gridDim.x - extra) * kWarpsRope;
     const uint32_t d0 = l * 8, R = a.latent_dim, D = a.rope.rot, step = parts * (32 / L);
     const bool live = d0 < D;
-    for (uint64_t w = (uint64_t)blockIdx.x * kWarpsRope + (threadIdx.x >> 5); w < a.tokens * parts;
+    for (uint64_t w = (uint64_t)(blockIdx.x - extra) * kWarpsRope + (threadIdx.x >> 5); w < a.tokens * parts;
          w += warps) {
         const uint64_t t = w / parts;
         const uint32_t part = (uint32_t)(w % parts);
@@ -444,7 +470,9 @@ int launch_l(const AppendArgs& a, cudaStream_t st)
     const uint64_t parts = want < 1 ? 1 : (want < groups ? want : (groups ? groups : 1));
     const uint64_t warps = a.tokens * parts, ctas = (warps + kWarpsRope - 1) / kWarpsRope;
     const uint64_t cap = (uint64_t)sms * 64;
-    const bool report_here = a.d_status && a.tokens > kReportTokens;
+    const uint64_t row = sizeof(T) * (LATENT ? 2ull * a.hq * a.dim + 2ull * (a.latent_dim + a.dim)
+                                             : (2ull * a.hq + 4ull * a.hkv) * a.dim);  // read and written
+    const bool report_here = a.d_status && a.tokens > kReportTokens && row < kReportBytes;
     if (report_here && cudaMemsetAsync(a.d_status, 0, sizeof(int), st) != cudaSuccess) return HP_ERR_CUDA;
     const unsigned grid = (unsigned)(ctas < cap ? ctas : cap) + (a.d_status && !report_here);
     if (LATENT && a.latent_dim <= 512)

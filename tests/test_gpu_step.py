@@ -1208,3 +1208,33 @@ def test_plans_of_short_and_long_tables(hp, pages):
         assert hp.hp_latent_decode(b.desc, 512, q, b.q_ptr, 2, 2, 0.1, out, ws, b.status) == 0
         torch.cuda.synchronize()
         assert hp.status_name(b.status.item()) == "HP_ERR_PAGE_ID" and (out == 9).all()
+
+
+def test_appends_report_whatever_the_rows(hp):
+    """3,000 tokens of 2 KiB and of 18 KiB, whose codes are gathered in two ways: the smallest code
+    of the batch, the tokens without a fault stored."""
+    import torch
+    T, D, P = 3000, 128, 16
+    cs = dev(ref.cos_sin(50, D))
+    for hq, hkv in ((1, 1), (32, 2)):
+        x = torch.randn((T, (hq + 2 * hkv) * D)).to(torch.bfloat16).cuda()
+        q, k, v = x.split([hq * D, hkv * D, hkv * D], 1)
+        for slots, far, name in (((), (), "HP_OK"), ((2999,), (), "HP_ERR_PAGE_ID"), ((5, 2050), (2998,), "HP_ERR_LEN"),
+                                 ((), (2049,), "HP_ERR_LEN")):
+            slot, pos = np.arange(T, dtype=np.int64), np.zeros((2, T), np.uint32)
+            for t in slots:
+                slot[t] = 190 * P
+            for t in far:
+                pos[1, t] = 50
+            kp = torch.zeros((190, P, hkv, D), dtype=torch.bfloat16, device="cuda")
+            vp, qo, st = torch.zeros_like(kp), torch.zeros((T, hq * D), dtype=torch.bfloat16, device="cuda"), status_tensor()
+            r = hp.rope_desc(cos_sin=cs, positions=index_tensor(pos, "cuda"), sections=(32, 32))
+            d = hp.qk_desc(q=q, k=k, v=v, q_out=qo, num_q_heads=hq, num_kv_heads=hkv, head_dim=D, dtype="bf16",
+                           slot_map=dev(slot), k_pool=kp, v_pool=vp, num_pages=190, page_size=P)
+            assert hp.hp_qk_norm_rope_append(d, r, st) == 0
+            torch.cuda.synchronize()
+            assert hp.status_name(st.item()) == name
+            live = np.ones(T, bool)
+            live[list(slots) + list(far)] = False
+            got = vp.view(-1, hkv * D)[:T].cpu()
+            assert torch.equal(got[live], v.cpu()[live]) and not got[~live].any() and not qo.cpu()[~live].any()
