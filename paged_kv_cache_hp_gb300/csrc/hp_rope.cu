@@ -311,6 +311,7 @@ __device__ __forceinline__ void heads_out(const AppendArgs& a, const Turn& turn,
 template <typename T, int L>
 __global__ void __launch_bounds__(kThreads, 3) qk_append_kernel(const AppendArgs a, uint32_t parts, bool report_here)
 {
+    pdl_wait();
     const unsigned extra = !report_here && a.d_status != nullptr;
     if (extra && blockIdx.x == 0) {
         report_all(a);
@@ -359,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, 3) qk_append_kernel(const AppendArgs
 template <typename T, int L, int kLatVec>
 __global__ void __launch_bounds__(kThreads, 3) latent_append_kernel(const AppendArgs a, uint32_t parts, bool report_here)
 {
+    pdl_wait();
     const unsigned extra = !report_here && a.d_status != nullptr;
     if (extra && blockIdx.x == 0) {
         report_all(a);
@@ -475,13 +477,12 @@ int launch_l(const AppendArgs& a, cudaStream_t st)
     const bool report_here = a.d_status && a.tokens > kReportTokens && row < kReportBytes;
     if (report_here && cudaMemsetAsync(a.d_status, 0, sizeof(int), st) != cudaSuccess) return HP_ERR_CUDA;
     const unsigned grid = (unsigned)(ctas < cap ? ctas : cap) + (a.d_status && !report_here);
-    if (LATENT && a.latent_dim <= 512)
-        latent_append_kernel<T, L, 2><<<grid, kThreads, 0, st>>>(a, (uint32_t)parts, report_here);
-    else if (LATENT)
-        latent_append_kernel<T, L, 4><<<grid, kThreads, 0, st>>>(a, (uint32_t)parts, report_here);
-    else
-        qk_append_kernel<T, L><<<grid, kThreads, 0, st>>>(a, (uint32_t)parts, report_here);
-    return cudaGetLastError() == cudaSuccess ? HP_OK : HP_ERR_CUDA;
+    // A dependent launch: the CTAs are there when the stream's last kernel ends, which each waits for
+    // before it looks at memory.
+    auto kernel = LATENT ? (a.latent_dim <= 512 ? latent_append_kernel<T, L, 2> : latent_append_kernel<T, L, 4>)
+                         : qk_append_kernel<T, L>;
+    return launch_dependent(kernel, grid, kThreads, 0, st, a, (uint32_t)parts, report_here) == cudaSuccess ? HP_OK
+                                                                                                        : HP_ERR_CUDA;
 }
 
 template <typename T, bool LATENT>

@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(kPlanThreads) step_fused_kernel(const StepArgs
     __shared__ uint32_t tok[kFusedSeqs + 1], pages[kFusedSeqs + 1], sp[kFusedSeqs + 1];
     __shared__ unsigned long long len[kFusedSeqs + 1];
     const hp_step_desc& d = a.d;
+    pdl_wait();
     const unsigned long long sp_first = static_cast<const IndexT*>(d.seq_ptr)[0];
     const unsigned long long sp_last = static_cast<const IndexT*>(d.seq_ptr)[d.num_seqs];
     const Sums all = scan_range<IndexT, true, uint32_t>(a, 0, d.num_seqs, tok, pages, sp, len);
@@ -215,6 +216,7 @@ template <typename IndexT>
 __global__ void __launch_bounds__(kPlanThreads) step_scan_kernel(const StepArgs a)
 {
     pdl_trigger();
+    pdl_wait();
     const uint64_t s0 = (uint64_t)blockIdx.x << a.block_log, s1 = umin(s0 + (1ull << a.block_log), a.d.num_seqs);
     const Sums r = scan_range<IndexT, false, unsigned long long>(a, s0, s1, a.ws.rows_off + s0, a.ws.units_off + s0);
     if (threadIdx.x == 0) {
@@ -346,8 +348,9 @@ int launch_t(const StepArgs& a, cudaStream_t st)
 {
     const hp_step_desc& d = a.d;
     if (d.num_seqs <= kFusedSeqs && d.table_cap + d.token_cap <= kFusedItems) {
-        step_fused_kernel<IndexT><<<1, kPlanThreads, 0, st>>>(a);
-        return cudaGetLastError() == cudaSuccess ? HP_OK : HP_ERR_CUDA;
+        // (a dependent launch, as the scan: there when the stream's last kernel ends, and waiting for it)
+        return launch_dependent(step_fused_kernel<IndexT>, 1, kPlanThreads, 0, st, a) == cudaSuccess ? HP_OK
+                                                                                                  : HP_ERR_CUDA;
     }
     const uint64_t ec = (d.table_cap + kFillItems - 1) / kFillItems, tc = (d.token_cap + kFillItems - 1) / kFillItems;
     const uint64_t grid = ec + tc + d.num_seqs / 256 + 1;
@@ -355,8 +358,7 @@ int launch_t(const StepArgs& a, cudaStream_t st)
     b.block_log = 10;
     while ((d.num_seqs >> b.block_log) >= kMaxBlocks) ++b.block_log;
     const unsigned blocks = (unsigned)(d.num_seqs >> b.block_log) + 1;
-    step_scan_kernel<IndexT><<<blocks, kPlanThreads, 0, st>>>(b);
-    if (cudaGetLastError() != cudaSuccess) return HP_ERR_CUDA;
+    if (launch_dependent(step_scan_kernel<IndexT>, blocks, kPlanThreads, 0, st, b) != cudaSuccess) return HP_ERR_CUDA;
     return launch_dependent(step_fill_kernel<IndexT>, (unsigned)grid, 256, 0, st, b, blocks, ec, tc) == cudaSuccess
                ? HP_OK
                : HP_ERR_CUDA;
