@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a)
     __shared__ unsigned long long s_key, s_len;
     __shared__ int s_fault;
     __shared__ unsigned long long s_carry_rows, s_carry_units;
+    if (MODE == kPlanLatent) pdl_wait();  // a dependent launch itself; nothing behind it starts before
     pdl_trigger();  // let the table check start scanning now
     unsigned long long sp_first = 0, sp_last = 0, np_first = 0, np_last = 0;  // thread 0's, needed last
     if (threadIdx.x == 0) {
@@ -342,8 +343,8 @@ int launch_plan_t(PlanMode mode, const PlanArgs& a, cudaStream_t st)
         plan_kernel<IndexT, kPlanAppend><<<1, kPlanThreads, 0, st>>>(a);
     else if (mode == kPlanAttention)
         plan_kernel<IndexT, kPlanAttention><<<1, kPlanThreads, 0, st>>>(a);
-    else
-        plan_kernel<IndexT, kPlanLatent><<<1, kPlanThreads, 0, st>>>(a);
+    else if (launch_dependent(plan_kernel<IndexT, kPlanLatent>, 1, kPlanThreads, 0, st, a) != cudaSuccess)
+        return HP_ERR_CUDA;
     if (cudaGetLastError() != cudaSuccess) return HP_ERR_CUDA;
     if (a.strict && a.table_len > 0 && !a.check_table) {
         int dev = 0;

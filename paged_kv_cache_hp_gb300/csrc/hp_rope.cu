@@ -13,7 +13,7 @@
 // batch of 64 tokens takes 3.5 us in a graph), or from a memset before the kernel and atomicMin over
 // the codes where that CTA would be the last to finish: it takes 2 ns a token, the others 0.23 ns a
 // KiB, so batches of more than kReportTokens go by the bytes of a token (8,193 tokens of 25 KiB:
-// 45.2 us against 47.2 with the memset; 16,001 of 6.7 KiB: 32.5 against 28.8).  Either way it is the
+// 42.7 us against 47.2 with the memset; 16,001 of 6.7 KiB: 30.6 against 28.8).  Either way it is the
 // smallest code of the batch, whatever the order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
