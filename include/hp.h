@@ -495,7 +495,10 @@ int hp_attention_decode_planned(const hp_paged_desc* k_desc, const void* v_pool,
  * output and stores it in those slots, layer by layer; then hp_attention_decode, or
  * hp_latent_decode / hp_latent_prefill, reads the pages.  (The pages cited above define the
  * layout these operators read and write; the operators themselves are this library's.)  Calls
- * whose work may overlap on the GPU need workspaces and status words of their own.
+ * whose work may overlap on the GPU need workspaces and status words of their own.  A call's first
+ * kernel may be set up while the stream's last kernel ends, and touches memory once that kernel is
+ * complete (a kernel of the caller's that is itself launched programmatically has to have waited for
+ * what it was launched behind, as this library's do).
  */
 
 /*
