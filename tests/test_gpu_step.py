@@ -1238,3 +1238,41 @@ def test_appends_report_whatever_the_rows(hp):
             live[list(slots) + list(far)] = False
             got = vp.view(-1, hkv * D)[:T].cpu()
             assert torch.equal(got[live], v.cpu()[live]) and not got[~live].any() and not qo.cpu()[~live].any()
+
+
+@pytest.mark.parametrize("form", ["decode", "prefill"])
+def test_a_large_batch_in_a_graph(hp, form):
+    """200 sequences, whose plan is a launch of its own, captured and replayed on other queries."""
+    import torch
+    lens = np.random.default_rng(4).integers(1, 150, 200)
+    b = Latent(hp, lens, np.ones(200, np.int64), 4, 512, 576, 16, "bf16", seed=4)
+    w = selecting_weights(4, 128, 128, 512, b.dt, 6)
+    wd, q = w.cuda(), b.queries(576 if form == "decode" else 192)
+    kv = int(lens.sum())
+    if form == "decode":
+        rc, n = hp.hp_latent_decode_workspace_bytes(b.desc, 512, b.T, 4)
+    else:
+        rc, n = hp.hp_latent_prefill_workspace_bytes(b.desc, 512, 128, 128, b.T, 4, kv)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    out = torch.zeros((b.T, 4, 512 if form == "decode" else 128), dtype=b.dt, device="cuda")
+
+    def call():
+        if form == "decode":
+            return hp.hp_latent_decode(b.desc, 512, q, b.q_ptr, b.T, 4, 0.07, out, ws, b.status)
+        return hp.hp_latent_prefill(b.desc, 512, wd, 128, 128, q, b.q_ptr, b.T, 4, 0.07, out, kv, ws, b.status)
+    assert call() == 0
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        assert call() == 0
+    for _ in range(2):
+        b.q = torch.randn(q.shape).to(b.dt)
+        q.copy_(b.q)
+        out.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert b.status.item() == 0
+        if form == "decode":
+            check_decode(b, host(out), 0.07)
+        else:
+            check_prefill(b, host(out), 128, 128, w, 0.07, exact_kv=True)
