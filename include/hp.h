@@ -687,7 +687,8 @@ int hp_latent_decode_workspace_bytes(const hp_paged_desc* desc, uint32_t latent_
  * nor written) may be NULL: one query per sequence, total_q = num_seqs.
  * out (device, [total_q, num_q_heads, latent_dim], the pool's type).  Scores, softmax
  * statistics and sums are fp32; on the tensor cores the weights enter the value product rounded
- * to the pool's type, and the result is rounded once.  The values of every token below seq_lens
+ * to the pool's type (f16: times a common 2^7, so that a small one is off by at most 2^-32 of the
+ * row's largest), and the result is rounded once.  The values of every token below seq_lens
  * have to be finite (a query's weight for a later token of its sequence is zero, not absent);
  * slots past a sequence's length may hold anything, and a NaN in a query stays in its own row
  * of out.

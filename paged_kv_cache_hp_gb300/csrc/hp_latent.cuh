@@ -54,7 +54,8 @@ struct LatentArgs {
     const WsHeader* hdr;
     const unsigned long long* units_off;
     float* part_acc;          // [2 * workers * group_rows, R]
-    float2* part_ml;          // their maxima (log2 units) and sums
+    float2* part_ml;          // their maxima (log2 units) and sums (tensor cores: sums and accumulators
+                              // times 2^kWeightLift)
     LatentMerge* merge;       // [workers], written by the attention kernel for the merge
     void* out;                // [total_q, H, R]
     int* d_status;

@@ -483,8 +483,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            const float mu = m == -INFINITY ? 0.0f : m;
-            const uint64_t qs2 = pair_of(qs, qs), mu2 = pair_of(-mu, -mu);
+            const float base = kWeightLift<T> - (m == -INFINITY ? 0.0f : m);
+            const uint64_t qs2 = pair_of(qs, qs), base2 = pair_of(base, base);
             uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float* x = reinterpret_cast<const float*>(xr[c]);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    float2 w = of_pair(fma2(pair_of(x[2 * i], x[2 * i + 1]), qs2, mu2));
+                    float2 w = of_pair(fma2(pair_of(x[2 * i], x[2 * i + 1]), qs2, base2));
                     w.x = exp2_approx(w.x);
                     w.y = exp2_approx(w.y);
                     sum[i & 1] = add2(sum[i & 1], pair_of(w.x, w.y));

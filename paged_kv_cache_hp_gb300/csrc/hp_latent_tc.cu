@@ -484,9 +484,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         named_sync(1, kSoftmax);  // corr_s is free again
                     }
                 }
-                // weights: summed in fp32, rounded to the element type for the product
+                // weights (times 2^kWeightLift): summed in fp32, rounded to the element type for the product
                 const float m0 = m[0] == -INFINITY ? 0.0f : m[0], m1 = m[1] == -INFINITY ? 0.0f : m[1];
-                const uint64_t qs2 = pair_of(qs, qs), n0 = pair_of(-m0, -m0), n1 = pair_of(-m1, -m1);
+                const float b0 = kWeightLift<T> - m0, b1 = kWeightLift<T> - m1;
+                const uint64_t qs2 = pair_of(qs, qs), n0 = pair_of(b0, b0), n1 = pair_of(b1, b1);
                 uint64_t sum0 = 0ull, sum1 = 0ull;
                 uint32_t w[16];
 #pragma unroll

@@ -209,6 +209,16 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// log2 of the common factor of a row's softmax weights where the latent attention rounds them to T
+// for the value product (which takes 16-bit operands only); the sum carries it too, so it cancels.
+// f16's smallest normal number is 2^-14, so that with the reference maximum's weight at 1 a weight of
+// 2^-18 was off by up to 2^-7 of itself and one of 2^-26 was lost, while the fp32 sum held it: a long
+// flat tail under one peak came out wrong (6% of it at 14.6 nats below, all at 17.6).  At 2^7 the
+// largest, 2^kTau above the reference, still fits (2^15 of 65,504), the normal range reaches 2^-21, and a
+// weight is off by 2^-32 of the reference's at most.  bf16 has fp32's range.
+template <typename T> constexpr float kWeightLift = 0.0f;
+template <> constexpr float kWeightLift<__half> = 7.0f;
+
 // Two fp32 at a time (one issue slot), and the largest of three.
 __device__ __forceinline__ uint64_t pair_of(float a, float b)
 {

@@ -1,0 +1,108 @@
+"""GPU parity of the serving-step operators where a sum, a mask or an index is at its edge, against
+the plain 64-bit implementations of step_ref.py; what its bounds do not cover is derived here."""
+import numpy as np
+import pytest
+
+import step_ref as ref
+from helpers import index_tensor
+from test_gpu_step import A, Latent, cores, run_decode, run_prefill
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ small weights in f16
+# A weight far below its row's largest is subnormal in f16: its rounding is off by half of the
+# smallest subnormal, 2^-25, however small it is.  The kernels hold a row's weights scaled so that
+# its reference maximum stands at 2^7, and that reference is at most the true maximum: in units of the
+# largest weight each is off by at most 2^-32 besides the relative u.  n weights then move the
+# value sum by at most n 2^-32 max |v|, divided by the sum of the weights (in the same units).
+SUBNORMAL = 2.0 ** -32
+TAIL = np.arange(23.0, 7.0, -1.0) + 0.625  # nats below the largest score, a head each
+
+
+def tail_rows(n, peak, W, dt, seed):
+    """Rows whose dim 0 is 1 at the peak and 0 elsewhere, dims 1 .. 8 the other way round; the
+    others are random."""
+    import torch
+    rows = torch.randn((n, W), generator=torch.Generator().manual_seed(seed))
+    rows[:, 0] = 0.0
+    rows[:, 1:9] = 1.0
+    rows[peak, 0] = 1.0
+    rows[peak, 1:9] = 0.0
+    return rows.to(dt)
+
+
+def fill(b, s, rows):
+    """Puts `rows` into sequence s of the batch's pool."""
+    import torch
+    table, sp = (t.cpu().numpy().astype(np.int64) for t in b.desc._keep[1:3])
+    t = np.arange(len(rows))
+    P = b.pool.shape[0] // b.desc.c.num_pages
+    b.pool[torch.from_numpy(table[sp[s] + t // P] * P + t % P).cuda()] = rows.cuda()
+    b.rows[s] = rows.double().numpy()
+
+
+def check_tail(b, s, q, k, v, scale, got, tag):
+    o, tol = ref.attention_row(q, k, v, scale, "f16")
+    x = k @ q * scale
+    tol = tol + len(k) * SUBNORMAL * np.abs(v).max(0) / np.exp(x - x.max()).sum()
+    err = np.abs(got - o)
+    assert np.isfinite(got).all() and (err <= tol).all(), (*tag, float((err / tol).max()))
+
+
+@pytest.mark.parametrize("kernel", ["cuda_cores", "default"])
+@pytest.mark.parametrize("peak", [0, 3000, 7999])
+def test_f16_flat_tail_under_one_peak(hp, kernel, peak):
+    """One token far above 7,999 equal ones, 8 to 24 nats by head: the tail's share of dims where
+    the peak has nothing is right, its weights being tiny and many.  200 sequences share the tokens'
+    pages, so that a worker's range holds whole ones."""
+    n, S, scale, H, P = 8000, 200, 1 / 16, len(TAIL), 64
+    b = Latent(hp, A([n]), A([1]), H, 512, 576, P, "f16", seed=31)
+    fill(b, 0, tail_rows(n, peak, 576, b.dt, 1))
+    table = b.desc._keep[1].cpu().numpy().view(np.uint32)
+    sp = (np.arange(S + 1) * len(table)).astype(np.uint32)
+    b.desc = hp.PagedDesc(b.pool, index_tensor(np.tile(table, S), "cuda"), index_tensor(sp, "cuda"),
+                          index_tensor(np.full(S, n, np.uint32), "cuda"), num_pages=b.desc.c.num_pages, page_size=P,
+                          num_heads=1, head_dim=576, dtype="f16", index_type=0, flags=cores(hp, kernel))
+    b.T, b.q_ptr = S, None
+    real = b.queries
+
+    def queries(width):
+        import torch
+        real(width)
+        b.q.zero_()
+        b.q[:, :, 0] = torch.from_numpy(16 * TAIL)
+        return b.q.cuda()
+    b.queries = queries
+    got = run_decode(b, scale)
+    for s in (0, 1, 77, 198, 199):
+        for h in range(H):
+            check_tail(b, 0, b.q[s, h].double().numpy(), b.rows[0], b.rows[0][:, :512], scale, got[s, h],
+                       ("decode", s, h))
+
+
+@pytest.mark.parametrize("kernel", ["cuda_cores", "default"])
+@pytest.mark.parametrize("peak", [0, 3000, 7999])
+def test_f16_flat_tail_under_one_peak_expanded(hp, kernel, peak):
+    """The same through the expanded form: three queries at the end of 8,000 tokens."""
+    import torch
+    n, scale, H = 8000, 1 / 16, len(TAIL)
+    b = Latent(hp, A([n]), A([3]), H, 512, 576, 64, "f16", seed=32, flags=cores(hp, kernel))
+    fill(b, 0, tail_rows(n, peak, 576, b.dt, 2))
+    w = torch.zeros((H, 256, 512), dtype=b.dt)  # every row picks one latent dim: K and V are exact
+    w[:, :128, 0] = 1.0
+    w[:, 128 + torch.arange(128), 1 + torch.arange(128)] = 1.0
+    real = b.queries
+
+    def queries(width):
+        real(width)
+        b.q.zero_()
+        b.q[:, :, 0] = torch.from_numpy(16 * TAIL)
+        return b.q.cuda()
+    b.queries = queries
+    got = run_prefill(b, 128, 128, w, scale)
+    for i in range(3):
+        c = b.rows[0][:n - 2 + i]
+        k = np.concatenate([np.repeat(c[:, :1], 128, 1), c[:, 512:]], 1)
+        for h in range(H):
+            check_tail(b, 0, b.q[i, h].double().numpy(), k, c[:, 1:129], scale, got[i, h], ("prefill", i, h))
