@@ -688,10 +688,9 @@ int hp_latent_decode_workspace_bytes(const hp_paged_desc* desc, uint32_t latent_
  * out (device, [total_q, num_q_heads, latent_dim], the pool's type).  Scores, softmax
  * statistics and sums are fp32; on the tensor cores the weights enter the value product rounded
  * to the pool's type (f16: times a common 2^7, so that a small one is off by at most 2^-32 of the
- * row's largest), and the result is rounded once.  The values of every token below seq_lens
- * have to be finite (a query's weight for a later token of its sequence is zero, not absent);
- * slots past a sequence's length may hold anything, and a NaN in a query stays in its own row
- * of out.
+ * row's largest), and the result is rounded once.  A row of the
+ * pool that is not finite spoils the queries that see its token and no others; slots past a
+ * sequence's length may hold anything, and a NaN in a query stays in its own row of out.
  * Supported: latent_dim a multiple of 64 up to 512; rope_dim a multiple of 8 from 8 to 64;
  * page_size <= 2^26 (HP_ERR_ARG otherwise).  latent_dim 512 with rope_dim 64 and pages of a
  * multiple of 8 slots run on the tensor cores, the others on the CUDA cores
@@ -732,7 +731,9 @@ int hp_latent_prefill_workspace_bytes(const hp_paged_desc* desc, uint32_t latent
  * num_q_heads, v_dim]).  K and V are rounded to the pool's type after fp32 accumulation over
  * latent_dim, on the tensor cores the weights before the value product, the result once;
  * scores, statistics and sums are fp32.  kv_tokens: at least the sum of seq_lens, or nothing is written and
- * HP_ERR_OUT_SIZE stored.  Finite values, empty rows and validation are as in hp_latent_decode.
+ * HP_ERR_OUT_SIZE stored.  The values of every token below seq_lens have to be finite (on the tensor
+ * cores a query's weight for a later token is zero, not absent).  Empty rows and validation are as in
+ * hp_latent_decode.
  * Supported: latent_dim and rope_dim as there; nope_dim a multiple of 16 and v_dim a multiple
  * of 16 up to 256 (HP_ERR_ARG otherwise).  latent_dim 512, rope_dim 64, nope_dim 128 and v_dim
  * 128 run on the tensor cores, the others on the CUDA cores.

@@ -73,6 +73,7 @@ constexpr float kTau = 8.0f;
 // token (k0 >= k1: nothing to compute).
 struct Segment {
     uint64_t s, len, q0, n, r0, k0, k1, ustart, steps;
+    uint64_t seen;  // tokens that the tile's last row sees, the most of its rows
     uint32_t rows;  // rows of the tile that exist, at least 1
 };
 
@@ -125,8 +126,8 @@ struct Walk {
             if (g.r0 >= all) continue;  // the group's last tile may have no rows
             g.rows = (uint32_t)umin(kRows, all - g.r0);
             const uint64_t last = (uint32_t)(g.r0 + g.rows - 1) / a.H;  // the tile's last query sees most
-            const uint64_t seen = g.len + 1 + last > g.n ? g.len + 1 + last - g.n : 0;
-            g.k1 = umin(g.k1, (seen + kTok - 1) / kTok);
+            g.seen = g.len + 1 + last > g.n ? g.len + 1 + last - g.n : 0;
+            g.k1 = umin(g.k1, (g.seen + kTok - 1) / kTok);
             return true;
         }
         return false;
@@ -403,6 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t r = row0 + 8 * i, qi = (g.r0 + r) / a.H;
                 vis[i] = r < g.rows && g.len + 1 + qi > g.n ? g.len + 1 + qi - g.n : 0;
             }
+            // tokens that all of them see
+            const uint64_t first = (uint32_t)g.r0 / a.H, all = g.len + 1 + first > g.n ? g.len + 1 + first - g.n : 0;
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
             for (uint64_t k = g.k0; k < g.k1; ++k, ++j) {
                 wait_one(&s_full[j % 2], (uint32_t)((j / 2) & 1), j);
@@ -511,12 +514,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     *reinterpret_cast<uint32_t*>(smem + kOffP + sw128_off(row0, c)) = w[2 * i];
                     *reinterpret_cast<uint32_t*>(smem + kOffP + sw128_off(row0 + 8, c)) = w[2 * i + 1];
                 }
-                // rows past the sequence become zeros before they meet their zero weights
-                if (t0 + kTok > g.len) {
+                // Values that meet zero weights have to be finite.  Tokens that no row of the tile sees, those
+                // past the sequence among them, become zeros; of tokens that some see, what is not finite
+                // does (the score of such a token is not finite either, so a row that sees it has its NaN
+                // from there, or the weight zero of a score of -inf).  With one query a sequence only
+                // the former occur.
+                if (t0 + kTok > all) {
+                    if (all < g.seen) wait_one(&c_full[j % 2], (uint32_t)((j / 2) & 1), j + 1);  // (read here too)
                     const uint32_t t = threadIdx.x - 64;  // chunk (t & 63) / 8, 16-byte piece t & 7
                     unsigned char* base = smem + kOffC + (uint32_t)(j % 2) * 8 * kGroup + ((t & 63) >> 3) * 1024 + (t & 7) * 16;
-                    for (uint32_t r = (uint32_t)(g.len - t0) + (t >> 6); r < kTok; r += 2)
-                        *reinterpret_cast<uint4*>(base + (r >> 3) * kGroup + (r & 7) * 128) = make_uint4(0, 0, 0, 0);
+                    for (uint32_t r = (all > t0 ? (uint32_t)(all - t0) : 0u) + (t >> 6); r < kTok; r += 2) {
+                        uint4* at = reinterpret_cast<uint4*>(base + (r >> 3) * kGroup + (r & 7) * 128);
+                        *at = t0 + r < g.seen ? finite_only<T>(*at) : make_uint4(0, 0, 0, 0);
+                    }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 mbar_arrive(smem_u32(&p_full[j % 2]));

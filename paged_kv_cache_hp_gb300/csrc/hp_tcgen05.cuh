@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 namespace hp {
 namespace tc {
@@ -218,6 +219,14 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
 // weight is off by 2^-32 of the reference's at most.  bf16 has fp32's range.
 template <typename T> constexpr float kWeightLift = 0.0f;
 template <> constexpr float kWeightLift<__half> = 7.0f;
+
+// Eight elements, those that are not finite (all ones in the exponent) replaced by zeros.
+template <typename T> __device__ __forceinline__ uint4 finite_only(uint4 x)
+{
+    constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7C007C00u : 0x7F807F80u;
+    return make_uint4(x.x & ~__vcmpeq2(x.x & e, e), x.y & ~__vcmpeq2(x.y & e, e), x.z & ~__vcmpeq2(x.z & e, e),
+                      x.w & ~__vcmpeq2(x.w & e, e));
+}
 
 // Two fp32 at a time (one issue slot), and the largest of three.
 __device__ __forceinline__ uint64_t pair_of(float a, float b)

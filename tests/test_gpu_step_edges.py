@@ -106,3 +106,38 @@ def test_f16_flat_tail_under_one_peak_expanded(hp, kernel, peak):
         k = np.concatenate([np.repeat(c[:, :1], 128, 1), c[:, 512:]], 1)
         for h in range(H):
             check_tail(b, 0, b.q[i, h].double().numpy(), k, c[:, 1:129], scale, got[i, h], ("prefill", i, h))
+
+
+# ------------------------------------------------- values a query does not see
+def spoil(b, s, t, row):
+    """Token t of sequence s holds `row` (the formula's rows are left as they were)."""
+    import torch
+    table, sp = (x.cpu().numpy().astype(np.int64) for x in b.desc._keep[1:3])
+    P = b.pool.shape[0] // b.desc.c.num_pages
+    b.pool[int(table[sp[s] + t // P]) * P + t % P] = torch.as_tensor(row, dtype=b.dt, device="cuda")
+
+
+@pytest.mark.parametrize("kernel", ["cuda_cores", "default"])
+@pytest.mark.parametrize("dtype,lens,nq,H,P,bad", [
+    ("bf16", A([300, 70, 64]), A([3, 40, 64]), 16, 16, (298, 51, 33)), ("f16", A([130, 20]), A([2, 3]), 100, 8, (129, 18)),
+    ("bf16", A([65, 128, 7]), A([5, 8, 9]), 1, 64, (64, 123, 0)), ("f16", A([4000, 640]), A([7, 200]), 40, 16, (3994, 640 - 130)),
+    ("bf16", A([30001]), A([4]), 128, 64, (29999,)), ("bf16", A([64, 128]), A([2, 66]), 64, 16, (63, 126)),
+])
+@pytest.mark.parametrize("value", ["nan", "inf", "-inf"])
+def test_decode_of_tokens_a_query_does_not_see(hp, kernel, dtype, lens, nq, H, P, bad, value):
+    """A token whose row is not finite spoils the queries that see it and no other: drafted tokens in
+    one step, in several, in one tile of heads and in more."""
+    b = Latent(hp, lens, nq, H, 512, 576, P, dtype, seed=41, flags=cores(hp, kernel))
+    for s, t in enumerate(bad):
+        spoil(b, s, t, [float(value)] * 576)
+    got = run_decode(b, 0.07)
+    q = b.q.double().numpy()
+    for s, i, n in b.seen():
+        if n > bad[s]:
+            assert np.isnan(got[i]).all(), (s, i)
+            continue
+        c = b.rows[s][:n]
+        for h in range(0, H, max(1, H // 5)):
+            o, tol = ref.attention_row(q[i, h], c, c[:, :512], 0.07, dtype)
+            assert (np.abs(got[i, h] - o) <= tol).all(), (s, i, h)
+        assert np.isfinite(got[i]).all(), (s, i)
