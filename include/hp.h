@@ -731,8 +731,8 @@ int hp_latent_prefill_workspace_bytes(const hp_paged_desc* desc, uint32_t latent
  * num_q_heads, v_dim]).  K and V are rounded to the pool's type after fp32 accumulation over
  * latent_dim, on the tensor cores the weights before the value product, the result once;
  * scores, statistics and sums are fp32.  kv_tokens: at least the sum of seq_lens, or nothing is written and
- * HP_ERR_OUT_SIZE stored.  The values of every token below seq_lens have to be finite (on the tensor
- * cores a query's weight for a later token is zero, not absent).  Empty rows and validation are as in
+ * HP_ERR_OUT_SIZE stored.  A key or value that is not finite (f16: one past 65,504 rounds to an infinity)
+ * spoils the queries that see its token and no others.  Empty rows and validation are as in
  * hp_latent_decode.
  * Supported: latent_dim and rope_dim as there; nope_dim a multiple of 16 and v_dim a multiple
  * of 16 up to 256 (HP_ERR_ARG otherwise).  latent_dim 512, rope_dim 64, nope_dim 128 and v_dim

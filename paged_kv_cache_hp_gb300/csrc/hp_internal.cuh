@@ -66,7 +66,8 @@ struct WsHeader {
     unsigned long long verdict;      // smallest failing key, kVerdictOk if none
     unsigned long long total_rows;   // sum of token counts (gather)
     unsigned long long total_units;  // units_off[S]
-    unsigned long long pad[5];
+    unsigned long long spoilt;       // expanded latent attention: 1 if a value is not finite
+    unsigned long long pad[4];
 };
 
 constexpr uint64_t kWsHeaderBytes = 256;

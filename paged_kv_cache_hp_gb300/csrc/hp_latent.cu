@@ -323,6 +323,7 @@ __global__ void __launch_bounds__(256) latent_rows_kernel(const LatentPrefillArg
     };
     const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (a.blocked) {  // the attention's units, from the last to the first: late queries see most
+        if (blockIdx.x == 0 && threadIdx.x == 0) a.plan.ws.hdr->spoilt = 0;  // (the expansion sets it)
         for (uint64_t e = (uint64_t)blockIdx.x * 256 + threadIdx.x; e < a.max_units; e += (uint64_t)gridDim.x * 256) {
             LatentUnit un{};
             if (e < units) {

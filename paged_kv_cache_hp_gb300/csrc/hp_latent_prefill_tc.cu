@@ -185,6 +185,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
                 // (the warp's last store has read the stage)
                 if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 __syncwarp();
+                uint32_t spoilt = 0;
 #pragma unroll
                 for (uint32_t v = 0; v < 8; ++v) {
                     const uint32_t* e = o[v >> 2] + 8 * (v & 3);
@@ -194,7 +195,9 @@ __global__ void __launch_bounds__(kGThreads, 1)
                     w.z = pack2<T>(__uint_as_float(e[4]), __uint_as_float(e[5]));
                     w.w = pack2<T>(__uint_as_float(e[6]), __uint_as_float(e[7]));
                     *reinterpret_cast<uint4*>(row + ((v ^ (lane & 7)) << 4)) = w;
+                    spoilt |= spoilt_bits<T>(w.x) | spoilt_bits<T>(w.y) | spoilt_bits<T>(w.z) | spoilt_bits<T>(w.w);
                 }
+                if (spoilt) a.plan.ws.hdr->spoilt = 1;  // (of K as well: nothing but time)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) bulk_store(out + c * kSlot, sm0 + stage, 4096, 0);
@@ -220,6 +223,32 @@ constexpr int kThreads = 18 * 32;           // warps 0-7 tile 0, 8-15 tile 1, 16
 constexpr int kTile = 256;                  // softmax threads of a tile: two to a query
 constexpr float kTau = 8.0f;
 
+// Values that meet zero weights have to be finite.  Of the rows from `first` on of a block of V in its two
+// slots, which some query of the unit does not see, what is not finite becomes zero; true if there
+// was any.  By the 256 threads of a tile, a row of 64 dims each.  Looked at where the expansion
+// found such a value anywhere in the batch (in every call it cost 570 cycles of each of a unit's last
+// three blocks: 2% of prompts of 2,000 tokens).
+template <typename T>
+__device__ __noinline__ bool clear_spoilt(unsigned char* slot0, unsigned char* slot1, uint32_t first)
+{
+    const uint32_t r = threadIdx.x & 127;
+    unsigned char* row = (threadIdx.x & 128 ? slot1 : slot0) + r * 128;
+    if (r < first) return false;
+    uint32_t any = 0;
+#pragma unroll
+    for (uint32_t v = 0; v < 8; ++v) {  // (pieces in an order that keeps the banks apart)
+        const uint4 x = *reinterpret_cast<const uint4*>(row + ((v ^ (r & 7)) << 4));
+        any |= spoilt_bits<T>(x.x) | spoilt_bits<T>(x.y) | spoilt_bits<T>(x.z) | spoilt_bits<T>(x.w);
+    }
+    if (!any) return false;
+    for (uint32_t v = 0; v < 8; ++v) {
+        uint4* at = reinterpret_cast<uint4*>(row + (v << 4));
+        *at = finite_only<T>(*at);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    return true;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_prefill_kernel(const LatentPrefillArgs a, const __grid_constant__ CUtensorMap tmq)
@@ -228,13 +257,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) unsigned long long k_full[2], v_full[2], k_free[2], v_free[2], q_full[2],
         s_full[2], p_full[2], o_done[2], all_done;
     __shared__ uint32_t tmem_base;
-    __shared__ int abort_flag, fail_s[2][2];
+    __shared__ int abort_flag, fail_s[2][2], spoilt;
     __shared__ float half_s[2][128];  // what a query's two threads tell each other
     pdl_wait();
     // everything the CTA needs to know, in one trip to memory (hp_latent.cu wrote the units, the
     // last queries of the batch first)
     const LatentUnit un = a.units[blockIdx.x % a.max_units];
     if (a.hdr->verdict != kVerdictOk || un.queries == 0) return;
+    const bool look = a.hdr->spoilt != 0;
     const uint32_t h = (uint32_t)(blockIdx.x / a.max_units);
     const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // blocks of 128 keys that each tile's last query reaches
@@ -262,6 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(smem_u32(&all_done), 1);
         abort_flag = 0;
+        spoilt = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 17) tmem_alloc(smem_u32(&tmem_base), kTmemCols);
@@ -409,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool real = qi < un.queries;
         const uint64_t vis = real && un.seen0 + qi > 0 ? (uint64_t)(un.seen0 + qi) : 0;
         const float qscale = a.scale * 1.4426950408889634f;
+        const int64_t every = un.seen0 > 0 ? un.seen0 : 0;  // tokens that all queries of the unit see
         float m = -INFINITY, l = 0.0f;
         bool stop = false;
         for (uint32_t j = 0; j < nblk[t]; ++j) {
@@ -504,6 +536,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             l += sums.x + sums.y;
             tmem_st_wait();
             fence_before();
+            // (the first tile's products of a block come first, so its threads look at V for both)
+            if (look && (int64_t)(j + 1) * 128 > every && (t == 0 || j >= nblk[0]) &&
+                warp_wait(&v_full[j & 1], (j / 2) & 1)) {
+                const int64_t first = every - (int64_t)j * 128;
+                unsigned char* kv = smem_raw + (sm0 - smem_u32(smem_raw)) + kOffKv;
+                if (clear_spoilt<T>(kv + (5 * j + 3) % kSlots * kSlot, kv + (5 * j + 4) % kSlots * kSlot,
+                                    first > 0 ? (uint32_t)first : 0u))
+                    *(volatile int*)&spoilt = 1;
+            }
             mbar_arrive(smem_u32(&p_full[t]));
         }
         if (!stop && nblk[t]) {
@@ -528,6 +569,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = 0u;
                 }
+                // what was cleared, for the queries that see it
+                if (*(volatile int*)&spoilt)
+                    for (int64_t k = every; k < (int64_t)vis; ++k) {
+                        const char* v = static_cast<const char*>(a.kv) +
+                                        ((h * (a.cap_rows / 128) + un.block + k / 128) * 4 + 2 + half) * kSlot + k % 128 * 128;
+#pragma unroll
+                        for (uint32_t p = 0; p < 4; ++p) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(v + (((c / 8 + p) ^ (uint32_t)(k & 7)) << 4));
+                            const T* e = reinterpret_cast<const T*>(&x);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float f = (float)e[i];
+                                if (!isfinite(f)) o[8 * p + i] = __float_as_uint(__uint_as_float(o[8 * p + i]) + f);
+                            }
+                        }
+                    }
                 if (real) {
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {

@@ -405,7 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 vis[i] = r < g.rows && g.len + 1 + qi > g.n ? g.len + 1 + qi - g.n : 0;
             }
             // tokens that all of them see
-            const uint64_t first = (uint32_t)g.r0 / a.H, all = g.len + 1 + first > g.n ? g.len + 1 + first - g.n : 0;
+            const uint64_t first = g.n > 1 ? (uint32_t)g.r0 / a.H : 0;
+            const uint64_t all = g.len + 1 + first > g.n ? g.len + 1 + first - g.n : 0;
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
             for (uint64_t k = g.k0; k < g.k1; ++k, ++j) {
                 wait_one(&s_full[j % 2], (uint32_t)((j / 2) & 1), j);
@@ -520,12 +521,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // from there, or the weight zero of a score of -inf).  With one query a sequence only
                 // the former occur.
                 if (t0 + kTok > all) {
-                    if (all < g.seen) wait_one(&c_full[j % 2], (uint32_t)((j / 2) & 1), j + 1);  // (read here too)
                     const uint32_t t = threadIdx.x - 64;  // chunk (t & 63) / 8, 16-byte piece t & 7
                     unsigned char* base = smem + kOffC + (uint32_t)(j % 2) * 8 * kGroup + ((t & 63) >> 3) * 1024 + (t & 7) * 16;
-                    for (uint32_t r = (all > t0 ? (uint32_t)(all - t0) : 0u) + (t >> 6); r < kTok; r += 2) {
-                        uint4* at = reinterpret_cast<uint4*>(base + (r >> 3) * kGroup + (r & 7) * 128);
-                        *at = t0 + r < g.seen ? finite_only<T>(*at) : make_uint4(0, 0, 0, 0);
+                    auto piece = [&](uint32_t r) { return reinterpret_cast<uint4*>(base + (r >> 3) * kGroup + (r & 7) * 128); };
+                    const uint32_t r1 = g.seen < t0 + kTok ? (uint32_t)(g.seen - t0) : kTok;  // (seen > t0)
+                    for (uint32_t r = r1 + (t >> 6); r < kTok; r += 2) *piece(r) = make_uint4(0, 0, 0, 0);
+                    if (all < g.seen) {
+                        wait_one(&c_full[j % 2], (uint32_t)((j / 2) & 1), j + 1);  // (its reader too)
+                        for (uint32_t r = (all > t0 ? (uint32_t)(all - t0) : 0u) + (t >> 6); r < r1; r += 2)
+                            *piece(r) = finite_only<T>(*piece(r));
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

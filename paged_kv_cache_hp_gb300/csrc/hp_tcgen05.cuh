@@ -8,7 +8,6 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <type_traits>
 
 namespace hp {
 namespace tc {
@@ -220,10 +219,20 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
 template <typename T> constexpr float kWeightLift = 0.0f;
 template <> constexpr float kWeightLift<__half> = 7.0f;
 
+// The exponent bits of two elements.
+template <typename T> constexpr uint32_t kExponents = 0x7F807F80u;
+template <> constexpr uint32_t kExponents<__half> = 0x7C007C00u;
+
+// Not zero if one of two elements is not finite: the exponent's carry.
+template <typename T> __device__ __forceinline__ uint32_t spoilt_bits(uint32_t x)
+{
+    return ((x & kExponents<T>) + (kExponents<T> & ~(kExponents<T> << 1))) & 0x80008000u;
+}
+
 // Eight elements, those that are not finite (all ones in the exponent) replaced by zeros.
 template <typename T> __device__ __forceinline__ uint4 finite_only(uint4 x)
 {
-    constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7C007C00u : 0x7F807F80u;
+    constexpr uint32_t e = kExponents<T>;
     return make_uint4(x.x & ~__vcmpeq2(x.x & e, e), x.y & ~__vcmpeq2(x.y & e, e), x.z & ~__vcmpeq2(x.z & e, e),
                       x.w & ~__vcmpeq2(x.w & e, e));
 }

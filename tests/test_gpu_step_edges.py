@@ -5,7 +5,7 @@ import pytest
 
 import step_ref as ref
 from helpers import index_tensor
-from test_gpu_step import A, Latent, cores, run_decode, run_prefill
+from test_gpu_step import A, Latent, cores, run_decode, run_prefill, selecting_weights
 
 pytestmark = pytest.mark.gpu
 
@@ -141,3 +141,72 @@ def test_decode_of_tokens_a_query_does_not_see(hp, kernel, dtype, lens, nq, H, P
             o, tol = ref.attention_row(q[i, h], c, c[:, :512], 0.07, dtype)
             assert (np.abs(got[i, h] - o) <= tol).all(), (s, i, h)
         assert np.isfinite(got[i]).all(), (s, i)
+
+
+@pytest.mark.parametrize("kernel", ["cuda_cores", "default"])
+@pytest.mark.parametrize("behind", [0, 1, 60, 127, 128, 129, 200, 254, 300])
+@pytest.mark.parametrize("value", ["nan", "inf"])
+def test_prefill_of_tokens_a_query_does_not_see(hp, kernel, behind, value):
+    """The same through the expanded form, the token at the end of its sequence and further before it:
+    in one tile's last block of keys, in both tiles', in blocks of a later unit of queries."""
+    lens, nq = A([700, 300, 129, 513]), A([257, 300, 129, 256])
+    b = Latent(hp, lens, nq, 2, 512, 576, 16, "bf16" if behind % 2 else "f16", seed=behind, flags=cores(hp, kernel))
+    w = selecting_weights(2, 128, 128, 512, b.dt, 7)
+    bad = [max(0, int(n) - 1 - behind) for n in lens]
+    for s, t in enumerate(bad):
+        spoil(b, s, t, [float(value)] * 576)
+    got = run_prefill(b, 128, 128, w, 0.07)
+    q, wd = b.q.double().numpy(), w.double().numpy()
+    for s, i, n in b.seen():
+        if n > bad[s]:
+            assert np.isnan(got[i]).all(), (s, i)
+            continue
+        assert np.isfinite(got[i]).all(), (s, i)
+        if i % 7 and n < bad[s] - 3:
+            continue
+        c = b.rows[s][:n]
+        for h in range(2):
+            kv = c[:, :512] @ wd[h].T
+            o, tol = ref.attention_row(q[i, h], np.concatenate([kv[:, :128], c[:, 512:]], 1), kv[:, 128:], 0.07, b.dtype)
+            assert (np.abs(got[i, h] - o) <= tol).all(), (s, i, h)
+
+
+@pytest.mark.parametrize("kernel", ["cuda_cores", "default"])
+@pytest.mark.parametrize("behind", [0, 5, 128, 200, 400])
+def test_prefill_values_past_the_range_of_f16(hp, kernel, behind):
+    """One expanded value of one token is past f16's range, with keys that are not: the infinity in
+    its dim for the queries that see the token, every other number as it would be."""
+    import torch
+    lens, nq = A([700, 300]), A([300, 300])
+    b = Latent(hp, lens, nq, 2, 512, 576, 16, "f16", seed=50 + behind, flags=cores(hp, kernel))
+    w = selecting_weights(2, 128, 128, 512, b.dt, 7)
+    w[:, :, 7] = 0.0
+    w[:, 128 + 69] = 0.0
+    w[:, 128 + 69, 7] = 2.0  # value dim 69 is twice latent dim 7
+    sign = {0: 1.0, 1: -1.0}
+    bad = [max(0, int(n) - 1 - behind) for n in lens]
+    for s, t in enumerate(bad):
+        row = torch.from_numpy(b.rows[s][t]).clone()
+        row[7] = sign[s] * 40000.0
+        spoil(b, s, t, row)
+        b.rows[s][t, 7] = 0.0
+    real = b.queries
+
+    def queries(width):
+        real(width)
+        b.q *= 0.25  # scores near zero: every weight is a normal number
+        return b.q.cuda()
+    b.queries = queries
+    got = run_prefill(b, 128, 128, w, 0.07)
+    q, wd = b.q.double().numpy(), w.double().numpy()
+    for s, i, n in b.seen():
+        if n > bad[s]:
+            assert (got[i, :, 69] == sign[s] * np.inf).all(), (s, i)
+        if i % 5 and abs(n - bad[s]) > 3:
+            continue
+        c = b.rows[s][:n]
+        for h in range(2):
+            kv = c[:, :512] @ wd[h].T
+            o, tol = ref.attention_row(q[i, h], np.concatenate([kv[:, :128], c[:, 512:]], 1), kv[:, 128:], 0.07, "f16")
+            ok = np.abs(got[i, h] - o) <= tol
+            assert ok[:69].all() and ok[70:].all() and (ok[69] or n > bad[s]), (s, i, h)
