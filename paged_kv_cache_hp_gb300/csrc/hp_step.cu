@@ -140,13 +140,16 @@ __device__ __forceinline__ IndexT page_entry(const hp_step_desc& d, unsigned lon
                     : static_cast<const IndexT*>(d.free_pages)[at - lo + j - have];
 }
 
-// Row t: the token at position pos of that sequence.
+// Row t: the token at position pos of that sequence.  A page whose slots lie past 2^63 - 1 gives that
+// number, which is in no pool (a product that wraps could name some other page's slot, or a padding row).
 template <typename IndexT>
 __device__ __forceinline__ void put_token(const StepArgs& a, uint64_t t, unsigned long long pos, unsigned long long lo,
                                           unsigned long long have, unsigned long long at)
 {
     const unsigned long long j = page_of(a, pos), page = page_entry<IndexT>(a.d, lo, have, at, j);
-    a.d.slot_map[t] = (int64_t)(page * a.d.page_size + (pos - j * a.d.page_size));
+    const unsigned long long slot = page * a.d.page_size + (pos - j * a.d.page_size);
+    const bool past = __umul64hi(page, a.d.page_size) != 0 || slot >> 63;
+    a.d.slot_map[t] = past ? INT64_MAX : (int64_t)slot;
     static_cast<IndexT*>(a.d.positions)[t] = (IndexT)pos;
 }
 

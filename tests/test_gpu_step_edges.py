@@ -5,7 +5,7 @@ import pytest
 
 import step_ref as ref
 from helpers import index_tensor
-from test_gpu_step import A, Latent, cores, run_decode, run_prefill, selecting_weights
+from test_gpu_step import A, Latent, cores, dev, make_step, run_decode, run_prefill, selecting_weights, status_tensor
 
 pytestmark = pytest.mark.gpu
 
@@ -210,3 +210,43 @@ def test_prefill_values_past_the_range_of_f16(hp, kernel, behind):
             o, tol = ref.attention_row(q[i, h], np.concatenate([kv[:, :128], c[:, 512:]], 1), kv[:, 128:], 0.07, "f16")
             ok = np.abs(got[i, h] - o) <= tol
             assert ok[:69].all() and ok[70:].all() and (ok[69] or n > bad[s]), (s, i, h)
+
+
+# ------------------------------------------------------------- pages past every pool
+@pytest.mark.parametrize("S", [3, 1500])
+@pytest.mark.parametrize("it,page,P", [
+    (1, 2 ** 64 - 1, 16), (1, 2 ** 60, 16), (1, 2 ** 60 + 1, 16), (1, 2 ** 59, 16), (1, 2 ** 63, 1), (1, 2 ** 58, 48),
+    (0, 2 ** 32 - 1, 16), (0, 2 ** 32 - 1, 2 ** 33), (0, 2 ** 31, 2 ** 33 + 8),
+])
+def test_slots_of_a_page_past_every_pool(hp, S, it, page, P):
+    """A table entry whose slots do not fit 63 bits names no slot of a pool (a product of 64 bits
+    wraps to another page's, or below zero to a padding row): the append refuses its tokens."""
+    import torch
+    lens, new = np.full(S, min(P, 40) - 1), np.full(S, 1)
+    s = make_step(hp, lens, new, np.full(S, 1), P, it)
+    table = s["d"].keep[0]
+    rows = s["d"].table_len
+    bad = (0, S - 1)
+    for b in bad:
+        table[b] = page - 2 ** (64 if it else 32) if page >= 2 ** (63 if it else 31) else page
+    assert hp.hp_step_tables(s["d"], s["ws"], s["status"]) == 0
+    torch.cuda.synchronize()
+    assert s["status"].item() == 0 and rows == S
+    slots = s["o"]["slot_map"].cpu().numpy()
+    want = min(page * P + int(lens[0]), 2 ** 63 - 1)
+    at = s["table"].astype(object) * P + lens
+    for i in range(S):
+        assert int(slots[i]) == (want if i in bad else at[i]), i
+    if P > 64:
+        return
+    T, pages = len(slots), S + 3
+    kv = torch.randn((T, 576)).to(torch.bfloat16).cuda()
+    pool = torch.zeros((pages, P, 576), dtype=torch.bfloat16, device="cuda")
+    rope = hp.rope_desc(cos_sin=dev(ref.cos_sin(60, 64)), sections=(32,), positions=s["o"]["positions"], index_type=it)
+    d = hp.latent_desc(latent=kv[:, :512], k_rope=kv[:, 512:], dtype="bf16", slot_map=s["o"]["slot_map"], pool=pool,
+                       num_pages=pages, page_size=P)
+    st = status_tensor()
+    assert hp.hp_latent_append(d, rope, st) == 0
+    torch.cuda.synchronize()
+    assert hp.status_name(st.item()) == "HP_ERR_PAGE_ID"
+    assert int((pool != 0).any(2).sum()) == S - 2
