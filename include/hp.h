@@ -551,7 +551,7 @@ int hp_step_tables_workspace_bytes(uint64_t num_seqs, uint64_t* bytes);
  * ASYNC.  Builds the tables of one step (hp_step_desc).  Host checks, in order: step NULL
  * (HP_ERR_NULL), index type, page_size 0 (HP_ERR_ZERO_PAGE_SIZE), reserved not 0 (HP_ERR_ARG),
  * sizes beyond 2^58, table_cap + token_cap beyond 2^41 or num_seqs beyond
- * 2^38 (HP_ERR_OVERFLOW), NULL and misaligned buffers (element alignment),
+ * 2^37 (HP_ERR_OVERFLOW), NULL and misaligned buffers (element alignment),
  * workspace.  On the device, in this order: seq_ptr (HP_ERR_SEQ_PTR_START, _ORDER, _END), a
  * sequence whose seq_lens exceed its slice, or whose grown length does not fit the index type
  * or 2^58 (HP_ERR_LEN), free_pages too short (HP_ERR_CAPACITY), more than table_cap entries or

@@ -48,8 +48,8 @@ HP_API int hp_step_tables(const hp_step_desc* step, void* workspace, uint64_t wo
     if (d.reserved) return HP_ERR_ARG;
     if (d.num_seqs >= kMost || d.page_size >= kMost || d.table_len >= kMost ||
         d.num_free >= kMost || d.table_cap >= kMost || d.token_cap >= kMost ||
-        d.table_cap + d.token_cap > (1ull << 41) || d.num_seqs > (1ull << 38))  // one launch's grid
-        return HP_ERR_OVERFLOW;
+        d.table_cap + d.token_cap > (1ull << 41) || d.num_seqs > (1ull << 37))
+        return HP_ERR_OVERFLOW;  // (2,048 entries or tokens or 256 sequences a CTA: 1.5 2^30 CTAs of 2^31 - 1)
     if (!d.seq_ptr || !d.seq_ptr_out || !d.new_ptr_out ||
         (d.num_seqs && (!d.seq_lens || !d.new_lens || !d.lens_out)) ||
         (d.table_len && !d.block_table) || (d.num_free && !d.free_pages) ||

@@ -46,6 +46,19 @@ def test_step_tables_refusals(hpc, kw, name):
         == "HP_ERR_" + name
 
 
+@pytest.mark.parametrize("kw", [
+    dict(num_seqs=1 << 38, table_cap=1 << 40, token_cap=1 << 40), dict(num_seqs=(1 << 37) + 1),
+    dict(num_seqs=1 << 38), dict(table_cap=1 << 41, token_cap=1),
+])
+def test_step_tables_beyond_one_grid(hpc, kw):
+    """Sizes whose fill would not fit one launch are refused before any launch, also together (a
+    CTA takes 2,048 entries or tokens, or 256 sequences; a grid has up to 2^31 - 1)."""
+    d = step(hpc, **kw)
+    assert hpc.status_name(hpc.lib().hp_step_tables(ctypes.byref(d), A, 1 << 60, None, None)) == "HP_ERR_OVERFLOW"
+    most = -(-(1 << 41) // 2048) + 2 + (1 << 37) // 256 + 1
+    assert most < 1 << 31
+
+
 def test_step_tables_workspace(hpc):
     rc, n = hpc.hp_step_tables_workspace_bytes(100)
     assert rc == 0 and n == 256 + 2 * 1024 + 3 * 8 * 256
