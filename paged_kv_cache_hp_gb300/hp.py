@@ -263,7 +263,6 @@ def lib():
             for name, (res, args) in sig.items():
                 f = getattr(L, name)
                 f.restype, f.argtypes = res, args
-            _find_current_stream()
             _lib = L
     return _lib
 
@@ -277,19 +276,17 @@ def _p(t):
 
 
 def _current_stream():
-    """torch's current stream on the current device, as an integer."""
-    import torch
-    return torch.cuda.current_stream().cuda_stream
-
-
-def _find_current_stream():
-    """The raw-handle query costs a tenth of building a Stream object (3 us on the Grace host,
-    half of a small call's time), where torch has it."""
+    """torch's current stream on the current device, as an integer.  The first call without a
+    stream finds the way to ask (the library itself needs no torch): the raw-handle query costs a
+    tenth of building a Stream object (3 us on the Grace host, half of a small call's time)."""
     global _current_stream
     import torch
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     if raw is not None:
         _current_stream = lambda: raw(torch.cuda.current_device())  # noqa: E731
+    else:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _current_stream()
 
 
 def _stream(stream):

@@ -1,6 +1,9 @@
 """The serving-step entry points without a GPU: workspace sizes, and every refusal the host
 makes, on made-up addresses (each call below fails a check before any launch)."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 
@@ -220,3 +223,26 @@ def test_latent_workspace_sizes(hpc):
     rows = -(-(5000 + 127 * 100) // 128) * 128
     units = -(-(1000 // 256 + 100) * 32 // 256) * 256  # blocks of 256 queries, 32 bytes each
     assert rc == 0 and n == 256 + 2 * 1024 + rows * 576 * 2 + rows * 16 * 256 * 2 + units
+
+
+def test_the_library_needs_no_torch(hpc):
+    """Loading, names of codes, workspace queries and refusals work where torch cannot be imported;
+    it is asked for the current stream by the first call that names none."""
+    code = """if True:
+        import sys
+        sys.modules["torch"] = None  # import torch raises ImportError
+        from paged_kv_cache_hp_gb300 import hp
+        assert hp.lib() is hp.lib()
+        assert hp.status_name(0) == "HP_OK"
+        assert hp.hp_step_tables_workspace_bytes(100)[0] == 0
+        d = hp.HpStepDesc()
+        d.index_type = 2
+        assert hp.status_name(hp.hp_step_tables(d, None, None, 0)) == "HP_ERR_INDEX_TYPE"
+        try:
+            hp.hp_step_tables(d, None)
+        except ImportError:
+            print("asked")
+    """
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "asked", r.stderr
