@@ -21,6 +21,8 @@
 namespace hp {
 namespace {
 
+// (Pool rows are read by plain loads: a kernel behind an append is resident while that one still writes
+// them, and the read-only path is for memory that does not change over a kernel's life.)
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <typename T> struct Pair;
@@ -127,7 +129,7 @@ __global__ void __launch_bounds__(256, 2) latent_cc_kernel(const LatentArgs a)
 #pragma unroll
                     for (int j = 0; j < kMaxPairs; ++j) {
                         const uint32_t p = lane + 32 * j;
-                        kv[u][j] = p < pairs ? __ldg(src + p) : 0u;
+                        kv[u][j] = p < pairs ? src[p] : 0u;
                     }
                 }
 #pragma unroll
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(256) latent_rows_kernel(const LatentPrefillArg
         for (uint32_t c = lane; c < vecs; c += 32) {
             uint4 x[kRowsWarp4];
 #pragma unroll
-            for (int i = 0; i < kRowsWarp4; ++i) x[i] = src[i] ? __ldg(src[i] + c) : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < kRowsWarp4; ++i) x[i] = src[i] ? src[i][c] : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int i = 0; i < kRowsWarp4; ++i) {
                 const uint64_t r = row0 + i;
