@@ -514,7 +514,7 @@ int hp_attention_decode_planned(const hp_paged_desc* k_desc, const void* v_pool,
  *   seq_ptr_out   num_seqs+1 entries; lens_out: seq_lens + new_lens
  *   new_ptr_out   num_seqs+1 entries: prefix sums of new_lens (an append's new_ptr)
  *   slot_map      token_cap entries, int64: page * page_size + slot of each new token, in
- *                 sequence order (2^63 - 1 where that is more); -1 from the last new token on
+ *                 sequence order (2^63 - 1 for a page whose slots reach further); -1 from the last new token on
  *                 (the rows of a padded batch)
  *   positions     token_cap entries: the token's index in its sequence; 0 past the last
  *   totals        3 uint64 (may be NULL): table entries, new tokens, pages taken

@@ -70,6 +70,7 @@ HP_API int hp_step_tables(const hp_step_desc* step, void* workspace, uint64_t wo
     a.blocks = a.ws.units_off + hp::round_up_256(8 * (d.num_seqs + 1)) / 8;
     a.div_ok = d.page_size <= (1ull << 31);
     if (a.div_ok) hp::invariant_divisor(d.page_size, &a.div_m, &a.div_l);
+    a.page_limit = (1ull << 63) / d.page_size;
     a.d_status = d_status;
     return hp::launch_step_tables(a, stream);
 }

@@ -140,7 +140,7 @@ __device__ __forceinline__ IndexT page_entry(const hp_step_desc& d, unsigned lon
                     : static_cast<const IndexT*>(d.free_pages)[at - lo + j - have];
 }
 
-// Row t: the token at position pos of that sequence.  A page whose slots lie past 2^63 - 1 gives that
+// Row t: the token at position pos of that sequence.  A page whose slots reach past 2^63 - 1 gives that
 // number, which is in no pool (a product that wraps could name some other page's slot, or a padding row).
 template <typename IndexT>
 __device__ __forceinline__ void put_token(const StepArgs& a, uint64_t t, unsigned long long pos, unsigned long long lo,
@@ -148,8 +148,7 @@ __device__ __forceinline__ void put_token(const StepArgs& a, uint64_t t, unsigne
 {
     const unsigned long long j = page_of(a, pos), page = page_entry<IndexT>(a.d, lo, have, at, j);
     const unsigned long long slot = page * a.d.page_size + (pos - j * a.d.page_size);
-    const bool past = __umul64hi(page, a.d.page_size) != 0 || slot >> 63;
-    a.d.slot_map[t] = past ? INT64_MAX : (int64_t)slot;
+    a.d.slot_map[t] = page < a.page_limit ? (int64_t)slot : INT64_MAX;
     static_cast<IndexT*>(a.d.positions)[t] = (IndexT)pos;
 }
 

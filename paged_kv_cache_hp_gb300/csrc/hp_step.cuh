@@ -14,6 +14,7 @@ struct StepArgs {
     hp_step_desc d;
     WsView ws;  // rows_off: prefix of the new tokens, units_off of the pages, within each block
     unsigned long long* blocks;  // [3][kStepBlocks]: each block's tokens, pages, verdict key
+    uint64_t page_limit;         // 2^63 / page_size: the slots of pages below it fit an int64
     uint32_t block_log;          // log2 of a block's sequences
     uint32_t div_ok, div_m, div_l;  // div_invariant constants of page_size, where it fits
     int* d_status;
