@@ -268,12 +268,25 @@ inline void invariant_divisor(uint64_t g, uint32_t* m, uint32_t* l)
 }
 
 // ------------------------------------------------------- dependent launches
-// The plan, the block-table check and the copy go into the stream back to back.  The
-// check and the copy are launched as programmatic dependents of the kernel before
-// them, so their CTAs are scheduled while it finishes; each waits (griddepcontrol.wait)
-// before it touches anything that kernel writes, and writes nothing before that wait.
-// The plan itself is launched normally: it overwrites the workspace a previous copy
-// may still be reading.
+// The kernels of a call go into the stream back to back, each behind the first as a
+// programmatic dependent of the kernel before it, so that its CTAs are scheduled while that one
+// finishes.  The first of a call:
+//   - is launched normally where it is a plan of the gather, the append or decode attention (it
+//     overwrites a workspace that a previous copy may still read, and starts at once), and
+//     where it is a kernel without a plan;
+//   - is itself a dependent, of whatever the stream holds, in a serving step: the latent plan,
+//     the step tables, the norm + rotation appends, latent attention that plans for itself, and
+//     every *_planned call.
+// What keeps this right:
+//   - a kernel launched as a dependent runs griddepcontrol.wait in every CTA, before any return,
+//     and before it reads or writes global memory that a call before may use.  (The table check
+//     reads the block table first: the plan before it lets it start only after its own wait, or
+//     was launched normally.)
+//   - completion is then transitive: a kernel that has waited knows that all before it in the
+//     stream is complete, so a kernel may let its dependents start as early as it likes, but
+//     one that returned without waiting would break every dependent behind it.
+//   - what such a kernel reads may have been written during its life: no read-only loads (__ldg) in
+//     a serving step's kernels.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger()
 {
