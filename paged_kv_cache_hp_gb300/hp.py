@@ -106,6 +106,26 @@ def _dtype(d):
     return DTYPES[d] if isinstance(d, str) else d
 
 
+def _contiguous(what, **tensors):
+    """Refuses tensors whose strides the descriptor has no field for."""
+    for name, t in tensors.items():
+        if t is not None and not t.is_contiguous():
+            raise ValueError("%s: %s has to be contiguous, its strides are %s" % (what, name, tuple(t.stride())))
+
+
+def _inner(what, dims, **tensors):
+    """Refuses tensors whose dimensions from `dims` on are not one contiguous piece."""
+    for name, t in tensors.items():
+        if t is None or t.numel() == 0:
+            continue
+        row = t
+        for _ in range(dims):
+            row = row[0]
+        if not row.is_contiguous():
+            raise ValueError("%s: %s has to be contiguous from dimension %d on, its strides are %s"
+                             % (what, name, dims, tuple(t.stride())))
+
+
 def step_desc(*, seq_ptr, seq_lens, new_lens, page_size, index_type, seq_ptr_out, lens_out,
               new_ptr_out, block_table=None, free_pages=None, table_out=None, slot_map=None,
               positions=None, totals=None, **fields):
@@ -116,6 +136,7 @@ def step_desc(*, seq_ptr, seq_lens, new_lens, page_size, index_type, seq_ptr_out
                 free_pages=free_pages, table_out=table_out, seq_ptr_out=seq_ptr_out,
                 lens_out=lens_out, new_ptr_out=new_ptr_out, slot_map=slot_map,
                 positions=positions, totals=totals)
+    _contiguous("step_desc", **bufs)
     d.index_type, d.page_size = index_type, page_size
     d.num_seqs, d.table_len, d.num_free = _numel(seq_lens), _numel(block_table), _numel(free_pages)
     d.table_cap, d.token_cap = _numel(table_out), _numel(slot_map)
@@ -128,8 +149,10 @@ def step_desc(*, seq_ptr, seq_lens, new_lens, page_size, index_type, seq_ptr_out
 
 
 def rope_desc(*, cos_sin, positions, sections, interleaved=False, index_type=IDX_U32, **fields):
-    """An hp_rope_desc: cos_sin fp32 [max_pos, rot_dim], positions [axes, num_tokens]."""
+    """An hp_rope_desc: cos_sin fp32 [max_pos, rot_dim], positions [axes, num_tokens], both
+    contiguous."""
     d = HpRopeDesc()
+    _contiguous("rope_desc", cos_sin=cos_sin, positions=positions)
     d.cos_sin, d.positions = _p(cos_sin), _p(positions)
     d.max_pos, d.rot_dim = cos_sin.shape
     d.axes = len(sections)
@@ -145,8 +168,11 @@ def rope_desc(*, cos_sin, positions, sections, interleaved=False, index_type=IDX
 def qk_desc(*, q, k, v, q_out, num_q_heads, num_kv_heads, head_dim, dtype, slot_map, k_pool,
             v_pool, num_pages, page_size, q_weight=None, k_weight=None, eps=1e-6, **fields):
     """An hp_qk_desc over device tensors: q, k, v and q_out with the token as their first
-    dimension (its stride is taken from the tensor), heads and dims contiguous in it."""
+    dimension (its stride is taken from the tensor), heads and dims contiguous in it; the others
+    contiguous."""
     d = HpQkDesc()
+    _inner("qk_desc", 1, q=q, k=k, v=v, q_out=q_out)
+    _contiguous("qk_desc", q_weight=q_weight, k_weight=k_weight, slot_map=slot_map, k_pool=k_pool, v_pool=v_pool)
     d.dtype, d.num_q_heads, d.num_kv_heads = _dtype(dtype), num_q_heads, num_kv_heads
     d.head_dim, d.eps, d.num_tokens = head_dim, eps, slot_map.numel()
     bufs = dict(q=q, k=k, v=v, q_out=q_out, q_weight=q_weight, k_weight=k_weight,
@@ -165,8 +191,12 @@ def qk_desc(*, q, k, v, q_out, num_q_heads, num_kv_heads, head_dim, dtype, slot_
 def latent_desc(*, latent, k_rope, dtype, slot_map, pool, num_pages, page_size, q_rope=None,
                 q_out=None, latent_weight=None, eps=1e-6, **fields):
     """An hp_latent_desc over device tensors: latent [tokens, latent_dim], k_rope [tokens,
-    rope_dim], q_rope and q_out [tokens, heads, rope_dim], each with its own strides."""
+    rope_dim], q_rope and q_out [tokens, heads, rope_dim], each with its own strides of tokens and
+    heads; the others contiguous."""
     d = HpLatentDesc()
+    _inner("latent_desc", 1, latent=latent, k_rope=k_rope)
+    _inner("latent_desc", 2, q_rope=q_rope, q_out=q_out)
+    _contiguous("latent_desc", latent_weight=latent_weight, slot_map=slot_map, pool=pool)
     d.dtype, d.latent_dim, d.eps = _dtype(dtype), latent.shape[1], eps
     d.num_q_heads = 0 if q_rope is None else q_rope.shape[1]
     d.num_tokens = slot_map.numel()

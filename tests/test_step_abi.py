@@ -246,3 +246,41 @@ def test_the_library_needs_no_torch(hpc):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "asked", r.stderr
+
+
+def test_descriptors_refuse_strides_they_cannot_say(hpc):
+    """A descriptor built over tensors has fields for some strides only; a tensor with others would
+    be read as if it had none."""
+    import torch
+    bf, i64 = torch.bfloat16, torch.int64
+    x, slot, pool = torch.zeros((4, 3 * 128), dtype=bf), torch.zeros(4, dtype=i64), torch.zeros((2, 16, 1, 128), dtype=bf)
+    q = dict(q=x[:, :128], k=x[:, 128:256], v=x[:, 256:], q_out=torch.zeros((4, 1, 128), dtype=bf), num_q_heads=1,
+             num_kv_heads=1, head_dim=128, dtype="bf16", slot_map=slot, k_pool=pool, v_pool=pool, num_pages=2, page_size=16)
+    assert hpc.qk_desc(**q).k_stride == 3 * 128
+    wide = torch.zeros((4, 256), dtype=bf)
+    for name, t in (("q", wide[:, ::2]), ("k", torch.zeros((128, 4), dtype=bf).t()), ("q_out", torch.zeros((4, 128, 2), dtype=bf)[..., 0]),
+                    ("v", torch.zeros((4, 4, 2, 32), dtype=bf).transpose(1, 2)), ("slot_map", torch.zeros(8, dtype=i64)[::2]),
+                    ("k_pool", torch.zeros((2, 1, 16, 128), dtype=bf).expand(2, 3, 16, 128).transpose(1, 2))):
+        with pytest.raises(ValueError, match=name):
+            hpc.qk_desc(**{**q, name: t})
+    lat = torch.zeros((4, 576), dtype=bf)
+    qr = torch.zeros((4, 2, 192), dtype=bf)
+    d = dict(latent=lat[:, :512], k_rope=lat[:, 512:], q_rope=qr[:, :, 128:], q_out=qr.transpose(0, 1).contiguous().transpose(0, 1)[:, :, 128:],
+             dtype="bf16", slot_map=slot, pool=torch.zeros((2, 16, 576), dtype=bf), num_pages=2, page_size=16)
+    got = hpc.latent_desc(**d)
+    assert (got.q_stride, got.q_head_stride, got.q_out_stride, got.q_out_head_stride) == (384, 192, 192, 768)
+    for name, t in (("latent", torch.zeros((512, 4), dtype=bf).t()), ("k_rope", lat[:, 448::2]), ("q_rope", qr.transpose(1, 2)),
+                    ("pool", torch.zeros((16, 2, 576), dtype=bf).transpose(0, 1))):
+        with pytest.raises(ValueError, match=name):
+            hpc.latent_desc(**{**d, name: t})
+    cs, pos = torch.zeros((50, 64)), torch.zeros((3, 4), dtype=torch.int32)
+    assert hpc.rope_desc(cos_sin=cs, positions=pos, sections=(8, 12, 12)).max_pos == 50
+    for kw in (dict(cos_sin=torch.zeros((50, 128))[:, :64]), dict(positions=torch.zeros((4, 3), dtype=torch.int32).t())):
+        with pytest.raises(ValueError, match=next(iter(kw))):
+            hpc.rope_desc(**{**dict(cos_sin=cs, positions=pos, sections=(8, 12, 12)), **kw})
+    one = torch.zeros(4, dtype=torch.int32)
+    s = dict(seq_ptr=one, seq_lens=one[:3], new_lens=one[:3], page_size=16, index_type=0, seq_ptr_out=one, lens_out=one[:3],
+             new_ptr_out=one)
+    assert hpc.step_desc(**s).num_seqs == 3
+    with pytest.raises(ValueError, match="new_lens"):
+        hpc.step_desc(**{**s, "new_lens": torch.zeros(6, dtype=torch.int32)[::2]})
