@@ -5,7 +5,8 @@ import pytest
 
 import step_ref as ref
 from helpers import index_tensor
-from test_gpu_step import A, Latent, cores, dev, make_step, run_decode, run_prefill, selecting_weights, status_tensor
+from test_gpu_step import (A, Latent, cores, dev, host, make_step, run_decode, run_prefill,
+                           selecting_weights, status_tensor)
 
 pytestmark = pytest.mark.gpu
 
@@ -250,3 +251,89 @@ def test_slots_of_a_page_past_every_pool(hp, S, it, page, P):
     torch.cuda.synchronize()
     assert hp.status_name(st.item()) == "HP_ERR_PAGE_ID"
     assert int((pool != 0).any(2).sum()) == S - 2
+
+
+# ------------------------------------------------------------- a step, number by number
+def test_steps_over_a_latent_cache_row_by_row(hp):
+    """Tables, append (queries rotated in place), prompts and decode of three steps on one stream, no wait
+    between them: the rotated queries, the rows in the pages and both forms' outputs, each against the
+    formula with its own bound."""
+    import torch
+    H, R, Dr, Dn, Dv, P, pages, S = 4, 512, 64, 128, 128, 16, 64, 3
+    dt, W, scale = torch.bfloat16, 576, 0.09
+    g = torch.Generator().manual_seed(12)
+    cs = ref.cos_sin(512, Dr)
+    csd, w = dev(cs), selecting_weights(H, Dn, Dv, R, dt, 2)
+    wd, w64 = w.cuda(), w.double().numpy()
+    gain = (1 + 0.2 * torch.randn(R, generator=g)).to(dt)
+    gd = gain.cuda()
+    pool = torch.full((pages, P, W), float("nan"), dtype=dt, device="cuda")
+    lens, have, table = A([0, 0, 0]), A([0, 0, 0]), np.zeros(0, np.uint32)
+    free = np.random.default_rng(1).permutation(pages).astype(np.uint32)
+    stream = torch.cuda.Stream()
+    for new in (A([33, 1, 140]), A([1, 3, 1]), A([0, 20, 2])):
+        need, T, total = np.maximum(have, -(-(lens + new) // P)), int(new.sum()), int((lens + new).sum())
+        i32 = dict(dtype=torch.int32, device="cuda")
+        o = dict(table_out=torch.empty(int(need.sum()), **i32), seq_ptr_out=torch.empty(S + 1, **i32),
+                 lens_out=torch.empty(S, **i32), new_ptr_out=torch.empty(S + 1, **i32),
+                 slot_map=torch.empty(T, dtype=torch.int64, device="cuda"), positions=torch.empty(T, **i32))
+        d = hp.step_desc(block_table=index_tensor(table, "cuda") if len(table) else None,
+                         seq_ptr=index_tensor(np.concatenate([[0], np.cumsum(have)]).astype(np.uint32), "cuda"),
+                         seq_lens=index_tensor(lens.astype(np.uint32), "cuda"),
+                         new_lens=index_tensor(new.astype(np.uint32), "cuda"),
+                         free_pages=index_tensor(free, "cuda"), page_size=P, index_type=0, **o)
+        kv = torch.randn((T, W), generator=g).to(dt)
+        q = torch.randn((T, H, Dn + Dr), generator=g).to(dt)
+        kvd, qd, ws1 = kv.cuda(), q.cuda(), torch.empty(hp.hp_step_tables_workspace_bytes(S)[1], dtype=torch.uint8, device="cuda")
+        rope = hp.rope_desc(cos_sin=csd, positions=o["positions"], sections=(Dr // 2,), interleaved=True)
+        ld = hp.latent_desc(latent=kvd[:, :R], k_rope=kvd[:, R:], q_rope=qd[:, :, Dn:], q_out=qd[:, :, Dn:],
+                            latent_weight=gd, dtype="bf16", slot_map=o["slot_map"], pool=pool, num_pages=pages, page_size=P)
+        pd = hp.PagedDesc(pool, o["table_out"], o["seq_ptr_out"], o["lens_out"], num_pages=pages, page_size=P,
+                          num_heads=1, head_dim=W, dtype="bf16", index_type=0)
+        n = max(hp.hp_latent_prefill_workspace_bytes(pd, R, Dn, Dv, T, H, total)[1],
+                hp.hp_latent_decode_workspace_bytes(pd, R, T, H)[1])
+        ws2 = torch.empty(n, dtype=torch.uint8, device="cuda")
+        out, lat = torch.empty((T, H, Dv), dtype=dt, device="cuda"), torch.empty((T, H, R), dtype=dt, device="cuda")
+        st = [status_tensor() for _ in range(4)]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            assert hp.hp_step_tables(d, ws1, st[0]) == 0
+            assert hp.hp_latent_append(ld, rope, st[1]) == 0
+            assert hp.hp_latent_prefill(pd, R, wd, Dn, Dv, qd, o["new_ptr_out"], T, H, scale, out, total, ws2, st[2]) == 0
+            qa = torch.cat([torch.einsum("thd,hdr->thr", qd[:, :, :Dn].float(), wd[:, :Dn].float()),
+                            qd[:, :, Dn:].float()], 2).to(dt)
+            assert hp.hp_latent_decode(pd, R, qa, o["new_ptr_out"], T, H, scale, lat, ws2, st[3]) == 0
+        stream.synchronize()
+        assert [x.item() for x in st] == [0] * 4
+        want = ref.step_tables(lens, new, np.concatenate([[0], np.cumsum(have)]), table, free, P)
+        assert o["table_out"].cpu().numpy().view(np.uint32).tolist() == want[0]
+        assert o["slot_map"].cpu().tolist() == want[4]
+        # the rows stored and the queries
+        pos, slots = np.array(want[5])[None], np.array(want[4])
+        cos, sin = ref.angles(cs, pos, (Dr // 2,))
+        x, rows = kv.double().numpy(), host(pool).reshape(-1, W)
+        c = ref.norm(x[:, :R], gain.double().numpy(), 1e-6)
+        k = ref.rotate(x[:, None, R:], cos, sin, True)[:, 0]
+        assert (np.abs(rows[slots, :R] - c) <= ref.rope_bound(c, c, "bf16")).all()
+        assert (np.abs(rows[slots, R:] - k) <= ref.rope_bound(k, x[:, R:], "bf16")).all()
+        x, turned = q.double().numpy(), host(qd)
+        y = ref.rotate(x[:, :, Dn:], cos, sin, True)
+        assert np.array_equal(turned[:, :, :Dn], x[:, :, :Dn])
+        assert (np.abs(turned[:, :, Dn:] - y) <= ref.rope_bound(y, x[:, :, Dn:], "bf16")).all()
+        # both forms, from the rows and queries as they are stored
+        qh, got, gat, i = host(qa), host(out), host(lat), 0
+        for s in range(S):
+            at = np.arange(lens[s] + new[s])
+            mine = np.array(want[0][want[1][s]:want[1][s + 1]])
+            cache = rows[mine[at // P] * P + at % P]
+            for j in range(new[s]):
+                seen = cache[:lens[s] + j + 1]
+                for h in range(H):
+                    e = seen[:, :R] @ w64[h].T
+                    r, tol = ref.attention_row(turned[i, h], np.concatenate([e[:, :Dn], seen[:, R:]], 1), e[:, Dn:], scale, "bf16")
+                    assert (np.abs(got[i, h] - r) <= tol).all(), (s, j, h)
+                    r, tol = ref.attention_row(qh[i, h], seen, seen[:, :R], scale, "bf16")
+                    assert (np.abs(gat[i, h] - r) <= tol).all(), (s, j, h)
+                i += 1
+        lens, have, table = lens + new, need, np.array(want[0], np.uint32)
+        free = np.array([p for p in free if p not in set(want[0])], np.uint32)
