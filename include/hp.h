@@ -706,7 +706,8 @@ int hp_latent_decode(const hp_paged_desc* desc, uint32_t latent_dim, const void*
 
 /* The two halves of hp_latent_decode, for layers that share a table: as hp_attention_plan and
  * hp_attention_decode_planned.  The planned calls name the plan's descriptor (but for
- * page_pool), q_ptr, total_q and num_q_heads. */
+ * page_pool), q_ptr, total_q and num_q_heads.  hp_latent_decode leaves its plan in the workspace
+ * too, so the first layer's call may be that one; whatever else uses the workspace ends the plan. */
 int hp_latent_plan(const hp_paged_desc* desc, uint32_t latent_dim, const void* q_ptr,
                    uint64_t total_q, uint32_t num_q_heads, void* workspace,
                    uint64_t workspace_bytes, int* d_status, void* stream);

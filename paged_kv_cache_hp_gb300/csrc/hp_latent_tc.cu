@@ -105,7 +105,7 @@ struct Walk {
     {
         while (pos < end) {
             while (pos >= past) {  // sequences without units are passed over
-                ++s;
+                if (++s >= a.num_seqs) return false;  // (not with a plan of this batch)
                 first = past;
                 past = units(s + 1);
             }
@@ -114,6 +114,7 @@ struct Walk {
             g.q0 = a.q_ptr ? index_at(a.q_ptr, a.idx64, s) : s;
             g.n = (a.q_ptr ? index_at(a.q_ptr, a.idx64, s + 1) : s + 1) - g.q0;
             g.steps = (g.len + kTok - 1) / kTok;
+            if (g.steps == 0) return false;  // (nor this)
             const uint64_t off = pos - first;
             // (the usual group is the sequence's only one)
             const uint64_t grp = off < g.steps ? 0 : off / g.steps;
@@ -189,7 +190,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t total;
     if (a.small) {
         const SmallPlan sp = small_plan(a.plan, a.idx64, units_s, nullptr);
-        if (blockIdx.x == 0 && threadIdx.x == 0) store_plan(a.plan, sp);
+        if (blockIdx.x == 0) {  // (whole, as a planned call may follow)
+            if (threadIdx.x == 0) store_plan(a.plan, sp);
+            if (threadIdx.x <= a.num_seqs) a.plan.ws.units_off[threadIdx.x] = units_s[threadIdx.x];
+        }
         planned = sp.key == kVerdictOk;
         total = planned ? sp.units : 0;
     } else {

@@ -337,3 +337,42 @@ def test_steps_over_a_latent_cache_row_by_row(hp):
                 i += 1
         lens, have, table = lens + new, need, np.array(want[0], np.uint32)
         free = np.array([p for p in free if p not in set(want[0])], np.uint32)
+
+
+# ------------------------------------------------------------------- plans, shared and reused
+@pytest.mark.parametrize("kernel", ["cuda_cores", "default"])
+@pytest.mark.parametrize("S", [1, 5, 128, 129])
+def test_planned_layers_behind_a_whole_call(hp, kernel, S):
+    """hp_latent_decode leaves its plan in the workspace, made by a launch of its own or by the first
+    kernel: planned calls over other layers' pools follow it, then again behind other queries."""
+    import torch
+    lens = np.random.default_rng(S).integers(0, 400, S)
+    nq = np.random.default_rng(S + 1).integers(0, 3, S)
+    nq[0] = 1
+    b = Latent(hp, lens, nq, 16, 512, 576, 16, "bf16", seed=S, flags=cores(hp, kernel))
+    q = b.queries(576)
+    rc, n = hp.hp_latent_decode_workspace_bytes(b.desc, 512, b.T, 16)
+    ws, alone = (torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(2))
+    pools = [b.pool, b.pool * 0.5, b.pool.flip(1).contiguous()]
+    layers = [b.desc] + [hp.PagedDesc(p, *b.desc._keep[1:4], num_pages=b.desc.c.num_pages, page_size=16, num_heads=1,
+                                      head_dim=576, dtype="bf16", index_type=0, flags=cores(hp, kernel)) for p in pools[1:]]
+    outs = [torch.full((b.T, 16, 512), 9.0, dtype=b.dt, device="cuda") for _ in layers]
+    want = [torch.full((b.T, 16, 512), 9.0, dtype=b.dt, device="cuda") for _ in layers]
+    for _ in range(2):
+        for i, d in enumerate(layers):
+            call = hp.hp_latent_decode_planned if i else hp.hp_latent_decode
+            assert call(d, 512, q, b.q_ptr, b.T, 16, 0.07, outs[i], ws, b.status) == 0
+        for d, o in zip(layers, want):
+            assert hp.hp_latent_decode(d, 512, q, b.q_ptr, b.T, 16, 0.07, o, alone, b.status) == 0
+        torch.cuda.synchronize()
+        assert b.status.item() == 0
+        for x, y in zip(outs, want):
+            assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+        check = host(outs[0])
+        for s, t, k in b.seen():
+            if t % 17 == 0:
+                c = b.rows[s][:k]
+                o, tol = ref.attention_row(b.q[t, 3].double().numpy(), c, c[:, :512], 0.07, "bf16")
+                assert (np.abs(check[t, 3] - o) <= tol).all()
+        b.q = torch.randn(b.q.shape).to(b.dt)
+        q.copy_(b.q)
