@@ -376,3 +376,205 @@ def test_planned_layers_behind_a_whole_call(hp, kernel, S):
                 assert (np.abs(check[t, 3] - o) <= tol).all()
         b.q = torch.randn(b.q.shape).to(b.dt)
         q.copy_(b.q)
+
+
+# ---------------------------------------------------------------- order, bounds, threads
+def small_step(hp, S, H, seed, form_q):
+    """Buffers and calls of one step over a latent cache: tables, append, decode and prompts' form."""
+    import torch
+    P, W, R, dt = 16, 576, 512, torch.bfloat16
+    rng = np.random.default_rng(seed)
+    lens = rng.integers(0, 150, S)
+    new = np.full(S, form_q)
+    s = make_step(hp, lens, new, -(-lens // P), P, 0, pad=0)
+    n = int(np.maximum(-(-lens // P), -(-(lens + new) // P)).sum())
+    s["o"]["table_out"] = s["o"]["table_out"][:n].clone()
+    s["d"] = hp.step_desc(block_table=s["d"].keep[0], seq_ptr=s["d"].keep[1], seq_lens=s["d"].keep[2],
+                          new_lens=s["d"].keep[3], free_pages=s["d"].keep[4], page_size=P, index_type=0, **s["o"])
+    T, pages = int(new.sum()), len(s["table"]) + len(s["free"])
+    x = dict(pool=torch.zeros((pages, P, W), dtype=dt, device="cuda"), kv=torch.zeros((T, W), dtype=dt, device="cuda"),
+             q=torch.zeros((T, H, W), dtype=dt, device="cuda"), qp=torch.zeros((T, H, 192), dtype=dt, device="cuda"),
+             out=torch.zeros((T, H, R), dtype=dt, device="cuda"), outp=torch.zeros((T, H, 128), dtype=dt, device="cuda"))
+    cs = dev(ref.cos_sin(200, 64))
+    rope = hp.rope_desc(cos_sin=cs, sections=(32,), positions=s["o"]["positions"])
+    ld = hp.latent_desc(latent=x["kv"][:, :R], k_rope=x["kv"][:, R:], q_rope=x["q"][:, :, R:], q_out=x["q"][:, :, R:],
+                        latent_weight=torch.ones(R, dtype=dt, device="cuda"), dtype="bf16", slot_map=s["o"]["slot_map"],
+                        pool=x["pool"], num_pages=pages, page_size=P)
+    pd = hp.PagedDesc(x["pool"], s["o"]["table_out"], s["o"]["seq_ptr_out"], s["o"]["lens_out"], num_pages=pages,
+                      page_size=P, num_heads=1, head_dim=W, dtype="bf16", index_type=0)
+    total = int((lens + new).sum())
+    w = selecting_weights(H, 128, 128, R, dt, seed).cuda()
+    sizes = (hp.hp_latent_decode_workspace_bytes(pd, R, T, H)[1],
+             hp.hp_latent_prefill_workspace_bytes(pd, R, 128, 128, T, H, total)[1])
+    wss = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for n in sizes]
+    st = [status_tensor() for _ in range(4)]
+    qptr = s["o"]["new_ptr_out"]
+    calls = [
+        lambda stream=None: hp.hp_step_tables(s["d"], s["ws"], st[0], stream),
+        lambda stream=None: hp.hp_latent_append(ld, rope, st[1], stream),
+        lambda stream=None: hp.hp_latent_decode(pd, R, x["q"], qptr, T, H, 0.07, x["out"], wss[0], st[2], stream),
+        lambda stream=None: hp.hp_latent_prefill(pd, R, w, 128, 128, x["qp"], qptr, T, H, 0.07, x["outp"], total, wss[1],
+                                                 st[3], stream),
+    ]
+    return x, calls, st, (s, wss, w, pd, ld, rope, cs)
+
+
+@pytest.mark.parametrize("S,H,n", [(3, 4, 1), (40, 16, 2), (130, 4, 1), (20, 80, 3)])
+def test_a_stream_without_waits_gives_what_waits_give(hp, S, H, n):
+    """Twenty steps in a row on one stream, each input written by a kernel just before the call that
+    reads it and overwritten just after: no call starts on what is not written yet, none loses what
+    it still reads."""
+    import torch
+    x, calls, st, keep = small_step(hp, S, H, 3, n)
+    rounds = 20
+    inputs = [{k: torch.randn(x[k].shape, device="cuda").to(x[k].dtype) for k in ("kv", "q", "qp")} for _ in range(rounds)]
+    torch.cuda.synchronize()
+    results = []
+    for wait in (True, False):
+        got = []
+        x["pool"].zero_()
+        for i in range(rounds):
+            for k, v in inputs[i].items():
+                torch.mul(v, 1.0, out=x[k])
+            for call in calls:
+                assert call() == 0
+                if wait:
+                    torch.cuda.synchronize()
+            got.append([x[k].clone() for k in ("out", "outp", "pool", "q")])
+            for k in ("kv", "q", "qp", "out", "outp"):
+                x[k].fill_(float("nan"))
+        torch.cuda.synchronize()
+        assert [t.item() for t in st] == [0] * 4
+        results.append(got)
+    for a, b in zip(*results):
+        for y, z in zip(a, b):
+            assert torch.equal(y, z) and torch.isfinite(y.float()).all()
+
+
+def test_two_threads_call_at_once(hp):
+    """Two host threads, a stream and buffers each: the same results as one after the other."""
+    import threading
+
+    import torch
+    runs = [small_step(hp, 30, 16, 5, 1), small_step(hp, 7, 4, 6, 2)]
+    for x, calls, st, keep in runs:
+        for k in ("kv", "q", "qp"):
+            x[k].normal_()
+    torch.cuda.synchronize()
+    start = [{k: v.clone() for k, v in x.items()} for x, *_ in runs]
+    want = []
+    for x, calls, st, keep in runs:
+        for call in calls:
+            assert call() == 0
+        torch.cuda.synchronize()
+        want.append({k: v.clone() for k, v in x.items()})
+    errors = []
+
+    def work(i):
+        x, calls, st, keep = runs[i]
+        stream = torch.cuda.Stream()
+        try:
+            for _ in range(30):
+                with torch.cuda.stream(stream):
+                    for k, v in start[i].items():
+                        x[k].copy_(v)
+                    assert [call(stream) for call in calls] == [0] * 4
+                stream.synchronize()
+                assert [t.item() for t in st] == [0] * 4
+                for k, v in want[i].items():
+                    assert torch.equal(x[k], v), k
+        except BaseException as e:  # noqa: BLE001
+            errors.append((i, e))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+
+
+@pytest.mark.parametrize("kernel", ["cuda_cores", "default"])
+def test_nothing_is_written_past_a_buffer(hp, kernel):
+    """Workspaces of exactly the size asked for and outputs of exactly the rows, between guards."""
+    import torch
+    from conftest import guarded, guards_intact
+    for lens, nq, H in ((A([300, 0, 70]), A([3, 2, 1]), 100), (A([9000]), A([1]), 16), (np.full(200, 60), np.full(200, 2), 4),
+                        (A([257, 1]), A([257, 1]), 3)):
+        b = Latent(hp, lens, nq, H, 512, 576, 16, "bf16", seed=9, flags=cores(hp, kernel))
+        w = selecting_weights(H, 128, 128, 512, b.dt, 3).cuda()
+        kv = int(lens.sum())
+        for form, width, dv in (("decode", 576, 512), ("prefill", 192, 128)):
+            q = b.queries(width)
+            n = (hp.hp_latent_decode_workspace_bytes(b.desc, 512, b.T, H) if form == "decode" else
+                 hp.hp_latent_prefill_workspace_bytes(b.desc, 512, 128, 128, b.T, H, kv))[1]
+            wbuf, ws = guarded(n)
+            obuf, out = guarded(b.T * H * dv * 2)
+            o = out.view(b.dt).view(b.T, H, dv)
+            if form == "decode":
+                rc = hp.hp_latent_decode(b.desc, 512, q, b.q_ptr, b.T, H, 0.07, o, ws, b.status)
+            else:
+                rc = hp.hp_latent_prefill(b.desc, 512, w, 128, 128, q, b.q_ptr, b.T, H, 0.07, o, kv, ws, b.status)
+            torch.cuda.synchronize()
+            assert rc == 0 and b.status.item() == 0
+            assert guards_intact(wbuf, n) and guards_intact(obuf, b.T * H * dv * 2)
+            assert torch.isfinite(o.float()).all()
+
+
+def test_large_steps_in_a_graph(hp):
+    """Tables of 1,500 sequences and appends that report in both ways, captured together and replayed on
+    other lengths and rows."""
+    import torch
+    P, dt = 16, torch.bfloat16
+    rng = np.random.default_rng(2)
+    S = 1500
+    lens, new = rng.integers(0, 100, S), rng.integers(0, 5, S)
+    s = make_step(hp, lens, new, np.full(S, 8), P, 0, pad=1000)  # slices that need not grow
+    T, pages = s["o"]["slot_map"].numel(), len(s["table"]) + len(s["free"])
+    cs = dev(ref.cos_sin(300, 128))
+    st = [status_tensor() for _ in range(2)]
+    kv = torch.zeros((T, 576), dtype=dt, device="cuda")
+    x = torch.zeros((T, 48 * 128), dtype=dt, device="cuda")
+    pool = torch.zeros((pages, P, 576), dtype=dt, device="cuda")
+    kp, vp = (torch.zeros((pages, P, 8, 128), dtype=dt, device="cuda") for _ in range(2))
+    cs64 = dev(ref.cos_sin(300, 64))
+    ld = hp.latent_desc(latent=kv[:, :512], k_rope=kv[:, 512:], dtype="bf16", slot_map=s["o"]["slot_map"], pool=pool,
+                        num_pages=pages, page_size=P)
+    qd = hp.qk_desc(q=x[:, :4096], k=x[:, 4096:5120], v=x[:, 5120:], q_out=x[:, :4096], num_q_heads=32, num_kv_heads=8,
+                    head_dim=128, dtype="bf16", slot_map=s["o"]["slot_map"], k_pool=kp, v_pool=vp, num_pages=pages,
+                    page_size=P)
+    r64 = hp.rope_desc(cos_sin=cs64, sections=(32,), positions=s["o"]["positions"])
+    r128 = hp.rope_desc(cos_sin=cs, sections=(64,), positions=s["o"]["positions"])
+
+    def calls():
+        assert hp.hp_step_tables(s["d"], s["ws"], s["status"]) == 0
+        assert hp.hp_latent_append(ld, r64, st[0]) == 0
+        assert hp.hp_qk_norm_rope_append(qd, r128, st[1]) == 0
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for seed in (1, 2):
+        r = np.random.default_rng(seed)
+        lens, new = r.integers(0, 100, S), r.integers(0, 5, S)
+        s["d"].keep[2].copy_(torch.from_numpy(lens.astype(np.int32)))
+        s["d"].keep[3].copy_(torch.from_numpy(new.astype(np.int32)))
+        kv.normal_()
+        rows = torch.randn(x.shape).to(dt).cuda()
+        results = []
+        for run in (graph.replay, calls):
+            x.copy_(rows)
+            for t in (pool, kp, vp):
+                t.fill_(3.0)
+            run()
+            torch.cuda.synchronize()
+            assert [t.item() for t in (s["status"], *st)] == [0] * 3
+            results.append([t.clone() for t in (pool, kp, vp, x, *s["o"].values())])
+        for a, c in zip(*results):
+            assert torch.equal(a, c)
+        n = int(new.sum())
+        want = ref.step_tables(lens, new, s["sp"], s["table"], s["free"], P)
+        assert s["o"]["slot_map"].cpu().tolist() == want[4] + [-1] * (T - n)
+        at = torch.tensor(want[4], device="cuda")
+        assert torch.equal(pool.view(-1, 576)[at][:, :512], kv[:n, :512])
+        assert torch.equal(vp.view(-1, 1024)[at], rows[:n, 5120:]) and torch.equal(x[n:], rows[n:])
