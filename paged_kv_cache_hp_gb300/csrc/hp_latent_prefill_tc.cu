@@ -12,9 +12,9 @@
 // operands come from L2.  KV goes to the workspace in blocks of 128 rows x 64 columns laid out as
 // shared memory will hold them (head, row block, K0 K1 V0 V1), so that the attention below loads
 // 16 KiB pieces with untiled bulk copies; the rope keys likewise (hp_latent.cu).  K and V are rounded
-to 16 bits there, as the attention's products take them (in 32 bits they would be twice the traffic and
-a product of split operands twice the time): against 64 bits the whole is off by 1.5 to 1.6 times
-what the result's own rounding is.
+// to 16 bits there, as the attention's products take them (in 32 bits they would be twice the traffic and
+// a product of split operands twice the time): against 64 bits the whole is off by 1.5 to 1.6 times
+// what the result's own rounding is.
 //
 // latent_prefill_kernel: softmax(scale Q K^T) V for one head and 256 queries of a sequence, as
 // two tiles of 128 queries that share the keys' 128-row blocks: K = [expanded 128 | rope 64], V =
