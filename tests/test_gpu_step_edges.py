@@ -578,3 +578,21 @@ def test_large_steps_in_a_graph(hp):
         at = torch.tensor(want[4], device="cuda")
         assert torch.equal(pool.view(-1, 576)[at][:, :512], kv[:n, :512])
         assert torch.equal(vp.view(-1, 1024)[at], rows[:n, 5120:]) and torch.equal(x[n:], rows[n:])
+
+
+@pytest.mark.parametrize("S", [2, 130])
+def test_planned_calls_behind_a_batch_that_fails(hp, S):
+    """A whole call whose batch breaks a rule leaves a plan that says so: a planned call behind it writes
+    nothing and keeps the code."""
+    import torch
+    b = Latent(hp, np.full(S, 40), np.full(S, 1), 16, 512, 576, 16, "bf16", seed=S)
+    q = b.queries(576)
+    ws = torch.full((hp.hp_latent_decode_workspace_bytes(b.desc, 512, b.T, 16)[1],), 0xFF, dtype=torch.uint8, device="cuda")
+    out = torch.full((b.T, 16, 512), 9.0, dtype=b.dt, device="cuda")
+    good = b.desc._keep[1].clone()
+    b.desc._keep[1][3 * S - 1] = 10 ** 6
+    assert hp.hp_latent_decode(b.desc, 512, q, b.q_ptr, b.T, 16, 0.07, out, ws, b.status) == 0
+    b.desc._keep[1].copy_(good)
+    assert hp.hp_latent_decode_planned(b.desc, 512, q, b.q_ptr, b.T, 16, 0.07, out, ws, b.status) == 0
+    torch.cuda.synchronize()
+    assert hp.status_name(b.status.item()) == "HP_ERR_PAGE_ID" and (out == 9).all()
