@@ -689,9 +689,9 @@ int hp_latent_decode_workspace_bytes(const hp_paged_desc* desc, uint32_t latent_
  * out (device, [total_q, num_q_heads, latent_dim], the pool's type).  Scores, softmax
  * statistics and sums are fp32; on the tensor cores the weights enter the value product rounded
  * to the pool's type (f16: times a common 2^7, so that a small one is off by at most 2^-32 of the
- * row's largest), and the result is rounded once.  A row of the
- * pool that is not finite spoils the queries that see its token and no others; slots past a
- * sequence's length may hold anything, and a NaN in a query stays in its own row of out.
+ * row's largest), and the result is rounded once.  A row of the pool that is not finite spoils the
+ * queries that see its token and no others; slots past a sequence's length may hold anything, and a
+ * NaN in a query stays in its own row of out.
  * Supported: latent_dim a multiple of 64 up to 512; rope_dim a multiple of 8 from 8 to 64;
  * page_size <= 2^26 (HP_ERR_ARG otherwise).  latent_dim 512 with rope_dim 64 and pages of a
  * multiple of 8 slots run on the tensor cores, the others on the CUDA cores
