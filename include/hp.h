@@ -20,6 +20,9 @@
  *   - the operators of a serving step around them: block tables and slot maps from the
  *     requests' lengths, norm + rotation + append in one pass, and attention over a cache
  *     of shared latent rows (absorbed for decode, expanded for prompts),
+ *   - decode over long contexts: bounds of each page's keys, the pages whose bounds promise a
+ *     query the highest scores, attention over those pages, and attention of sequences that
+ *     share a long prefix, which is read once for all of them,
  *   - conversions between a kernel-internal cache layout and the interchange layout,
  *     and between a padded block table and the descriptor's slices.
  *
@@ -31,7 +34,8 @@
  *   current CUDA device; pointers described as "host" point to CPU memory.
  *   The page pool and the output of the gathers (dequantising ones included), the
  *   pool and new rows of the appends, the pool of hp_copy_pages, the buffers of the
- *   lane operations, the K and V pools of decode attention and the pool of latent
+ *   lane operations, the K and V pools of decode attention (over all, over selected pages
+ *   or behind shared prefixes; of the page bounds K's) and the pool of latent
  *   attention may instead be page-locked host memory (from the CUDA host allocator or
  *   cudaHostRegister, mapped): those operations then read and write it in place over the host link.
  *   The caller says so with HP_HOST_MEMORY (the copies then take the register
@@ -116,8 +120,12 @@ typedef enum hp_status {
     HP_ERR_NOALLOC_LIMIT = -33, /* hp_gather_noalloc: more than HP_NOALLOC_MAX_SEQS sequences */
     HP_ERR_QUANT_SCHEME = -34,  /* unknown scheme tag, or per-channel on an axis other than
                                    1 (num_heads) or 2 (head_dim)                             */
-    HP_ERR_QUANT_BLOCK = -35    /* [HF] Per-scheme composition: per-block-affine whose axis is
+    HP_ERR_QUANT_BLOCK = -35,   /* [HF] Per-scheme composition: per-block-affine whose axis is
                                    not 0 or whose block_size is not page_size                */
+    /* shared prefixes, after the storage invariants and the queries' offsets */
+    HP_ERR_GROUP = -36,         /* group_ptr does not start at 0, falls, or does not end at
+                                   num_seqs                                                  */
+    HP_ERR_PREFIX = -37         /* a group's prefix is longer than what one of its queries sees */
 } hp_status;
 
 /* Name of a status code ("HP_OK", "HP_ERR_RANK", ...); "HP_ERR_UNKNOWN" otherwise. */
@@ -745,6 +753,134 @@ int hp_latent_prefill(const hp_paged_desc* desc, uint32_t latent_dim, const void
                       uint64_t total_q, uint32_t num_q_heads, float scale, void* out,
                       uint64_t kv_tokens, void* workspace, uint64_t workspace_bytes,
                       int* d_status, void* stream);
+
+/* ------------------------------------------------------------- long contexts */
+/*
+ * Decode steps over long sequences.  hp_page_bounds keeps, beside a K pool, each page's largest
+ * and smallest key; hp_page_scores turns a query and those bounds into an upper bound of what the
+ * page's tokens can score; hp_select_pages picks the pages with the highest, and hp_attention_pages
+ * attends to those alone.  hp_attention_prefix attends to everything, but reads the tokens that
+ * sequences share ([HF] Prefix Sharing) once for all of them.  (The operators are this library's;
+ * the pages cited above define the layout they read.)
+ *
+ * Common to the five:
+ * - the K pool HP_F16 or HP_BF16, head_dim 64, 128 or 256, page_size up to 4096, at most 65,536 K/V
+ *   heads, 1 to 16 query heads a K/V head (HP_ERR_ARG otherwise); sequences below 2^31 tokens (HP_ERR_LEN
+ *   on the device).  seq_lens are the lengths AFTER the step's append.
+ * - q (device, [total_q, num_q_heads, head_dim] of the pool's type, 16-byte aligned): sequence s has
+ *   the n = q_ptr[s+1] - q_ptr[s] queries q_ptr[s] ..., its last n tokens in order, so query i of them
+ *   sees the tokens t < len_s - n + 1 + i, as in hp_latent_decode.  q_ptr (device, num_seqs+1 entries of
+ *   the index type) may be NULL: one query per sequence, total_q = num_seqs (HP_ERR_ARG otherwise).  Rows
+ *   that q_ptr gives to no sequence (q_ptr[num_seqs] < total_q: a padded batch) are neither read nor
+ *   written, in any buffer.
+ * - they are a serving step's calls: each is launched as a dependent of the stream's last kernel.
+ * - but for hp_attention_prefix they need no plan and no workspace, and check what they read as they
+ *   read it, as the appends do: a query (a page, for hp_page_bounds) whose slice, length or pages do not
+ *   hold is skipped, its outputs left as they were.  *d_status gets the lowest of the codes found:
+ *   HP_ERR_LEN (a slice too short for the tokens, outside the table or reversed; a page that the
+ *   sequence does not have), HP_ERR_PAGE_ID, HP_ERR_OUT_SIZE, and HP_ERR_NEW_PTR_START, _ORDER or _END for
+ *   the offsets (NEW_PTR_END: they end past total_q).  HP_PERMISSIVE changes nothing.
+ */
+
+/*
+ * ASYNC.  Bounds of the keys of the pages that new tokens fell into.  bounds (device, [num_pages,
+ * num_heads, 2, head_dim] of the pool's type, 64-byte aligned): for every page that holds one of the
+ * last new_ptr[s+1] - new_ptr[s] tokens of a sequence s, element (page, h, 0, d) becomes the largest and
+ * (page, h, 1, d) the smallest K of dimension d of head h over all the page's tokens before seq_lens[s]
+ * (of the page's slots, those and no others are read).  Other pages' bounds are left as they were.  new_ptr (device,
+ * num_seqs+1 entries, an append's new_ptr; new_ptr[num_seqs] <= total_new) may be NULL: each
+ * sequence's last token is new (none of an empty one), total_new = num_seqs.  A key that is not a number makes both bounds of its
+ * dimension NaN.  Nothing is rounded.  A page that two sequences of different lengths fill
+ * gets the bounds of either, or a mix.
+ */
+int hp_page_bounds(const hp_paged_desc* k_desc, const void* new_ptr, uint64_t total_new, void* bounds,
+                   int* d_status, void* stream);
+
+/*
+ * ASYNC.  Upper bounds of the scores in each page: for query row r, K/V head g and each page j <
+ * ceil(seen / page_size) of its sequence,
+ *   scores[r, g, j] = scale * max over the group's query heads of
+ *                     sum_d max(q_d * hi_d, q_d * lo_d),
+ * hi and lo the bounds of the page: no token of it scores higher for any of those heads.  scores
+ * (device, fp32, [total_q, num_heads, max_pages]); entries from that count on are left as
+ * they were; max_pages smaller than the count skips the query (HP_ERR_OUT_SIZE).  scale >= 0
+ * (HP_ERR_ARG).  Products are exact, sums fp32.  A NaN among the bounds of a page or in a query of the group
+ * gives NaN.  desc->page_pool is not read (and may be NULL).
+ */
+int hp_page_scores(const hp_paged_desc* desc, const void* bounds, const void* q, const void* q_ptr,
+                   uint64_t total_q, uint32_t num_q_heads, float scale, float* scores,
+                   uint64_t max_pages, int* d_status, void* stream);
+
+/*
+ * ASYNC.  The pages to read: selected (device, int32, [total_q, num_heads, k]) gets, for query row r
+ * and K/V head g, the first `sinks` and the last `recent` of the n pages that hold what it sees
+ * (n = ceil(seen / page_size)) and of the others those with the highest scores[r, g, j], k in all
+ * (all n where n <= k), in ascending order, then -1.  Of equal scores the lower page goes first; NaN is
+ * above everything, and both zeros are equal.  scores and max_pages as hp_page_scores leaves them, or any others of that
+ * form.  sinks + recent <= k, k >= 1 (HP_ERR_ARG).  Of desc the lengths, page_size and num_heads are
+ * used; table and pool are not read.
+ */
+int hp_select_pages(const hp_paged_desc* desc, const void* q_ptr, uint64_t total_q,
+                    const float* scores, uint64_t max_pages, uint32_t sinks, uint32_t recent,
+                    uint32_t k, int32_t* selected, int* d_status, void* stream);
+
+/*
+ * ASYNC.  Decode attention over selected pages: for query row r and each query head of K/V head g,
+ * softmax(scale q . K) V over the tokens of the pages selected[r, g, 0 .. k) (indices into the
+ * sequence's slice; negative ones name no page) that the query sees.  A page named twice counts
+ * twice; any order will do.  An index of a page that the sequence does not have skips the query's heads of
+ * g (HP_ERR_LEN).  K from k_desc's pool, V from v_pool (same geometry and type).  out (device,
+ * [total_q, num_q_heads, head_dim], the pool's type) gets zeros where there is nothing to see.  Scores,
+ * softmax statistics and sums are fp32; the weights are rounded to the pool's type for the value
+ * product (f16: times 2^7), the result once.  A key or value that is not finite spoils the queries that see its token
+ * and no others.  k * page_size below 2^31 (HP_ERR_ARG).  Tokens are cut among up to 8 CTAs a
+ * (query, K/V head): the same call gives the same bits.
+ */
+int hp_attention_pages(const hp_paged_desc* k_desc, const void* v_pool, const void* q,
+                       const void* q_ptr, uint64_t total_q, uint32_t num_q_heads, float scale,
+                       const int32_t* selected, uint32_t k, void* out, int* d_status, void* stream);
+
+/*
+ * Bytes of device workspace (256-byte aligned) hp_attention_prefix needs: an entry per query row and
+ * group, and fp32 records (max, sum, head_dim accumulators) of every (query, head) row and of 256 rows
+ * for each SM.
+ */
+int hp_attention_prefix_workspace_bytes(const hp_paged_desc* k_desc, uint64_t num_groups,
+                                        uint64_t total_q, uint32_t num_q_heads, uint64_t* bytes);
+
+/*
+ * ASYNC.  Decode attention of groups of sequences that share their first tokens.  Group i is the
+ * sequences group_ptr[i] .. group_ptr[i+1] (device, num_groups+1 entries of the index type; together
+ * all of them), and the first prefix_lens[i] tokens (device, num_groups entries) of each of them are
+ * read through the slice of its first sequence, once for all its queries; the others through each
+ * sequence's own slice.  The prefix need not end at a page's end: what a sequence's own slice
+ * holds for the prefix's tokens is not read.  (A sequence by itself is a group of one, with any prefix; a prefix of 0 shares nothing.)
+ *   out[r, qh] = softmax over t < seen_r (scale q . K(t)) V(t)
+ * with K, V, q, q_ptr, out, rounding and empty rows as in hp_attention_pages.  Every query of a group
+ * has to see its whole prefix (HP_ERR_PREFIX).  num_groups at most num_seqs, and 0 only without
+ * sequences (HP_ERR_ARG).  The descriptor is always validated, as in hp_attention_decode (q_ptr with the
+ * codes of an append's new_ptr, then HP_ERR_GROUP, HP_ERR_PREFIX): if a rule fails nothing is written but
+ * *d_status.
+ */
+int hp_attention_prefix(const hp_paged_desc* k_desc, const void* v_pool, const void* group_ptr,
+                        const void* prefix_lens, uint64_t num_groups, const void* q,
+                        const void* q_ptr, uint64_t total_q, uint32_t num_q_heads, float scale,
+                        void* out, void* workspace, uint64_t workspace_bytes, int* d_status,
+                        void* stream);
+
+/* The two halves of hp_attention_prefix, for layers that share a table: as hp_attention_plan and
+ * hp_attention_decode_planned.  The planned calls name the plan's descriptor (but for page_pool),
+ * groups, q_ptr, total_q and num_q_heads; whatever else uses the workspace ends the plan.  Planned
+ * calls whose work may overlap on the GPU need workspaces (and plans) of their own. */
+int hp_attention_prefix_plan(const hp_paged_desc* k_desc, const void* group_ptr,
+                             const void* prefix_lens, uint64_t num_groups, const void* q_ptr,
+                             uint64_t total_q, uint32_t num_q_heads, void* workspace,
+                             uint64_t workspace_bytes, int* d_status, void* stream);
+int hp_attention_prefix_planned(const hp_paged_desc* k_desc, const void* v_pool,
+                                const void* group_ptr, const void* prefix_lens, uint64_t num_groups,
+                                const void* q, const void* q_ptr, uint64_t total_q,
+                                uint32_t num_q_heads, float scale, void* out, void* workspace,
+                                uint64_t workspace_bytes, int* d_status, void* stream);
 
 /* --------------------------------------------------------- layout conversions */
 /*

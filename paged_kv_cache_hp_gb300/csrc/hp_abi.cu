@@ -295,6 +295,8 @@ HP_API const char* hp_status_string(int s)
         HP_NAME(HP_ERR_NOALLOC_LIMIT)
         HP_NAME(HP_ERR_QUANT_SCHEME)
         HP_NAME(HP_ERR_QUANT_BLOCK)
+        HP_NAME(HP_ERR_GROUP)
+        HP_NAME(HP_ERR_PREFIX)
 #undef HP_NAME
     default: return "HP_ERR_UNKNOWN";
     }

@@ -1,0 +1,368 @@
+// hp_abi_pages.cu -- the entry points of long contexts (include/hp.h): page bounds, page scores, page
+// selection, attention over selected pages, attention behind shared prefixes.  Host-side checks,
+// then launches on the caller's stream.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "hp_abi_checks.cuh"
+#include "hp_rows.cuh"
+
+namespace {
+
+constexpr u64 kGrid = (1ull << 31) - 1;
+
+u64 index_bytes(uint32_t index_type) { return index_type == HP_IDX_U64 ? 8 : 4; }
+
+// The descriptor as these operators take it: what they read is checked on the device.
+int check_pages(const hp_paged_desc* desc, const void* pool, hp_paged_desc* d)
+{
+    if (!desc) return HP_ERR_NULL;
+    *d = *desc;
+    if (pool) d->page_pool = pool;
+    d->flags &= ~(HP_PERMISSIVE | HP_HAS_QUANT);
+    const int rc = check_desc(d);
+    if (rc) return rc;
+    if (d->dtype != HP_F16 && d->dtype != HP_BF16) return HP_ERR_DTYPE;
+    if ((d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256) || d->page_size > hp::kPagesMaxPage ||
+        d->num_heads > (1u << 16))
+        return HP_ERR_ARG;
+    return HP_OK;
+}
+
+int check_heads(const hp_paged_desc& d, uint32_t num_q_heads, float scale)
+{
+    if (num_q_heads == 0 || num_q_heads % d.num_heads || num_q_heads / d.num_heads > hp::kPagesMaxGroup ||
+        !(scale == scale))
+        return HP_ERR_ARG;
+    return HP_OK;
+}
+
+// Offsets of queries or new tokens: NULL for one a sequence.
+int check_offsets(const hp_paged_desc& d, const void* ptr, u64 total)
+{
+    if (total >> 40) return HP_ERR_OVERFLOW;
+    if (!ptr) return total == d.num_seqs ? HP_OK : HP_ERR_ARG;
+    return misaligned(ptr, index_bytes(d.index_type)) ? HP_ERR_ALIGN : HP_OK;
+}
+
+hp::QueryArgs query_args(const hp_paged_desc& d, const void* q_ptr, u64 total_q)
+{
+    return hp::QueryArgs{q_ptr, d.seq_lens, d.num_seqs, total_q, d.index_type == HP_IDX_U64};
+}
+
+hp::PageTable page_table(const hp_paged_desc& d)
+{
+    return hp::PageTable{d.seq_ptr, d.block_table, d.table_len, d.num_pages};
+}
+
+int reset_status(int* d_status, void* stream)
+{
+    if (!d_status) return HP_OK;
+    return cudaMemsetAsync(d_status, 0, sizeof(int), static_cast<cudaStream_t>(stream)) == cudaSuccess ? HP_OK
+                                                                                                       : HP_ERR_CUDA;
+}
+
+// CTAs of a (row, K/V head): as many as fill the SMs twice, while each has a block for its warps.
+uint32_t cluster_of(u64 units, u64 tokens, int sms)
+{
+    uint32_t c = 1;
+    while (c < 8 && units * c < 2 * (u64)sms && tokens / (2 * c) >= 64) c *= 2;
+    return c;
+}
+
+}  // namespace
+
+HP_API int hp_page_bounds(const hp_paged_desc* desc, const void* new_ptr, uint64_t total_new, void* bounds,
+                          int* d_status, void* stream)
+{
+    hp_paged_desc d;
+    int rc = check_pages(desc, nullptr, &d);
+    if (rc) return rc;
+    rc = check_offsets(d, new_ptr, total_new);
+    if (rc) return rc;
+    if (d.num_pages && !bounds) return HP_ERR_NULL;
+    if (misaligned(bounds, 64)) return HP_ERR_ALIGN;
+    hp::BoundsArgs a{};
+    a.q = query_args(d, new_ptr, total_new);
+    a.t = page_table(d);
+    a.pool = d.page_pool;
+    a.bounds = bounds;
+    a.P = (uint32_t)d.page_size;
+    a.row_half = (uint32_t)d.head_dim / 8;
+    a.columns = (uint32_t)d.num_heads * a.row_half;
+    a.units = d.num_seqs == 0 ? 0 : new_ptr ? total_new / a.P + 2 * d.num_seqs : d.num_seqs;
+    if ((u128)a.units * ((a.columns + 127) / 128) + 1 > kGrid) return HP_ERR_OVERFLOW;
+    if (a.units == 0) return reset_status(d_status, stream);
+    a.bf16 = d.dtype == HP_BF16;
+    a.check_all = total_new + d.num_seqs <= hp::kPagesChecked;
+    a.d_status = d_status;
+    return hp::launch_page_bounds(a, stream);
+}
+
+HP_API int hp_page_scores(const hp_paged_desc* desc, const void* bounds, const void* q, const void* q_ptr,
+                          uint64_t total_q, uint32_t num_q_heads, float scale, float* scores, uint64_t max_pages,
+                          int* d_status, void* stream)
+{
+    if (desc && desc->num_pages && !bounds) return HP_ERR_NULL;
+    hp_paged_desc d;
+    int rc = check_pages(desc, bounds, &d);
+    if (rc) return rc;
+    rc = check_heads(d, num_q_heads, scale);
+    if (rc) return rc;
+    if (scale < 0.0f) return HP_ERR_ARG;
+    rc = check_offsets(d, q_ptr, total_q);
+    if (rc) return rc;
+    if (max_pages >> 31 || ((u128)total_q * d.num_heads * max_pages) >> 60) return HP_ERR_OVERFLOW;
+    if (total_q && (!q || (max_pages && !scores))) return HP_ERR_NULL;
+    if (misaligned(q, 16) || misaligned(scores, 4)) return HP_ERR_ALIGN;
+    if (total_q == 0 || d.num_seqs == 0) return reset_status(d_status, stream);
+    int dev = 0;
+    const u64 sms = (u64)hp::current_sms(&dev);
+    if (sms == 0) return HP_ERR_CUDA;
+    hp::ScoreArgs a{};
+    a.q = query_args(d, q_ptr, total_q);
+    a.t = page_table(d);
+    a.bounds = bounds;
+    a.queries = q;
+    a.scores = scores;
+    a.max_pages = max_pages;
+    a.P = (uint32_t)d.page_size;
+    a.H = (uint32_t)d.num_heads;
+    a.G = num_q_heads / a.H;
+    a.D = (uint32_t)d.head_dim;
+    // a CTA's eight warps take (16 pages, head) pairs: one each while the SMs are not filled twice
+    // over, then up to eight
+    const u64 blocks = std::max<u64>(1, (max_pages + 15) / 16);
+    const u64 each = std::min<u64>(8, std::max<u64>(1, total_q * blocks * a.H / (sms * 32)));
+    a.chunk_blocks = (uint32_t)std::max<u64>(1, (each * 8 + a.H - 1) / a.H);
+    a.chunks = (blocks + a.chunk_blocks - 1) / a.chunk_blocks;
+    if ((u128)total_q * a.chunks + 1 > kGrid) return HP_ERR_OVERFLOW;
+    a.scale = scale;
+    a.bf16 = d.dtype == HP_BF16;
+    a.check_all = std::max<u64>(total_q, q_ptr ? total_q * max_pages : d.table_len) <= hp::kPagesChecked;
+    a.d_status = d_status;
+    return hp::launch_page_scores(a, stream);
+}
+
+HP_API int hp_select_pages(const hp_paged_desc* desc, const void* q_ptr, uint64_t total_q, const float* scores,
+                           uint64_t max_pages, uint32_t sinks, uint32_t recent, uint32_t k, int32_t* selected,
+                           int* d_status, void* stream)
+{
+    hp_paged_desc d;
+    int rc = check_pages(desc, nullptr, &d);
+    if (rc) return rc;
+    rc = check_offsets(d, q_ptr, total_q);
+    if (rc) return rc;
+    if (k == 0 || k >> 31 || (u64)sinks + recent > k) return HP_ERR_ARG;
+    if (max_pages >> 31 || ((u128)total_q * d.num_heads * std::max<u64>(max_pages, k)) >> 60) return HP_ERR_OVERFLOW;
+    if (total_q && ((max_pages && !scores) || !selected)) return HP_ERR_NULL;
+    if (misaligned(scores, 4) || misaligned(selected, 4)) return HP_ERR_ALIGN;
+    if ((u128)total_q * d.num_heads + 1 > kGrid) return HP_ERR_OVERFLOW;
+    if (total_q == 0 || d.num_seqs == 0) return reset_status(d_status, stream);
+    hp::SelectArgs a{};
+    a.q = query_args(d, q_ptr, total_q);
+    a.scores = scores;
+    a.selected = selected;
+    a.max_pages = max_pages;
+    a.P = (uint32_t)d.page_size;
+    a.H = (uint32_t)d.num_heads;
+    a.sinks = sinks;
+    a.recent = recent;
+    a.k = k;
+    a.check_all = total_q <= hp::kPagesChecked;
+    a.d_status = d_status;
+    return hp::launch_select_pages(a, stream);
+}
+
+namespace {
+
+// Checks and arguments that the two attention calls share.
+int rows_args(const hp_paged_desc& d, const void* v_pool, const void* q, const void* q_ptr, u64 total_q,
+              uint32_t num_q_heads, float scale, void* out, hp::RowsArgs* a)
+{
+    int rc = check_heads(d, num_q_heads, scale);
+    if (rc) return rc;
+    rc = check_offsets(d, q_ptr, total_q);
+    if (rc) return rc;
+    if ((u128)total_q * num_q_heads >> 40 || (u128)total_q * d.num_heads * 8 + 8 > kGrid) return HP_ERR_OVERFLOW;
+    if ((d.num_pages && !v_pool) || (total_q && (!q || !out))) return HP_ERR_NULL;
+    if (misaligned(v_pool, 64) || misaligned(q, 16) || misaligned(out, 16)) return HP_ERR_ALIGN;
+    a->q = query_args(d, q_ptr, total_q);
+    a->t = page_table(d);
+    a->k_pool = d.page_pool;
+    a->v_pool = v_pool;
+    a->queries = q;
+    a->out = out;
+    a->P = (uint32_t)d.page_size;
+    hp::invariant_divisor(a->P, &a->p_m, &a->p_l);
+    a->H = (uint32_t)d.num_heads;
+    a->G = num_q_heads / a->H;
+    a->D = (uint32_t)d.head_dim;
+    a->scale = scale;
+    a->bf16 = d.dtype == HP_BF16;
+    return HP_OK;
+}
+
+}  // namespace
+
+HP_API int hp_attention_pages(const hp_paged_desc* k_desc, const void* v_pool, const void* q, const void* q_ptr,
+                              uint64_t total_q, uint32_t num_q_heads, float scale, const int32_t* selected,
+                              uint32_t k, void* out, int* d_status, void* stream)
+{
+    hp_paged_desc d;
+    int rc = check_pages(k_desc, nullptr, &d);
+    if (rc) return rc;
+    hp::RowsArgs a{};
+    rc = rows_args(d, v_pool, q, q_ptr, total_q, num_q_heads, scale, out, &a);
+    if (rc) return rc;
+    if (k == 0 || (u64)k * d.page_size >> 31) return HP_ERR_ARG;
+    if (total_q && !selected) return HP_ERR_NULL;
+    if (misaligned(selected, 4)) return HP_ERR_ALIGN;
+    if (total_q == 0 || d.num_seqs == 0) return reset_status(d_status, stream);
+    int dev = 0;
+    const int sms = hp::current_sms(&dev);
+    if (sms == 0) return HP_ERR_CUDA;
+    a.selected = selected;
+    a.k = k;
+    a.cluster = cluster_of(total_q * a.H, (u64)k * a.P, sms);
+    a.check_all = total_q * a.H * k <= hp::kPagesChecked;
+    a.d_status = d_status;
+    return hp::launch_rows(a, stream);
+}
+
+namespace {
+
+// Byte offsets of the workspace of hp_attention_prefix.
+struct PrefixWs {
+    u64 rows, groups, ml, acc, total;
+};
+
+int prefix_ws(u64 num_groups, u64 total_q, uint32_t num_q_heads, u64 head_dim, PrefixWs* w)
+{
+    if (num_groups >> 32 || total_q >> 32 || ((u128)total_q * num_q_heads) >> 40 || head_dim > 256) return HP_ERR_OVERFLOW;
+    const u64 records = total_q * num_q_heads + (u64)hp::kPrefixMaxSms * hp::kPrefixRows;
+    w->rows = 256;
+    w->groups = w->rows + hp::round_up_256(total_q * sizeof(hp::PrefixRow));
+    w->ml = w->groups + hp::round_up_256(num_groups * sizeof(hp::PrefixGroup));
+    w->acc = w->ml + hp::round_up_256(records * sizeof(float2));
+    w->total = w->acc + hp::round_up_256(records * head_dim * 4);
+    return HP_OK;
+}
+
+struct PrefixCall {
+    hp_paged_desc d;
+    hp::RowsArgs rows;
+    hp::PrefixPlanArgs plan;
+};
+
+int prefix_prepare(const hp_paged_desc* k_desc, const void* v_pool, const void* group_ptr, const void* prefix_lens,
+                   u64 num_groups, const void* q, const void* q_ptr, u64 total_q, uint32_t num_q_heads, float scale,
+                   void* out, void* workspace, u64 workspace_bytes, int* d_status, PrefixCall* c)
+{
+    int rc = check_pages(k_desc, nullptr, &c->d);
+    if (rc) return rc;
+    const hp_paged_desc& d = c->d;
+    c->rows = hp::RowsArgs{};
+    rc = rows_args(d, v_pool, q, q_ptr, total_q, num_q_heads, scale, out, &c->rows);
+    if (rc) return rc;
+    if (num_groups > d.num_seqs || (num_groups == 0 && d.num_seqs)) return HP_ERR_ARG;
+    if (!group_ptr || (num_groups && !prefix_lens)) return HP_ERR_NULL;
+    if (misaligned(group_ptr, index_bytes(d.index_type)) || misaligned(prefix_lens, index_bytes(d.index_type)))
+        return HP_ERR_ALIGN;
+    PrefixWs w;
+    rc = prefix_ws(num_groups, total_q, num_q_heads, d.head_dim, &w);
+    if (rc) return rc;
+    if (!workspace || misaligned(workspace, 256) || workspace_bytes < w.total) return HP_ERR_WORKSPACE;
+    char* ws = static_cast<char*>(workspace);
+    hp::PrefixPlanArgs& p = c->plan;
+    p = hp::PrefixPlanArgs{};
+    p.seq_ptr = d.seq_ptr;
+    p.lens = d.seq_lens;
+    p.table = d.block_table;
+    p.q_ptr = q_ptr;
+    p.group_ptr = group_ptr;
+    p.prefix_lens = prefix_lens;
+    p.num_seqs = d.num_seqs;
+    p.num_groups = num_groups;
+    p.total_q = total_q;
+    p.table_len = d.table_len;
+    p.num_pages = d.num_pages;
+    p.P = c->rows.P;
+    p.H = c->rows.H;
+    p.G = c->rows.G;
+    p.idx64 = d.index_type == HP_IDX_U64;
+    p.hdr = reinterpret_cast<hp::PrefixHeader*>(ws);
+    p.rows = reinterpret_cast<hp::PrefixRow*>(ws + w.rows);
+    p.groups = reinterpret_cast<hp::PrefixGroup*>(ws + w.groups);
+    p.d_status = d_status;
+    hp::RowsArgs& a = c->rows;
+    a.hdr = p.hdr;
+    a.rows = p.rows;
+    a.groups = p.groups;
+    a.rec.ml = reinterpret_cast<float2*>(ws + w.ml);
+    a.rec.acc = reinterpret_cast<float*>(ws + w.acc);
+    a.d_status = d_status;
+    return HP_OK;
+}
+
+int prefix_run(PrefixCall& c, void* stream)
+{
+    hp::RowsArgs& a = c.rows;
+    if (c.d.num_seqs == 0 || a.q.total_q == 0) return HP_OK;
+    int dev = 0;
+    const int sms = hp::current_sms(&dev);
+    if (sms == 0) return HP_ERR_CUDA;
+    a.cluster = cluster_of(a.q.total_q * a.H, c.d.table_len * c.d.page_size / c.d.num_seqs, sms);
+    return hp::launch_rows(a, stream);
+}
+
+}  // namespace
+
+HP_API int hp_attention_prefix_workspace_bytes(const hp_paged_desc* k_desc, uint64_t num_groups, uint64_t total_q,
+                                               uint32_t num_q_heads, uint64_t* bytes)
+{
+    if (!k_desc || !bytes) return HP_ERR_NULL;
+    PrefixWs w;
+    const int rc = prefix_ws(num_groups, total_q, num_q_heads, k_desc->head_dim, &w);
+    if (rc) return rc;
+    *bytes = w.total;
+    return HP_OK;
+}
+
+HP_API int hp_attention_prefix_plan(const hp_paged_desc* k_desc, const void* group_ptr, const void* prefix_lens,
+                                    uint64_t num_groups, const void* q_ptr, uint64_t total_q, uint32_t num_q_heads,
+                                    void* workspace, uint64_t workspace_bytes, int* d_status, void* stream)
+{
+    PrefixCall c;
+    // (no buffers of a layer: the descriptor's pool stands in for them in the checks)
+    const void* any = k_desc ? k_desc->page_pool : nullptr;
+    void* stand_in = const_cast<void*>(any ? any : workspace);
+    const int rc = prefix_prepare(k_desc, any, group_ptr, prefix_lens, num_groups, stand_in, q_ptr, total_q,
+                                  num_q_heads, 1.0f, stand_in, workspace, workspace_bytes, d_status, &c);
+    return rc ? rc : hp::launch_prefix_plan(c.plan, stream);
+}
+
+HP_API int hp_attention_prefix_planned(const hp_paged_desc* k_desc, const void* v_pool, const void* group_ptr,
+                                       const void* prefix_lens, uint64_t num_groups, const void* q, const void* q_ptr,
+                                       uint64_t total_q, uint32_t num_q_heads, float scale, void* out,
+                                       void* workspace, uint64_t workspace_bytes, int* d_status, void* stream)
+{
+    PrefixCall c;
+    const int rc = prefix_prepare(k_desc, v_pool, group_ptr, prefix_lens, num_groups, q, q_ptr, total_q, num_q_heads,
+                                  scale, out, workspace, workspace_bytes, d_status, &c);
+    return rc ? rc : prefix_run(c, stream);
+}
+
+HP_API int hp_attention_prefix(const hp_paged_desc* k_desc, const void* v_pool, const void* group_ptr,
+                               const void* prefix_lens, uint64_t num_groups, const void* q, const void* q_ptr,
+                               uint64_t total_q, uint32_t num_q_heads, float scale, void* out, void* workspace,
+                               uint64_t workspace_bytes, int* d_status, void* stream)
+{
+    PrefixCall c;
+    int rc = prefix_prepare(k_desc, v_pool, group_ptr, prefix_lens, num_groups, q, q_ptr, total_q, num_q_heads, scale,
+                            out, workspace, workspace_bytes, d_status, &c);
+    if (rc) return rc;
+    rc = hp::launch_prefix_plan(c.plan, stream);
+    return rc ? rc : prefix_run(c, stream);
+}

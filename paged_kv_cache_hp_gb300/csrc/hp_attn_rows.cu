@@ -1,0 +1,476 @@
+// hp_attn_rows.cu -- attention of single query rows over some pages of their sequences: the pages of
+// a list (hp_attention_pages), or the stretch behind a prefix that is shared (hp_attention_prefix).
+//
+// For query row r and K/V head g, the G query heads of g at once:
+//   x_t = scale q . K(t),  m = max x_t,  o = sum_t 2^((x_t - m) log2 e) V(t) / sum_t 2^(...)
+// over the tokens t that the row's pages hold and it sees; one pass, with a maximum, a sum and a
+// value sum that are rescaled together.  Each element of K and V is used G times only, so what bounds it
+// is memory: 4 D bytes a token and head.  The two products keep up on mma.sync with the tokens as its
+// 16 rows and the queries as its 8 columns (S^T = K Q^T, O^T = V^T P^T), which wastes nothing at G = 8
+// and needs neither TMEM nor more than a warp; the weights go from one product's accumulators to the
+// other's operand by a transposed move inside the warp.
+//
+// A cluster of 1 to 16 CTAs takes a (row, head): its pages, cut into as many runs, and each run's
+// blocks of kTokens tokens to the CTA's four warps in turn.  Each warp has its own ring of stages
+// (cp.async) and its own maximum, sum and value sum; they meet in the CTA's shared memory, the CTAs'
+// in distributed shared memory (the answer is the same whichever finishes first, and no workspace is
+// needed), and what the prefix's kernel left joins there.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "hp_attn_merge.cuh"
+#include "hp_mma.cuh"
+#include "hp_resolve.cuh"
+#include "hp_rows.cuh"
+#include "hp_tcgen05.cuh"
+#include "hp_tma.cuh"
+
+namespace hp {
+namespace {
+
+namespace cg = cooperative_groups;
+using tc::kWeightLift;
+using tc::pack2;
+using tma::smem_u32;
+
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr uint32_t kWindow = 512;  // pages whose places lie in shared memory (a multiple of kTokens)
+constexpr float kTau = 8.0f;       // log2 units a score may exceed its query's reference by
+
+template <int D> struct Shape {
+    static constexpr int kTokens = D == 64 ? 32 : 16;     // of a block
+    static constexpr int kRow = D * 2, kPieces = kRow / 16;
+    static constexpr int kStage = 2 * kTokens * kRow;     // K rows, then V rows
+    static constexpr int kStages = 3;
+    static constexpr int kRing = kWarps * kStages * kStage;
+    static constexpr int kPad = D + 4;                    // floats of a row of the merge
+};
+
+struct Place {      // a page of the row's tokens
+    uint64_t row0;  // its first slot in the pool
+    uint32_t lo, hi;  // the slots that count
+};
+
+// Where the row's tokens lie: pages 0 .. count - 1 of a list or of up to two stretches.
+struct Source {
+    uint64_t lo, hi;           // the sequence's slice (list)
+    const int32_t* list;
+    uint32_t len, seen;
+    uint64_t table[2];         // stretches: entry of page 0 of each slice
+    uint32_t from, mid;        // tokens [0, mid) of the first if from is 0, [mid, seen) of the second
+    uint32_t first_pages;      // pages of the first stretch
+};
+
+template <bool LIST>
+__device__ __forceinline__ int place_at(const RowsArgs& a, const Source& s, uint32_t e, Place* p)
+{
+    *p = Place{0, 0, 0};
+    uint64_t phys;
+    if (LIST) {
+        const int32_t j = s.list[e];
+        if (j < 0) return HP_OK;
+        const uint64_t t0 = (uint64_t)(uint32_t)j * a.P;
+        if (t0 >= s.len) return HP_ERR_LEN;
+        const int code = page_at(a.t, a.q.idx64, s.lo, s.hi, (uint32_t)j, &phys);
+        if (code != HP_OK) return code;
+        p->hi = t0 < s.seen ? (uint32_t)umin(a.P, s.seen - t0) : 0u;
+    } else {
+        const bool own = e >= s.first_pages;
+        const uint32_t j = own ? s.mid / a.P + (e - s.first_pages) : e, t0 = j * a.P;
+        const uint32_t t_lo = own ? s.mid : 0u, t_hi = own ? s.seen : s.mid;
+        phys = index_at(a.t.table, a.q.idx64, (own ? s.table[1] : s.table[0]) + j);
+        if (phys >= a.t.num_pages) return HP_ERR_PAGE_ID;  // (the plan has looked)
+        p->lo = t_lo > t0 ? t_lo - t0 : 0u;
+        p->hi = t_hi > t0 ? (t_hi - t0 < a.P ? t_hi - t0 : a.P) : 0u;
+    }
+    p->row0 = phys * a.P;
+    return HP_OK;
+}
+
+template <typename T, int D, int NT, bool LIST>
+__global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
+{
+    using Sh = Shape<D>;
+    constexpr int kTokens = Sh::kTokens, kSub = kTokens / 16, kStages = Sh::kStages;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ Place window[kWindow];
+    __shared__ float s_m[kWarps][8 * NT], s_l[kWarps][8 * NT];
+    __shared__ float2 s_ml[8 * NT];  // the CTA's
+    __shared__ int s_code;
+    const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    pdl_wait();
+    const uint64_t unit = blockIdx.x / a.cluster;
+    const uint32_t rank = (uint32_t)(blockIdx.x % a.cluster);
+    const uint64_t r = unit / a.H;
+    const uint32_t h = (uint32_t)(unit % a.H);
+    if (LIST && r >= a.q.total_q) {  // the extra cluster's first CTA
+        if (rank) return;
+        int code = offsets_code(a.q.q_ptr, a.q.idx64, a.q.num_seqs, a.q.total_q);
+        if (a.check_all)
+            for (uint64_t i = warp; i < a.q.total_q; i += kWarps) {
+                const Query q = find_query(a.q, i);
+                code = lower(code, q.code);
+                if (q.seq >= a.q.num_seqs || q.code != HP_OK) continue;
+                Source s{};
+                s.lo = index_at(a.t.seq_ptr, a.q.idx64, q.seq);
+                s.hi = index_at(a.t.seq_ptr, a.q.idx64, q.seq + 1);
+                s.len = (uint32_t)q.len;
+                s.seen = q.seen;
+                s.list = a.selected + i * a.H * a.k;
+                Place p;
+                for (uint64_t e = lane; e < (uint64_t)a.H * a.k; e += 32)
+                    code = lower(code, place_at<true>(a, s, (uint32_t)e, &p));
+            }
+        report_codes(code, a.d_status, a.check_all);
+        return;
+    }
+    // what the row reads
+    Source src{};
+    uint32_t count = 0, skip = 0, last = a.P;  // pages; slots before the first token, up to the last
+    PrefixRow row{};
+    if (LIST) {
+        const Query q = find_query(a.q, r);
+        if (q.code != HP_OK && a.d_status && !a.check_all && rank == 0 && threadIdx.x == 0)
+            atomicMin(a.d_status, q.code);
+        if (q.seq >= a.q.num_seqs || q.code != HP_OK) return;  // (the whole cluster)
+        src.lo = index_at(a.t.seq_ptr, a.q.idx64, q.seq);
+        src.hi = index_at(a.t.seq_ptr, a.q.idx64, q.seq + 1);
+        src.len = (uint32_t)q.len;
+        src.seen = q.seen;
+        src.list = a.selected + unit * a.k;
+        count = a.k;
+    } else {
+        if (a.hdr->verdict != kVerdictOk) return;
+        row = a.rows[r];
+        if (row.group == 0xFFFFFFFFu) return;
+        src.seen = row.seen;
+        src.mid = row.prefix < row.seen ? row.prefix : row.seen;
+        src.table[1] = row.table;
+        if (a.rec.workers == 0 && src.mid) {
+            src.table[0] = a.groups[row.group].table;
+            src.first_pages = (src.mid + a.P - 1) / a.P;
+        }
+        const uint32_t own = src.seen > src.mid ? (src.seen + a.P - 1) / a.P - src.mid / a.P : 0u;
+        count = src.first_pages + own;
+        if (own) last = (src.seen - 1) % a.P + 1;
+        else if (src.mid) last = (src.mid - 1) % a.P + 1;
+        if (src.first_pages == 0 && own) skip = src.mid % a.P;
+    }
+    if (threadIdx.x == 0) s_code = HP_OK;
+    // the queries: rows dims 2 t4 + {0, 1} and + 8 of every 16, columns the heads
+    uint32_t qb[NT][D / 16][2];
+    {
+        const T* q = static_cast<const T*>(a.queries) + (r * a.H + h) * a.G * D;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    qb[nt][c][x] = 8 * nt + g < a.G ? *reinterpret_cast<const uint32_t*>(
+                                                          q + (8 * nt + g) * D + 16 * c + 8 * x + 2 * t4)
+                                                    : 0u;
+    }
+    float o[NT][D / 16][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][c][e] = 0.0f;
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.0f;
+    }
+    const float qs = a.scale * 1.4426950408889634f;
+    const uint64_t row_bytes = (uint64_t)a.H * Sh::kRow;
+    const char* kp = static_cast<const char*>(a.k_pool) + (uint64_t)h * Sh::kRow;
+    const char* vp = static_cast<const char*>(a.v_pool) + (uint64_t)h * Sh::kRow;
+    const uint32_t ring = smem_u32(smem) + warp * kStages * Sh::kStage;
+
+    // this CTA's blocks: places x of all pages' slots, kTokens to a block
+    const uint64_t x_end = count ? (uint64_t)(count - 1) * a.P + last : 0;
+    const uint64_t b0 = skip / kTokens, b1 = (x_end + kTokens - 1) / kTokens, all = b1 > b0 ? b1 - b0 : 0;
+    const uint64_t per = (all + a.cluster - 1) / a.cluster;
+    const uint64_t bb = b0 + umin(rank * per, all), be = umin(bb + per, b0 + all);
+    const uint64_t wblocks = (uint64_t)kWindow * a.P / kTokens;
+    for (uint64_t w0 = bb / wblocks * wblocks; w0 < be; w0 += wblocks) {
+        const uint64_t wb = bb > w0 ? bb : w0, we = umin(be, w0 + wblocks);
+        const uint32_t page0 = (uint32_t)(w0 * kTokens / a.P);
+        {
+            const uint32_t e0 = (uint32_t)(wb * kTokens / a.P), e1 = (uint32_t)umin(count, (we * kTokens + a.P - 1) / a.P);
+            __syncthreads();  // (the last window has been read)
+            int code = HP_OK;
+            for (uint32_t e = e0 + threadIdx.x; e < e1; e += kThreads)
+                code = lower(code, place_at<LIST>(a, src, e, &window[e - page0]));
+            if (code != HP_OK) {
+                atomicMin(&s_code, code);
+                if (LIST && a.d_status && !a.check_all) atomicMin(a.d_status, code);
+            }
+            __syncthreads();
+        }
+        const uint32_t x_base = page0 * a.P;  // (x below 2^32)
+        const uint32_t pages = count - page0 < kWindow ? count - page0 : kWindow;
+        const uint32_t nb = (uint32_t)(we - wb), iters = nb > warp ? (nb - warp + kWarps - 1) / kWarps : 0;
+        uint32_t mask_of[kStages];  // which tokens of a stage count
+        auto issue = [&](uint32_t it, int st, uint32_t& mask) {
+            mask = 0;
+            if (it < iters) {
+                const uint32_t x = (uint32_t)((wb + warp + it * kWarps) * kTokens) - x_base + (lane % kTokens);
+                const uint32_t e = div_invariant(x, a.p_m, a.p_l), slot = x - e * a.P;
+                const Place p = e < pages ? window[e] : Place{0, 0, 0};
+                const bool in = slot >= p.lo && slot < p.hi;
+                const uint64_t off = in ? (p.row0 + slot) * row_bytes : 0;
+                mask = __ballot_sync(0xffffffffu, in);
+                if (mask) {
+                    constexpr int kLanes = Sh::kPieces, kAt = kLanes >= 32 ? 1 : 32 / kLanes;
+                    const uint32_t sk = ring + st * Sh::kStage, sv = sk + kTokens * Sh::kRow;
+#pragma unroll
+                    for (int i = 0; i < kTokens / kAt; ++i) {
+                        const uint32_t tok = i * kAt + lane / kLanes, piece = lane % kLanes;
+                        const uint64_t at = __shfl_sync(0xffffffffu, off, tok) + piece * 16;
+                        const uint32_t ok = (mask >> tok & 1) ? 16u : 0u;
+                        const uint32_t d = tok * Sh::kRow + ((piece ^ (tok & 7)) << 4);
+                        mma::copy16(sk + d, kp + at, ok);
+                        mma::copy16(sv + d, vp + at, ok);
+                    }
+                }
+            }
+            mma::copies_commit();
+        };
+#pragma unroll
+        for (int st = 0; st < kStages - 1; ++st) issue(st, st, mask_of[st]);
+        for (uint32_t base = 0; base < iters; base += kStages) {
+#pragma unroll
+            for (int st = 0; st < kStages; ++st) {
+                const uint32_t it = base + st;
+                if (it >= iters) break;
+                issue(it + kStages - 1, (st + kStages - 1) % kStages, mask_of[(st + kStages - 1) % kStages]);
+                mma::copies_wait<kStages - 1>();
+                __syncwarp();
+                const uint32_t mask = mask_of[st];
+                if (mask == 0) continue;
+                const uint32_t sk = ring + st * Sh::kStage, sv = sk + kTokens * Sh::kRow;
+                // S^T: 16 tokens x 8 queries each
+                float s[kSub][NT][4];
+#pragma unroll
+                for (int b = 0; b < kSub; ++b)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[b][nt][e] = 0.0f;
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+                    for (int b = 0; b < kSub; ++b) {
+                        uint32_t k4[4];
+                        const uint32_t tok = 16 * b + (lane & 15), piece = 2 * c + (lane >> 4);
+                        mma::load4(k4, sk + tok * Sh::kRow + ((piece ^ (tok & 7)) << 4));
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma::product<T>(s[b][nt], k4[0], k4[1], k4[2], k4[3], qb[nt][c][0], qb[nt][c][1]);
+                    }
+                bool move = false;
+#pragma unroll
+                for (int b = 0; b < kSub; ++b)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const bool in = mask >> (16 * b + g + 8 * (e >> 1)) & 1;
+                            s[b][nt][e] = in ? s[b][nt][e] * qs : -INFINITY;
+                            move |= s[b][nt][e] > m[nt][e & 1] + kTau;
+                        }
+                if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            float top = m[nt][x];
+#pragma unroll
+                            for (int b = 0; b < kSub; ++b) top = fmaxf(top, fmaxf(s[b][nt][x], s[b][nt][x + 2]));
+#pragma unroll
+                            for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+                            const float f = m[nt][x] == -INFINITY ? 0.0f : exp2_approx(m[nt][x] - top);
+                            m[nt][x] = top;
+                            l[nt][x] *= f;
+#pragma unroll
+                            for (int c = 0; c < D / 16; ++c) {
+                                o[nt][c][x] *= f;
+                                o[nt][c][x + 2] *= f;
+                            }
+                        }
+                }
+#pragma unroll
+                for (int b = 0; b < kSub; ++b) {
+                    // weights, rounded to T for the value product (it takes 16-bit operands only)
+                    uint32_t p[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float base = m[nt][e & 1] == -INFINITY ? 0.0f : m[nt][e & 1];
+                            w[e] = exp2_approx(s[b][nt][e] - base + kWeightLift<T>);
+                            l[nt][e & 1] += w[e];
+                        }
+                        p[nt][0] = mma::transposed(pack2<T>(w[0], w[1]));
+                        p[nt][1] = mma::transposed(pack2<T>(w[2], w[3]));
+                    }
+                    // O^T += V^T P^T
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t v4[4];
+                        const uint32_t tok = 16 * b + (lane & 7) + ((lane >> 4) << 3), piece = 2 * c + ((lane >> 3) & 1);
+                        mma::load4_transposed(v4, sv + tok * Sh::kRow + ((piece ^ (tok & 7)) << 4));
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma::product<T>(o[nt][c], v4[0], v4[1], v4[2], v4[3], p[nt][0], p[nt][1]);
+                    }
+                }
+                __syncwarp();  // the stage may be filled again
+            }
+        }
+        mma::copies_wait<0>();
+    }
+    // ---- the warps' parts meet
+    __syncthreads();
+    float* part = reinterpret_cast<float*>(smem);  // [warp][query][kPad]
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            float sum = l[nt][x];
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+            const int n = 8 * nt + 2 * t4 + x;
+            if (g == 0) {
+                s_m[warp][n] = m[nt][x];
+                s_l[warp][n] = sum;
+            }
+            float* dst = part + (warp * 8 * NT + n) * Sh::kPad + g;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+                dst[16 * c] = o[nt][c][x];
+                dst[16 * c + 8] = o[nt][c][x + 2];
+            }
+        }
+    __syncthreads();
+    if (threadIdx.x < 8 * NT) {
+        float top = -INFINITY, sum = 0.0f;
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][threadIdx.x]);
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = s_m[w][threadIdx.x] == -INFINITY ? 0.0f : exp2_approx(s_m[w][threadIdx.x] - top);
+            sum += s_l[w][threadIdx.x] * f;
+            s_m[w][threadIdx.x] = f;  // the warp's factor
+        }
+        s_ml[threadIdx.x] = make_float2(top, sum);
+    }
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < a.G * (D / 4); i += kThreads) {
+        const uint32_t n = i / (D / 4), d = i % (D / 4) * 4;
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float4 y = *reinterpret_cast<const float4*>(part + (w * 8 * NT + n) * Sh::kPad + d);
+            const float f = s_m[w][n];
+            x.x += y.x * f, x.y += y.y * f, x.z += y.z * f, x.w += y.w * f;
+        }
+        *reinterpret_cast<float4*>(part + n * Sh::kPad + d) = x;  // (only this thread reads these places)
+    }
+    // ---- the CTAs' parts meet, each CTA finishing a share of the dimensions
+    cg::cluster_group cluster = cg::this_cluster();
+    if (a.cluster > 1) cluster.sync();
+    else __syncthreads();
+    int code = s_code;
+    for (uint32_t c = 0; c < a.cluster; ++c) code = lower(code, *cluster.map_shared_rank(&s_code, c));
+    const uint32_t share = (a.G * (D / 4) + a.cluster - 1) / a.cluster;
+    const uint32_t i0 = rank * share, i1 = (uint32_t)umin(i0 + share, a.G * (D / 4));
+    if (code == HP_OK)
+        for (uint32_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
+            const uint32_t n = i / (D / 4), d = i % (D / 4) * 4;
+            float top = -INFINITY;
+            for (uint32_t c = 0; c < a.cluster; ++c) top = fmaxf(top, cluster.map_shared_rank(s_ml, c)[n].x);
+            uint64_t rec = 0, recs = 0;
+            if (!LIST && a.rec.workers && row.prefix) {
+                const PrefixGroup gr = a.groups[row.group];
+                const uint32_t qt = kPrefixRows / a.G, tile = row.local / qt, in = row.local % qt * a.G + n;
+                const uint64_t steps = a.hdr->steps, lw = (steps + a.rec.workers - 1) / a.rec.workers;
+                const uint64_t s0 = gr.step0 + ((uint64_t)h * gr.tiles + tile) * gr.blocks;
+                const uint64_t v0 = s0 / lw, v1 = (s0 + gr.blocks - 1) / lw;
+                rec = gr.rows0 + ((uint64_t)h * gr.rows + (uint64_t)tile * qt) * a.G + v0 * kPrefixRows + in;
+                recs = v1 - v0 + 1;
+            }
+            for (uint64_t v = 0; v < recs; ++v) top = fmaxf(top, __ldcg(&a.rec.ml[rec + v * kPrefixRows]).x);
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float sum = 0.0f;
+            auto add = [&](float2 ml, float4 y) {
+                if (ml.x == -INFINITY && ml.y == 0.0f) return;  // saw nothing
+                const float f = exp2_approx(ml.x - top);
+                sum += ml.y * f;
+                x.x += y.x * f, x.y += y.y * f, x.z += y.z * f, x.w += y.w * f;
+            };
+            for (uint32_t c = 0; c < a.cluster; ++c)
+                add(cluster.map_shared_rank(s_ml, c)[n],
+                    *reinterpret_cast<const float4*>(cluster.map_shared_rank(part, c) + n * Sh::kPad + d));
+            for (uint64_t v = 0; v < recs; ++v)
+                add(__ldcg(&a.rec.ml[rec + v * kPrefixRows]),
+                    __ldcg(reinterpret_cast<const float4*>(a.rec.acc + (rec + v * kPrefixRows) * D + d)));
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            uint2 y;
+            y.x = pack2<T>(x.x * inv, x.y * inv);
+            y.y = pack2<T>(x.z * inv, x.w * inv);
+            *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + ((r * a.H + h) * a.G + n) * D + d) = y;
+        }
+    if (a.cluster > 1) cluster.sync();  // (the others have read this CTA's)
+}
+
+template <typename T, int D, int NT, bool LIST>
+int launch_k(const RowsArgs& a, cudaStream_t st)
+{
+    int dev = 0;
+    constexpr int kMerge = kWarps * 8 * NT * Shape<D>::kPad * 4;
+    constexpr int kSmem = Shape<D>::kRing > kMerge ? Shape<D>::kRing : kMerge;
+    if (current_sms(&dev) == 0 || !allow_dynamic_smem<rows_kernel<T, D, NT, LIST>>(dev, kSmem)) return HP_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    const uint64_t units = a.q.total_q * a.H;
+    cfg.gridDim = dim3((unsigned)((units + (LIST && a.d_status != nullptr)) * a.cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {a.cluster, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+    if (cfg.gridDim.x == 0) return HP_OK;
+    return cudaLaunchKernelEx(&cfg, rows_kernel<T, D, NT, LIST>, a) == cudaSuccess ? HP_OK : HP_ERR_CUDA;
+}
+
+template <typename T, int D>
+int launch_d(const RowsArgs& a, cudaStream_t st)
+{
+    if (a.selected) return a.G <= 8 ? launch_k<T, D, 1, true>(a, st) : launch_k<T, D, 2, true>(a, st);
+    return a.G <= 8 ? launch_k<T, D, 1, false>(a, st) : launch_k<T, D, 2, false>(a, st);
+}
+
+template <typename T>
+int launch_t(const RowsArgs& a, cudaStream_t st)
+{
+    return a.D == 64 ? launch_d<T, 64>(a, st) : a.D == 128 ? launch_d<T, 128>(a, st) : launch_d<T, 256>(a, st);
+}
+
+}  // namespace
+
+int launch_rows(const RowsArgs& a, void* stream)
+{
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (a.selected && a.d_status && !a.check_all && cudaMemsetAsync(a.d_status, 0, sizeof(int), st) != cudaSuccess)
+        return HP_ERR_CUDA;
+    return a.bf16 ? launch_t<__nv_bfloat16>(a, st) : launch_t<__half>(a, st);
+}
+
+}  // namespace hp

@@ -31,6 +31,8 @@ enum Rank : unsigned {
     kRankNewPtrEnd = 8,
     kRankCapacity = 9,
     kRankOutSize = 10,
+    kRankGroup = 11,
+    kRankPrefix = 12,
 };
 constexpr unsigned long long kVerdictOk = ~0ull;
 constexpr unsigned long long kIndexMask = (1ull << 58) - 1;
@@ -53,6 +55,8 @@ __host__ __device__ inline int rank_status(unsigned rank)
     case kRankNewPtrEnd: return HP_ERR_NEW_PTR_END;
     case kRankCapacity: return HP_ERR_CAPACITY;
     case kRankOutSize: return HP_ERR_OUT_SIZE;
+    case kRankGroup: return HP_ERR_GROUP;
+    case kRankPrefix: return HP_ERR_PREFIX;
     default: return HP_OK;
     }
 }

@@ -1,0 +1,86 @@
+// hp_rows.cuh -- launch interface of attention for single query rows over lists or stretches of
+// pages (hp_attn_rows.cu) and of the shared prefix in front of them (hp_prefix.cu, hp_prefix_tc.cu).
+#pragma once
+
+#include <cstdint>
+
+#include "hp_pages.cuh"
+
+namespace hp {
+
+constexpr uint32_t kPrefixKeys = 128;      // keys of a step of the shared prefix
+constexpr uint32_t kPrefixRows = 256;      // (query, head) rows of a tile: two tiles of 128 to the tensor core
+constexpr uint32_t kPrefixMaxSms = 160;    // workers are counted for at most this many SMs
+constexpr uint32_t kPrefixPlanCtas = 8;    // one cluster
+
+// A query row of hp_attention_prefix, as the plan leaves it.
+struct PrefixRow {
+    uint64_t table;      // first entry of its sequence's slice
+    uint32_t prefix;     // tokens that its group shares
+    uint32_t seen;       // tokens it sees (of its whole sequence)
+    uint32_t group;      // 0xFFFFFFFF: no sequence has this row
+    uint32_t local;      // row within its group
+};
+
+// A group: its prefix is read through the slice of its first sequence.
+struct PrefixGroup {
+    uint64_t table;      // first entry of that slice
+    uint64_t row0;       // first query row
+    uint64_t step0;      // steps before it: tile after tile (head after head), the blocks of keys of each
+    uint64_t rows0;      // record rows before it
+    uint32_t rows;       // query rows
+    uint32_t prefix;
+    uint32_t blocks;     // of kPrefixKeys keys
+    uint32_t tiles;      // of a head
+};
+
+struct PrefixHeader {
+    unsigned long long verdict;
+    unsigned long long steps;  // of all groups
+    unsigned long long pad[6];
+};
+
+struct PrefixPlanArgs {
+    const void *seq_ptr, *lens, *table, *q_ptr, *group_ptr, *prefix_lens;
+    uint64_t num_seqs, num_groups, total_q, table_len, num_pages;
+    uint32_t P, H, G;
+    int idx64;
+    PrefixHeader* hdr;
+    PrefixRow* rows;
+    PrefixGroup* groups;   // [num_groups]
+    int* d_status;
+};
+int launch_prefix_plan(const PrefixPlanArgs& a, void* stream);
+
+// The records that the prefix's workers leave: worker v's part of a tile whose rows begin at record
+// row R (of all tiles, in order) at rows R + v * kPrefixRows ...
+struct PrefixRecords {
+    float* acc;            // [rows, D]
+    float2* ml;            // [rows]: maximum (log2 units) and sum
+    uint64_t workers;      // 0: no records (the rows read their prefixes themselves)
+};
+
+struct RowsArgs {
+    QueryArgs q;           // lists
+    PageTable t;
+    const void *k_pool, *v_pool, *queries;
+    void* out;             // [total_q, H * G, D]
+    uint32_t P, p_m, p_l;  // page size and its div_invariant constants
+    uint32_t H, G, D;
+    float scale;
+    int bf16;
+    uint32_t cluster;      // CTAs of a (row, K/V head)
+    // lists
+    const int32_t* selected;  // [total_q, H, k]; NULL: stretches
+    uint32_t k;
+    int check_all;
+    int* d_status;
+    // stretches behind a plan
+    const PrefixHeader* hdr;
+    const PrefixRow* rows;
+    const PrefixGroup* groups;
+    PrefixRecords rec;
+};
+int launch_rows(const RowsArgs& a, void* stream);
+
+}  // namespace hp

@@ -289,6 +289,17 @@ def lib():
                 "hp_latent_prefill_workspace_bytes": (i, [D, u32, u32, u32, u64, u32, u64, pu64]),
                 "hp_latent_prefill": (i, [D, u32, vp, u32, u32, vp, vp, u64, u32, ctypes.c_float,
                                           vp, u64, vp, u64, vp, vp]),
+                "hp_page_bounds": (i, [D, vp, u64, vp, vp, vp]),
+                "hp_page_scores": (i, [D, vp, vp, vp, u64, u32, ctypes.c_float, vp, u64, vp, vp]),
+                "hp_select_pages": (i, [D, vp, u64, vp, u64, u32, u32, u32, vp, vp, vp]),
+                "hp_attention_pages": (i, [D, vp, vp, vp, u64, u32, ctypes.c_float, vp, u32, vp,
+                                           vp, vp]),
+                "hp_attention_prefix_workspace_bytes": (i, [D, u64, u64, u32, pu64]),
+                "hp_attention_prefix": (i, [D, vp, vp, vp, u64, vp, vp, u64, u32, ctypes.c_float,
+                                            vp, vp, u64, vp, vp]),
+                "hp_attention_prefix_plan": (i, [D, vp, vp, u64, vp, u64, u32, vp, u64, vp, vp]),
+                "hp_attention_prefix_planned": (i, [D, vp, vp, vp, u64, vp, vp, u64, u32,
+                                                    ctypes.c_float, vp, vp, u64, vp, vp]),
             }
             for name, (res, args) in sig.items():
                 f = getattr(L, name)
@@ -564,6 +575,73 @@ def hp_latent_prefill(desc, latent_dim, w_kv, nope_dim, v_dim, q, q_ptr, total_q
                                    _p(q_ptr), total_q, num_q_heads, float(scale), _p(out),
                                    kv_tokens, _p(workspace), _wsn(workspace), _p(d_status),
                                    _stream(stream))
+
+
+def hp_page_bounds(desc, new_ptr, total_new, bounds, d_status=None, stream=None):
+    _contiguous("hp_page_bounds", new_ptr=new_ptr, bounds=bounds)
+    return lib().hp_page_bounds(desc.ref, _p(new_ptr), total_new, _p(bounds), _p(d_status),
+                                _stream(stream))
+
+
+def hp_page_scores(desc, bounds, q, q_ptr, total_q, num_q_heads, scale, scores, max_pages,
+                   d_status=None, stream=None):
+    _contiguous("hp_page_scores", bounds=bounds, q=q, q_ptr=q_ptr, scores=scores)
+    return lib().hp_page_scores(desc.ref, _p(bounds), _p(q), _p(q_ptr), total_q, num_q_heads,
+                                float(scale), _p(scores), max_pages, _p(d_status),
+                                _stream(stream))
+
+
+def hp_select_pages(desc, q_ptr, total_q, scores, max_pages, sinks, recent, k, selected,
+                    d_status=None, stream=None):
+    _contiguous("hp_select_pages", q_ptr=q_ptr, scores=scores, selected=selected)
+    return lib().hp_select_pages(desc.ref, _p(q_ptr), total_q, _p(scores), max_pages, sinks,
+                                 recent, k, _p(selected), _p(d_status), _stream(stream))
+
+
+def hp_attention_pages(desc, v_pool, q, q_ptr, total_q, num_q_heads, scale, selected, k, out,
+                       d_status=None, stream=None):
+    _contiguous("hp_attention_pages", v_pool=v_pool, q=q, q_ptr=q_ptr, selected=selected, out=out)
+    return lib().hp_attention_pages(desc.ref, _p(v_pool), _p(q), _p(q_ptr), total_q, num_q_heads,
+                                    float(scale), _p(selected), k, _p(out), _p(d_status),
+                                    _stream(stream))
+
+
+def hp_attention_prefix_workspace_bytes(desc, num_groups, total_q, num_q_heads):
+    n = ctypes.c_uint64(0)
+    rc = lib().hp_attention_prefix_workspace_bytes(desc.ref, num_groups, total_q, num_q_heads,
+                                                   ctypes.byref(n))
+    return rc, n.value
+
+
+def hp_attention_prefix(desc, v_pool, group_ptr, prefix_lens, num_groups, q, q_ptr, total_q,
+                        num_q_heads, scale, out, workspace, d_status=None, stream=None):
+    _contiguous("hp_attention_prefix", v_pool=v_pool, group_ptr=group_ptr,
+                prefix_lens=prefix_lens, q=q, q_ptr=q_ptr, out=out)
+    return lib().hp_attention_prefix(desc.ref, _p(v_pool), _p(group_ptr), _p(prefix_lens),
+                                     num_groups, _p(q), _p(q_ptr), total_q, num_q_heads,
+                                     float(scale), _p(out), _p(workspace), _wsn(workspace),
+                                     _p(d_status), _stream(stream))
+
+
+def hp_attention_prefix_plan(desc, group_ptr, prefix_lens, num_groups, q_ptr, total_q,
+                             num_q_heads, workspace, d_status=None, stream=None):
+    _contiguous("hp_attention_prefix_plan", group_ptr=group_ptr, prefix_lens=prefix_lens,
+                q_ptr=q_ptr)
+    return lib().hp_attention_prefix_plan(desc.ref, _p(group_ptr), _p(prefix_lens), num_groups,
+                                          _p(q_ptr), total_q, num_q_heads, _p(workspace),
+                                          _wsn(workspace), _p(d_status), _stream(stream))
+
+
+def hp_attention_prefix_planned(desc, v_pool, group_ptr, prefix_lens, num_groups, q, q_ptr,
+                                total_q, num_q_heads, scale, out, workspace, d_status=None,
+                                stream=None):
+    _contiguous("hp_attention_prefix_planned", v_pool=v_pool, group_ptr=group_ptr,
+                prefix_lens=prefix_lens, q=q, q_ptr=q_ptr, out=out)
+    return lib().hp_attention_prefix_planned(desc.ref, _p(v_pool), _p(group_ptr),
+                                             _p(prefix_lens), num_groups, _p(q), _p(q_ptr),
+                                             total_q, num_q_heads, float(scale), _p(out),
+                                             _p(workspace), _wsn(workspace), _p(d_status),
+                                             _stream(stream))
 
 
 def hp_from_kernel_layout(src, dst, num_blocks, block_size, num_heads, head_dim, x, dtype,
