@@ -860,7 +860,9 @@ int hp_attention_prefix_workspace_bytes(const hp_paged_desc* k_desc, uint64_t nu
  * has to see its whole prefix (HP_ERR_PREFIX).  num_groups at most num_seqs, and 0 only without
  * sequences (HP_ERR_ARG).  The descriptor is always validated, as in hp_attention_decode (q_ptr with the
  * codes of an append's new_ptr, then HP_ERR_GROUP, HP_ERR_PREFIX): if a rule fails nothing is written but
- * *d_status.
+ * *d_status.  Head_dim 64 and 128 with pages of a multiple of 8 slots read the prefix on the tensor
+ * cores; otherwise each query reads its prefix by itself (HP_ATTN_CUDA_CORES in the descriptor's flags
+ * asks for that always, and so does HP_HOST_MEMORY).
  */
 int hp_attention_prefix(const hp_paged_desc* k_desc, const void* v_pool, const void* group_ptr,
                         const void* prefix_lens, uint64_t num_groups, const void* q,

@@ -241,7 +241,7 @@ struct PrefixWs {
 int prefix_ws(u64 num_groups, u64 total_q, uint32_t num_q_heads, u64 head_dim, PrefixWs* w)
 {
     if (num_groups >> 32 || total_q >> 32 || ((u128)total_q * num_q_heads) >> 40 || head_dim > 256) return HP_ERR_OVERFLOW;
-    const u64 records = total_q * num_q_heads + (u64)hp::kPrefixMaxSms * hp::kPrefixRows;
+    const u64 records = 2 * total_q * num_q_heads + (u64)hp::kPrefixMaxSms * hp::kPrefixRows;
     w->rows = 256;
     w->groups = w->rows + hp::round_up_256(total_q * sizeof(hp::PrefixRow));
     w->ml = w->groups + hp::round_up_256(num_groups * sizeof(hp::PrefixGroup));
@@ -314,6 +314,32 @@ int prefix_run(PrefixCall& c, void* stream)
     const int sms = hp::current_sms(&dev);
     if (sms == 0) return HP_ERR_CUDA;
     a.cluster = cluster_of(a.q.total_q * a.H, c.d.table_len * c.d.page_size / c.d.num_seqs, sms);
+    if (!(c.d.flags & (HP_ATTN_CUDA_CORES | HP_HOST_MEMORY)) &&
+        hp::prefix_tc_fits(c.d.head_dim, c.d.page_size, c.d.num_pages)) {
+        a.rec.workers = std::min<u64>((u64)sms, hp::kPrefixMaxSms);
+        hp::PrefixTcArgs t{};
+        t.k_pool = a.k_pool;
+        t.v_pool = a.v_pool;
+        t.q = a.queries;
+        t.table = c.d.block_table;
+        t.num_groups = c.plan.num_groups;
+        t.num_pages = c.d.num_pages;
+        t.workers = a.rec.workers;
+        t.P = a.P;
+        t.H = a.H;
+        t.G = a.G;
+        t.box = hp::prefix_tc_box(a.P);
+        t.scale = a.scale;
+        t.bf16 = a.bf16;
+        t.idx64 = a.q.idx64;
+        t.test_stall = (c.d.flags & HP_TEST_STALL) != 0;
+        t.hdr = a.hdr;
+        t.groups = a.groups;
+        t.rec = a.rec;
+        t.d_status = a.d_status;
+        const int rc = hp::launch_prefix_tc(t, a.D, stream);
+        if (rc) return rc;
+    }
     return hp::launch_rows(a, stream);
 }
 

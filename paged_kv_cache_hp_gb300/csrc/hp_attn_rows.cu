@@ -392,17 +392,22 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
             const uint32_t n = i / (D / 4), d = i % (D / 4) * 4;
             float top = -INFINITY;
             for (uint32_t c = 0; c < a.cluster; ++c) top = fmaxf(top, cluster.map_shared_rank(s_ml, c)[n].x);
-            uint64_t rec = 0, recs = 0;
+            uint64_t rec = 0, recs = 0, second = 0;  // records: first, count, where a second of each lies
             if (!LIST && a.rec.workers && row.prefix) {
                 const PrefixGroup gr = a.groups[row.group];
                 const uint32_t qt = kPrefixRows / a.G, tile = row.local / qt, in = row.local % qt * a.G + n;
                 const uint64_t steps = a.hdr->steps, lw = (steps + a.rec.workers - 1) / a.rec.workers;
                 const uint64_t s0 = gr.step0 + ((uint64_t)h * gr.tiles + tile) * gr.blocks;
                 const uint64_t v0 = s0 / lw, v1 = (s0 + gr.blocks - 1) / lw;
-                rec = gr.rows0 + ((uint64_t)h * gr.rows + (uint64_t)tile * qt) * a.G + v0 * kPrefixRows + in;
+                const uint32_t left = gr.rows - tile * qt, trows = (left < qt ? left : qt) * a.G;
+                rec = gr.rows0 + h * gr.records + (uint64_t)tile * qt * a.G + v0 * kPrefixRows + in;
                 recs = v1 - v0 + 1;
+                if (trows <= kPrefixRows / 2) second = trows;
             }
-            for (uint64_t v = 0; v < recs; ++v) top = fmaxf(top, __ldcg(&a.rec.ml[rec + v * kPrefixRows]).x);
+            for (uint64_t v = 0; v < recs; ++v) {
+                top = fmaxf(top, __ldcg(&a.rec.ml[rec + v * kPrefixRows]).x);
+                if (second) top = fmaxf(top, __ldcg(&a.rec.ml[rec + v * kPrefixRows + second]).x);
+            }
             float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             float sum = 0.0f;
             auto add = [&](float2 ml, float4 y) {
@@ -415,8 +420,8 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
                 add(cluster.map_shared_rank(s_ml, c)[n],
                     *reinterpret_cast<const float4*>(cluster.map_shared_rank(part, c) + n * Sh::kPad + d));
             for (uint64_t v = 0; v < recs; ++v)
-                add(__ldcg(&a.rec.ml[rec + v * kPrefixRows]),
-                    __ldcg(reinterpret_cast<const float4*>(a.rec.acc + (rec + v * kPrefixRows) * D + d)));
+                for (uint64_t at = rec + v * kPrefixRows, left = second ? 2 : 1; left; --left, at += second)
+                    add(__ldcg(&a.rec.ml[at]), __ldcg(reinterpret_cast<const float4*>(a.rec.acc + at * D + d)));
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             uint2 y;
             y.x = pack2<T>(x.x * inv, x.y * inv);

@@ -103,7 +103,9 @@ __global__ void __launch_bounds__(kPlanThreads) __cluster_dims__(kPrefixPlanCtas
                 gr.blocks = (uint32_t)((prefix + kPrefixKeys - 1) / kPrefixKeys);
                 gr.tiles = (uint32_t)((gr.rows + qt - 1) / qt);
                 st = (uint64_t)a.H * gr.tiles * gr.blocks;
-                rr = (uint64_t)a.H * a.G * gr.rows;
+                const uint64_t last = gr.tiles ? (gr.rows - (gr.tiles - 1) * qt) * a.G : 0;
+                gr.records = gr.tiles ? (gr.tiles - 1) * qt * a.G + (last <= kPrefixRows / 2 ? 2 * last : last) : 0;
+                rr = a.H * gr.records;
             }
             unsigned long long es, er, ts, tr;
             block_scan2(st, rr, es, er, ts, tr);

@@ -32,6 +32,7 @@ struct PrefixGroup {
     uint32_t prefix;
     uint32_t blocks;     // of kPrefixKeys keys
     uint32_t tiles;      // of a head
+    uint64_t records;    // record rows of a head: a tile's rows, twice those of a tile of up to 128
 };
 
 struct PrefixHeader {
@@ -52,13 +53,30 @@ struct PrefixPlanArgs {
 };
 int launch_prefix_plan(const PrefixPlanArgs& a, void* stream);
 
-// The records that the prefix's workers leave: worker v's part of a tile whose rows begin at record
-// row R (of all tiles, in order) at rows R + v * kPrefixRows ...
+// The records that the prefix's workers leave: worker v's part of a tile whose record rows begin at R
+// (of all tiles, in order) at rows R + v * kPrefixRows ..., no two of them in one place since a part has at
+// most kPrefixRows record rows.  A tile of up to 128 rows has two records a part, one behind the other.
 struct PrefixRecords {
     float* acc;            // [rows, D]
     float2* ml;            // [rows]: maximum (log2 units) and sum
     uint64_t workers;      // 0: no records (the rows read their prefixes themselves)
 };
+
+struct PrefixTcArgs {
+    const void *k_pool, *v_pool, *q, *table;
+    uint64_t num_groups, num_pages, workers;
+    uint32_t P, H, G;
+    uint32_t box;          // slots of a load: the largest power of two up to 128 that divides P
+    float scale;
+    int bf16, idx64, test_stall;
+    const PrefixHeader* hdr;
+    const PrefixGroup* groups;
+    PrefixRecords rec;
+    int* d_status;
+};
+bool prefix_tc_fits(uint64_t head_dim, uint64_t page_size, uint64_t num_pages);
+uint32_t prefix_tc_box(uint64_t page_size);
+int launch_prefix_tc(const PrefixTcArgs& a, uint32_t head_dim, void* stream);
 
 struct RowsArgs {
     QueryArgs q;           // lists
