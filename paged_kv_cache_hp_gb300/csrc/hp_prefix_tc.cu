@@ -90,6 +90,25 @@ __device__ __forceinline__ Part part_at(const PrefixTcArgs& a, uint64_t pos, uin
     return p;
 }
 
+// Half of row x of the part's tile to its place in the S product's operand: zeros past the tile's rows.
+template <typename T, int D>
+__device__ __forceinline__ void load_queries(const PrefixTcArgs& a, const Part& p, uint32_t x, uint32_t half,
+                                             unsigned char* dst)
+{
+    const uint32_t qi = x / a.G;
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
+                                                    ((p.q_row + qi) * a.H * a.G + p.head * a.G + (x - qi * a.G)) * D) +
+                     half * (D / 16);
+    uint4 v[D / 16];
+#pragma unroll
+    for (uint32_t i = 0; i < D / 16; ++i) v[i] = x < p.rows ? q[i] : uint4{};
+#pragma unroll
+    for (uint32_t i = 0; i < D / 16; ++i) {
+        const uint32_t piece = D == 128 ? i : half * (D / 16) + i;
+        *reinterpret_cast<uint4*>(dst + (D == 128 ? half * kSlot : 0) + ((piece ^ (threadIdx.x & 7)) << 4)) = v[i];
+    }
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_kernel(const PrefixTcArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv)
@@ -194,11 +213,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t vd0 = sw128_desc(sm0 + R::kOffKv + kS * kSlot, kSlot, 1024);
         bool ok = true;
         uint32_t n0 = 0, np = 0, c[2] = {0, 0};  // blocks before the part, parts, S issued for each half
-        // S of half t for the part's block i; K goes back behind it if `last`
-        auto issue_s = [&](int t, uint32_t i, bool last) {
-            const uint32_t n = n0 + i, b = n % kBufs;
-            if (ok) ok = warp_wait(&k_full[b], (n / kBufs) & 1);
-            if (!ok) return;
+        // S of half t for block n; K goes back behind it if `last`
+        auto issue_s = [&](int t, uint32_t n, bool last) {
+            const uint32_t b = n % kBufs;
             fence_after();
             const uint64_t qd = qd0 + ((t * kS * kSlot) >> 4), kd = kd0 + ((2 * b * kS * kSlot) >> 4);
             if (elect_one()) {
@@ -213,12 +230,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             ++c[t];
         };
-        // O of half t for block i, the half's first of the part or not, its last or not
-        auto issue_o = [&](int t, uint32_t i, bool first, bool done, bool last) {
-            const uint32_t n = n0 + i, b = n % kBufs;
-            if (ok) ok = warp_wait(&v_full[b], (n / kBufs) & 1);
-            if (ok) ok = warp_wait(&p_full[t], (c[t] - 1) & 1);
-            if (!ok) return;
+        // O of half t for block n, the half's first of the part or not, its last or not; V goes back
+        // behind it if `last`
+        auto issue_o = [&](int t, uint32_t n, bool first, bool done, bool last) {
+            const uint32_t b = n % kBufs;
             fence_after();
             const uint64_t vd = vd0 + ((2 * b * kS * kSlot) >> 4);
             if (elect_one()) {
@@ -231,6 +246,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         };
+        // What a round begins with: V of block n - back and P of half t (`has_o`), K of block n
+        // (`has_s`).  A wait costs some 200 cycles even when its phase is complete, so the three are
+        // polled together; K is waited for behind the O products.
+        auto round = [&](int t, uint32_t n, uint32_t back, bool has_o, bool has_s, auto&& o, auto&& s) {
+            const uint32_t nv = n - back;
+            bool v_ok = !has_o, p_ok = !has_o, k_ok = !has_s;
+            if (has_o) v_ok = mbar_try_wait(smem_u32(&v_full[nv % kBufs]), (nv / kBufs) & 1);
+            if (has_s) k_ok = mbar_test(smem_u32(&k_full[n % kBufs]), (n / kBufs) & 1);
+            if (has_o) p_ok = mbar_try_wait(smem_u32(&p_full[t]), (c[t] - 1) & 1);
+            const unsigned polls = __reduce_and_sync(0xffffffffu, (v_ok ? 1u : 0u) | (k_ok ? 2u : 0u) | (p_ok ? 4u : 0u));
+            if (!(polls & 1)) ok = warp_wait(&v_full[nv % kBufs], (nv / kBufs) & 1);
+            if (ok && !(polls & 4)) ok = warp_wait(&p_full[t], (c[t] - 1) & 1);
+            if (!ok) return;
+            if (has_o) o();
+            if (!(polls & 2)) ok = warp_wait(&k_full[n % kBufs], (n / kBufs) & 1);
+            if (ok && has_s) s();
+        };
         for (uint64_t pos = beg; pos < end && ok; ++np) {
             const Part p = part_at(a, pos, end);
             const uint32_t blocks = p.j1 - p.j0;
@@ -239,16 +271,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (p.split) {
                 for (uint32_t i = 0; i < blocks + 2 && ok; ++i) {
                     const int t = i & 1;
-                    if (i >= 2 && i - 2 < blocks) issue_o(t, i - 2, i < 4, i >= blocks, true);
-                    if (i < blocks) issue_s(t, i, true);
+                    round(t, n0 + i, 2, i >= 2 && i - 2 < blocks, i < blocks,
+                          [&] { issue_o(t, n0 + i - 2, i < 4, i >= blocks, true); }, [&] { issue_s(t, n0 + i, true); });
                 }
             } else {
-                for (uint32_t i = 0; i <= blocks && ok; ++i)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (i > 0) issue_o(t, i - 1, i == 1, i == blocks, t == 1);
-                        if (i < blocks) issue_s(t, i, t == 1);
-                    }
+                for (uint32_t i = 0; i <= blocks && ok; ++i) {
+                    const bool has_o = i > 0, has_s = i < blocks;
+                    round(0, n0 + i, 1, has_o, has_s, [&] { issue_o(0, n0 + i - 1, i == 1, i == blocks, false); },
+                          [&] { issue_s(0, n0 + i, false); });
+                    if (ok && has_o) ok = warp_wait(&p_full[1], (c[1] - 1) & 1);
+                    if (ok && has_o) issue_o(1, n0 + i - 1, i == 1, i == blocks, true);
+                    if (ok && has_s) issue_s(1, n0 + i, true);
+                }
             }
             n0 += blocks;
             pos += blocks;
@@ -260,51 +294,67 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         const int t = warp >> 3;
         const uint32_t q4 = warp & 3, half = (warp >> 2) & 1, row = q4 * 32 + lane;
-        const uint32_t sa = tmem + ((q4 * 32) << 16) + kSCol + t * 128;
+        const uint32_t sa = tmem + ((q4 * 32) << 16) + kSCol + t * 128 + 64 * half;
         const uint32_t oa = tmem + ((q4 * 32) << 16) + kOCol + t * 128 + half * (D / 2);
         float* const told = &half_s[t][row];  // the second one's value, then what the first made of it
         const float qscale = a.scale * 1.4426950408889634f;
-        const uint32_t Hq = a.H * a.G;
         uint32_t c = 0, n0 = 0, done = 0;  // S taken, blocks before the part, parts with blocks for this half
         bool stop = false;
+        // V past the prefix's end, `left` keys into block b of the part (the products of half 0 come
+        // first where both take the block)
+        auto clear_v = [&](uint32_t left, uint32_t n) {
+            const uint32_t b = n % kBufs, r = threadIdx.x & 127, s = (threadIdx.x >> 7) & 1;
+            if (warp_wait(&v_full[b], (n / kBufs) & 1) && r >= left && s < kS) {
+                uint4* v = reinterpret_cast<uint4*>(smem + R::kOffKv + ((2 * b + 1) * kS + s) * kSlot + r * 128);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = uint4{};
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+        };
         for (uint64_t pos = beg; pos < end && !stop;) {
-            const Part p = part_at(a, pos, end);
-            const uint32_t blocks = p.blocks(t), x = p.split ? row : 128 * t + row;  // x: row of the tile
-            const bool real = x < p.rows, any = (x & ~31u) < p.rows;  // this row; some row of the warp
-            // this half's queries: zeros past the tile's rows (its last S has been taken, so they are free)
+            uint32_t blocks, stride, first, left;  // this half's blocks: first, first + stride, ... of the part's
+            bool any, clears;                      // some row of the warp; this half clears V
+            float m = -INFINITY, l = 0.0f;
             {
-                const uint32_t qi = x / a.G;
-                const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
-                                                                ((p.q_row + qi) * Hq + p.head * a.G + (x - qi * a.G)) * D) +
-                                 half * (D / 16);
-                unsigned char* dst = smem + t * kS * kSlot + (D == 128 ? half * kSlot : 0);
-                uint4 v[D / 16];
-#pragma unroll
-                for (uint32_t i = 0; i < D / 16; ++i) v[i] = real ? q[i] : uint4{};
-#pragma unroll
-                for (uint32_t i = 0; i < D / 16; ++i) {
-                    const uint32_t piece = D == 128 ? i : half * (D / 16) + i;
-                    *reinterpret_cast<uint4*>(dst + row * 128 + ((piece ^ (row & 7)) << 4)) = v[i];
-                }
+                const Part p = part_at(a, pos, end);
+                const uint32_t x = p.split ? row : 128 * t + row;  // row of the tile
+                blocks = p.blocks(t);
+                stride = p.split ? 2 : 1;
+                first = p.split ? t : 0;
+                left = p.prefix - (p.j0 + first) * 128;
+                any = (x & ~31u) < p.rows;
+                clears = p.split || t == 0;
+                load_queries<T, D>(a, p, x, half, smem + t * kS * kSlot + row * 128);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 mbar_arrive(smem_u32(&q_full[t]));
             }
-            float m = -INFINITY, l = 0.0f;
-            for (uint32_t i = 0; i < blocks; ++i, ++c) {
-                const uint32_t bi = p.split ? 2 * i + t : i;           // of the part
-                const uint32_t left = p.prefix - (p.j0 + bi) * 128;    // keys from the block's first on
-                // a wait that runs out marks its block; the half's threads stop together, at the vote
-                if (!warp_wait(&s_full[t], c & 1)) fail_s[t][c & 1] = 1;
-                fence_after();
-                uint32_t xr[2][32];
-                float mx = -INFINITY, qs = qscale;
-                const int lim = left > 64 * half ? (int)(left - 64 * half) : 0;
-                if (any) {
-                    tmem_issue<32>(sa + 64 * half, xr[0]);
-                    tmem_issue<32>(sa + 64 * half + 32, xr[1]);
+            if (!any) {  // 32 rows that nobody asked for: the warp votes and arrives, no more
+                for (uint32_t i = 0; i < blocks; ++i, ++c, left -= 128 * stride) {
+                    if (!warp_wait(&s_full[t], c & 1)) fail_s[t][c & 1] = 1;
+                    const bool need = named_or(1 + t, kHalf, false);
+                    if (*(volatile int*)&fail_s[t][c & 1]) {
+                        stop = true;
+                        break;
+                    }
+                    if (need) named_sync(1 + t, kHalf);
+                    if (left < 128 && clears) clear_v(left, n0 + first + i * stride);
+                    mbar_arrive(smem_u32(&p_full[t]));
+                }
+            } else {
+                for (uint32_t i = 0; i < blocks; ++i, ++c, left -= 128 * stride) {  // left: keys from the block's first on
+                    // a wait that runs out marks its block; the half's threads stop together, at the vote
+                    if (!warp_wait(&s_full[t], c & 1)) fail_s[t][c & 1] = 1;
+                    fence_after();
+                    uint32_t xr[2][32];
+                    tmem_issue<32>(sa, xr[0]);
+                    tmem_issue<32>(sa + 32, xr[1]);
                     tmem_wait<32>(xr[0]);
                     tmem_wait<32>(xr[1]);
-                    if (lim < 64) qs = 1.0f;  // the prefix ends in this block: scaled scores, -inf past it
+                    // the largest scaled score: the extreme of the raw ones on the scale's side; in the
+                    // block in which the prefix ends, scaled scores with -inf past it
+                    const int lim = left > 64 * half ? (int)(left - 64 * half) : 0;
+                    float mx = -INFINITY, qs = qscale;
+                    if (lim < 64) qs = 1.0f;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float* s = reinterpret_cast<float*>(xr[h]);
@@ -332,37 +382,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mx = fmaxf(mx, fminf(min3(e0, s[30], s[31]), e1) * qscale);
                         }
                     }
-                }
-                // (past this barrier every thread of the half has its scores, and P may overwrite them)
-                if (half) *told = mx;
-                fence_before();
-                const bool need = named_or(1 + t, kHalf, mx > m + kTau);
-                fence_after();
-                if (*(volatile int*)&fail_s[t][c & 1]) {
-                    stop = true;
-                    break;
-                }
-                if (need) {  // the same in the whole half
-                    float mn;
-                    if (!half) *told = mn = fmaxf(m, fmaxf(mx, *told));
-                    named_sync(1 + t, kHalf);
-                    if (half) mn = *told;
-                    const float f = m == -INFINITY ? 0.0f : exp2_approx(m - mn);
-                    m = mn;
-                    l *= f;
-                    if (i > 0 && any) {  // the scores of this block are complete, so O of the last one is
+                    // (past this barrier every thread of the half has its scores, and P may overwrite them)
+                    if (half) *told = mx;
+                    fence_before();
+                    const bool need = named_or(1 + t, kHalf, mx > m + kTau);
+                    fence_after();
+                    if (*(volatile int*)&fail_s[t][c & 1]) {
+                        stop = true;
+                        break;
+                    }
+                    if (need) {  // the same in the whole half
+                        float mn;
+                        if (!half) *told = mn = fmaxf(m, fmaxf(mx, *told));
+                        named_sync(1 + t, kHalf);
+                        if (half) mn = *told;
+                        const float f = m == -INFINITY ? 0.0f : exp2_approx(m - mn);
+                        m = mn;
+                        l *= f;
+                        if (i > 0) {  // the scores of this block are complete, so O of the last one is
 #pragma unroll 1
-                        for (uint32_t k = 0; k < D / 2; k += 16) {
-                            uint32_t o[16];
-                            tmem_issue<16>(oa + k, o);
-                            tmem_wait<16>(o);
+                            for (uint32_t k = 0; k < D / 2; k += 16) {
+                                uint32_t o[16];
+                                tmem_issue<16>(oa + k, o);
+                                tmem_wait<16>(o);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st16(oa + k, o);
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st16(oa + k, o);
+                            }
                         }
                     }
-                }
-                if (any) {
                     const float base = kWeightLift<T> - (m == -INFINITY ? 0.0f : m);
                     const uint64_t qs2 = pair_of(qs, qs), base2 = pair_of(base, base);
                     uint64_t sum[2] = {0ull, 0ull};
@@ -378,25 +426,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                             sum[k & 1] = add2(sum[k & 1], pair_of(w.x, w.y));
                             w16[k] = pack2<T>(w.x, w.y);
                         }
-                        tmem_st16(sa + 32 * half + 16 * h, w16);
+                        tmem_st16(sa - 32 * half + 16 * h, w16);
                     }
                     const float2 sums = of_pair(add2(sum[0], sum[1]));
                     l += sums.x + sums.y;
                     tmem_st_wait();
+                    fence_before();
+                    if (left < 128 && clears) clear_v(left, n0 + first + i * stride);
+                    mbar_arrive(smem_u32(&p_full[t]));
                 }
-                fence_before();
-                // V past the prefix's end (the products of half 0 come first where both take the block)
-                if (left < 128 && (p.split || t == 0)) {
-                    const uint32_t b = (n0 + bi) % kBufs, r = threadIdx.x & 127, s = (threadIdx.x >> 7) & 1;
-                    if (warp_wait(&v_full[b], ((n0 + bi) / kBufs) & 1) && r >= left && s < kS) {
-                        uint4* v = reinterpret_cast<uint4*>(smem + R::kOffKv + ((2 * b + 1) * kS + s) * kSlot + r * 128);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = uint4{};
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    }
-                }
-                mbar_arrive(smem_u32(&p_full[t]));
             }
+            const Part p = part_at(a, pos, end);
             if (!stop && blocks) {
                 const bool ok = warp_wait(&o_done[t], done & 1);
                 ++done;
@@ -405,24 +445,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_after();
                 if (!half) l += *told;
             }
-            if (!stop && real) {
+            if (!stop && any) {
+                const uint32_t x = p.split ? row : 128 * t + row;
+                const bool real = x < p.rows;
                 const uint64_t rec = p.record + (p.split && t ? p.rows + x : x);
-                if (!half) a.rec.ml[rec] = make_float2(m, l);
-            }
-            if (!stop && blocks && any) {
-                float4* o4 = reinterpret_cast<float4*>(a.rec.acc + (p.record + (p.split && t ? p.rows + x : x)) * D + half * (D / 2));
+                if (real && !half) a.rec.ml[rec] = make_float2(m, l);
+                if (blocks) {
+                    float4* o4 = reinterpret_cast<float4*>(a.rec.acc + rec * D + half * (D / 2));
 #pragma unroll 1
-                for (uint32_t k = 0; k < D / 2; k += 32) {
-                    uint32_t o[32];
-                    tmem_issue<32>(oa + k, o);
-                    tmem_wait<32>(o);
-                    if (real)
+                    for (uint32_t k = 0; k < D / 2; k += 32) {
+                        uint32_t o[32];
+                        tmem_issue<32>(oa + k, o);
+                        tmem_wait<32>(o);
+                        if (real)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            o4[k / 4 + e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                                        __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+                            for (int e = 0; e < 8; ++e)
+                                o4[k / 4 + e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                            __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+                    }
+                    fence_before();
                 }
-                fence_before();
             }
             n0 += p.j1 - p.j0;
             pos += p.j1 - p.j0;
