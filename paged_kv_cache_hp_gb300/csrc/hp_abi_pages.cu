@@ -242,7 +242,7 @@ int prefix_ws(u64 num_groups, u64 total_q, uint32_t num_q_heads, u64 head_dim, P
 {
     if (num_groups >> 32 || total_q >> 32 || ((u128)total_q * num_q_heads) >> 40 || head_dim > 256) return HP_ERR_OVERFLOW;
     const u64 records = 2 * total_q * num_q_heads + (u64)hp::kPrefixMaxSms * hp::kPrefixRows;
-    w->rows = 256;
+    w->rows = hp::round_up_256(sizeof(hp::PrefixHeader));
     w->groups = w->rows + hp::round_up_256(total_q * sizeof(hp::PrefixRow));
     w->ml = w->groups + hp::round_up_256(num_groups * sizeof(hp::PrefixGroup));
     w->acc = w->ml + hp::round_up_256(records * sizeof(float2));
@@ -295,9 +295,10 @@ int prefix_prepare(const hp_paged_desc* k_desc, const void* v_pool, const void* 
     p.hdr = reinterpret_cast<hp::PrefixHeader*>(ws);
     p.rows = reinterpret_cast<hp::PrefixRow*>(ws + w.rows);
     p.groups = reinterpret_cast<hp::PrefixGroup*>(ws + w.groups);
-    p.d_status = d_status;
+    p.ctas = hp::prefix_plan_ctas(d.table_len);
     hp::RowsArgs& a = c->rows;
     a.hdr = p.hdr;
+    a.num_keys = p.ctas;
     a.rows = p.rows;
     a.groups = p.groups;
     a.rec.ml = reinterpret_cast<float2*>(ws + w.ml);
@@ -306,10 +307,13 @@ int prefix_prepare(const hp_paged_desc* k_desc, const void* v_pool, const void* 
     return HP_OK;
 }
 
-int prefix_run(PrefixCall& c, void* stream)
+// The kernels behind the plan; the first of them stores the status (first 1: in any case, 2: an error).
+int prefix_run(PrefixCall& c, int first, void* stream)
 {
     hp::RowsArgs& a = c.rows;
-    if (c.d.num_seqs == 0 || a.q.total_q == 0) return HP_OK;
+    if (c.d.num_seqs == 0 || a.q.total_q == 0)
+        return first == 1 ? hp::launch_prefix_status(c.plan.hdr, c.plan.ctas, a.d_status, stream) : HP_OK;
+    a.first = first;
     int dev = 0;
     const int sms = hp::current_sms(&dev);
     if (sms == 0) return HP_ERR_CUDA;
@@ -335,6 +339,9 @@ int prefix_run(PrefixCall& c, void* stream)
         t.test_stall = (c.d.flags & HP_TEST_STALL) != 0;
         t.hdr = a.hdr;
         t.groups = a.groups;
+        t.num_keys = a.num_keys;
+        t.first = first;
+        a.first = 0;
         t.rec = a.rec;
         t.d_status = a.d_status;
         const int rc = hp::launch_prefix_tc(t, a.D, stream);
@@ -364,9 +371,11 @@ HP_API int hp_attention_prefix_plan(const hp_paged_desc* k_desc, const void* gro
     // (no buffers of a layer: the descriptor's pool stands in for them in the checks)
     const void* any = k_desc ? k_desc->page_pool : nullptr;
     void* stand_in = const_cast<void*>(any ? any : workspace);
-    const int rc = prefix_prepare(k_desc, any, group_ptr, prefix_lens, num_groups, stand_in, q_ptr, total_q,
+    int rc = prefix_prepare(k_desc, any, group_ptr, prefix_lens, num_groups, stand_in, q_ptr, total_q,
                                   num_q_heads, 1.0f, stand_in, workspace, workspace_bytes, d_status, &c);
-    return rc ? rc : hp::launch_prefix_plan(c.plan, stream);
+    if (rc) return rc;
+    rc = hp::launch_prefix_plan(c.plan, stream);
+    return rc ? rc : hp::launch_prefix_status(c.plan.hdr, c.plan.ctas, d_status, stream);
 }
 
 HP_API int hp_attention_prefix_planned(const hp_paged_desc* k_desc, const void* v_pool, const void* group_ptr,
@@ -377,7 +386,7 @@ HP_API int hp_attention_prefix_planned(const hp_paged_desc* k_desc, const void* 
     PrefixCall c;
     const int rc = prefix_prepare(k_desc, v_pool, group_ptr, prefix_lens, num_groups, q, q_ptr, total_q, num_q_heads,
                                   scale, out, workspace, workspace_bytes, d_status, &c);
-    return rc ? rc : prefix_run(c, stream);
+    return rc ? rc : prefix_run(c, 2, stream);
 }
 
 HP_API int hp_attention_prefix(const hp_paged_desc* k_desc, const void* v_pool, const void* group_ptr,
@@ -390,5 +399,5 @@ HP_API int hp_attention_prefix(const hp_paged_desc* k_desc, const void* v_pool, 
                             out, workspace, workspace_bytes, d_status, &c);
     if (rc) return rc;
     rc = hp::launch_prefix_plan(c.plan, stream);
-    return rc ? rc : prefix_run(c, stream);
+    return rc ? rc : prefix_run(c, 1, stream);
 }

@@ -22,6 +22,7 @@
 
 #include "hp_attn_merge.cuh"
 #include "hp_mma.cuh"
+#include "hp_prefix.cuh"
 #include "hp_resolve.cuh"
 #include "hp_rows.cuh"
 #include "hp_tcgen05.cuh"
@@ -35,7 +36,7 @@ using tc::kWeightLift;
 using tc::pack2;
 using tma::smem_u32;
 
-constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kRowWarps = 4, kThreads = kRowWarps * 32;
 constexpr uint32_t kWindow = 512;  // pages whose places lie in shared memory (a multiple of kTokens)
 constexpr float kTau = 8.0f;       // log2 units a score may exceed its query's reference by
 
@@ -44,7 +45,7 @@ template <int D> struct Shape {
     static constexpr int kRow = D * 2, kPieces = kRow / 16;
     static constexpr int kStage = 2 * kTokens * kRow;     // K rows, then V rows
     static constexpr int kStages = 3;
-    static constexpr int kRing = kWarps * kStages * kStage;
+    static constexpr int kRing = kRowWarps * kStages * kStage;
     static constexpr int kPad = D + 4;                    // floats of a row of the merge
 };
 
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
     constexpr int kTokens = Sh::kTokens, kSub = kTokens / 16, kStages = Sh::kStages;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ Place window[kWindow];
-    __shared__ float s_m[kWarps][8 * NT], s_l[kWarps][8 * NT];
+    __shared__ float s_m[kRowWarps][8 * NT], s_l[kRowWarps][8 * NT];
     __shared__ float2 s_ml[8 * NT];  // the CTA's
     __shared__ int s_code;
     const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
         if (rank) return;
         int code = offsets_code(a.q.q_ptr, a.q.idx64, a.q.num_seqs, a.q.total_q);
         if (a.check_all)
-            for (uint64_t i = warp; i < a.q.total_q; i += kWarps) {
+            for (uint64_t i = warp; i < a.q.total_q; i += kRowWarps) {
                 const Query q = find_query(a.q, i);
                 code = lower(code, q.code);
                 if (q.seq >= a.q.num_seqs || q.code != HP_OK) continue;
@@ -142,9 +143,8 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
         src.list = a.selected + unit * a.k;
         count = a.k;
     } else {
-        if (a.hdr->verdict != kVerdictOk) return;
         row = a.rows[r];
-        if (row.group == 0xFFFFFFFFu) return;
+        if (!plan_holds(a.hdr, a.num_keys, a.d_status, a.first && blockIdx.x == 0, a.first == 2) || row.group == 0xFFFFFFFFu) return;
         src.seen = row.seen;
         src.mid = row.prefix < row.seen ? row.prefix : row.seen;
         src.table[1] = row.table;
@@ -212,12 +212,12 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
         }
         const uint32_t x_base = page0 * a.P;  // (x below 2^32)
         const uint32_t pages = count - page0 < kWindow ? count - page0 : kWindow;
-        const uint32_t nb = (uint32_t)(we - wb), iters = nb > warp ? (nb - warp + kWarps - 1) / kWarps : 0;
+        const uint32_t nb = (uint32_t)(we - wb), iters = nb > warp ? (nb - warp + kRowWarps - 1) / kRowWarps : 0;
         uint32_t mask_of[kStages];  // which tokens of a stage count
         auto issue = [&](uint32_t it, int st, uint32_t& mask) {
             mask = 0;
             if (it < iters) {
-                const uint32_t x = (uint32_t)((wb + warp + it * kWarps) * kTokens) - x_base + (lane % kTokens);
+                const uint32_t x = (uint32_t)((wb + warp + it * kRowWarps) * kTokens) - x_base + (lane % kTokens);
                 const uint32_t e = div_invariant(x, a.p_m, a.p_l), slot = x - e * a.P;
                 const Place p = e < pages ? window[e] : Place{0, 0, 0};
                 const bool in = slot >= p.lo && slot < p.hi;
@@ -359,8 +359,8 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
     __syncthreads();
     if (threadIdx.x < 8 * NT) {
         float top = -INFINITY, sum = 0.0f;
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][threadIdx.x]);
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < kRowWarps; ++w) top = fmaxf(top, s_m[w][threadIdx.x]);
+        for (int w = 0; w < kRowWarps; ++w) {
             const float f = s_m[w][threadIdx.x] == -INFINITY ? 0.0f : exp2_approx(s_m[w][threadIdx.x] - top);
             sum += s_l[w][threadIdx.x] * f;
             s_m[w][threadIdx.x] = f;  // the warp's factor
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
         const uint32_t n = i / (D / 4), d = i % (D / 4) * 4;
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < kRowWarps; ++w) {
             const float4 y = *reinterpret_cast<const float4*>(part + (w * 8 * NT + n) * Sh::kPad + d);
             const float f = s_m[w][n];
             x.x += y.x * f, x.y += y.y * f, x.z += y.z * f, x.w += y.w * f;
@@ -387,42 +387,72 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
     for (uint32_t c = 0; c < a.cluster; ++c) code = lower(code, *cluster.map_shared_rank(&s_code, c));
     const uint32_t share = (a.G * (D / 4) + a.cluster - 1) / a.cluster;
     const uint32_t i0 = rank * share, i1 = (uint32_t)umin(i0 + share, a.G * (D / 4));
+    // the prefix's records of query head 0: first, count, and where a second of each lies
+    uint64_t rec = 0;
+    uint32_t recs = 0, second = 0;
+    if (!LIST && a.rec.workers && row.prefix) {
+        const PrefixGroup gr = a.groups[row.group];
+        const uint32_t qt = kPrefixRows / a.G, tile = row.local / qt, left = gr.rows - tile * qt;
+        const uint32_t rows = (left < qt ? left : qt) * a.G;
+        const uint64_t lw = (a.hdr->steps + a.rec.workers - 1) / a.rec.workers;
+        const uint64_t s0 = gr.step0 + ((uint64_t)h * gr.tiles + tile) * gr.blocks;
+        const uint64_t v0 = s0 / lw, v1 = (s0 + gr.blocks - 1) / lw;
+        rec = gr.rows0 + h * gr.records + (uint64_t)tile * qt * a.G + v0 * kPrefixRows + row.local % qt * a.G;
+        recs = (uint32_t)(v1 - v0 + 1);
+        if (rows <= kPrefixRows / 2) {
+            second = rows;
+            recs *= 2;
+        }
+    }
+    auto record = [&](uint32_t v) {  // the v-th record's row of query head 0
+        return second ? rec + (uint64_t)(v >> 1) * kPrefixRows + (v & 1) * second : rec + (uint64_t)v * kPrefixRows;
+    };
+    // each source's weight for each query head (negative: it saw nothing), the CTAs' first, and one over
+    // the heads' sums; a warp a head
+    const uint32_t sources = a.cluster + recs;
+    float* const weight = reinterpret_cast<float*>(smem) + kRowWarps * 8 * NT * Sh::kPad;  // [head][sources]
+    for (uint32_t n = warp; n < a.G; n += kRowWarps) {
+        auto source = [&](uint32_t v) {
+            return v < a.cluster ? cluster.map_shared_rank(s_ml, v)[n] : a.rec.ml[record(v - a.cluster) + n];
+        };
+        float top = -INFINITY, sum = 0.0f;
+        for (uint32_t v = lane; v < sources; v += 32) top = fmaxf(top, source(v).x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (uint32_t v = lane; v < sources; v += 32) {
+            const float2 ml = source(v);
+            const bool none = ml.x == -INFINITY && ml.y == 0.0f;
+            const float f = none ? -1.0f : exp2_approx(ml.x - top);
+            weight[n * sources + v] = f;
+            if (!none) sum += ml.y * f;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) s_l[0][n] = sum == 0.0f ? 0.0f : 1.0f / sum;
+    }
+    __syncthreads();
     if (code == HP_OK)
         for (uint32_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
             const uint32_t n = i / (D / 4), d = i % (D / 4) * 4;
-            float top = -INFINITY;
-            for (uint32_t c = 0; c < a.cluster; ++c) top = fmaxf(top, cluster.map_shared_rank(s_ml, c)[n].x);
-            uint64_t rec = 0, recs = 0, second = 0;  // records: first, count, where a second of each lies
-            if (!LIST && a.rec.workers && row.prefix) {
-                const PrefixGroup gr = a.groups[row.group];
-                const uint32_t qt = kPrefixRows / a.G, tile = row.local / qt, in = row.local % qt * a.G + n;
-                const uint64_t steps = a.hdr->steps, lw = (steps + a.rec.workers - 1) / a.rec.workers;
-                const uint64_t s0 = gr.step0 + ((uint64_t)h * gr.tiles + tile) * gr.blocks;
-                const uint64_t v0 = s0 / lw, v1 = (s0 + gr.blocks - 1) / lw;
-                const uint32_t left = gr.rows - tile * qt, trows = (left < qt ? left : qt) * a.G;
-                rec = gr.rows0 + h * gr.records + (uint64_t)tile * qt * a.G + v0 * kPrefixRows + in;
-                recs = v1 - v0 + 1;
-                if (trows <= kPrefixRows / 2) second = trows;
-            }
-            for (uint64_t v = 0; v < recs; ++v) {
-                top = fmaxf(top, __ldcg(&a.rec.ml[rec + v * kPrefixRows]).x);
-                if (second) top = fmaxf(top, __ldcg(&a.rec.ml[rec + v * kPrefixRows + second]).x);
-            }
+            const float* w = weight + n * sources;
             float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            float sum = 0.0f;
-            auto add = [&](float2 ml, float4 y) {
-                if (ml.x == -INFINITY && ml.y == 0.0f) return;  // saw nothing
-                const float f = exp2_approx(ml.x - top);
-                sum += ml.y * f;
+            auto add = [&](float f, const float4& y) {
+                if (f < 0.0f) return;
                 x.x += y.x * f, x.y += y.y * f, x.z += y.z * f, x.w += y.w * f;
             };
             for (uint32_t c = 0; c < a.cluster; ++c)
-                add(cluster.map_shared_rank(s_ml, c)[n],
-                    *reinterpret_cast<const float4*>(cluster.map_shared_rank(part, c) + n * Sh::kPad + d));
-            for (uint64_t v = 0; v < recs; ++v)
-                for (uint64_t at = rec + v * kPrefixRows, left = second ? 2 : 1; left; --left, at += second)
-                    add(__ldcg(&a.rec.ml[at]), __ldcg(reinterpret_cast<const float4*>(a.rec.acc + at * D + d)));
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                add(w[c], *reinterpret_cast<const float4*>(cluster.map_shared_rank(part, c) + n * Sh::kPad + d));
+            for (uint32_t v0 = 0; v0 < recs; v0 += 8) {  // eight records in flight
+                float4 y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (v0 + e < recs && !(w[a.cluster + v0 + e] < 0.0f))
+                        y[e] = *reinterpret_cast<const float4*>(a.rec.acc + (record(v0 + e) + n) * D + d);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (v0 + e < recs) add(w[a.cluster + v0 + e], y[e]);
+            }
+            const float inv = s_l[0][n];
             uint2 y;
             y.x = pack2<T>(x.x * inv, x.y * inv);
             y.y = pack2<T>(x.z * inv, x.w * inv);
@@ -435,7 +465,8 @@ template <typename T, int D, int NT, bool LIST>
 int launch_k(const RowsArgs& a, cudaStream_t st)
 {
     int dev = 0;
-    constexpr int kMerge = kWarps * 8 * NT * Shape<D>::kPad * 4;
+    // the merge: the warps' parts, then a weight for each source and query head
+    constexpr int kMerge = (kRowWarps * 8 * NT * Shape<D>::kPad + kPagesMaxGroup * (8 + 2 * (int)kPrefixMaxSms)) * 4;
     constexpr int kSmem = Shape<D>::kRing > kMerge ? Shape<D>::kRing : kMerge;
     if (current_sms(&dev) == 0 || !allow_dynamic_smem<rows_kernel<T, D, NT, LIST>>(dev, kSmem)) return HP_ERR_CUDA;
     cudaLaunchConfig_t cfg{};

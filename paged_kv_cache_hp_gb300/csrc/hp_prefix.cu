@@ -1,13 +1,13 @@
 // hp_prefix.cu -- the plan of attention behind shared prefixes (hp_attention_prefix): validation, and
 // what the kernels behind it need to know of each query row and each group.
 //
-// One cluster of eight CTAs, one launch: the block table, the sequences and the rows are spread over
-// its 8,192 threads, the sums over the groups are its first CTA's, and the verdicts meet in
-// distributed shared memory, so that a table of half a million entries costs 64 loads a thread and
-// no second launch.
-#include <cooperative_groups.h>
+// One launch: the block table, the sequences and the rows are spread over all its CTAs (one more for
+// every 8,192 table entries: a thread's eight are in flight together), the sums over the groups are the
+// first one's.  Each CTA leaves a verdict of its own, which every CTA of the next kernel reads and
+// meets (hp_prefix.cuh), so no CTA waits for another and nothing has to be cleared first.
 #include <cuda_runtime.h>
 
+#include "hp_prefix.cuh"
 #include "hp_resolve.cuh"
 #include "hp_rows.cuh"
 #include "hp_scan.cuh"
@@ -15,16 +15,12 @@
 namespace hp {
 namespace {
 
-namespace cg = cooperative_groups;
-
-__global__ void __launch_bounds__(kPlanThreads) __cluster_dims__(kPrefixPlanCtas, 1, 1)
-    prefix_plan_kernel(const PrefixPlanArgs a)
+__global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixPlanArgs a)
 {
     __shared__ unsigned long long s_key;
     pdl_wait();
-    cg::cluster_group cluster = cg::this_cluster();
-    const unsigned rank = cluster.block_rank();
-    const uint64_t tid = rank * (uint64_t)kPlanThreads + threadIdx.x, threads = kPrefixPlanCtas * (uint64_t)kPlanThreads;
+    const unsigned rank = blockIdx.x;
+    const uint64_t tid = rank * (uint64_t)kPlanThreads + threadIdx.x, threads = a.ctas * (uint64_t)kPlanThreads;
     const uint64_t S = a.num_seqs, N = a.num_groups;
     if (threadIdx.x == 0) s_key = kVerdictOk;
     __syncthreads();
@@ -119,23 +115,33 @@ __global__ void __launch_bounds__(kPlanThreads) __cluster_dims__(kPrefixPlanCtas
         }
         steps = c_steps;
     }
-    cluster.sync();
-    if (tid == 0) {
-        unsigned long long key = s_key;
-        for (unsigned c = 1; c < kPrefixPlanCtas; ++c) key = min(key, *cluster.map_shared_rank(&s_key, c));
-        a.hdr->steps = steps;
-        a.hdr->verdict = key;
-        if (a.d_status) *a.d_status = key_status(key);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        a.hdr->keys[rank] = s_key;
+        if (rank == 0) a.hdr->steps = steps;
     }
-    cluster.sync();
+}
+
+__global__ void __launch_bounds__(kPrefixPlanCtas) prefix_status_kernel(const PrefixHeader* hdr, uint32_t n, int* d_status)
+{
+    pdl_wait();
+    plan_holds(hdr, n, d_status, true, false);
 }
 
 }  // namespace
 
 int launch_prefix_plan(const PrefixPlanArgs& a, void* stream)
 {
-    return launch_dependent(prefix_plan_kernel, kPrefixPlanCtas, kPlanThreads, 0, static_cast<cudaStream_t>(stream),
-                            a) == cudaSuccess
+    return launch_dependent(prefix_plan_kernel, a.ctas, kPlanThreads, 0, static_cast<cudaStream_t>(stream), a) == cudaSuccess
+               ? HP_OK
+               : HP_ERR_CUDA;
+}
+
+int launch_prefix_status(const PrefixHeader* hdr, uint32_t ctas, int* d_status, void* stream)
+{
+    if (!d_status) return HP_OK;
+    return launch_dependent(prefix_status_kernel, 1, kPrefixPlanCtas, 0, static_cast<cudaStream_t>(stream), hdr, ctas,
+                            d_status) == cudaSuccess
                ? HP_OK
                : HP_ERR_CUDA;
 }

@@ -30,6 +30,7 @@
 #include <cuda_runtime.h>
 
 #include "hp_attn_merge.cuh"
+#include "hp_prefix.cuh"
 #include "hp_resolve.cuh"
 #include "hp_rows.cuh"
 #include "hp_scan.cuh"
@@ -122,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int abort_flag, fail_s[2][2];
     __shared__ float half_s[2][128];  // what a row's two threads tell each other
     pdl_wait();
-    if (a.hdr->verdict != kVerdictOk) return;
+    if (!plan_holds(a.hdr, a.num_keys, a.d_status, a.first && blockIdx.x == 0, a.first == 2)) return;
     const uint64_t steps = a.hdr->steps, lw = (steps + a.workers - 1) / a.workers;
     const uint64_t beg = umin(blockIdx.x * lw, steps), end = umin(beg + lw, steps);
     if (beg >= end) return;

@@ -11,7 +11,8 @@ namespace hp {
 constexpr uint32_t kPrefixKeys = 128;      // keys of a step of the shared prefix
 constexpr uint32_t kPrefixRows = 256;      // (query, head) rows of a tile: two tiles of 128 to the tensor core
 constexpr uint32_t kPrefixMaxSms = 160;    // workers are counted for at most this many SMs
-constexpr uint32_t kPrefixPlanCtas = 8;    // one cluster
+constexpr uint32_t kPrefixPlanCtas = 128;  // at most, and as many verdicts
+constexpr uint64_t kPrefixPlanPart = 8192; // table entries that a CTA of the plan looks at (more in a longer table)
 
 // A query row of hp_attention_prefix, as the plan leaves it.
 struct PrefixRow {
@@ -36,10 +37,15 @@ struct PrefixGroup {
 };
 
 struct PrefixHeader {
-    unsigned long long verdict;
     unsigned long long steps;  // of all groups
-    unsigned long long pad[6];
+    unsigned long long keys[kPrefixPlanCtas];  // the verdict of each of the plan's CTAs
 };
+
+inline uint32_t prefix_plan_ctas(uint64_t table_len)
+{
+    const uint64_t n = 1 + table_len / kPrefixPlanPart;
+    return n < kPrefixPlanCtas ? (uint32_t)n : kPrefixPlanCtas;
+}
 
 struct PrefixPlanArgs {
     const void *seq_ptr, *lens, *table, *q_ptr, *group_ptr, *prefix_lens;
@@ -49,9 +55,11 @@ struct PrefixPlanArgs {
     PrefixHeader* hdr;
     PrefixRow* rows;
     PrefixGroup* groups;   // [num_groups]
-    int* d_status;
+    uint32_t ctas;         // prefix_plan_ctas(table_len)
 };
 int launch_prefix_plan(const PrefixPlanArgs& a, void* stream);
+// The plan's verdict to the status word (a call that runs the plan alone, or has no rows).
+int launch_prefix_status(const PrefixHeader* hdr, uint32_t ctas, int* d_status, void* stream);
 
 // The records that the prefix's workers leave: worker v's part of a tile whose record rows begin at R
 // (of all tiles, in order) at rows R + v * kPrefixRows ..., no two of them in one place since a part has at
@@ -71,6 +79,8 @@ struct PrefixTcArgs {
     int bf16, idx64, test_stall;
     const PrefixHeader* hdr;
     const PrefixGroup* groups;
+    uint32_t num_keys;     // verdicts in hdr
+    int first;             // the call's first kernel behind its plan: it stores the status
     PrefixRecords rec;
     int* d_status;
 };
@@ -95,6 +105,8 @@ struct RowsArgs {
     int* d_status;
     // stretches behind a plan
     const PrefixHeader* hdr;
+    uint32_t num_keys;
+    int first;
     const PrefixRow* rows;
     const PrefixGroup* groups;
     PrefixRecords rec;
