@@ -63,11 +63,11 @@ int reset_status(int* d_status, void* stream)
                                                                                                        : HP_ERR_CUDA;
 }
 
-// CTAs of a (row, K/V head): as many as fill the SMs twice, while each has a block for its warps.
+// CTAs of a (row, K/V head): as many as fill the SMs four times over, while each has a block for its warps.
 uint32_t cluster_of(u64 units, u64 tokens, int sms)
 {
     uint32_t c = 1;
-    while (c < 8 && units * c < 2 * (u64)sms && tokens / (2 * c) >= 64) c *= 2;
+    while (c < 8 && units * c < 4 * (u64)sms && tokens / (2 * c) >= 64) c *= 2;
     return c;
 }
 

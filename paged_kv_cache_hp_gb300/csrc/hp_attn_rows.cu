@@ -37,15 +37,15 @@ using tc::pack2;
 using tma::smem_u32;
 
 constexpr int kRowWarps = 4, kThreads = kRowWarps * 32;
-constexpr uint32_t kWindow = 512;  // pages whose places lie in shared memory (a multiple of kTokens)
+constexpr uint32_t kWindow = 256;  // pages whose places lie in shared memory (a multiple of kTokens)
 constexpr float kTau = 8.0f;       // log2 units a score may exceed its query's reference by
 
 template <int D> struct Shape {
     static constexpr int kTokens = D == 64 ? 32 : 16;     // of a block
     static constexpr int kRow = D * 2, kPieces = kRow / 16;
-    static constexpr int kStage = 2 * kTokens * kRow;     // K rows, then V rows
-    static constexpr int kStages = 3;
-    static constexpr int kRing = kRowWarps * kStages * kStage;
+    static constexpr int kUnit = kTokens * kRow;          // its rows of K, or of V
+    static constexpr int kUnits = 3;                      // of a warp's ring
+    static constexpr int kRing = kRowWarps * kUnits * kUnit;
     static constexpr int kPad = D + 4;                    // floats of a row of the merge
 };
 
@@ -91,10 +91,10 @@ __device__ __forceinline__ int place_at(const RowsArgs& a, const Source& s, uint
 }
 
 template <typename T, int D, int NT, bool LIST>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
+__global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : 4) rows_kernel(const RowsArgs a)
 {
     using Sh = Shape<D>;
-    constexpr int kTokens = Sh::kTokens, kSub = kTokens / 16, kStages = Sh::kStages;
+    constexpr int kTokens = Sh::kTokens, kSub = kTokens / 16;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ Place window[kWindow];
     __shared__ float s_m[kRowWarps][8 * NT], s_l[kRowWarps][8 * NT];
@@ -159,6 +159,23 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
         if (src.first_pages == 0 && own) skip = src.mid % a.P;
     }
     if (threadIdx.x == 0) s_code = HP_OK;
+    // the prefix's records of query head 0: first, count, and where a second of each lies
+    uint64_t rec = 0;
+    uint32_t recs = 0, second = 0;
+    if (!LIST && a.rec.workers && row.prefix) {
+        const PrefixGroup gr = a.groups[row.group];
+        const uint32_t qt = kPrefixRows / a.G, tile = row.local / qt, left = gr.rows - tile * qt;
+        const uint32_t rows = (left < qt ? left : qt) * a.G;
+        const uint64_t lw = (a.hdr->steps + a.rec.workers - 1) / a.rec.workers;
+        const uint64_t s0 = gr.step0 + ((uint64_t)h * gr.tiles + tile) * gr.blocks;
+        const uint64_t v0 = s0 / lw, v1 = (s0 + gr.blocks - 1) / lw;
+        rec = gr.rows0 + h * gr.records + (uint64_t)tile * qt * a.G + v0 * kPrefixRows + row.local % qt * a.G;
+        recs = (uint32_t)(v1 - v0 + 1);
+        if (rows <= kPrefixRows / 2) {
+            second = rows;
+            recs *= 2;
+        }
+    }
     // the queries: rows dims 2 t4 + {0, 1} and + 8 of every 16, columns the heads
     uint32_t qb[NT][D / 16][2];
     {
@@ -187,7 +204,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
     const uint64_t row_bytes = (uint64_t)a.H * Sh::kRow;
     const char* kp = static_cast<const char*>(a.k_pool) + (uint64_t)h * Sh::kRow;
     const char* vp = static_cast<const char*>(a.v_pool) + (uint64_t)h * Sh::kRow;
-    const uint32_t ring = smem_u32(smem) + warp * kStages * Sh::kStage;
+    const uint32_t ring = smem_u32(smem) + warp * Sh::kUnits * Sh::kUnit;
 
     // this CTA's blocks: places x of all pages' slots, kTokens to a block
     const uint64_t x_end = count ? (uint64_t)(count - 1) * a.P + last : 0;
@@ -213,47 +230,44 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
         const uint32_t x_base = page0 * a.P;  // (x below 2^32)
         const uint32_t pages = count - page0 < kWindow ? count - page0 : kWindow;
         const uint32_t nb = (uint32_t)(we - wb), iters = nb > warp ? (nb - warp + kRowWarps - 1) / kRowWarps : 0;
-        uint32_t mask_of[kStages];  // which tokens of a stage count
-        auto issue = [&](uint32_t it, int st, uint32_t& mask) {
-            mask = 0;
-            if (it < iters) {
-                const uint32_t x = (uint32_t)((wb + warp + it * kRowWarps) * kTokens) - x_base + (lane % kTokens);
-                const uint32_t e = div_invariant(x, a.p_m, a.p_l), slot = x - e * a.P;
-                const Place p = e < pages ? window[e] : Place{0, 0, 0};
-                const bool in = slot >= p.lo && slot < p.hi;
-                const uint64_t off = in ? (p.row0 + slot) * row_bytes : 0;
-                mask = __ballot_sync(0xffffffffu, in);
-                if (mask) {
-                    constexpr int kLanes = Sh::kPieces, kAt = kLanes >= 32 ? 1 : 32 / kLanes;
-                    const uint32_t sk = ring + st * Sh::kStage, sv = sk + kTokens * Sh::kRow;
+        uint64_t off = 0;  // this lane's token of the block placed last: where its rows begin
+        auto place = [&](uint32_t it) {  // which tokens of the warp's block `it` count
+            if (it >= iters) return 0u;
+            const uint32_t x = (uint32_t)((wb + warp + it * kRowWarps) * kTokens) - x_base + (lane % kTokens);
+            const uint32_t e = div_invariant(x, a.p_m, a.p_l), slot = x - e * a.P;
+            const Place p = e < pages ? window[e] : Place{0, 0, 0};
+            const bool in = slot >= p.lo && slot < p.hi;
+            off = in ? (p.row0 + slot) * row_bytes : 0;
+            return __ballot_sync(0xffffffffu, in);
+        };
+        auto copy = [&](const char* pool, uint32_t unit, uint32_t mask) {  // that block's rows
+            if (mask) {
+                constexpr int kLanes = Sh::kPieces, kAt = kLanes >= 32 ? 1 : 32 / kLanes;
 #pragma unroll
-                    for (int i = 0; i < kTokens / kAt; ++i) {
-                        const uint32_t tok = i * kAt + lane / kLanes, piece = lane % kLanes;
-                        const uint64_t at = __shfl_sync(0xffffffffu, off, tok) + piece * 16;
-                        const uint32_t ok = (mask >> tok & 1) ? 16u : 0u;
-                        const uint32_t d = tok * Sh::kRow + ((piece ^ (tok & 7)) << 4);
-                        mma::copy16(sk + d, kp + at, ok);
-                        mma::copy16(sv + d, vp + at, ok);
-                    }
+                for (int i = 0; i < kTokens / kAt; ++i) {
+                    const uint32_t tok = i * kAt + lane / kLanes, piece = lane % kLanes;
+                    const uint64_t at = __shfl_sync(0xffffffffu, off, tok) + piece * 16;
+                    mma::copy16(ring + unit * Sh::kUnit + tok * Sh::kRow + ((piece ^ (tok & 7)) << 4), pool + at,
+                                (mask >> tok & 1) ? 16u : 0u);
                 }
             }
             mma::copies_commit();
         };
-#pragma unroll
-        for (int st = 0; st < kStages - 1; ++st) issue(st, st, mask_of[st]);
-        for (uint32_t base = 0; base < iters; base += kStages) {
-#pragma unroll
-            for (int st = 0; st < kStages; ++st) {
-                const uint32_t it = base + st;
-                if (it >= iters) break;
-                issue(it + kStages - 1, (st + kStages - 1) % kStages, mask_of[(st + kStages - 1) % kStages]);
-                mma::copies_wait<kStages - 1>();
-                __syncwarp();
-                const uint32_t mask = mask_of[st];
-                if (mask == 0) continue;
-                const uint32_t sk = ring + st * Sh::kStage, sv = sk + kTokens * Sh::kRow;
+        // units in flight: K of a block goes where V of the one before the last was, V where K of the
+        // last was, each as soon as it has been read
+        uint32_t mask = place(0), next, at = 0;  // at: the unit of this block's K, its V's at + 1
+        copy(kp, 0, mask);
+        copy(vp, 1, mask);
+        next = place(1);
+        copy(kp, 2, next);
+        for (uint32_t it = 0; it < iters; ++it) {
+            const uint32_t at_v = at == 2 ? 0 : at + 1;
+            const uint32_t sk = ring + at * Sh::kUnit, sv = ring + at_v * Sh::kUnit;
+            float s[kSub][NT][4];
+            mma::copies_wait<2>();
+            __syncwarp();
+            if (mask) {
                 // S^T: 16 tokens x 8 queries each
-                float s[kSub][NT][4];
 #pragma unroll
                 for (int b = 0; b < kSub; ++b)
 #pragma unroll
@@ -271,6 +285,10 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
                         for (int nt = 0; nt < NT; ++nt)
                             mma::product<T>(s[b][nt], k4[0], k4[1], k4[2], k4[3], qb[nt][c][0], qb[nt][c][1]);
                     }
+            }
+            __syncwarp();  // K has been read
+            copy(vp, at, next);
+            if (mask) {
                 bool move = false;
 #pragma unroll
                 for (int b = 0; b < kSub; ++b)
@@ -302,10 +320,10 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
                             }
                         }
                 }
+                // weights, rounded to T for the value product (it takes 16-bit operands only)
+                uint32_t p[kSub][NT][2];
 #pragma unroll
-                for (int b = 0; b < kSub; ++b) {
-                    // weights, rounded to T for the value product (it takes 16-bit operands only)
-                    uint32_t p[NT][2];
+                for (int b = 0; b < kSub; ++b)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float w[4];
@@ -315,9 +333,13 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
                             w[e] = exp2_approx(s[b][nt][e] - base + kWeightLift<T>);
                             l[nt][e & 1] += w[e];
                         }
-                        p[nt][0] = mma::transposed(pack2<T>(w[0], w[1]));
-                        p[nt][1] = mma::transposed(pack2<T>(w[2], w[3]));
+                        p[b][nt][0] = mma::transposed(pack2<T>(w[0], w[1]));
+                        p[b][nt][1] = mma::transposed(pack2<T>(w[2], w[3]));
                     }
+                mma::copies_wait<2>();
+                __syncwarp();
+#pragma unroll
+                for (int b = 0; b < kSub; ++b) {
                     // O^T += V^T P^T
 #pragma unroll
                     for (int c = 0; c < D / 16; ++c) {
@@ -326,11 +348,15 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
                         mma::load4_transposed(v4, sv + tok * Sh::kRow + ((piece ^ (tok & 7)) << 4));
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            mma::product<T>(o[nt][c], v4[0], v4[1], v4[2], v4[3], p[nt][0], p[nt][1]);
+                            mma::product<T>(o[nt][c], v4[0], v4[1], v4[2], v4[3], p[b][nt][0], p[b][nt][1]);
                     }
                 }
-                __syncwarp();  // the stage may be filled again
             }
+            __syncwarp();  // V has been read
+            mask = next;
+            next = place(it + 2);
+            copy(kp, at_v, next);
+            at = at == 0 ? 2 : at - 1;
         }
         mma::copies_wait<0>();
     }
@@ -387,23 +413,6 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
     for (uint32_t c = 0; c < a.cluster; ++c) code = lower(code, *cluster.map_shared_rank(&s_code, c));
     const uint32_t share = (a.G * (D / 4) + a.cluster - 1) / a.cluster;
     const uint32_t i0 = rank * share, i1 = (uint32_t)umin(i0 + share, a.G * (D / 4));
-    // the prefix's records of query head 0: first, count, and where a second of each lies
-    uint64_t rec = 0;
-    uint32_t recs = 0, second = 0;
-    if (!LIST && a.rec.workers && row.prefix) {
-        const PrefixGroup gr = a.groups[row.group];
-        const uint32_t qt = kPrefixRows / a.G, tile = row.local / qt, left = gr.rows - tile * qt;
-        const uint32_t rows = (left < qt ? left : qt) * a.G;
-        const uint64_t lw = (a.hdr->steps + a.rec.workers - 1) / a.rec.workers;
-        const uint64_t s0 = gr.step0 + ((uint64_t)h * gr.tiles + tile) * gr.blocks;
-        const uint64_t v0 = s0 / lw, v1 = (s0 + gr.blocks - 1) / lw;
-        rec = gr.rows0 + h * gr.records + (uint64_t)tile * qt * a.G + v0 * kPrefixRows + row.local % qt * a.G;
-        recs = (uint32_t)(v1 - v0 + 1);
-        if (rows <= kPrefixRows / 2) {
-            second = rows;
-            recs *= 2;
-        }
-    }
     auto record = [&](uint32_t v) {  // the v-th record's row of query head 0
         return second ? rec + (uint64_t)(v >> 1) * kPrefixRows + (v & 1) * second : rec + (uint64_t)v * kPrefixRows;
     };
