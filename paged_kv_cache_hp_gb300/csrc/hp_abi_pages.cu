@@ -95,7 +95,7 @@ HP_API int hp_page_bounds(const hp_paged_desc* desc, const void* new_ptr, uint64
     if ((u128)a.units * ((a.columns + 127) / 128) + 1 > kGrid) return HP_ERR_OVERFLOW;
     if (a.units == 0) return reset_status(d_status, stream);
     a.bf16 = d.dtype == HP_BF16;
-    a.check_all = total_new + d.num_seqs <= hp::kPagesChecked;
+    a.check_all = a.units <= hp::kPagesChecked;
     a.d_status = d_status;
     return hp::launch_page_bounds(a, stream);
 }
@@ -113,7 +113,7 @@ HP_API int hp_page_scores(const hp_paged_desc* desc, const void* bounds, const v
     if (scale < 0.0f) return HP_ERR_ARG;
     rc = check_offsets(d, q_ptr, total_q);
     if (rc) return rc;
-    if (max_pages >> 31 || ((u128)total_q * d.num_heads * max_pages) >> 60) return HP_ERR_OVERFLOW;
+    if (max_pages >> 31 || total_q >= kGrid || ((u128)total_q * d.num_heads * max_pages) >> 60) return HP_ERR_OVERFLOW;
     if (total_q && (!q || (max_pages && !scores))) return HP_ERR_NULL;
     if (misaligned(q, 16) || misaligned(scores, 4)) return HP_ERR_ALIGN;
     if (total_q == 0 || d.num_seqs == 0) return reset_status(d_status, stream);
@@ -140,7 +140,7 @@ HP_API int hp_page_scores(const hp_paged_desc* desc, const void* bounds, const v
     if ((u128)total_q * a.chunks + 1 > kGrid) return HP_ERR_OVERFLOW;
     a.scale = scale;
     a.bf16 = d.dtype == HP_BF16;
-    a.check_all = std::max<u64>(total_q, q_ptr ? total_q * max_pages : d.table_len) <= hp::kPagesChecked;
+    a.check_all = total_q <= hp::kRowsChecked && total_q * max_pages <= 4 * hp::kPagesChecked;
     a.d_status = d_status;
     return hp::launch_page_scores(a, stream);
 }
@@ -170,7 +170,7 @@ HP_API int hp_select_pages(const hp_paged_desc* desc, const void* q_ptr, uint64_
     a.sinks = sinks;
     a.recent = recent;
     a.k = k;
-    a.check_all = total_q <= hp::kPagesChecked;
+    a.check_all = q_ptr ? total_q <= hp::kRowsChecked : total_q <= hp::kPagesChecked;
     a.d_status = d_status;
     return hp::launch_select_pages(a, stream);
 }
@@ -226,7 +226,7 @@ HP_API int hp_attention_pages(const hp_paged_desc* k_desc, const void* v_pool, c
     a.selected = selected;
     a.k = k;
     a.cluster = cluster_of(total_q * a.H, (u64)k * a.P, sms);
-    a.check_all = total_q * a.H * k <= hp::kPagesChecked;
+    a.check_all = total_q <= hp::kRowsChecked && total_q * a.H * k <= hp::kPagesChecked;
     a.d_status = d_status;
     return hp::launch_rows(a, stream);
 }

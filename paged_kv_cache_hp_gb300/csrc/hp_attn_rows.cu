@@ -109,21 +109,29 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : 4) rows_ke
     if (LIST && r >= a.q.total_q) {  // the extra cluster's first CTA
         if (rank) return;
         int code = offsets_code(a.q.q_ptr, a.q.idx64, a.q.num_seqs, a.q.total_q);
-        if (a.check_all)
-            for (uint64_t i = warp; i < a.q.total_q; i += kRowWarps) {
-                const Query q = find_query(a.q, i);
+        if (a.check_all) {
+            Source* const rows = reinterpret_cast<Source*>(smem);  // (kRowsChecked of them; the ring is larger)
+            for_each_query(a.q, [&](uint64_t i, const Query& q) {
+                Source s{};  // (no list: nothing to look at)
                 code = lower(code, q.code);
-                if (q.seq >= a.q.num_seqs || q.code != HP_OK) continue;
-                Source s{};
-                s.lo = index_at(a.t.seq_ptr, a.q.idx64, q.seq);
-                s.hi = index_at(a.t.seq_ptr, a.q.idx64, q.seq + 1);
-                s.len = (uint32_t)q.len;
-                s.seen = q.seen;
-                s.list = a.selected + i * a.H * a.k;
-                Place p;
-                for (uint64_t e = lane; e < (uint64_t)a.H * a.k; e += 32)
-                    code = lower(code, place_at<true>(a, s, (uint32_t)e, &p));
+                if (q.seq < a.q.num_seqs && q.code == HP_OK) {
+                    s.lo = index_at(a.t.seq_ptr, a.q.idx64, q.seq);
+                    s.hi = index_at(a.t.seq_ptr, a.q.idx64, q.seq + 1);
+                    s.len = (uint32_t)q.len;
+                    s.seen = q.seen;
+                    s.list = a.selected + i * a.H * a.k;
+                }
+                rows[i] = s;
+            });
+            __syncthreads();
+            const uint32_t each = a.H * a.k;
+            Place p;
+#pragma unroll 4
+            for (uint32_t e = threadIdx.x; e < (uint32_t)a.q.total_q * each; e += kThreads) {
+                const Source& s = rows[e / each];
+                if (s.list) code = lower(code, place_at<true>(a, s, e % each, &p));
             }
+        }
         report_codes(code, a.d_status, a.check_all);
         return;
     }

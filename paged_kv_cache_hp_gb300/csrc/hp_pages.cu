@@ -90,20 +90,28 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsArgs
     const uint32_t parts = (a.columns + kBoundsThreads - 1) / kBoundsThreads;
     const uint64_t u = blockIdx.x / parts;
     const bool offsets = a.q.q_ptr != nullptr;
+    auto first = [&](uint64_t i) { return index_at(a.q.q_ptr, a.q.idx64, i) / a.P + 2 * i; };
     if (u >= a.units) {  // the extra CTA
         int code = offsets_code(a.q.q_ptr, a.q.idx64, a.q.num_seqs, a.q.total_q);
         if (a.check_all)
-            for (uint64_t s = threadIdx.x >> 5; s < a.q.num_seqs; s += kBoundsThreads / 32) {
-                const uint64_t n = offsets ? index_at(a.q.q_ptr, a.q.idx64, s + 1) - index_at(a.q.q_ptr, a.q.idx64, s) : 1;
-                const uint64_t pages = n <= a.q.total_q ? n / a.P + 2 : 0;
-                for (uint64_t k = threadIdx.x & 31; k < pages; k += 32) code = lower(code, bounds_unit(a, s, k).code);
+            for (uint64_t i = threadIdx.x; i < a.units; i += kBoundsThreads) {
+                uint64_t s = i, lo = 0;
+                if (offsets) {
+                    uint64_t end = a.q.num_seqs;
+                    for (s = 0; end - s > 1;) {
+                        const uint64_t mid = (s + end) >> 1;
+                        if (first(mid) <= i) s = mid;
+                        else end = mid;
+                    }
+                    lo = first(s);
+                }
+                if (!offsets || lo <= i) code = lower(code, bounds_unit(a, s, offsets ? i - lo : 0).code);
             }
         report_codes(code, a.d_status, a.check_all);
         return;
     }
     uint64_t s = u, k = 0;
     if (offsets) {
-        auto first = [&](uint64_t i) { return index_at(a.q.q_ptr, a.q.idx64, i) / a.P + 2 * i; };
         s = warp_last(a.q.num_seqs, [&](uint64_t i) { return first(i) <= u; });
         if (first(s) > u) return;
         k = u - first(s);
@@ -187,22 +195,26 @@ __device__ __forceinline__ ScoreRow score_row(const ScoreArgs& a, const Query& q
 // same 16 bytes of q.)  The warps of a CTA take the heads of the same pages, whose bounds lie
 // together.  What bounds it is memory: 512 bytes a page and head at D = 128.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(32 * kScoreWarps) scores_kernel(const ScoreArgs a)
+__global__ void __launch_bounds__(32 * kScoreWarps, D == 256 || NT == 2 ? 1 : 3) scores_kernel(const ScoreArgs a)
 {
     constexpr int kSeg = D / 32;   // 64-byte segments of a row of D elements
-    constexpr int kPart = kSeg < 4 ? kSeg : 4;
+    constexpr int kPart = 2 * kSeg < 4 ? 2 * kSeg : 4;
     pdl_wait();
     const uint64_t r = blockIdx.x / a.chunks;
     const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     if (r >= a.q.total_q) {  // the extra CTA
         int code = offsets_code(a.q.q_ptr, a.q.idx64, a.q.num_seqs, a.q.total_q);
-        if (a.check_all)
-            for (uint64_t i = warp; i < a.q.total_q; i += kScoreWarps) {
-                const ScoreRow row = score_row(a, find_query(a.q, i));
-                code = lower(code, row.code);
-                for (uint32_t j = lane; j < row.n; j += 32)
-                    if (index_at(a.t.table, a.q.idx64, row.lo + j) >= a.t.num_pages) code = lower(code, HP_ERR_PAGE_ID);
-            }
+        if (a.check_all) {
+            __shared__ ScoreRow rows[kRowsChecked];
+            for_each_query(a.q, [&](uint64_t i, const Query& q) {
+                rows[i] = score_row(a, q);
+                code = lower(code, rows[i].code);
+            });
+            __syncthreads();
+            for (uint64_t i = warp; i < a.q.total_q; i += kScoreWarps)
+                for (uint32_t j = lane; j < rows[i].n; j += 32)
+                    if (index_at(a.t.table, a.q.idx64, rows[i].lo + j) >= a.t.num_pages) code = lower(code, HP_ERR_PAGE_ID);
+        }
         report_codes(code, a.d_status, a.check_all);
         return;
     }
@@ -216,19 +228,24 @@ __global__ void __launch_bounds__(32 * kScoreWarps) scores_kernel(const ScoreArg
     const T* queries = static_cast<const T*>(a.queries) + r * a.H * a.G * D;
     uint4 up[NT][kSeg], dn[NT][kSeg];
     uint32_t head = 0xFFFFFFFFu;
-    for (uint64_t i = warp; i < (uint64_t)blocks * a.H; i += kScoreWarps) {
-        const uint32_t h = (uint32_t)(i % a.H), p0 = first + (uint32_t)(i / a.H) * 16;
-        uint64_t phys[2];
-        bool ok[2];
+    // the pages of this lane's two rows of an item (16 pages, a head), as the table has them
+    const uint32_t items = blocks * a.H;  // (a CTA's: the host holds them below 2^31)
+    auto pages_of = [&](uint32_t i, uint64_t (&phys)[2]) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const uint32_t j = p0 + g + 8 * x;
-            phys[x] = j < end ? index_at(a.t.table, a.q.idx64, row.lo + j) : 0;
-            ok[x] = j < end && phys[x] < a.t.num_pages;
-            if (j < end && !ok[x]) {
-                if (tell && t == 0) atomicMin(a.d_status, (int)HP_ERR_PAGE_ID);
-            }
+            const uint32_t j = first + i / a.H * 16 + g + 8 * x;
+            phys[x] = i < items && j < end ? index_at(a.t.table, a.q.idx64, row.lo + j) : 0;
         }
+    };
+    uint64_t next[2];
+    pages_of(warp, next);
+    for (uint32_t i = warp; i < items; i += kScoreWarps) {
+        const uint32_t block = i / a.H, h = i - block * a.H, p0 = first + block * 16;
+        const uint64_t phys[2] = {next[0], next[1]};
+        const bool ok[2] = {p0 + g < end && phys[0] < a.t.num_pages, p0 + g + 8 < end && phys[1] < a.t.num_pages};
+        if (tell && t == 0 && ((p0 + g < end && !ok[0]) || (p0 + g + 8 < end && !ok[1])))
+            atomicMin(a.d_status, (int)HP_ERR_PAGE_ID);
+        pages_of(i + kScoreWarps, next);  // (on its way while this item is summed)
         if (h != head) {
             head = h;
 #pragma unroll
@@ -249,26 +266,24 @@ __global__ void __launch_bounds__(32 * kScoreWarps) scores_kernel(const ScoreArg
             at[x] = reinterpret_cast<const uint4*>(static_cast<const T*>(a.bounds) +
                                                    ((ok[x] ? phys[x] : 0) * a.H + h) * 2 * D) + t;
         float acc[NT][4] = {};
+        // a row's 2 D numbers in parts, the loads of each in flight together
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+        for (int c0 = 0; c0 < 2 * kSeg; c0 += kPart) {
+            uint4 x[kPart], y[kPart];
 #pragma unroll
-            for (int c0 = 0; c0 < kSeg; c0 += kPart) {
-                uint4 x[kPart], y[kPart];
-#pragma unroll
-                for (int c = 0; c < kPart; ++c) {
-                    const int at16 = half * (D / 8) + (c0 + c) * 4;
-                    x[c] = ok[0] ? at[0][at16] : uint4{};
-                    y[c] = ok[1] ? at[1][at16] : uint4{};
-                }
-#pragma unroll
-                for (int c = 0; c < kPart; ++c)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const uint4 b = half ? dn[nt][c0 + c] : up[nt][c0 + c];
-                        mma::product<T>(acc[nt], x[c].x, y[c].x, x[c].y, y[c].y, b.x, b.y);
-                        mma::product<T>(acc[nt], x[c].z, y[c].z, x[c].w, y[c].w, b.z, b.w);
-                    }
+            for (int c = 0; c < kPart; ++c) {
+                x[c] = ok[0] ? at[0][(c0 + c) * 4] : uint4{};
+                y[c] = ok[1] ? at[1][(c0 + c) * 4] : uint4{};
             }
+#pragma unroll
+            for (int c = 0; c < kPart; ++c)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint4 b = c0 + c < kSeg ? up[nt][c0 + c] : dn[nt][c0 + c - kSeg];
+                    mma::product<T>(acc[nt], x[c].x, y[c].x, x[c].y, y[c].y, b.x, b.y);
+                    mma::product<T>(acc[nt], x[c].z, y[c].z, x[c].w, y[c].w, b.z, b.w);
+                }
+        }
         // the largest of the group's queries: columns 2 t and 2 t + 1 here, the others in the lane's quad
         float best[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -317,27 +332,51 @@ __device__ __forceinline__ uint32_t score_key(float x)
     return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
 
+// The sum over the warps before this one, and over all, of a warp's number; `room` has kWarps words.
+// (Two barriers: before the words are written and before they are read.)
+template <int kWarps>
+__device__ __forceinline__ uint32_t warps_before(uint32_t mine, uint32_t* room, uint32_t& all)
+{
+    const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __syncthreads();
+    if (lane == 0) room[warp] = mine;
+    __syncthreads();
+    const uint32_t x = lane < kWarps ? room[lane] : 0u;
+    uint32_t sum = x;
+#pragma unroll
+    for (int o = 1; o < kWarps; o <<= 1) {
+        const uint32_t up = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= (unsigned)o) sum += up;
+    }
+    all = __shfl_sync(0xffffffffu, sum, kWarps - 1);
+    return __shfl_sync(0xffffffffu, sum - x, warp);
+}
+
 // One CTA a (query, K/V head).  Warp w holds the scores w * 32 * PER ... of a tile, score i * 32 + lane
-// of them in register i: coalesced loads, and ballots give their order.  Rows of more than a tile
-// are read again in each pass (they lie in L2).
+// of them in register i: coalesced loads, and ballots give their order.  Only the first pass counts
+// all scores; those in its threshold bin (a few hundred) are gathered in shared memory for the other two.
+// In the last one lane i of a warp writes what ballot i found: few bits are set where few pages are
+// taken.  Rows of more than a tile are read again each time (they lie in L2).  What bounds it is issue: 700
+// instructions a warp of 512 scores, a third of them loading and converting.
 template <int THREADS, int PER>
-__global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a)
+__global__ void __launch_bounds__(THREADS, 1536 / THREADS) select_kernel(const SelectArgs a)
 {
     constexpr int kWarps = THREADS / 32, kPerThread = kBins / THREADS;
-    constexpr uint32_t kTile = THREADS * PER;
-    __shared__ uint32_t hist[kBins];
-    __shared__ uint32_t s_warp[2][kWarps], s_bin, s_left;
+    constexpr uint32_t kTile = THREADS * PER, kCand = 2048;
+    static_assert(PER <= 32 && kPerThread % 4 == 0, "a lane a ballot, bins in vectors");
+    __shared__ __align__(16) uint32_t hist[kBins];
+    __shared__ uint32_t cand[kCand];
+    __shared__ uint32_t s_room[kWarps], s_bin, s_left, s_cand;
     pdl_wait();
     const uint64_t r = blockIdx.x / a.H;
     const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (r >= a.q.total_q) {  // the extra CTA
         int code = offsets_code(a.q.q_ptr, a.q.idx64, a.q.num_seqs, a.q.total_q);
         if (a.check_all)
-            for (uint64_t i = warp; i < a.q.total_q; i += kWarps) {
-                const Query q = find_query(a.q, i);
+            for_each_query(a.q, [&](uint64_t, const Query& q) {
                 code = lower(code, q.code != HP_OK ? q.code
                                    : q.seen && (q.seen + a.P - 1) / a.P > a.max_pages ? HP_ERR_OUT_SIZE : HP_OK);
-            }
+            });
         report_codes(code, a.d_status, a.check_all);
         return;
     }
@@ -359,90 +398,121 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a)
     if (need == 0) return;
     const float* scores = a.scores + (r * a.H + blockIdx.x % a.H) * a.max_pages + a.sinks;
     const bool one = count <= kTile;
+    const uint32_t mine = warp * (PER * 32) + lane;
     uint32_t key[PER];
     auto load = [&](uint32_t base) {  // (places past the end are told apart by their index)
+        const float* from = scores + base + mine;
+        const uint32_t left = count - base > mine ? count - base - mine : 0u;
+        float x[PER];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const uint32_t at = base + (warp * PER + i) * 32 + lane;
-            key[i] = at < count ? score_key(scores[at]) : 0u;
+        for (int i = 0; i < PER; ++i) x[i] = 32u * i < left ? from[32 * i] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) key[i] = score_key(x[i]);
+        return left;
+    };
+    // f(key, place within the thread's 32 PER of the tile) for every score
+    auto every = [&](auto&& f) {
+        for (uint32_t base = 0; base < count; base += kTile) {
+            uint32_t left = count - base > mine ? count - base - mine : 0u;
+            if (!one) left = load(base);
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (32u * i < left) f(key[i]);
         }
     };
     if (one) load(0);
     uint32_t prefix = 0;
     int shift = 32;
+    bool gathered = false;
     for (int pass = 0; pass < 3; ++pass) {
-        const int bits = pass < 2 ? 11 : 10;
-        for (uint32_t i = threadIdx.x; i < kBins; i += THREADS) hist[i] = 0;
+        const int bits = pass < 2 ? 11 : 10, down = shift - bits;
+        for (uint32_t i = threadIdx.x; i < kBins / 4; i += THREADS) reinterpret_cast<uint4*>(hist)[i] = uint4{};
+        if (threadIdx.x == 0 && pass == 0) s_cand = 0;
         __syncthreads();
-        for (uint32_t base = 0; base < count; base += kTile) {
-            if (!one) load(base);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const uint32_t at = base + (warp * PER + i) * 32 + lane;
-                if (at < count && (pass == 0 || key[i] >> shift == prefix))
-                    atomicAdd(&hist[(key[i] >> (shift - bits)) & ((1u << bits) - 1)], 1u);
+        const uint32_t low = (1u << bits) - 1;
+        if (pass == 0) every([&](uint32_t x) { atomicAdd(&hist[x >> down], 1u); });
+        else if (gathered)
+            for (uint32_t i = threadIdx.x; i < s_cand; i += THREADS) {
+                if (cand[i] >> shift == prefix) atomicAdd(&hist[cand[i] >> down & low], 1u);
             }
-        }
+        else every([&](uint32_t x) {
+                if (x >> shift == prefix) atomicAdd(&hist[x >> down & low], 1u);
+            });
         __syncthreads();
         // from the highest bin down: thread i has bins kBins - 1 - i * kPerThread ...
-        uint32_t mine = 0;
+        uint32_t h[kPerThread], part = 0;
 #pragma unroll
-        for (int i = 0; i < kPerThread; ++i) mine += hist[kBins - 1 - threadIdx.x * kPerThread - i];
-        uint32_t sum = mine;
+        for (int i = 0; i < kPerThread / 4; ++i) {
+            const uint4 v = reinterpret_cast<const uint4*>(hist)[(kBins - (threadIdx.x + 1) * kPerThread) / 4 + kPerThread / 4 - 1 - i];
+            h[4 * i] = v.w, h[4 * i + 1] = v.z, h[4 * i + 2] = v.y, h[4 * i + 3] = v.x;
+            part += v.x + v.y + v.z + v.w;
+        }
+        uint32_t sum = part, all;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t up = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= (unsigned)o) sum += up;
         }
-        if (lane == 31) s_warp[0][warp] = sum;
-        __syncthreads();
-        uint32_t before = sum - mine;
-        for (unsigned w = 0; w < warp; ++w) before += s_warp[0][w];
-        if (before < need && need <= before + mine) {  // one thread's
+        const uint32_t total = __shfl_sync(0xffffffffu, sum, 31);
+        uint32_t before = warps_before<kWarps>(total, s_room, all) + sum - part;
+        if (before < need && need <= before + part) {  // one thread's
             uint32_t b = kBins - 1 - threadIdx.x * kPerThread;
-            while (before + hist[b] < need) before += hist[b--];
-            s_bin = b;
-            s_left = need - before;
+#pragma unroll
+            for (int i = 0; i < kPerThread; ++i) {
+                if (before < need && need <= before + h[i]) {
+                    s_bin = b - i;
+                    s_left = need - before;
+                }
+                before += h[i];
+            }
         }
         __syncthreads();
         prefix = (prefix << bits) | s_bin;
         need = s_left;
-        shift -= bits;
+        shift = down;
+        if (pass == 0) {
+            const uint32_t in = hist[s_bin];  // scores in the threshold's bin
+            gathered = in <= kCand;
+            if (gathered)
+                every([&](uint32_t x) {
+                    if (x >> down == prefix) cand[atomicAdd(&s_cand, 1u)] = x;
+                });
+            __syncthreads();  // (the bin has been read, the scores are gathered)
+        }
     }
     // above the threshold `prefix`, and the first `need` at it, in order
     uint32_t above_base = 0, equal_base = 0;
     for (uint32_t base = 0; base < count; base += kTile) {
-        if (!one) load(base);
-        uint32_t above = 0, equal = 0;
+        uint32_t left = count - base > mine ? count - base - mine : 0u;
+        if (!one) left = load(base);
+        uint32_t ma = 0, me = 0;  // of ballot `lane`
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const bool in = base + (warp * PER + i) * 32 + lane < count;
-            above += __popc(__ballot_sync(0xffffffffu, in && key[i] > prefix));
-            equal += __popc(__ballot_sync(0xffffffffu, in && key[i] == prefix));
+            const unsigned va = __ballot_sync(0xffffffffu, 32u * i < left && key[i] > prefix);
+            const unsigned ve = __ballot_sync(0xffffffffu, 32u * i < left && key[i] == prefix);
+            if (lane == (unsigned)i) ma = va, me = ve;
         }
-        __syncthreads();  // (the last tile's sums have been read)
-        if (lane == 0) {
-            s_warp[0][warp] = above;
-            s_warp[1][warp] = equal;
-        }
-        __syncthreads();
-        uint32_t pa = above_base, pe = equal_base;
-        for (unsigned w = 0; w < kWarps; ++w) {
-            if (w < warp) pa += s_warp[0][w], pe += s_warp[1][w];
-            above_base += s_warp[0][w];
-            equal_base += s_warp[1][w];
-        }
-        const unsigned below = (1u << lane) - 1u;
+        // counts of both, packed: a tile has at most 2^14 scores
+        const uint32_t both = __popc(ma) << 16 | __popc(me);
+        uint32_t sum = both, all;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const uint32_t at = base + (warp * PER + i) * 32 + lane;
-            const unsigned ma = __ballot_sync(0xffffffffu, at < count && key[i] > prefix);
-            const unsigned me = __ballot_sync(0xffffffffu, at < count && key[i] == prefix);
-            const uint32_t xa = pa + __popc(ma & below), xe = pe + __popc(me & below);
-            if ((ma >> lane & 1) || ((me >> lane & 1) && xe < need))
-                out[a.sinks + xa + (xe < need ? xe : need)] = (int32_t)(a.sinks + at);
-            pa += __popc(ma);
-            pe += __popc(me);
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t up = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= (unsigned)o) sum += up;
+        }
+        const uint32_t total = __shfl_sync(0xffffffffu, sum, 31);
+        const uint32_t at = warps_before<kWarps>(total, s_room, all) + sum - both;
+        uint32_t pa = above_base + (at >> 16), pe = equal_base + (at & 0xFFFF);
+        above_base += all >> 16;
+        equal_base += all & 0xFFFF;
+        if (pe >= need) me = 0;
+        for (unsigned taken = ma | me; taken; taken &= taken - 1) {
+            const unsigned bit = __ffs(taken) - 1;
+            const bool equal = me >> bit & 1;
+            if (!equal || pe < need)
+                out[a.sinks + pa + (pe < need ? pe : need)] = (int32_t)(a.sinks + base + warp * (PER * 32) + 32 * lane + bit);
+            if (equal) ++pe;
+            else ++pa;
         }
     }
 }

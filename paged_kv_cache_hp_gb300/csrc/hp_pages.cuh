@@ -13,10 +13,10 @@ namespace hp {
 constexpr uint32_t kPagesMaxPage = 4096;        // slots of a page
 constexpr uint32_t kPagesMaxGroup = 16;         // query heads of a K/V head
 constexpr uint64_t kPagesMaxTokens = 1u << 31;  // tokens of a sequence stay below (32-bit token numbers)
-// Up to this many entries one extra CTA looks at them all and stores the status; beyond it the
-// word is cleared by a memset before the kernel (3 us, lost in a call of that size) and whoever meets
-// an error lowers it.
-constexpr uint64_t kPagesChecked = 8192;
+// Up to this many entries (pages, list entries) of up to so many rows one extra CTA looks at them all,
+// beside the others, and stores the status (under 5 us); beyond it the word is cleared by a memset before
+// the kernel (3 us) and whoever meets an error lowers it.
+constexpr uint64_t kPagesChecked = 1024, kRowsChecked = 128;
 
 // The queries of a batch: sequence s has q_ptr[s] .. q_ptr[s+1], its last tokens in order (q_ptr
 // NULL: one each).
@@ -124,6 +124,20 @@ __device__ __forceinline__ Query find_query(const QueryArgs& a, uint64_t r)
     if (a.num_seqs == 0) return Query{0, 0, 0, HP_OK};
     const uint64_t s = warp_last(a.num_seqs, [&](uint64_t i) { return index_at(a.q_ptr, a.idx64, i) <= r; });
     return query_of(a, s, r, index_at(a.q_ptr, a.idx64, s), index_at(a.q_ptr, a.idx64, s + 1));
+}
+
+// f(r, query r) for every row, each by one thread of the CTA.
+template <typename F>
+__device__ __forceinline__ void for_each_query(const QueryArgs& a, F f)
+{
+    if (!a.q_ptr) {
+        for (uint64_t r = threadIdx.x; r < a.total_q; r += blockDim.x) f(r, query_of(a, r, r, r, r + 1));
+    } else {
+        for (uint64_t r = threadIdx.x >> 5; r < a.total_q; r += blockDim.x >> 5) {
+            const Query q = find_query(a, r);
+            if ((threadIdx.x & 31) == 0) f(r, q);
+        }
+    }
 }
 
 __device__ __forceinline__ int lower(int a, int b) { return a < b ? a : b; }
