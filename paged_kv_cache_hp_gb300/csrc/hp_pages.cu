@@ -359,7 +359,7 @@ __device__ __forceinline__ uint32_t warps_before(uint32_t mine, uint32_t* room, 
 // taken.  Rows of more than a tile are read again each time (they lie in L2).  What bounds it is issue: 700
 // instructions a warp of 512 scores, a third of them loading and converting.
 template <int THREADS, int PER>
-__global__ void __launch_bounds__(THREADS, 1536 / THREADS) select_kernel(const SelectArgs a)
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_kernel(const SelectArgs a)
 {
     constexpr int kWarps = THREADS / 32, kPerThread = kBins / THREADS;
     constexpr uint32_t kTile = THREADS * PER, kCand = 2048;
@@ -575,7 +575,7 @@ int launch_select_pages(const SelectArgs& a, void* stream)
     cudaError_t e;
     if (a.max_pages <= 512) e = launch_dependent(select_kernel<128, 4>, grid, 128, 0, st, a);
     else if (a.max_pages <= 2048) e = launch_dependent(select_kernel<256, 8>, grid, 256, 0, st, a);
-    else e = launch_dependent(select_kernel<512, 16>, grid, 512, 0, st, a);
+    else e = launch_dependent(select_kernel<256, 32>, grid, 256, 0, st, a);
     return e == cudaSuccess ? HP_OK : HP_ERR_CUDA;
 }
 
