@@ -279,8 +279,8 @@ inline void invariant_divisor(uint64_t g, uint32_t* m, uint32_t* l)
 //     overwrites a workspace that a previous copy may still read, and starts at once), and
 //     where it is a kernel without a plan;
 //   - is itself a dependent, of whatever the stream holds, in a serving step: the latent plan,
-//     the step tables, the norm + rotation appends, latent attention that plans for itself, and
-//     every *_planned call.
+//     the step tables, the norm + rotation appends, latent attention that plans for itself, the
+//     operators of long contexts, and every *_planned call.
 // What keeps this right:
 //   - a kernel launched as a dependent runs griddepcontrol.wait in every CTA, before any return,
 //     and before it reads or writes global memory that a call before may use.  (The table check

@@ -110,7 +110,7 @@ def test_sequences_of_2_31_tokens_are_refused_on_the_device(hp):
     assert b.code() == "HP_ERR_LEN"
 
 
-@pytest.mark.parametrize("kernel", ["default", "cuda_cores"])
+@pytest.mark.parametrize("kernel", ["tensor_cores", "cuda_cores"])
 @pytest.mark.parametrize("what,code", [
     ("ptr_start", "SEQ_PTR_START"), ("ptr_order", "SEQ_PTR_ORDER"), ("ptr_end", "SEQ_PTR_END"), ("page", "PAGE_ID"),
     ("len", "LEN"), ("group_start", "GROUP"), ("group_order", "GROUP"), ("group_end", "GROUP"), ("prefix", "PREFIX"),
@@ -168,7 +168,7 @@ def test_prefix_verdict_of_a_long_table(hp):
     b.check(everything, rows={1})
 
 
-@pytest.mark.parametrize("kernel", ["default", "cuda_cores"])
+@pytest.mark.parametrize("kernel", ["tensor_cores", "cuda_cores"])
 def test_prefix_without_queries(hp, kernel):
     import torch
     b = make(hp, [(2, 20)], [3, 4], 1, 2, 128, 16, kernel=kernel, nq=[0, 0], behind=2)
@@ -184,7 +184,7 @@ def test_prefix_without_queries(hp, kernel):
 def test_values_that_are_not_finite_spoil_their_own_queries(hp, op):
     """A NaN key of one sequence's own token, an infinite value of another's, a NaN query."""
     import torch
-    kernel = "cuda_cores" if op.endswith("cores") else "default"
+    kernel = "cuda_cores" if op.endswith("cores") else "tensor_cores"
     b = make(hp, [(4, 200)], [40, 50, 60, 20], 2, 4, 128, 16, kernel=kernel, nq=[1, 3, 1, 1], seed=8)
     at = lambda s, t: (int(b.table[b.ptr[s] + t // 16]), t % 16)  # noqa: E731
     p, i = at(1, 249)                  # sequence 1's last token: its last query alone sees it
@@ -223,7 +223,7 @@ def test_values_that_are_not_finite_spoil_their_own_queries(hp, op):
 @pytest.mark.parametrize("op", ["pages", "prefix", "prefix_cuda_cores"])
 @pytest.mark.parametrize("scale", [0.0, -0.3, 4.0])
 def test_scales_of_any_sign_and_peaked_scores(hp, op, scale):
-    kernel = "cuda_cores" if op.endswith("cores") else "default"
+    kernel = "cuda_cores" if op.endswith("cores") else "tensor_cores"
     b = make(hp, [(3, 300)], [20, 0, 7], 1, 8, 64, 16, "f16", kernel, seed=9, k_scale=3.0)
     b.scale = scale
     if op == "pages":
@@ -241,7 +241,7 @@ def test_scales_of_any_sign_and_peaked_scores(hp, op, scale):
 def test_a_rising_score_moves_the_reference_in_every_block(hp):
     """Keys that grow along the prefix: every block of 128 keys, and every block of a warp, rescales."""
     import torch
-    for kernel in ("default", "cuda_cores"):
+    for kernel in ("tensor_cores", "cuda_cores"):
         b = make(hp, [(3, 1500)], [40, 0, 9], 1, 2, 128, 16, kernel=kernel, seed=10)
         for s in range(3):
             for t in range(int(b.lens[s])):
@@ -401,7 +401,7 @@ def test_a_wait_that_runs_out_is_reported(hp):
     """The loads of the first block are never issued: every role gives up, the call reports it, the next one
     is right."""
     b = make(hp, [(20, 500)], [3] * 20, 1, 8, 128, 16, seed=31)
-    b.desc = b.describe(flags=hp.TEST_STALL)
+    b.desc = b.describe(flags=hp.TEST_STALL | hp.ATTN_TENSOR_CORES)
     run(b)
     assert b.code() == "HP_ERR_TIMEOUT"
     b.desc = b.describe()

@@ -8,10 +8,10 @@ from pages_ref import Batch
 pytestmark = pytest.mark.gpu
 
 
-def make(hp, groups, tails, H, G, D, P, dtype="bf16", kernel="default", **kw):
+def make(hp, groups, tails, H, G, D, P, dtype="bf16", kernel="tensor_cores", **kw):
     """groups: (sequences, prefix); tails: each sequence's tokens behind it."""
     pre = np.repeat([p for _, p in groups], [n for n, _ in groups])
-    flags = hp.ATTN_CUDA_CORES if kernel == "cuda_cores" else 0
+    flags = {"cuda_cores": hp.ATTN_CUDA_CORES, "tensor_cores": hp.ATTN_TENSOR_CORES, "default": 0}[kernel]
     return Batch(hp, pre + np.array(tails), H, G, D, P, dtype, groups=groups, flags=flags, **kw)
 
 
@@ -34,7 +34,7 @@ def everything(row, s, seen, h):
     return np.arange(seen)
 
 
-@pytest.mark.parametrize("kernel", ["default", "cuda_cores"])
+@pytest.mark.parametrize("kernel", ["tensor_cores", "cuda_cores"])
 @pytest.mark.parametrize("dtype,groups,tails,nq,H,G,D,P,it,behind", [
     ("bf16", [(1, 1)], [0], None, 1, 1, 128, 16, 0, 0),
     ("f16", [(2, 16)], [0, 5], None, 2, 4, 128, 16, 1, 0),
@@ -55,7 +55,7 @@ def test_attention_prefix(hp, kernel, dtype, groups, tails, nq, H, G, D, P, it, 
     b.check(everything)
 
 
-@pytest.mark.parametrize("kernel", ["default", "cuda_cores"])
+@pytest.mark.parametrize("kernel", ["tensor_cores", "cuda_cores"])
 @pytest.mark.parametrize("S,H,G,D,pre,tail", [(130, 2, 4, 128, 700, 90), (33, 8, 8, 64, 2000, 40), (3, 1, 4, 128, 9000, 3),
                                               (300, 1, 1, 128, 260, 20)])
 def test_attention_prefix_of_many_rows(hp, kernel, S, H, G, D, pre, tail):
@@ -65,3 +65,19 @@ def test_attention_prefix_of_many_rows(hp, kernel, S, H, G, D, pre, tail):
     run(b)
     assert b.code() == "HP_OK"
     b.check(everything, rows={0, 1, S // 2, S - 1})
+
+
+@pytest.mark.parametrize("S,pre", [(3, 3000), (60, 3600)])
+def test_the_librarys_choice(hp, S, pre):
+    """Below and above the size from which the prefix is read on the tensor cores (60 x 3,600 tokens of 8
+    heads of 128: 885 MB, most of it the same pages)."""
+    b = make(hp, [(S, pre)], [(3 * i) % 50 for i in range(S)], 8, 4, 128, 16, kernel="default", seed=S)
+    run(b)
+    assert b.code() == "HP_OK"
+    b.check(everything, rows={0, S // 2, S - 1})
+    out = b.out.clone()
+    other = hp.ATTN_TENSOR_CORES if S * pre * 4096 >= 384 << 20 else hp.ATTN_CUDA_CORES
+    b.desc = b.describe(flags=other)
+    b.out.fill_(7.0)
+    run(b)
+    assert (b.out.view(-1) == out.view(-1)).all()  # the same kernels
