@@ -132,9 +132,9 @@ HP_API int hp_page_scores(const hp_paged_desc* desc, const void* bounds, const v
     a.G = num_q_heads / a.H;
     a.D = (uint32_t)d.head_dim;
     // a CTA's eight warps take (16 pages, head) pairs: one each while the SMs are not filled twice
-    // over, then up to eight
+    // over, then up to sixteen (eight: 212 us where sixteen take 206, at 300,000 pages of 8 heads of 128)
     const u64 blocks = std::max<u64>(1, (max_pages + 15) / 16);
-    const u64 each = std::min<u64>(8, std::max<u64>(1, total_q * blocks * a.H / (sms * 32)));
+    const u64 each = std::min<u64>(16, std::max<u64>(1, total_q * blocks * a.H / (sms * 32)));
     a.chunk_blocks = (uint32_t)std::max<u64>(1, (each * 8 + a.H - 1) / a.H);
     a.chunks = (blocks + a.chunk_blocks - 1) / a.chunk_blocks;
     if ((u128)total_q * a.chunks + 1 > kGrid) return HP_ERR_OVERFLOW;

@@ -195,10 +195,10 @@ __device__ __forceinline__ ScoreRow score_row(const ScoreArgs& a, const Query& q
 // same 16 bytes of q.)  The warps of a CTA take the heads of the same pages, whose bounds lie
 // together.  What bounds it is memory: 512 bytes a page and head at D = 128.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(32 * kScoreWarps, D == 256 || NT == 2 ? 1 : 3) scores_kernel(const ScoreArgs a)
+__global__ void __launch_bounds__(32 * kScoreWarps, D == 256 || NT == 2 ? 1 : D == 128 ? 2 : 3) scores_kernel(const ScoreArgs a)
 {
     constexpr int kSeg = D / 32;   // 64-byte segments of a row of D elements
-    constexpr int kPart = 2 * kSeg < 4 ? 2 * kSeg : 4;
+    constexpr int kPart = 2 * kSeg < 8 ? 2 * kSeg : 8;
     pdl_wait();
     const uint64_t r = blockIdx.x / a.chunks;
     const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -246,6 +246,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps, D == 256 || NT == 2 ? 1 : 3)
         if (tell && t == 0 && ((p0 + g < end && !ok[0]) || (p0 + g + 8 < end && !ok[1])))
             atomicMin(a.d_status, (int)HP_ERR_PAGE_ID);
         pages_of(i + kScoreWarps, next);  // (on its way while this item is summed)
+        if (!__any_sync(0xffffffffu, ok[0] || ok[1])) continue;
         if (h != head) {
             head = h;
 #pragma unroll
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps, D == 256 || NT == 2 ? 1 : 3)
                     dn[nt][c] = uint4{least2<T>(x.x, 0u), least2<T>(x.y, 0u), least2<T>(x.z, 0u), least2<T>(x.w, 0u)};
                 }
         }
-        const uint4* at[2];
+        const uint4* at[2];  // (a row without a page reads the pool's first, for nothing)
 #pragma unroll
         for (int x = 0; x < 2; ++x)
             at[x] = reinterpret_cast<const uint4*>(static_cast<const T*>(a.bounds) +
@@ -272,8 +273,8 @@ __global__ void __launch_bounds__(32 * kScoreWarps, D == 256 || NT == 2 ? 1 : 3)
             uint4 x[kPart], y[kPart];
 #pragma unroll
             for (int c = 0; c < kPart; ++c) {
-                x[c] = ok[0] ? at[0][(c0 + c) * 4] : uint4{};
-                y[c] = ok[1] ? at[1][(c0 + c) * 4] : uint4{};
+                x[c] = at[0][(c0 + c) * 4];
+                y[c] = at[1][(c0 + c) * 4];
             }
 #pragma unroll
             for (int c = 0; c < kPart; ++c)
