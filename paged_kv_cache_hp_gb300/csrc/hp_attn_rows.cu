@@ -521,8 +521,10 @@ int launch_t(const RowsArgs& a, cudaStream_t st)
 int launch_rows(const RowsArgs& a, void* stream)
 {
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (a.selected && a.d_status && !a.check_all && cudaMemsetAsync(a.d_status, 0, sizeof(int), st) != cudaSuccess)
-        return HP_ERR_CUDA;
+    if (a.selected && a.d_status && !a.check_all) {
+        const int rc = launch_clear_status(a.d_status, stream);
+        if (rc) return rc;
+    }
     return a.bf16 ? launch_t<__nv_bfloat16>(a, st) : launch_t<__half>(a, st);
 }
 

@@ -518,10 +518,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_kernel(const S
     }
 }
 
+// (a dependent launch on either side: a memset takes 3 us of a stream of such calls)
+__global__ void clear_status_kernel(int* d_status)
+{
+    pdl_wait();
+    *d_status = HP_OK;
+}
+
 int start_status(bool all, int* d_status, cudaStream_t st)
 {
-    if (!d_status || all) return HP_OK;
-    return cudaMemsetAsync(d_status, 0, sizeof(int), st) == cudaSuccess ? HP_OK : HP_ERR_CUDA;
+    return !d_status || all ? (int)HP_OK : launch_clear_status(d_status, st);
 }
 
 template <typename T, int D>
@@ -541,6 +547,13 @@ int launch_scores_t(const ScoreArgs& a, unsigned grid, cudaStream_t st)
 }
 
 }  // namespace
+
+int launch_clear_status(int* d_status, void* stream)
+{
+    return launch_dependent(clear_status_kernel, 1, 1, 0, static_cast<cudaStream_t>(stream), d_status) == cudaSuccess
+               ? HP_OK
+               : HP_ERR_CUDA;
+}
 
 int launch_page_bounds(const BoundsArgs& a, void* stream)
 {

@@ -14,8 +14,8 @@ constexpr uint32_t kPagesMaxPage = 4096;        // slots of a page
 constexpr uint32_t kPagesMaxGroup = 16;         // query heads of a K/V head
 constexpr uint64_t kPagesMaxTokens = 1u << 31;  // tokens of a sequence stay below (32-bit token numbers)
 // Up to this many entries (pages, list entries) of up to so many rows one extra CTA looks at them all,
-// beside the others, and stores the status (under 5 us); beyond it the word is cleared by a memset before
-// the kernel (3 us) and whoever meets an error lowers it.
+// beside the others, and stores the status (under 5 us); beyond it a kernel of one thread before
+// this one clears the word, and whoever meets an error lowers it.
 constexpr uint64_t kPagesChecked = 1024, kRowsChecked = 128;
 
 // The queries of a batch: sequence s has q_ptr[s] .. q_ptr[s+1], its last tokens in order (q_ptr
@@ -74,6 +74,9 @@ struct SelectArgs {
     int* d_status;
 };
 int launch_select_pages(const SelectArgs& a, void* stream);
+
+// Clears the status word ahead of a kernel whose CTAs report what they meet.
+int launch_clear_status(int* d_status, void* stream);
 
 #ifdef __CUDACC__
 

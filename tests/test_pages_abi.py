@@ -159,4 +159,4 @@ def test_dependent_kernels_wait_before_they_look_at_memory():
             before = body[:at]
             assert "return" not in before and not re.search(r"a\.\w+\s*(\[|->)|index_at|find_query", before), (name, before)
             seen += 1
-    assert seen == 7
+    assert seen == 8
