@@ -10,11 +10,14 @@
 // and needs neither TMEM nor more than a warp; the weights go from one product's accumulators to the
 // other's operand by a transposed move inside the warp.
 //
-// A cluster of 1 to 16 CTAs takes a (row, head): its pages, cut into as many runs, and each run's
-// blocks of kTokens tokens to the CTA's four warps in turn.  Each warp has its own ring of stages
-// (cp.async) and its own maximum, sum and value sum; they meet in the CTA's shared memory, the CTAs'
-// in distributed shared memory (the answer is the same whichever finishes first, and no workspace is
-// needed), and what the prefix's kernel left joins there.
+// A cluster of 1 to 8 CTAs takes a (row, head): its pages, cut into as many runs, and each run's
+// blocks of kTokens tokens to the CTA's four warps in turn.  Each warp has its own ring (cp.async) of
+// three units, K or V of a block, refilled as each has been read, and its own maximum, sum and value
+// sum; they meet in the CTA's shared memory, the CTAs' in distributed shared memory (the answer is the
+// same whichever finishes first, and no workspace is needed), and what the prefix's kernel left joins
+// there.  Start and merge are 6 us of a CTA, so four of them share an SM (48 KiB of rings and 128
+// registers each): 64 sequences x 8 heads x 2,048 tokens of 128 dims take 83 us, 5.9 TB/s; 128 x 8 x 540
+// tokens behind a prefix 57 us, 5.2 TB/s (two CTAs with rings half as large again: 61).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -49,6 +52,12 @@ template <int D> struct Shape {
     static constexpr int kPad = D + 4;                    // floats of a row of the merge
 };
 
+// a / b, in 32 bits where both fit.
+__device__ __forceinline__ uint64_t small_quotient(uint64_t a, uint64_t b)
+{
+    return (a | b) >> 32 ? a / b : (uint32_t)a / (uint32_t)b;
+}
+
 struct Place {      // a page of the row's tokens
     uint64_t row0;  // its first slot in the pool
     uint32_t lo, hi;  // the slots that count
@@ -62,6 +71,7 @@ struct Source {
     uint64_t table[2];         // stretches: entry of page 0 of each slice
     uint32_t from, mid;        // tokens [0, mid) of the first if from is 0, [mid, seen) of the second
     uint32_t first_pages;      // pages of the first stretch
+    uint32_t mid_page;         // mid / P
 };
 
 template <bool LIST>
@@ -79,7 +89,7 @@ __device__ __forceinline__ int place_at(const RowsArgs& a, const Source& s, uint
         p->hi = t0 < s.seen ? (uint32_t)umin(a.P, s.seen - t0) : 0u;
     } else {
         const bool own = e >= s.first_pages;
-        const uint32_t j = own ? s.mid / a.P + (e - s.first_pages) : e, t0 = j * a.P;
+        const uint32_t j = own ? s.mid_page + (e - s.first_pages) : e, t0 = j * a.P;
         const uint32_t t_lo = own ? s.mid : 0u, t_hi = own ? s.seen : s.mid;
         phys = index_at(a.t.table, a.q.idx64, (own ? s.table[1] : s.table[0]) + j);
         if (phys >= a.t.num_pages) return HP_ERR_PAGE_ID;  // (the plan has looked)
@@ -102,10 +112,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : 4) rows_ke
     __shared__ int s_code;
     const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     pdl_wait();
-    const uint64_t unit = blockIdx.x / a.cluster;
-    const uint32_t rank = (uint32_t)(blockIdx.x % a.cluster);
+    const uint32_t unit = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster, h = unit % a.H;
     const uint64_t r = unit / a.H;
-    const uint32_t h = (uint32_t)(unit % a.H);
     if (LIST && r >= a.q.total_q) {  // the extra cluster's first CTA
         if (rank) return;
         int code = offsets_code(a.q.q_ptr, a.q.idx64, a.q.num_seqs, a.q.total_q);
@@ -148,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : 4) rows_ke
         src.hi = index_at(a.t.seq_ptr, a.q.idx64, q.seq + 1);
         src.len = (uint32_t)q.len;
         src.seen = q.seen;
-        src.list = a.selected + unit * a.k;
+        src.list = a.selected + (uint64_t)unit * a.k;
         count = a.k;
     } else {
         row = a.rows[r];
@@ -158,13 +166,15 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : 4) rows_ke
         src.table[1] = row.table;
         if (a.rec.workers == 0 && src.mid) {
             src.table[0] = a.groups[row.group].table;
-            src.first_pages = (src.mid + a.P - 1) / a.P;
+            src.first_pages = div_invariant(src.mid - 1, a.p_m, a.p_l) + 1;
         }
-        const uint32_t own = src.seen > src.mid ? (src.seen + a.P - 1) / a.P - src.mid / a.P : 0u;
+        src.mid_page = div_invariant(src.mid, a.p_m, a.p_l);
+        const uint32_t end = src.seen > src.mid ? src.seen : src.mid;  // the last token is end - 1
+        const uint32_t end_page = end ? div_invariant(end - 1, a.p_m, a.p_l) : 0u;
+        const uint32_t own = src.seen > src.mid ? end_page + 1 - src.mid_page : 0u;
         count = src.first_pages + own;
-        if (own) last = (src.seen - 1) % a.P + 1;
-        else if (src.mid) last = (src.mid - 1) % a.P + 1;
-        if (src.first_pages == 0 && own) skip = src.mid % a.P;
+        if (end) last = end - end_page * a.P;
+        if (src.first_pages == 0 && own) skip = src.mid - src.mid_page * a.P;
     }
     if (threadIdx.x == 0) s_code = HP_OK;
     // the prefix's records of query head 0: first, count, and where a second of each lies
@@ -174,9 +184,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : 4) rows_ke
         const PrefixGroup gr = a.groups[row.group];
         const uint32_t qt = kPrefixRows / a.G, tile = row.local / qt, left = gr.rows - tile * qt;
         const uint32_t rows = (left < qt ? left : qt) * a.G;
-        const uint64_t lw = (a.hdr->steps + a.rec.workers - 1) / a.rec.workers;
+        const uint64_t lw = small_quotient(a.hdr->steps + a.rec.workers - 1, a.rec.workers);
         const uint64_t s0 = gr.step0 + ((uint64_t)h * gr.tiles + tile) * gr.blocks;
-        const uint64_t v0 = s0 / lw, v1 = (s0 + gr.blocks - 1) / lw;
+        const uint64_t v0 = small_quotient(s0, lw), v1 = small_quotient(s0 + gr.blocks - 1, lw);
         rec = gr.rows0 + h * gr.records + (uint64_t)tile * qt * a.G + v0 * kPrefixRows + row.local % qt * a.G;
         recs = (uint32_t)(v1 - v0 + 1);
         if (rows <= kPrefixRows / 2) {
@@ -215,16 +225,18 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : 4) rows_ke
     const uint32_t ring = smem_u32(smem) + warp * Sh::kUnits * Sh::kUnit;
 
     // this CTA's blocks: places x of all pages' slots, kTokens to a block
-    const uint64_t x_end = count ? (uint64_t)(count - 1) * a.P + last : 0;
-    const uint64_t b0 = skip / kTokens, b1 = (x_end + kTokens - 1) / kTokens, all = b1 > b0 ? b1 - b0 : 0;
-    const uint64_t per = (all + a.cluster - 1) / a.cluster;
-    const uint64_t bb = b0 + umin(rank * per, all), be = umin(bb + per, b0 + all);
-    const uint64_t wblocks = (uint64_t)kWindow * a.P / kTokens;
-    for (uint64_t w0 = bb / wblocks * wblocks; w0 < be; w0 += wblocks) {
-        const uint64_t wb = bb > w0 ? bb : w0, we = umin(be, w0 + wblocks);
-        const uint32_t page0 = (uint32_t)(w0 * kTokens / a.P);
+    // (all below 2^32: the pages' slots number at most 2^31 and two pages more)
+    const uint32_t x_end = count ? (count - 1) * a.P + last : 0u;
+    const uint32_t b0 = skip / kTokens, b1 = (x_end + kTokens - 1) / kTokens, all = b1 > b0 ? b1 - b0 : 0u;
+    const uint32_t per = (all + a.cluster - 1) / a.cluster, at0 = rank * per;
+    const uint32_t bb = b0 + (at0 < all ? at0 : all), be = bb + per < b0 + all ? bb + per : b0 + all;
+    const uint32_t wblocks = kWindow * a.P / kTokens;
+    for (uint32_t win = bb / wblocks, w0 = win * wblocks; bb < be && w0 < be; ++win, w0 += wblocks) {
+        const uint32_t wb = bb > w0 ? bb : w0, we = be - w0 < wblocks ? be : w0 + wblocks;
+        const uint32_t page0 = win * kWindow;
         {
-            const uint32_t e0 = (uint32_t)(wb * kTokens / a.P), e1 = (uint32_t)umin(count, (we * kTokens + a.P - 1) / a.P);
+            const uint32_t e0 = div_invariant(wb * kTokens, a.p_m, a.p_l);
+            const uint32_t e_last = div_invariant(we * kTokens - 1, a.p_m, a.p_l), e1 = e_last < count ? e_last + 1 : count;
             __syncthreads();  // (the last window has been read)
             int code = HP_OK;
             for (uint32_t e = e0 + threadIdx.x; e < e1; e += kThreads)
@@ -237,11 +249,11 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : 4) rows_ke
         }
         const uint32_t x_base = page0 * a.P;  // (x below 2^32)
         const uint32_t pages = count - page0 < kWindow ? count - page0 : kWindow;
-        const uint32_t nb = (uint32_t)(we - wb), iters = nb > warp ? (nb - warp + kRowWarps - 1) / kRowWarps : 0;
+        const uint32_t nb = we - wb, iters = nb > warp ? (nb - warp + kRowWarps - 1) / kRowWarps : 0;
         uint64_t off = 0;  // this lane's token of the block placed last: where its rows begin
         auto place = [&](uint32_t it) {  // which tokens of the warp's block `it` count
             if (it >= iters) return 0u;
-            const uint32_t x = (uint32_t)((wb + warp + it * kRowWarps) * kTokens) - x_base + (lane % kTokens);
+            const uint32_t x = (wb + warp + it * kRowWarps) * kTokens - x_base + (lane % kTokens);
             const uint32_t e = div_invariant(x, a.p_m, a.p_l), slot = x - e * a.P;
             const Place p = e < pages ? window[e] : Place{0, 0, 0};
             const bool in = slot >= p.lo && slot < p.hi;

@@ -1,5 +1,5 @@
 // hp_tcgen05.cuh -- tcgen05 products, TMEM access and tensor-map loads shared by the
-// tensor-core kernels (hp_attn_tc.cu, hp_latent_tc.cu, hp_latent_prefill_tc.cu).
+// tensor-core kernels (hp_attn_tc.cu, hp_latent_tc.cu, hp_latent_prefill_tc.cu, hp_prefix_tc.cu).
 #pragma once
 
 #include <cuda.h>
