@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_kernel(const S
     constexpr uint32_t kTile = THREADS * PER, kCand = 2048;
     static_assert(PER <= 32 && kPerThread % 4 == 0, "a lane a ballot, bins in vectors");
     __shared__ __align__(16) uint32_t hist[kBins];
-    __shared__ uint32_t cand[kCand];
+    __shared__ __align__(16) uint32_t cand[kCand];
     __shared__ uint32_t s_room[kWarps], s_bin, s_left, s_cand;
     pdl_wait();
     const uint64_t r = blockIdx.x / a.H;
@@ -476,13 +476,35 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_kernel(const S
         need = s_left;
         shift = down;
         if (pass == 0) {
-            const uint32_t in = hist[s_bin];  // scores in the threshold's bin
+            const uint32_t in = hist[prefix];  // scores in the threshold's bin
             gathered = in <= kCand;
             if (gathered)
                 every([&](uint32_t x) {
                     if (x >> down == prefix) cand[atomicAdd(&s_cand, 1u)] = x;
                 });
             __syncthreads();  // (the bin has been read, the scores are gathered)
+            if (in <= THREADS) {
+                // few: a thread each counts those above and those equal (0 is no score's key)
+                if (threadIdx.x < 4) cand[in + threadIdx.x] = 0;
+                __syncthreads();
+                const uint32_t x = cand[threadIdx.x];
+                if (warp * 32 < in) {
+                    uint32_t above = 0, equal = 0;
+                    for (uint32_t j = 0; j < in; j += 4) {
+                        const uint4 y = *reinterpret_cast<const uint4*>(cand + j);
+                        above += (y.x > x) + (y.y > x) + (y.z > x) + (y.w > x);
+                        equal += (y.x == x) + (y.y == x) + (y.z == x) + (y.w == x);
+                    }
+                    if (threadIdx.x < in && above < need && need <= above + equal) {  // equal ones all say the same
+                        s_bin = x;
+                        s_left = need - above;
+                    }
+                }
+                __syncthreads();
+                prefix = s_bin;
+                need = s_left;
+                break;
+            }
         }
     }
     // above the threshold `prefix`, and the first `need` at it, in order
