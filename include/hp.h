@@ -862,12 +862,14 @@ int hp_attention_prefix_workspace_bytes(const hp_paged_desc* k_desc, uint64_t nu
  * codes of an append's new_ptr, then HP_ERR_GROUP, HP_ERR_PREFIX): if a rule fails nothing is written but
  * *d_status.  Head_dim 64 and 128 with pages of a multiple of 8 slots can read the prefix on the tensor
  * cores, and do where the slots that the table names (a page as often as it is named) hold
- * HP_PREFIX_TC_MIN_BYTES of keys and values or more; otherwise each query reads its prefix by itself.
- * (Measured on GB300: the former is the faster from about that size on.)  HP_ATTN_TENSOR_CORES in the descriptor's flags
+ * HP_PREFIX_TC_MIN_BYTES of keys and values or more, or HP_PREFIX_TC_MIN_TOKENS a sequence on average;
+ * otherwise each query reads its prefix by itself.
+ * (Measured on GB300: the former is the faster from about those sizes on.)  HP_ATTN_TENSOR_CORES in the descriptor's flags
  * asks for the former wherever the shape allows it, HP_ATTN_CUDA_CORES for the latter always, and so does
  * HP_HOST_MEMORY.
  */
 #define HP_PREFIX_TC_MIN_BYTES (384ull << 20)
+#define HP_PREFIX_TC_MIN_TOKENS 32768
 int hp_attention_prefix(const hp_paged_desc* k_desc, const void* v_pool, const void* group_ptr,
                         const void* prefix_lens, uint64_t num_groups, const void* q,
                         const void* q_ptr, uint64_t total_q, uint32_t num_q_heads, float scale,

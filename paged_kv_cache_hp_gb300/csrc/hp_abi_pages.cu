@@ -322,10 +322,13 @@ int prefix_run(PrefixCall& c, int first, void* stream)
     // merge are 8 us and more.  One group, 16-slot pages, 128 dims, a few tokens behind the prefix, us on the
     // tensor cores and without (by the bytes of K and V that the table's slots hold): 8 sequences and 8 K/V
     // heads at 67 MB 26 and 18, at 264 MB 36 and 33; 16 at 527 MB 51 and 58; 64 at 145 MB 38 and 30, at 538 MB 41 and
-    // 57, at 2.1 GB 57 and 159; 64 with one head at 67 MB 32 and 19, at 264 MB 41 and 34.
+    // 57, at 2.1 GB 57 and 159; 64 with one head at 67 MB 32 and 19, at 264 MB 41 and 34.  Sequences so long that
+    // eight CTAs a (query, head) are few: one sequence with 2 heads at 16,000 tokens 41 and 35, at 30,000 44 and 54, at
+    // 60,000 48 and 95; with one head 50 and 34, 55 and 54, 59 and 95.
     const u128 bytes = (u128)c.d.table_len * c.d.page_size * c.d.num_heads * c.d.head_dim * 4;
     if (!(c.d.flags & (HP_ATTN_CUDA_CORES | HP_HOST_MEMORY)) &&
-        ((c.d.flags & HP_ATTN_TENSOR_CORES) || bytes >= HP_PREFIX_TC_MIN_BYTES) &&
+        ((c.d.flags & HP_ATTN_TENSOR_CORES) || bytes >= HP_PREFIX_TC_MIN_BYTES ||
+         (u128)c.d.table_len * c.d.page_size >= (u128)HP_PREFIX_TC_MIN_TOKENS * c.d.num_seqs) &&
         hp::prefix_tc_fits(c.d.head_dim, c.d.page_size, c.d.num_pages)) {
         a.rec.workers = std::min<u64>((u64)sms, hp::kPrefixMaxSms);
         hp::PrefixTcArgs t{};

@@ -16,7 +16,7 @@
 // sum; they meet in the CTA's shared memory, the CTAs' in distributed shared memory (the answer is the
 // same whichever finishes first, and no workspace is needed), and what the prefix's kernel left joins
 // there.  Start and merge are 6 us of a CTA, so four of them share an SM (48 KiB of rings and 128
-// registers each): 64 sequences x 8 heads x 2,048 tokens of 128 dims take 83 us, 5.9 TB/s; 128 x 8 x 540
+// registers each): 64 sequences x 8 heads x 2,048 tokens of 128 dims take 80 us, 6.07 TB/s; 128 x 8 x 540
 // tokens behind a prefix 57 us, 5.2 TB/s (two CTAs with rings half as large again: 61).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>

@@ -12,9 +12,10 @@
 // are fp32.  Where an infinity meets a zero of the other half, the sum is not a number: such a page
 // (rare) is summed again from the definition.
 //
-// Selection.  Scores as integers in the order of the numbers; the threshold by three passes over 11,
-// 11 and 10 bits of them (a histogram in shared memory each), then one pass that writes the pages
-// above it and the first of those at it, in ascending order.
+// Selection.  Scores as integers in the order of the numbers; the threshold's 11 high bits by a histogram in
+// shared memory, the others by ranking the few scores that share those (or, where they are many, by two more
+// histograms of 11 and 10 bits), then one pass that writes the pages above it and the first of those at
+// it, in ascending order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -358,7 +359,7 @@ __device__ __forceinline__ uint32_t warps_before(uint32_t mine, uint32_t* room, 
 
 // One CTA a (query, K/V head).  Warp w holds the scores w * 32 * PER ... of a tile, score i * 32 + lane
 // of them in register i: coalesced loads, and ballots give their order.  Only the first pass counts
-// all scores; those in its threshold bin (a few hundred) are gathered in shared memory for the other two.
+// all scores; those in its threshold bin (a few hundred) are gathered in shared memory.
 // In the last one lane i of a warp writes what ballot i found: few bits are set where few pages are
 // taken.  Rows of more than a tile are read again each time (they lie in L2).  What bounds it is issue
 // and barriers: 1,900 instructions a warp of 1,024 scores and a dozen barriers (2,048 rows of up to 8,192 scores: 45

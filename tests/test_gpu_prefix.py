@@ -67,16 +67,16 @@ def test_attention_prefix_of_many_rows(hp, kernel, S, H, G, D, pre, tail):
     b.check(everything, rows={0, 1, S // 2, S - 1})
 
 
-@pytest.mark.parametrize("S,pre", [(3, 3000), (60, 3600)])
+@pytest.mark.parametrize("S,pre", [(3, 3000), (60, 3600), (1, 33000)])
 def test_the_librarys_choice(hp, S, pre):
-    """Below and above the size from which the prefix is read on the tensor cores (60 x 3,600 tokens of 8
-    heads of 128: 885 MB, most of it the same pages)."""
+    """Below and above the sizes from which the prefix is read on the tensor cores (60 x 3,600 tokens of 8
+    heads of 128: 885 MB, most of it the same pages; one sequence of 33,000 tokens)."""
     b = make(hp, [(S, pre)], [(3 * i) % 50 for i in range(S)], 8, 4, 128, 16, kernel="default", seed=S)
     run(b)
     assert b.code() == "HP_OK"
     b.check(everything, rows={0, S // 2, S - 1})
     out = b.out.clone()
-    other = hp.ATTN_TENSOR_CORES if S * pre * 4096 >= 384 << 20 else hp.ATTN_CUDA_CORES
+    other = hp.ATTN_TENSOR_CORES if S * pre * 4096 >= 384 << 20 or pre >= 32768 else hp.ATTN_CUDA_CORES
     b.desc = b.describe(flags=other)
     b.out.fill_(7.0)
     run(b)
