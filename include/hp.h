@@ -833,7 +833,9 @@ int hp_select_pages(const hp_paged_desc* desc, const void* q_ptr, uint64_t total
  * [total_q, num_q_heads, head_dim], the pool's type) gets zeros where there is nothing to see.  Scores,
  * softmax statistics and sums are fp32; the weights are rounded to the pool's type for the value
  * product (f16: times 2^7), the result once.  A key or value that is not finite spoils the queries that see its token
- * and no others.  k * page_size below 2^31 (HP_ERR_ARG).  Tokens are cut among up to 8 CTAs a
+ * and no others, as the formula has it: a score of NaN or +inf makes the row of out NaN; one of -inf weighs
+ * nothing (its value counts, as 0 times it), but where a query's tokens all score -inf its row is NaN (0 / 0).
+ * k * page_size below 2^31 (HP_ERR_ARG).  Tokens are cut among up to 8 CTAs a
  * (query, K/V head): the same call gives the same bits.
  */
 int hp_attention_pages(const hp_paged_desc* k_desc, const void* v_pool, const void* q,

@@ -4,7 +4,9 @@
 // For query row r and K/V head g, the G query heads of g at once:
 //   x_t = scale q . K(t),  m = max x_t,  o = sum_t 2^((x_t - m) log2 e) V(t) / sum_t 2^(...)
 // over the tokens t that the row's pages hold and it sees; one pass, with a maximum, a sum and a
-// value sum that are rescaled together.  Each element of K and V is used G times only, so what bounds it
+// value sum that are rescaled together.  (A part that saw a token has a maximum of at least kLowest, even where
+// all its scores are -inf: its value sum counts, 0 times infinities and all, and a row of such parts is 0 / 0.
+// Only a part without tokens has -inf.)  Each element of K and V is used G times only, so what bounds it
 // is memory: 4 D bytes a token and head.  The two products keep up on mma.sync with the tokens as its
 // 16 rows and the queries as its 8 columns (S^T = K Q^T, O^T = V^T P^T), which wastes nothing at G = 8
 // and needs neither TMEM nor more than a warp; the weights go from one product's accumulators to the
@@ -309,6 +311,10 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : 4) rows_ke
             __syncwarp();  // K has been read
             copy(vp, at, next);
             if (mask) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) m[nt][x] = fmaxf(m[nt][x], kLowest);
                 bool move = false;
 #pragma unroll
                 for (int b = 0; b < kSub; ++b)
@@ -330,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : 4) rows_ke
                             for (int b = 0; b < kSub; ++b) top = fmaxf(top, fmaxf(s[b][nt][x], s[b][nt][x + 2]));
 #pragma unroll
                             for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-                            const float f = m[nt][x] == -INFINITY ? 0.0f : exp2_approx(m[nt][x] - top);
+                            const float f = exp2_approx(m[nt][x] - top);
                             m[nt][x] = top;
                             l[nt][x] *= f;
 #pragma unroll
@@ -349,8 +355,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : 4) rows_ke
                         float w[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float base = m[nt][e & 1] == -INFINITY ? 0.0f : m[nt][e & 1];
-                            w[e] = exp2_approx(s[b][nt][e] - base + kWeightLift<T>);
+                            w[e] = exp2_approx(s[b][nt][e] - m[nt][e & 1] + kWeightLift<T>);
                             l[nt][e & 1] += w[e];
                         }
                         p[b][nt][0] = mma::transposed(pack2<T>(w[0], w[1]));
@@ -436,8 +441,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : 4) rows_ke
     auto record = [&](uint32_t v) {  // the v-th record's row of query head 0
         return second ? rec + (uint64_t)(v >> 1) * kPrefixRows + (v & 1) * second : rec + (uint64_t)v * kPrefixRows;
     };
-    // each source's weight for each query head (negative: it saw nothing), the CTAs' first, and one over
-    // the heads' sums; a warp a head
+    // each source's weight for each query head (negative: it saw no token), the CTAs' first, and one over
+    // the heads' sums (0 where no source saw one); a warp a head
     const uint32_t sources = a.cluster + recs;
     float* const weight = reinterpret_cast<float*>(smem) + kRowWarps * 8 * NT * Sh::kPad;  // [head][sources]
     for (uint32_t n = warp; n < a.G; n += kRowWarps) {
@@ -450,14 +455,14 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : 4) rows_ke
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         for (uint32_t v = lane; v < sources; v += 32) {
             const float2 ml = source(v);
-            const bool none = ml.x == -INFINITY && ml.y == 0.0f;
+            const bool none = ml.x == -INFINITY;
             const float f = none ? -1.0f : exp2_approx(ml.x - top);
             weight[n * sources + v] = f;
             if (!none) sum += ml.y * f;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) s_l[0][n] = sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (lane == 0) s_l[0][n] = top == -INFINITY ? 0.0f : 1.0f / sum;
     }
     __syncthreads();
     if (code == HP_OK)

@@ -321,11 +321,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint64_t pos = beg; pos < end && !stop;) {
             uint32_t blocks, stride, first, left;  // this half's blocks: first, first + stride, ... of the part's
             bool any, clears;                      // some row of the warp; this half clears V
-            float m = -INFINITY, l = 0.0f;
+            float m, l = 0.0f;
             {
                 const Part p = part_at(a, pos, end);
                 const uint32_t x = p.split ? row : 128 * t + row;  // row of the tile
                 blocks = p.blocks(t);
+                m = blocks ? kLowest : -INFINITY;  // (each of its blocks has a key)
                 stride = p.split ? 2 : 1;
                 first = p.split ? t : 0;
                 left = p.prefix - (p.j0 + first) * 128;
@@ -403,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!half) *told = mn = fmaxf(m, fmaxf(mx, *told));
                         named_sync(1 + t, kHalf);
                         if (half) mn = *told;
-                        const float f = m == -INFINITY ? 0.0f : exp2_approx(m - mn);
+                        const float f = exp2_approx(m - mn);
                         m = mn;
                         l *= f;
                         if (i > 0) {  // the scores of this block are complete, so O of the last one is
@@ -418,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    const float base = kWeightLift<T> - (m == -INFINITY ? 0.0f : m);
+                    const float base = kWeightLift<T> - m;
                     const uint64_t qs2 = pair_of(qs, qs), base2 = pair_of(base, base);
                     uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll

@@ -2,12 +2,15 @@
 // pages (hp_attn_rows.cu) and of the shared prefix in front of them (hp_prefix.cu, hp_prefix_tc.cu).
 #pragma once
 
+#include <cfloat>
 #include <cstdint>
 
 #include "hp_pages.cuh"
 
 namespace hp {
 
+// The least reference maximum (log2 units) of a part that saw a token; -inf where it saw none.
+constexpr float kLowest = -FLT_MAX;
 constexpr uint32_t kPrefixKeys = 128;      // keys of a step of the shared prefix
 constexpr uint32_t kPrefixRows = 256;      // (query, head) rows of a tile: two tiles of 128 to the tensor core
 constexpr uint32_t kPrefixMaxSms = 160;    // workers are counted for at most this many SMs
