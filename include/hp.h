@@ -831,8 +831,9 @@ int hp_select_pages(const hp_paged_desc* desc, const void* q_ptr, uint64_t total
  * twice; any order will do.  An index of a page that the sequence does not have skips the query's heads of
  * g (HP_ERR_LEN).  K from k_desc's pool, V from v_pool (same geometry and type).  out (device,
  * [total_q, num_q_heads, head_dim], the pool's type) gets zeros where there is nothing to see.  Scores,
- * softmax statistics and sums are fp32; the weights are rounded to the pool's type for the value
- * product (f16: times 2^7), the result once.  A key or value that is not finite spoils the queries that see its token
+ * softmax statistics and sums are fp32; a weight goes to the value product as two parts of the pool's
+ * type (f16: times 2^7), within 2^-15 (f16: 2^-21) of itself and 2^-32 of the row's largest, and the result is
+ * rounded once.  A key or value that is not finite spoils the queries that see its token
  * and no others, as the formula has it: a score of NaN or +inf makes the row of out NaN; one of -inf weighs
  * nothing (its value counts, as 0 times it), but where a query's tokens all score -inf its row is NaN (0 / 0).
  * k * page_size below 2^31 (HP_ERR_ARG).  Tokens are cut among up to 8 CTAs a
@@ -858,7 +859,8 @@ int hp_attention_prefix_workspace_bytes(const hp_paged_desc* k_desc, uint64_t nu
  * sequence's own slice.  The prefix need not end at a page's end: what a sequence's own slice
  * holds for the prefix's tokens is not read.  (A sequence by itself is a group of one, with any prefix; a prefix of 0 shares nothing.)
  *   out[r, qh] = softmax over t < seen_r (scale q . K(t)) V(t)
- * with K, V, q, q_ptr, out, rounding and empty rows as in hp_attention_pages.  Every query of a group
+ * with K, V, q, q_ptr, out, rounding and empty rows as in hp_attention_pages (on the tensor cores the weights
+ * of a prefix's tokens are rounded to the pool's type once).  Every query of a group
  * has to see its whole prefix, and every sequence to hold it (HP_ERR_PREFIX).  num_groups at most num_seqs, and 0 only without
  * sequences (HP_ERR_ARG).  The descriptor is always validated, as in hp_attention_decode (q_ptr with the
  * codes of an append's new_ptr, then HP_ERR_GROUP, HP_ERR_PREFIX): if a rule fails nothing is written but

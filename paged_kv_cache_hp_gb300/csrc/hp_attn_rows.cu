@@ -39,6 +39,7 @@ namespace {
 namespace cg = cooperative_groups;
 using tc::kWeightLift;
 using tc::pack2;
+using tc::split2;
 using tma::smem_u32;
 
 constexpr int kRowWarps = 4, kThreads = kRowWarps * 32;
@@ -346,8 +347,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : 4) rows_ke
                             }
                         }
                 }
-                // weights, rounded to T for the value product (it takes 16-bit operands only)
-                uint32_t p[kSub][NT][2];
+                // weights, as two parts of T for the value product (it takes 16-bit operands only, and waits
+                // for memory: the second part's products cost nothing that shows)
+                uint32_t p[kSub][NT][2], rest[kSub][NT][2];
 #pragma unroll
                 for (int b = 0; b < kSub; ++b)
 #pragma unroll
@@ -358,8 +360,13 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : 4) rows_ke
                             w[e] = exp2_approx(s[b][nt][e] - m[nt][e & 1] + kWeightLift<T>);
                             l[nt][e & 1] += w[e];
                         }
-                        p[b][nt][0] = mma::transposed(pack2<T>(w[0], w[1]));
-                        p[b][nt][1] = mma::transposed(pack2<T>(w[2], w[3]));
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            uint32_t hi, lo;
+                            split2<T>(w[2 * x], w[2 * x + 1], hi, lo);
+                            p[b][nt][x] = mma::transposed(hi);
+                            rest[b][nt][x] = mma::transposed(lo);
+                        }
                     }
                 mma::copies_wait<2>();
                 __syncwarp();
@@ -372,8 +379,10 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : 4) rows_ke
                         const uint32_t tok = 16 * b + (lane & 7) + ((lane >> 4) << 3), piece = 2 * c + ((lane >> 3) & 1);
                         mma::load4_transposed(v4, sv + tok * Sh::kRow + ((piece ^ (tok & 7)) << 4));
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                        for (int nt = 0; nt < NT; ++nt) {
                             mma::product<T>(o[nt][c], v4[0], v4[1], v4[2], v4[3], p[b][nt][0], p[b][nt][1]);
+                            mma::product<T>(o[nt][c], v4[0], v4[1], v4[2], v4[3], rest[b][nt][0], rest[b][nt][1]);
+                        }
                     }
                 }
             }

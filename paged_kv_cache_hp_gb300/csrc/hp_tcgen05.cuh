@@ -209,7 +209,26 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// log2 of the common factor of a row's softmax weights where the latent attention rounds them to T
+// Two weights (not negative) as hi + lo, each part of T: hi is the weight cut off (less than u of it is left, u a
+// unit of its last place: 2^-7 for bf16, 2^-10 for f16), lo the rest, rounded: the weight within u^2 / 2 of
+// itself.  lo has 2^-20 of the weight besides, so that it is not zero where hi is not (f16: down to a weight
+// of 2^-5): the products of both parts with an infinite value are that infinity.
+template <typename T> __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo);
+template <> __device__ __forceinline__ void split2<__nv_bfloat16>(float a, float b, uint32_t& hi, uint32_t& lo)
+{
+    hi = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+    lo = pack2<__nv_bfloat16>(fmaf(a, 1.0f + 0x1p-20f, -__uint_as_float(hi << 16)),
+                              fmaf(b, 1.0f + 0x1p-20f, -__uint_as_float(hi & 0xFFFF0000u)));
+}
+template <> __device__ __forceinline__ void split2<__half>(float a, float b, uint32_t& hi, uint32_t& lo)
+{
+    const __half2 h = __halves2half2(__float2half_rz(a), __float2half_rz(b));
+    const float2 x = __half22float2(h);
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    lo = pack2<__half>(fmaf(a, 1.0f + 0x1p-20f, -x.x), fmaf(b, 1.0f + 0x1p-20f, -x.y));
+}
+
+// log2 of the common factor of a row's softmax weights where they are rounded to T
 // for the value product (which takes 16-bit operands only); the sum carries it too, so it cancels.
 // f16's smallest normal number is 2^-14, so that with the reference maximum's weight at 1 a weight of
 // 2^-18 was off by up to 2^-7 of itself and one of 2^-26 was lost, while the fp32 sum held it: a long

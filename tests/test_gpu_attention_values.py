@@ -108,3 +108,37 @@ def test_queries_without_tokens_beside_minus_infinity(hp, op):
     b.hq[2, 1, 3] = -1.0
     got = attend(b, op)
     assert (got[0] == 0.0).all() and np.isnan(got[1:]).all()
+
+
+# --------------------------------------------------------------------------- weights
+@pytest.mark.parametrize("op", OPS[:2])
+@pytest.mark.parametrize("dtype,step", [("bf16", 2.0 ** -10), ("f16", 2.0 ** -13)])
+@pytest.mark.parametrize("S,pre,tails,G,D", [(1, 2, [0], 1, 128), (3, 40, [2, 0, 60], 4, 128), (2, 2000, [6, 10], 8, 64),
+                                             (1, 96, [32], 16, 64), (2, 640, [64, 2], 3, 256),
+                                             (70, 300, [2 * i for i in range(70)], 4, 128)])
+def test_weights_keep_more_bits_than_the_pool(hp, op, dtype, step, S, pre, tails, G, D):
+    """Half of the tokens score 0 and have value 1, half -step and -1: out = (1 - e^-step) / (1 + e^-step), about
+    step / 2.  Rounded to the pool's type the two weights are equal (step is an eighth of bf16's 2^-7 above 1 and
+    of f16's 2^-10, a quarter of those below), and out is zero.
+
+    The scores are exact.  A weight as two parts of the pool's type: the first leaves less than u of it (u = 2^-7,
+    2^-10, a unit of the last place), the second is rounded to half a unit of its own, u^2 / 2, with 2^-20
+    of the weight besides.  The scaled score and the exponential are off by less than 2^-21.  The value sum of n tokens
+    adds ones of both signs in turn, 16 at a time, so that its partial sums stay below 16 and its n / 8
+    additions (both parts') are off by 2^-20 each at most: 2^-23 of the n that it is divided by, and as much for
+    what joins the parts.  The sum of the weights is off by a factor.  The result is rounded once: half a unit."""
+    b = batch(hp, op, S, pre, tails, 1, G, D, dtype, seed=S)
+    for s in range(S):
+        for t in range(int(b.lens[s])):
+            p, i = place(b, s, t)
+            b.hk[p, i], b.hv[p, i] = 0.0, 1.0 - 2 * (t % 2)
+            b.hk[p, i, 0, 0] = -float(t % 2)
+    b.hq[:] = 0.0
+    b.hq[:, :, 0] = 1.0
+    b.scale = step
+    got = attend(b, op)
+    want = np.tanh(step / 2)
+    u = {"bf16": 2.0 ** -7, "f16": 2.0 ** -10}[dtype]
+    tol = want * u / 2 + u * u / 2 + 2.0 ** -20 + 2.0 ** -21 + 2.0 ** -22
+    assert tol < want / 4
+    assert np.abs(got - want).max() <= tol, np.abs(got - want).max() / want
