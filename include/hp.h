@@ -860,7 +860,8 @@ int hp_attention_prefix_workspace_bytes(const hp_paged_desc* k_desc, uint64_t nu
  * holds for the prefix's tokens is not read.  (A sequence by itself is a group of one, with any prefix; a prefix of 0 shares nothing.)
  *   out[r, qh] = softmax over t < seen_r (scale q . K(t)) V(t)
  * with K, V, q, q_ptr, out, rounding and empty rows as in hp_attention_pages (on the tensor cores the weights
- * of a prefix's tokens are rounded to the pool's type once).  Every query of a group
+ * of a prefix's tokens are rounded to the pool's type once, within 2^-8 of themselves, f16 2^-11:
+ * HP_ATTN_CUDA_CORES is for callers that want the two parts there too).  Every query of a group
  * has to see its whole prefix, and every sequence to hold it (HP_ERR_PREFIX).  num_groups at most num_seqs, and 0 only without
  * sequences (HP_ERR_ARG).  The descriptor is always validated, as in hp_attention_decode (q_ptr with the
  * codes of an append's new_ptr, then HP_ERR_GROUP, HP_ERR_PREFIX): if a rule fails nothing is written but
