@@ -56,6 +56,7 @@ hp::PageTable page_table(const hp_paged_desc& d)
     return hp::PageTable{d.seq_ptr, d.block_table, d.table_len, d.num_pages};
 }
 
+// (A call without rows, whose offsets say so, launches its extra CTA alone: they may not hold.)
 int reset_status(int* d_status, void* stream)
 {
     if (!d_status) return HP_OK;
@@ -93,7 +94,7 @@ HP_API int hp_page_bounds(const hp_paged_desc* desc, const void* new_ptr, uint64
     a.columns = (uint32_t)d.num_heads * a.row_half;
     a.units = d.num_seqs == 0 ? 0 : new_ptr ? total_new / a.P + 2 * d.num_seqs : d.num_seqs;
     if ((u128)a.units * ((a.columns + 127) / 128) + 1 > kGrid) return HP_ERR_OVERFLOW;
-    if (a.units == 0) return reset_status(d_status, stream);
+    if (!new_ptr && a.units == 0) return reset_status(d_status, stream);
     a.bf16 = d.dtype == HP_BF16;
     a.check_all = a.units <= hp::kPagesChecked;
     a.d_status = d_status;
@@ -116,7 +117,7 @@ HP_API int hp_page_scores(const hp_paged_desc* desc, const void* bounds, const v
     if (max_pages >> 31 || total_q >= kGrid || ((u128)total_q * d.num_heads * max_pages) >> 60) return HP_ERR_OVERFLOW;
     if (total_q && (!q || (max_pages && !scores))) return HP_ERR_NULL;
     if (misaligned(q, 16) || misaligned(scores, 4)) return HP_ERR_ALIGN;
-    if (total_q == 0 || d.num_seqs == 0) return reset_status(d_status, stream);
+    if (!q_ptr && total_q == 0) return reset_status(d_status, stream);
     int dev = 0;
     const u64 sms = (u64)hp::current_sms(&dev);
     if (sms == 0) return HP_ERR_CUDA;
@@ -159,7 +160,7 @@ HP_API int hp_select_pages(const hp_paged_desc* desc, const void* q_ptr, uint64_
     if (total_q && ((max_pages && !scores) || !selected)) return HP_ERR_NULL;
     if (misaligned(scores, 4) || misaligned(selected, 4)) return HP_ERR_ALIGN;
     if ((u128)total_q * d.num_heads + 1 > kGrid) return HP_ERR_OVERFLOW;
-    if (total_q == 0 || d.num_seqs == 0) return reset_status(d_status, stream);
+    if (!q_ptr && total_q == 0) return reset_status(d_status, stream);
     hp::SelectArgs a{};
     a.q = query_args(d, q_ptr, total_q);
     a.scores = scores;
@@ -219,7 +220,7 @@ HP_API int hp_attention_pages(const hp_paged_desc* k_desc, const void* v_pool, c
     if (k == 0 || (u64)k * d.page_size >> 31) return HP_ERR_ARG;
     if (total_q && !selected) return HP_ERR_NULL;
     if (misaligned(selected, 4)) return HP_ERR_ALIGN;
-    if (total_q == 0 || d.num_seqs == 0) return reset_status(d_status, stream);
+    if (!q_ptr && total_q == 0) return reset_status(d_status, stream);
     int dev = 0;
     const int sms = hp::current_sms(&dev);
     if (sms == 0) return HP_ERR_CUDA;
