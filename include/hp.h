@@ -775,8 +775,12 @@ int hp_latent_prefill(const hp_paged_desc* desc, uint32_t latent_dim, const void
  *   written, in any buffer.
  * - they are a serving step's calls: each is launched as a dependent of the stream's last kernel.
  * - but for hp_attention_prefix they need no plan and no workspace, and check what they read as they
- *   read it, as the appends do: a query (a page, for hp_page_bounds) whose slice, length or pages do not
- *   hold is skipped, its outputs left as they were.  *d_status gets the lowest of the codes found:
+ *   read it, as the appends do: a query whose slice or length does not hold (hp_attention_pages: or, for that
+ *   K/V head, whose list names a page that does not) is skipped, its outputs left as they were.
+ *   hp_page_bounds leaves out the pages that do not hold, hp_page_scores those whose entry of the table does
+ *   not, so that such a row of scores has new numbers beside what it had there before; hp_select_pages reads no table
+ *   and would take that for a score.  *d_status gets the lowest of the codes found (the call's own: a word that
+ *   several calls share has the last one's):
  *   HP_ERR_LEN (a slice too short for the tokens, outside the table or reversed; a page that the
  *   sequence does not have), HP_ERR_PAGE_ID, HP_ERR_OUT_SIZE, and HP_ERR_NEW_PTR_START, _ORDER or _END for
  *   the offsets (NEW_PTR_END: they end past total_q).  HP_PERMISSIVE changes nothing.
