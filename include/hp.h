@@ -849,8 +849,9 @@ int hp_attention_pages(const hp_paged_desc* k_desc, const void* v_pool, const vo
 
 /*
  * Bytes of device workspace (256-byte aligned) hp_attention_prefix needs: an entry per query row and
- * group, and fp32 records (max, sum, head_dim accumulators) of every (query, head) row and of 256 rows
- * for each SM.
+ * group and, for the shapes whose prefix can be read on the tensor cores (below; whatever the flags say), fp32
+ * records (max, sum, head_dim accumulators): two of every (query, head) row and 160 * 256 besides (256 for each SM,
+ * of up to 160).  It depends on the descriptor's head_dim and page_size and on the other arguments alone.
  */
 int hp_attention_prefix_workspace_bytes(const hp_paged_desc* k_desc, uint64_t num_groups,
                                         uint64_t total_q, uint32_t num_q_heads, uint64_t* bytes);

@@ -239,10 +239,13 @@ struct PrefixWs {
     u64 rows, groups, ml, acc, total;
 };
 
-int prefix_ws(u64 num_groups, u64 total_q, uint32_t num_q_heads, u64 head_dim, PrefixWs* w)
+int prefix_ws(u64 num_groups, u64 total_q, uint32_t num_q_heads, u64 head_dim, u64 page_size, PrefixWs* w)
 {
     if (num_groups >> 32 || total_q >> 32 || ((u128)total_q * num_q_heads) >> 40 || head_dim > 256) return HP_ERR_OVERFLOW;
-    const u64 records = 2 * total_q * num_q_heads + (u64)hp::kPrefixMaxSms * hp::kPrefixRows;
+    // (the tensor cores' kernel alone leaves records: two of a row where a tile has up to 128 of them)
+    const u64 records = hp::prefix_tc_shape(head_dim, page_size)
+                            ? 2 * total_q * num_q_heads + (u64)hp::kPrefixMaxSms * hp::kPrefixRows
+                            : 0;
     w->rows = hp::round_up_256(sizeof(hp::PrefixHeader));
     w->groups = w->rows + hp::round_up_256(total_q * sizeof(hp::PrefixRow));
     w->ml = w->groups + hp::round_up_256(num_groups * sizeof(hp::PrefixGroup));
@@ -272,7 +275,7 @@ int prefix_prepare(const hp_paged_desc* k_desc, const void* v_pool, const void* 
     if (misaligned(group_ptr, index_bytes(d.index_type)) || misaligned(prefix_lens, index_bytes(d.index_type)))
         return HP_ERR_ALIGN;
     PrefixWs w;
-    rc = prefix_ws(num_groups, total_q, num_q_heads, d.head_dim, &w);
+    rc = prefix_ws(num_groups, total_q, num_q_heads, d.head_dim, d.page_size, &w);
     if (rc) return rc;
     if (!workspace || misaligned(workspace, 256) || workspace_bytes < w.total) return HP_ERR_WORKSPACE;
     char* ws = static_cast<char*>(workspace);
@@ -368,7 +371,7 @@ HP_API int hp_attention_prefix_workspace_bytes(const hp_paged_desc* k_desc, uint
 {
     if (!k_desc || !bytes) return HP_ERR_NULL;
     PrefixWs w;
-    const int rc = prefix_ws(num_groups, total_q, num_q_heads, k_desc->head_dim, &w);
+    const int rc = prefix_ws(num_groups, total_q, num_q_heads, k_desc->head_dim, k_desc->page_size, &w);
     if (rc) return rc;
     *bytes = w.total;
     return HP_OK;

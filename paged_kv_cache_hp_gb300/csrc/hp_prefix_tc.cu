@@ -518,9 +518,14 @@ int launch_d(const PrefixTcArgs& a, cudaStream_t st)
 
 }  // namespace
 
+bool prefix_tc_shape(uint64_t head_dim, uint64_t page_size)
+{
+    return (head_dim == 64 || head_dim == 128) && page_size % 8 == 0;
+}
+
 bool prefix_tc_fits(uint64_t head_dim, uint64_t page_size, uint64_t num_pages)
 {
-    return (head_dim == 64 || head_dim == 128) && page_size % 8 == 0 && num_pages > 0 && num_pages * page_size < (1ull << 31);
+    return prefix_tc_shape(head_dim, page_size) && num_pages > 0 && num_pages * page_size < (1ull << 31);
 }
 
 uint32_t prefix_tc_box(uint64_t page_size)

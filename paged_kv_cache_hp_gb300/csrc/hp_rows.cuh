@@ -87,6 +87,7 @@ struct PrefixTcArgs {
     PrefixRecords rec;
     int* d_status;
 };
+bool prefix_tc_shape(uint64_t head_dim, uint64_t page_size);
 bool prefix_tc_fits(uint64_t head_dim, uint64_t page_size, uint64_t num_pages);
 uint32_t prefix_tc_box(uint64_t page_size);
 int launch_prefix_tc(const PrefixTcArgs& a, uint32_t head_dim, void* stream);

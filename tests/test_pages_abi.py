@@ -120,6 +120,29 @@ def test_prefix_workspace(hpc):
         assert hpc.status_name(f(ctypes.byref(d), *big, ctypes.byref(n))) == "HP_ERR_OVERFLOW"
 
 
+def test_prefix_workspace_holds_records_where_the_tensor_cores_can_leave_any(hpc):
+    """A row's 24 bytes of plan each, and for head_dim 64 and 128 with pages of a multiple of 8 two records a
+    (query, head) of a float2 and head_dim floats, with 160 x 256 more; the flags change nothing."""
+    f = hpc.lib().hp_attention_prefix_workspace_bytes
+
+    def size(total, hq, **kw):
+        n = ctypes.c_uint64(0)
+        assert f(ctypes.byref(desc(hpc, **kw)), 2, total, hq, ctypes.byref(n)) == 0
+        return n.value
+
+    for dim, page, records in ((64, 16, 1), (128, 8, 1), (128, 24, 1), (128, 4096, 1), (256, 16, 0), (128, 12, 0), (64, 1, 0)):
+        small = size(0, 32, head_dim=dim, page_size=page)
+        grown = size(4096, 32, head_dim=dim, page_size=page) - small
+        assert grown >= 4096 * 24 + records * 2 * 4096 * 32 * (dim * 4 + 8)
+        assert grown <= 4096 * 40 + records * 2 * 4096 * 32 * (dim * 4 + 8) + 1024
+        assert (small > 160 * 256 * dim * 4) == bool(records)
+        for flags in (hpc.ATTN_CUDA_CORES, hpc.ATTN_TENSOR_CORES, hpc.HOST_MEMORY):
+            assert size(0, 32, head_dim=dim, page_size=page, flags=flags) == small
+    d = desc(hpc, head_dim=256)
+    need = size(3, 4, head_dim=256)
+    assert call(hpc, "hp_attention_prefix", d, wsn=need - 1) == "HP_ERR_WORKSPACE"
+
+
 def test_status_names(hpc):
     assert hpc.status_name(-36) == "HP_ERR_GROUP" and hpc.status_name(-37) == "HP_ERR_PREFIX"
 
