@@ -64,7 +64,8 @@ int reset_status(int* d_status, void* stream)
                                                                                                        : HP_ERR_CUDA;
 }
 
-// CTAs of a (row, K/V head): as many as fill the SMs four times over, while each has a block for its warps.
+// CTAs of a (row, K/V head), up to eight: doubled while the grid has fewer than four to an SM (it can end at almost
+// eight; an SM holds four, two at head_dim 256 or more than 8 query heads a K/V head) and each then has 64 tokens.
 uint32_t cluster_of(u64 units, u64 tokens, int sms)
 {
     uint32_t c = 1;
@@ -323,12 +324,16 @@ int prefix_run(PrefixCall& c, int first, void* stream)
     if (sms == 0) return HP_ERR_CUDA;
     a.cluster = cluster_of(a.q.total_q * a.H, c.d.table_len * c.d.page_size / c.d.num_seqs, sms);
     // Each query reads its prefix by itself (through L2) while that is little: a launch, the records and their
-    // merge are 8 us and more.  One group, 16-slot pages, 128 dims, a few tokens behind the prefix, us on the
+    // merge are 8 us and more.  The host knows neither the prefixes nor who shares them, so this takes the table for
+    // one of prefixes that many share; where it is not, the tensor cores lose (below), and HP_ATTN_CUDA_CORES helps.  One group, 16-slot pages, 128 dims, a few tokens behind the prefix, us on the
     // tensor cores and without (by the bytes of K and V that the table's slots hold): 8 sequences and 8 K/V
     // heads at 67 MB 26 and 18, at 264 MB 36 and 33; 16 at 527 MB 51 and 58; 64 at 145 MB 38 and 30, at 538 MB 41 and
     // 57, at 2.1 GB 57 and 159; 64 with one head at 67 MB 32 and 19, at 264 MB 41 and 34.  Sequences so long that
     // eight CTAs a (query, head) are few: one sequence with 2 heads at 16,000 tokens 41 and 35, at 30,000 44 and 54, at
-    // 60,000 48 and 95; with one head 50 and 34, 55 and 54, 59 and 95.
+    // 60,000 48 and 95; with one head 50 and 34, 55 and 54, 59 and 95.  Little shared, 8 K/V heads: 256 sequences of 1,024
+    // tokens behind 16 shared ones 191 and 169, behind 128 189 and 174, of 500 behind 512 123 and 125, of 100 behind
+    // 900 68 and 95; groups of one: 64 of 2,000 tokens 132 and 94, 256 of 400 167 and 85, 4 of 33,000 122 and 92;
+    // prefixes of 0: 64 of 2,000 96 and 93, 256 of 500 101 and 98.
     const u128 bytes = (u128)c.d.table_len * c.d.page_size * c.d.num_heads * c.d.head_dim * 4;
     if (!(c.d.flags & (HP_ATTN_CUDA_CORES | HP_HOST_MEMORY)) &&
         ((c.d.flags & HP_ATTN_TENSOR_CORES) || bytes >= HP_PREFIX_TC_MIN_BYTES ||

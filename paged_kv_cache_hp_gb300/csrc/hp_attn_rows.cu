@@ -17,9 +17,10 @@
 // three units, K or V of a block, refilled as each has been read, and its own maximum, sum and value
 // sum; they meet in the CTA's shared memory, the CTAs' in distributed shared memory (the answer is the
 // same whichever finishes first, and no workspace is needed), and what the prefix's kernel left joins
-// there.  Start and merge are 6 us of a CTA, so four of them share an SM (48 KiB of rings and 128
-// registers each): 64 sequences x 8 heads x 2,048 tokens of 128 dims take 80 us, 6.07 TB/s; 128 x 8 x 540
-// tokens behind a prefix 57 us, 5.2 TB/s (two CTAs with rings half as large again: 61).
+// there.  Start and merge are 6 us of a CTA, so four of them share an SM (head_dim 64 and 128: 48 KiB of rings and
+// 128 registers each; two at 256, with 96 KiB, and with more than 8 query heads a K/V
+// head): 64 sequences x 8 heads x 2,048 tokens of 128 dims take 81 us, 6.0 TB/s; 128 x 8 x 540 tokens behind a
+// prefix 57 us, 5.2 TB/s (two CTAs with rings half as large again: 61).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
