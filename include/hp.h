@@ -839,7 +839,9 @@ int hp_select_pages(const hp_paged_desc* desc, const void* q_ptr, uint64_t total
  * type (f16: times 2^7), within 2^-15 (f16: 2^-21) of itself and 2^-32 of the row's largest, and the result is
  * rounded once.  A key or value that is not finite spoils the queries that see its token
  * and no others, as the formula has it: a score of NaN or +inf makes the row of out NaN; one of -inf weighs
- * nothing (its value counts, as 0 times it), but where a query's tokens all score -inf its row is NaN (0 / 0).
+ * nothing (its value counts, as 0 times it), but where a query's tokens all score -inf its row is NaN (0 / 0);
+ * an infinite value is that infinity in its dimension, NaN where its weight is so small that it is rounded to zero
+ * (f16: may be from 2^-12 of the row's largest on down).
  * k * page_size below 2^31 (HP_ERR_ARG).  Tokens are cut among up to 8 CTAs a
  * (query, K/V head): the same call gives the same bits.
  */

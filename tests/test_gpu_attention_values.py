@@ -110,6 +110,21 @@ def test_queries_without_tokens_beside_minus_infinity(hp, op):
     assert (got[0] == 0.0).all() and np.isnan(got[1:]).all()
 
 
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("t", [0, 77, 230])
+def test_an_infinite_value_with_a_weight_is_infinite(hp, op, dtype, t):
+    """Its token's key is zero, so that its weight is e^-4 of the largest or so: both parts of it times the infinity
+    have the infinity's sign."""
+    b = batch(hp, op, 2, 200, [31, 31], 1, 4, 128, dtype, seed=t)
+    for s in range(2):
+        p, i = place(b, s, t)
+        b.hk[p, i], b.hv[p, i, 0, 9], b.hv[p, i, 0, 10] = 0.0, float("inf"), float("-inf")
+    got = attend(b, op)
+    assert (got[:, :, 9] == np.inf).all() and (got[:, :, 10] == -np.inf).all()
+    assert np.isfinite(np.delete(got, (9, 10), 2)).all()
+
+
 # --------------------------------------------------------------------------- weights
 @pytest.mark.parametrize("op", OPS[:2])
 @pytest.mark.parametrize("dtype,step", [("bf16", 2.0 ** -10), ("f16", 2.0 ** -13)])
