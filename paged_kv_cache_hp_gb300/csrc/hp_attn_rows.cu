@@ -19,8 +19,8 @@
 // same whichever finishes first, and no workspace is needed), and what the prefix's kernel left joins
 // there.  Start and merge are 6 us of a CTA, so four of them share an SM (head_dim 64 and 128: 48 KiB of rings and
 // 128 registers each; two at 256, with 96 KiB, and with more than 8 query heads a K/V
-// head): 64 sequences x 8 heads x 2,048 tokens of 128 dims take 81 us, 6.0 TB/s; 128 x 8 x 540 tokens behind a
-// prefix 57 us, 5.2 TB/s (two CTAs with rings half as large again: 61).
+// head): 64 sequences x 8 heads x 2,048 tokens of 128 dims take 83 us, 5.9 TB/s; 128 x 8 x 540 tokens behind a
+// prefix 58 us, 5.1 TB/s (two CTAs with rings half as large again: 61).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -348,8 +348,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : 4) rows_ke
                             }
                         }
                 }
-                // weights, as two parts of T for the value product (it takes 16-bit operands only, and waits
-                // for memory: the second part's products cost nothing that shows)
+                // weights, as two parts of T for the value product, which takes 16-bit operands only (rounded
+                // once, two weights a step of T apart are equal; the second part's products are 1% of the
+                // time: 82.3 us without and 83.2 with them at the lists above)
                 uint32_t p[kSub][NT][2], rest[kSub][NT][2];
 #pragma unroll
                 for (int b = 0; b < kSub; ++b)
