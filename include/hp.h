@@ -836,7 +836,7 @@ int hp_select_pages(const hp_paged_desc* desc, const void* q_ptr, uint64_t total
  * g (HP_ERR_LEN).  K from k_desc's pool, V from v_pool (same geometry and type).  out (device,
  * [total_q, num_q_heads, head_dim], the pool's type) gets zeros where there is nothing to see.  Scores,
  * softmax statistics and sums are fp32; a weight goes to the value product as two parts of the pool's
- * type (f16: times 2^7), within 2^-15 (f16: 2^-21) of itself and 2^-32 of the row's largest, and the result is
+ * type (f16: times 2^7), within 2^-14 (f16: 2^-19) of itself and 2^-32 of the row's largest, and the result is
  * rounded once.  A key or value that is not finite spoils the queries that see its token
  * and no others, as the formula has it: a score of NaN or +inf makes the row of out NaN; one of -inf weighs
  * nothing (its value counts, as 0 times it), but where a query's tokens all score -inf its row is NaN (0 / 0);

@@ -210,8 +210,8 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
 }
 
 // Two weights (not negative) as hi + lo, each part of T: hi is the weight cut off (less than u of it is left, u a
-// unit of its last place: 2^-7 for bf16, 2^-10 for f16), lo the rest, rounded: the weight within u^2 / 2 of
-// itself.  lo has 2^-20 of the weight besides, so that it is not zero where hi is not (f16: down to a weight
+// unit of its last place: 2^-7 for bf16, 2^-10 for f16), lo the rest, rounded: together within u^2 / 2 of the
+// weight.  lo has 2^-20 of the weight besides, so that it is not zero where hi is not (f16: down to a weight
 // of 2^-5): the products of both parts with an infinite value are that infinity.
 template <typename T> __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo);
 template <> __device__ __forceinline__ void split2<__nv_bfloat16>(float a, float b, uint32_t& hi, uint32_t& lo)
