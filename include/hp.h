@@ -877,7 +877,7 @@ int hp_attention_prefix_workspace_bytes(const hp_paged_desc* k_desc, uint64_t nu
  * HP_PREFIX_TC_MIN_BYTES of keys and values or more, or HP_PREFIX_TC_MIN_TOKENS a sequence on average;
  * otherwise each query reads its prefix by itself.  (Measured on GB300: the former is the faster from about those sizes on
  * where several sequences share a prefix that is at least as long as what each has behind it.  The library
- * cannot see that.  Where prefixes are short beside what is behind them, or 0, the former takes 3 to 15% longer, where groups
+ * cannot see that.  Where prefixes are short beside what is behind them, or 0, the former takes 3 to 30% longer, where groups
  * are single sequences up to twice as long, unless the K/V heads of all are very few: then the latter is the one
  * to ask for.)  HP_ATTN_TENSOR_CORES in the descriptor's flags
  * asks for the former wherever the shape allows it, HP_ATTN_CUDA_CORES for the latter always, and so does

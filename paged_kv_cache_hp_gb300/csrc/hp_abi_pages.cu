@@ -331,7 +331,8 @@ int prefix_run(PrefixCall& c, int first, void* stream)
     // 57, at 2.1 GB 57 and 159; 64 with one head at 67 MB 32 and 19, at 264 MB 41 and 34.  Sequences so long that
     // eight CTAs a (query, head) are few: one sequence with 2 heads at 16,000 tokens 41 and 35, at 30,000 44 and 54, at
     // 60,000 48 and 95; with one head 50 and 34, 55 and 54, 59 and 95.  Little shared, 8 K/V heads: 256 sequences of 1,024
-    // tokens behind 16 shared ones 191 and 169, behind 128 189 and 174, of 500 behind 512 123 and 125, of 100 behind
+    // tokens behind 16 shared ones 191 and 169, behind 128 189 and 174, of 450 with 8
+    // query heads each behind 16 114 and 88, of 500 behind 512 123 and 125, of 100 behind
     // 900 68 and 95; groups of one: 64 of 2,000 tokens 132 and 94, 256 of 400 167 and 85, 4 of 33,000 122 and 92;
     // prefixes of 0: 64 of 2,000 96 and 93, 256 of 500 101 and 98.
     const u128 bytes = (u128)c.d.table_len * c.d.page_size * c.d.num_heads * c.d.head_dim * 4;
